@@ -8,7 +8,14 @@
  *   uly_attention     joint text+image attention on the head-sharded layout,
  *   uly_to_seq        head-sharded -> seq-sharded exchange of the output,
  *   uly_sp_attention  the three fused: attention that reads the seq-sharded
- *                     shards directly and writes the seq-sharded output.
+ *                     shards directly and writes the seq-sharded output,
+ *
+ * and, around it in a layer and in training:
+ *
+ *   uly_norm_rope     the RMS norm of the q and k heads and the rotation by
+ *                     position, on the shards, before the exchange,
+ *   uly_*_backward    the gradients of the attention (staged and fused) and
+ *                     of uly_norm_rope.
  *
  * Sources (web pages, cited by title and section):
  *  [cp]   flashdreams core/attention/cp.py, ContextParallelAttention.
@@ -142,7 +149,9 @@ int uly_plan_set_wait_limit(uly_plan* plan, uint64_t ns);
  * K_0, V_0, K_1, V_1, ...), so the consumer's bounded wait expires and the
  * call reports ULY_ERR_TIMEOUT through uly_sync_status (nothing hangs or
  * faults; the kernels drain and free TMEM).  -1 (the default) disables it.
- * Outputs of a call made with the hook set are undefined. */
+ * The backward kernels withhold the load of that number of each CTA's moving
+ * tiles (Q for dk and dv, K for dq).  Outputs of a call made with the hook set
+ * are undefined. */
 int uly_plan_test_withhold_fill(uly_plan* plan, int32_t fill);
 
 /* Checked build (the library compiled with -DULY_CHECKED=1): every index
@@ -371,6 +380,123 @@ int uly_ring_attention(uly_plan* plan, const void* const* qh, const void* const*
                        const int32_t* chunk_bounds, float scale, int32_t head_groups, const float* q_scale,
                        const float* k_scale, const float* v_scale, void* const* oh, float* const* lse,
                        void* stream);
+
+/* The gradient of uly_attention on the head-sharded layout: from the forward's
+ * inputs qh, kh, vh, its outputs oh and lse and the output's gradient doh, the
+ * gradients dqh, dkh, dvh (bf16, the shapes of qh, kh, vh).  The probabilities
+ * are recomputed: with s, the admitted keys and the masked-row convention as in
+ * the forward, for rank r, head j, batch b,
+ *   P_nm  = exp(s_nm - lse_n) over admitted (n, m)
+ *   delta_n = <oh_n, doh_n>           dS_nm = P_nm (<doh_n, v_m> - delta_n)
+ *   dqh_n = scale sum_m dS_nm k_m
+ *   dkh_m = scale sum_n dS_nm q_n     dvh_m = sum_n P_nm doh_n
+ * where the sums over n also run over the Hq/Hkv query heads that share a kv
+ * head.  Sums are held in f32 (P and dS are rounded to bf16 as operands of the
+ * products); every output is rounded to bf16 once, is written in full, and is
+ * the same bits on every call.  A query row whose lse is -inf, and one that
+ * ULY_ROWS_ZERO zeroes, has dqh = 0 and adds nothing to dkh and dvh; a key that
+ * no query attends to has dkh = dvh = 0.  What q, o, lse and do hold in a row
+ * that ULY_ROWS_ZERO zeroes, and k and v in a masked key (ULY_ROWS_SDPA and
+ * _ZERO), does not matter, NaN included.
+ *   The forms of the forward that give the same oh and lse (head groups,
+ *   uly_attention_merge and uly_ring_attention over all chunks) have this
+ *   gradient too: pass the mask of all keys.
+ *   lse: host array of P device pointers to f32 [B, Nq, Hq/P], required.
+ *   key_mask, key_ranges, n_ranges, scale: the forward's.
+ *   workspace: device memory of at least
+ *   uly_attention_backward_workspace(plan) bytes, 256-byte aligned, owned by
+ *   the caller; its contents mean nothing before and after the call.  The call
+ *   uses no other scratch of the plan, so calls with one plan may overlap on
+ *   the GPU, also with its forward calls, when their workspaces differ.
+ * Outputs and workspace must not overlap each other or any input.
+ * bf16 plans only: ULY_ERR_UNSUPPORTED for e4m3.  ULY_ERR_INVALID for NULL,
+ * misaligned or overlapping pointers, a workspace that is too small, a NULL lse
+ * and as uly_attention.  The call may be captured into a CUDA graph (not the
+ * first one on a device, which sets the kernels' shared-memory limit). */
+int uly_attention_backward(const uly_plan* plan, const void* const* qh, const void* const* kh, const void* const* vh,
+                           const void* const* oh, const float* const* lse, const void* const* doh,
+                           const uint8_t* key_mask, const int32_t* key_ranges, int32_t n_ranges, float scale,
+                           void* const* dqh, void* const* dkh, void* const* dvh, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* The gradient of uly_sp_attention: as uly_attention_backward, read from the
+ * seq-sharded shards q, k, v, o, lse (f32 [B, Rq, Hq]), dout and written to
+ * seq-sharded dq, dk, dv, with no staging copy.  It is the gradient of the
+ * call as a function of the P shards:
+ *  - the replicated rows' output reaches every shard, so their output gradient
+ *    is the sum of the shards' dout (formed in f32, rounded to bf16);
+ *  - the owner of a head (rank h / (Hq/P), k/v: h / (Hkv/P)) reads the
+ *    replicated rows of its own shard, so its copies of dq, dk, dv hold that
+ *    head's gradient and the other shards' copies hold zero.  The gradient of
+ *    text rows that all shards share is the sum over the copies.
+ *  - of o and lse in replicated rows the owner's copy is read. */
+int uly_sp_attention_backward(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
+                              const void* const* o, const float* const* lse, const void* const* dout,
+                              const uint8_t* key_mask, const int32_t* key_ranges, int32_t n_ranges, float scale,
+                              void* const* dq, void* const* dk, void* const* dv, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of the two calls above for this plan (about 8 bytes per
+ * query row and head, 12 with ULY_ROWS_SELF, and the replicated rows of one
+ * q shard), or -1 for a NULL plan. */
+int64_t uly_attention_backward_workspace(const uly_plan* plan);
+
+/* ---- pairs that the rotation turns -------------------------------------- */
+#define ULY_PAIRS_INTERLEAVED 0 /* (2i, 2i + 1) */
+#define ULY_PAIRS_HALF 1        /* (i, i + D/2) */
+
+/* RMS norm of every q and k head and the rotation by its row's position, one
+ * pass over the seq-sharded shards, before the exchange or the fused
+ * attention.  For a head x (D values) of the row with global key index g:
+ *   n = x / sqrt(mean(x^2) + eps) * weight
+ *   out[a_i] = n[a_i] cos[g][i] - n[b_i] sin[g][i]
+ *   out[b_i] = n[a_i] sin[g][i] + n[b_i] cos[g][i]     for the D/2 pairs (a_i, b_i)
+ * in f32, rounded to bf16 once.  Every shard's copy of the replicated rows is
+ * computed.
+ *   q, k: shards [B, rows, H, D] as in uly_sp_attention, except that
+ *     consecutive rows may be q_row_stride (k_row_stride) elements apart, a
+ *     multiple of 8 and at least H * D, with batches rows * stride apart: the
+ *     q and k parts of a packed projection are read in place.  0 = dense.
+ *   q_weight, k_weight: device f32 [D], or NULL for ones.
+ *   cos_table, sin_table: device f32 [table_batches, Nk, D/2] (16-byte
+ *     aligned), rows in the global key order (uly_plan_rows(plan, 3) rows; for
+ *     KV_PREFIX the q rows use the rows from R on); table_batches is B, or 1
+ *     for tables that all batches share.  Both NULL: no rotation (then
+ *     table_batches is ignored).
+ *   pairs: ULY_PAIRS_INTERLEAVED or ULY_PAIRS_HALF.  eps > 0.
+ *   q_out, k_out: dense bf16 shards; q_out[p] may be q[p] when q is dense.
+ *   q and q_out (or k and k_out) may both be NULL: that tensor is skipped.
+ * bf16 plans only: ULY_ERR_UNSUPPORTED for e4m3.  ULY_ERR_INVALID for bad
+ * strides, tables, pairs, eps, NULL or misaligned pointers, or outputs that
+ * overlap each other or an input (other than as above).  The call uses no
+ * scratch of the plan, so calls with one plan may overlap on the GPU. */
+int uly_norm_rope(const uly_plan* plan, const void* const* q, const void* const* k, int64_t q_row_stride,
+                  int64_t k_row_stride, const float* q_weight, const float* k_weight, const float* cos_table,
+                  const float* sin_table, int32_t table_batches, int32_t pairs, float eps, void* const* q_out,
+                  void* const* k_out, void* stream);
+
+/* The gradient of uly_norm_rope: from its inputs and the gradients of its
+ * outputs (dq_out, dk_out, dense bf16 shards), the gradients dq, dk of q and k
+ * (dense bf16 shards) and dq_weight, dk_weight of the weights (device f32 [D];
+ * NULL: not computed).  With z = x / sqrt(mean(x^2) + eps) and dn the gradient
+ * turned back by the rotation:
+ *   dx = (dn weight - z mean(dn weight z)) / sqrt(mean(x^2) + eps)
+ *   dweight = sum of dn z over all heads of all rows of all shards
+ * in f32; dweight is added up in a fixed order (the same bits on every call on
+ * a device).  dq[p] may be dq_out[p], or q[p] when q is dense (then q is gone).
+ *   workspace: device memory of uly_norm_rope_backward_workspace(plan) bytes,
+ *   256-byte aligned, owned by the caller, for its own use during the call;
+ *   may be NULL when both dweights are.
+ * Other arguments and errors as uly_norm_rope. */
+int uly_norm_rope_backward(const uly_plan* plan, const void* const* q, const void* const* k, int64_t q_row_stride,
+                           int64_t k_row_stride, const void* const* dq_out, const void* const* dk_out,
+                           const float* q_weight, const float* k_weight, const float* cos_table,
+                           const float* sin_table, int32_t table_batches, int32_t pairs, float eps, void* const* dq,
+                           void* const* dk, float* dq_weight, float* dk_weight, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of uly_norm_rope_backward, or -1 for a NULL plan. */
+int64_t uly_norm_rope_backward_workspace(const uly_plan* plan);
 
 /* Allocation-free fused attention.  The source pages have no counterpart:
  * this entry point exists for callers that cannot call cudaMalloc -- an

@@ -24,6 +24,7 @@ ULY_OK, ULY_ERR_INVALID, ULY_ERR_UNSUPPORTED, ULY_ERR_CUDA, ULY_ERR_TIMEOUT = 0,
 REP_MODES = {"none": 0, "prefix": 1, "suffix": 2, "kv_prefix": 3}
 DTYPES = {"bf16": 0, "e4m3": 1}
 MASKED_ROWS = {"sdpa": 0, "zero": 1, "self": 2}
+PAIRS = {"interleaved": 0, "half": 1}
 MAX_RANKS = 16
 
 # every symbol include/uly.h declares
@@ -32,7 +33,9 @@ EXPORTS = ("uly_plan_create", "uly_plan_destroy", "uly_plan_set_wait_limit", "ul
            "uly_sp_attention", "uly_sync_status", "uly_status_string", "uly_device_sm_count",
            "uly_sp_attention_noalloc", "uly_lse_merge", "uly_pipelined_attention", "uly_plan_create_varlen",
            "uly_plan_shard_rows", "uly_sp_attention_host", "uly_checked_violations",
-           "uly_plan_test_check_narrow", "uly_attention_merge", "uly_noalloc_sync_status", "uly_ring_attention")
+           "uly_plan_test_check_narrow", "uly_attention_merge", "uly_noalloc_sync_status", "uly_ring_attention",
+           "uly_attention_backward", "uly_sp_attention_backward", "uly_attention_backward_workspace",
+           "uly_norm_rope", "uly_norm_rope_backward", "uly_norm_rope_backward_workspace")
 
 
 class UlyError(RuntimeError):
@@ -97,6 +100,16 @@ def lib():
                                               i32, vp, vp, vp, vpp, vp, vp]
         L.uly_sp_attention_host.argtypes = [vp, vpp, vpp, vpp, vpp, vpp, vpp, vp, vp, i32, ctypes.c_float, i32,
                                             vp, vp, vp, vpp, vpp, vp]
+        bwd = [vp, vpp, vpp, vpp, vpp, vpp, vpp, vp, vp, i32, ctypes.c_float, vpp, vpp, vpp, vp, i64, vp]
+        L.uly_attention_backward.argtypes = bwd
+        L.uly_sp_attention_backward.argtypes = bwd
+        L.uly_attention_backward_workspace.argtypes = [vp]
+        L.uly_attention_backward_workspace.restype = i64
+        L.uly_norm_rope.argtypes = [vp, vpp, vpp, i64, i64, vp, vp, vp, vp, i32, i32, ctypes.c_float, vpp, vpp, vp]
+        L.uly_norm_rope_backward.argtypes = [vp, vpp, vpp, i64, i64, vpp, vpp, vp, vp, vp, vp, i32, i32,
+                                             ctypes.c_float, vpp, vpp, vp, vp, vp, i64, vp]
+        L.uly_norm_rope_backward_workspace.argtypes = [vp]
+        L.uly_norm_rope_backward_workspace.restype = i64
         L.uly_device_sm_count.argtypes = [ctypes.c_int]
         L.uly_device_sm_count.restype = i32
         L.uly_checked_violations.argtypes = [i32]
@@ -162,6 +175,51 @@ def _want_scales(dtype, q_scale, k_scale, v_scale, Hq, Hkv, device):
         if t is None:
             raise ValueError("%s: e4m3 inputs need per-head scales" % what)
         _want(t, (n,), ("torch.float32",), what, device)
+
+
+def _want_rows(ts, shapes, what, device):
+    """bf16 shards whose rows may be more than a row apart (a part of a packed
+    projection); returns the row stride in elements, 0 for dense ones."""
+    import torch
+    if ts is None or len(ts) != len(shapes):
+        raise ValueError("%s: expected %d tensors, got %s" % (what, len(shapes), None if ts is None else len(ts)))
+    stride = None
+    for i, (t, (B, rows, H, D)) in enumerate(zip(ts, shapes)):
+        w = "%s[%d]" % (what, i)
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.device.index != device:
+            raise ValueError("%s: expected a CUDA tensor on device %d" % (w, device))
+        if t.dtype != torch.bfloat16:
+            raise ValueError("%s: element type %s, expected torch.bfloat16" % (w, t.dtype))
+        if tuple(t.shape) != (B, rows, H, D):
+            raise ValueError("%s: shape %s, expected %s" % (w, tuple(t.shape), (B, rows, H, D)))
+        sb, sr, sh, sd = t.stride()
+        if sd != 1 or (H > 1 and sh != D):
+            raise ValueError("%s: the heads of a row must be contiguous" % w)
+        if rows == 1 and B == 1:
+            continue  # any stride
+        rs = sr if rows > 1 else sb
+        if rs < H * D or rs % 8 or (B > 1 and sb != rows * rs):
+            raise ValueError("%s: rows must be a multiple of 8 elements apart, at least %d, and batches rows * that "
+                             "apart" % (w, H * D))
+        if stride not in (None, rs):
+            raise ValueError("%s: the shards' rows must be the same distance apart" % w)
+        stride = rs
+    return stride or 0
+
+
+def _workspace(ws, nbytes, device, stream):
+    """The caller's workspace, checked, or a new one on the call's stream."""
+    import torch
+    if ws is None:
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(ws, torch.Tensor) or ws.device.type != "cuda" or ws.device.index != device \
+            or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < nbytes:
+        raise ValueError("workspace: expected a contiguous uint8 tensor of at least %d bytes on device %d"
+                         % (nbytes, device))
+    return ws
 
 
 def _ptr(t) -> int | None:
@@ -323,30 +381,30 @@ class Plan:
         _check(lib().uly_plan_test_check_narrow(self._h, int(rows)), "uly_plan_test_check_narrow")
 
     # ---- argument checks against the plan's shape
-    def _check_seq(self, q=None, k=None, v=None, o=None, lse=None):
+    def _check_seq(self, q=None, k=None, v=None, o=None, lse=None, names=("q", "k", "v", "o")):
         B, D, dev, P = self.B, self.D, self.device, self.P
         el = _ELEM[self.dtype]
         if q is not None:
-            _want_list(q, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], el, "q", dev)
-        for t, what in ((k, "k"), (v, "v")):
+            _want_list(q, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], el, names[0], dev)
+        for t, what in ((k, names[1]), (v, names[2])):
             if t is not None:
                 _want_list(t, [(B, self.shard_rows(p, True), self.Hkv, D) for p in range(P)], el, what, dev)
         if o is not None:
-            _want_list(o, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], ("torch.bfloat16",), "o", dev)
+            _want_list(o, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], ("torch.bfloat16",), names[3], dev)
         if lse is not None:
             _want_list(lse, [(B, self.shard_rows(p), self.Hq) for p in range(P)], ("torch.float32",), "lse", dev)
 
-    def _check_heads(self, qh=None, kh=None, vh=None, oh=None, lse=None):
+    def _check_heads(self, qh=None, kh=None, vh=None, oh=None, lse=None, names=("qh", "kh", "vh", "oh")):
         B, D, dev, P = self.B, self.D, self.device, self.P
         el = _ELEM[self.dtype]
         hq, hkv = self.Hq // P, self.Hkv // P
         if qh is not None:
-            _want_list(qh, [(B, self.heads_rows_q, hq, D)] * P, el, "qh", dev)
-        for t, what in ((kh, "kh"), (vh, "vh")):
+            _want_list(qh, [(B, self.heads_rows_q, hq, D)] * P, el, names[0], dev)
+        for t, what in ((kh, names[1]), (vh, names[2])):
             if t is not None:
                 _want_list(t, [(B, self.heads_rows_kv, hkv, D)] * P, el, what, dev)
         if oh is not None:
-            _want_list(oh, [(B, self.heads_rows_q, hq, D)] * P, ("torch.bfloat16",), "oh", dev)
+            _want_list(oh, [(B, self.heads_rows_q, hq, D)] * P, ("torch.bfloat16",), names[3], dev)
         if lse is not None:
             _want_list(lse, [(B, self.heads_rows_q, hq)] * P, ("torch.float32",), "lse", dev)
 
@@ -421,6 +479,117 @@ class Plan:
                      q_scale=None, k_scale=None, v_scale=None, lse=None, stream=None):
         self._attn(lib().uly_sp_attention, "uly_sp_attention", q, k, v, o, key_mask, key_ranges, scale,
                    head_groups, q_scale, k_scale, v_scale, lse, stream, fused=True)
+
+    # ---- gradients
+    def attention_backward_workspace(self) -> int:
+        """Bytes of workspace of attention_backward and sp_attention_backward."""
+        return int(lib().uly_attention_backward_workspace(self._h))
+
+    def _attn_backward(self, fn, name, q, k, v, o, lse, do, dq, dk, dv, key_mask, key_ranges, scale, workspace,
+                       stream, check):
+        for t, what in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"), (dk, "dk"),
+                        (dv, "dv")):
+            if t is None:
+                raise ValueError("%s: %s is missing" % (name[4:], what))
+        if self.dtype != "bf16":
+            raise UlyError(ULY_ERR_UNSUPPORTED, name)
+        check(q, k, v, o, lse)
+        check(do, dk, dv, dq, names=("do", "dk", "dv", "dq"))
+        _want_mask(key_mask, key_ranges, self.B, self.heads_rows_kv, self.device)
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.D)
+        n_ranges = 0 if key_ranges is None else int(key_ranges.shape[1])
+        workspace = _workspace(workspace, self.attention_backward_workspace(), self.device, stream)
+        _check(fn(self._h, _ptr_array(q), _ptr_array(k), _ptr_array(v), _ptr_array(o), _ptr_array(lse),
+                  _ptr_array(do), _ptr(key_mask), _ptr(key_ranges), n_ranges, ctypes.c_float(scale), _ptr_array(dq),
+                  _ptr_array(dk), _ptr_array(dv), _ptr(workspace), workspace.numel(), _stream(stream)), name)
+
+    def attention_backward(self, qh, kh, vh, oh, lse, doh, dqh, dkh, dvh, key_mask=None, key_ranges=None, scale=None,
+                           workspace=None, stream=None):
+        """The gradient of attention (uly_attention_backward): dqh, dkh, dvh
+        from the forward's inputs, its outputs oh and lse, and doh.  workspace:
+        a uint8 tensor of attention_backward_workspace() bytes; by default one
+        is allocated on the call's stream."""
+        self._attn_backward(lib().uly_attention_backward, "uly_attention_backward", qh, kh, vh, oh, lse, doh, dqh,
+                            dkh, dvh, key_mask, key_ranges, scale, workspace, stream, self._check_heads)
+
+    def sp_attention_backward(self, q, k, v, o, lse, do, dq, dk, dv, key_mask=None, key_ranges=None, scale=None,
+                              workspace=None, stream=None):
+        """The gradient of sp_attention (uly_sp_attention_backward) on the
+        seq-sharded shards.  Replicated rows: the shards' do add up, and the
+        gradients go to the copy of the shard that owns the head."""
+        self._attn_backward(lib().uly_sp_attention_backward, "uly_sp_attention_backward", q, k, v, o, lse, do, dq,
+                            dk, dv, key_mask, key_ranges, scale, workspace, stream, self._check_seq)
+
+    # ---- norm and rotation of q and k heads
+    def norm_rope_backward_workspace(self) -> int:
+        """Bytes of workspace of norm_rope_backward."""
+        return int(lib().uly_norm_rope_backward_workspace(self._h))
+
+    def _norm_args(self, q, k, outs, q_weight, k_weight, cos, sin, pairs):
+        """Check one norm_rope call; returns (row strides, table batches, pairs)."""
+        B, D, dev, P = self.B, self.D, self.device, self.P
+        if self.dtype == "bf16":
+            strides = []
+            for x, is_kv, what in ((q, False, "q"), (k, True, "k")):
+                shapes = [(B, self.shard_rows(p, is_kv), self.Hkv if is_kv else self.Hq, D) for p in range(P)]
+                strides.append(0 if x is None else _want_rows(x, shapes, what, dev))
+                for t, name in outs[is_kv]:
+                    if (t is None) != (x is None):
+                        raise ValueError("%s: given or left out with %s" % (name, what))
+                    if t is not None:
+                        _want_list(t, shapes, ("torch.bfloat16",), name, dev)
+        else:
+            strides = [0, 0]  # the C ABI refuses the plan
+        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _want(w, (D,), ("torch.float32",), what, dev)
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin: both or neither")
+        batches = 1
+        if cos is not None:
+            batches = cos.shape[0] if cos.dim() == 3 else 1
+            shape = (self.heads_rows_kv, D // 2) if cos.dim() == 2 else (batches, self.heads_rows_kv, D // 2)
+            if batches not in (1, B):
+                raise ValueError("cos: %d batches, expected 1 or %d" % (batches, B))
+            _want(cos, shape, ("torch.float32",), "cos", dev)
+            _want(sin, shape, ("torch.float32",), "sin", dev)
+        if pairs not in PAIRS:
+            raise ValueError("pairs: %r, expected one of %s" % (pairs, ", ".join(PAIRS)))
+        return strides, batches, PAIRS[pairs]
+
+    def norm_rope(self, q, k, q_out, k_out, q_weight=None, k_weight=None, cos=None, sin=None, pairs="interleaved",
+                  eps=1e-6, stream=None):
+        """RMS norm of every q and k head and the rotation by its row's
+        position, in one pass over the seq-sharded shards (uly_norm_rope).
+        cos, sin: f32 [Nk, D/2] or [B, Nk, D/2] in the global key order.  q and
+        k may be parts of a packed projection (rows a fixed stride apart); q
+        with q_out, or k with k_out, may be None."""
+        strides, batches, pr = self._norm_args(q, k, (((q_out, "q_out"),), ((k_out, "k_out"),)), q_weight, k_weight,
+                                               cos, sin, pairs)
+        _check(lib().uly_norm_rope(self._h, _ptr_array(q), _ptr_array(k), strides[0], strides[1], _ptr(q_weight),
+                                   _ptr(k_weight), _ptr(cos), _ptr(sin), batches, pr, ctypes.c_float(eps),
+                                   _ptr_array(q_out), _ptr_array(k_out), _stream(stream)), "uly_norm_rope")
+
+    def norm_rope_backward(self, q, k, dq_out, dk_out, dq, dk, q_weight=None, k_weight=None, cos=None, sin=None,
+                           dq_weight=None, dk_weight=None, pairs="interleaved", eps=1e-6, workspace=None,
+                           stream=None):
+        """The gradient of norm_rope (uly_norm_rope_backward): dq, dk and, when
+        given, dq_weight and dk_weight (f32 [D]) from the gradients dq_out,
+        dk_out of its outputs."""
+        outs = (((dq_out, "dq_out"), (dq, "dq")), ((dk_out, "dk_out"), (dk, "dk")))
+        strides, batches, pr = self._norm_args(q, k, outs, q_weight, k_weight, cos, sin, pairs)
+        for w, what in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+            if w is not None:
+                _want(w, (self.D,), ("torch.float32",), what, self.device)
+        if dq_weight is not None or dk_weight is not None or workspace is not None:
+            workspace = _workspace(workspace, self.norm_rope_backward_workspace(), self.device, stream)
+        _check(lib().uly_norm_rope_backward(self._h, _ptr_array(q), _ptr_array(k), strides[0], strides[1],
+                                            _ptr_array(dq_out), _ptr_array(dk_out), _ptr(q_weight), _ptr(k_weight),
+                                            _ptr(cos), _ptr(sin), batches, pr, ctypes.c_float(eps), _ptr_array(dq),
+                                            _ptr_array(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+                                            0 if workspace is None else workspace.numel(), _stream(stream)),
+               "uly_norm_rope_backward")
 
     def pipelined_attention(self, q, k, v, qh, kh, vh, oh, o, key_mask=None, key_ranges=None, scale=None,
                             head_groups=0, q_scale=None, k_scale=None, v_scale=None, stream=None,

@@ -693,9 +693,14 @@ int uly_plan_test_check_narrow(uly_plan* plan, int32_t rows) {
 int64_t uly_checked_violations(int32_t reset) {
   if (!kChecked) return -1;
   if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-  const uint64_t a = layout_violations(reset != 0), b = attn_violations(reset != 0);
-  if (a == ~0ull || b == ~0ull) return -1;
-  return static_cast<int64_t>(a + b);
+  const uint64_t n[4] = {layout_violations(reset != 0), attn_violations(reset != 0), bwd_violations(reset != 0),
+                         norm_violations(reset != 0)};
+  uint64_t sum = 0;
+  for (uint64_t v : n) {
+    if (v == ~0ull) return -1;
+    sum += v;
+  }
+  return static_cast<int64_t>(sum);
 }
 
 int uly_plan_test_withhold_fill(uly_plan* plan, int32_t fill) {
@@ -1122,6 +1127,353 @@ int32_t uly_device_sm_count(int device) {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return -1;
   return n;
 }
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------
+// Gradients of the attention, norm and rotation of q and k heads and its
+// gradient.  These calls keep nothing in the plan: their scratch is the
+// caller's workspace.
+namespace {
+
+// Memory that a call reads (in) or writes (out).
+struct Span {
+  uintptr_t lo, hi;
+  bool out;
+  int pair;  // >= 0: an output may be exactly the input of the same pair number
+};
+constexpr int kMaxSpans = 9 * kMaxRanks + 8;
+struct Spans {
+  Span s[kMaxSpans];
+  int n = 0;
+  void add(const void* p, int64_t bytes, bool out, int pair = -1) {
+    if (!p || bytes <= 0) return;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    s[n++] = Span{a, a + static_cast<uintptr_t>(bytes), out, pair};
+  }
+  // does an output overlap anything else?
+  bool clash() const {
+    for (int i = 0; i < n; ++i) {
+      if (!s[i].out) continue;
+      for (int j = 0; j < n; ++j) {
+        if (j == i || s[i].lo >= s[j].hi || s[j].lo >= s[i].hi) continue;
+        if (!s[j].out && s[i].pair >= 0 && s[i].pair == s[j].pair && s[i].lo == s[j].lo && s[i].hi == s[j].hi) continue;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+int64_t align256(int64_t n) { return (n + 255) & ~static_cast<int64_t>(255); }
+
+int bwd_q_tiles(const uly_plan* pl) {
+  Seg segs[kMaxSegs];
+  return count_units(segs, build_segs(pl, 0, 0, segs), kTileRows);
+}
+
+// Workspace of the attention's gradient: the tile tables, the row statistics,
+// and (fused) the replicated rows of do summed over the shards.
+struct BwdWork {
+  int64_t bits, active_bits, active_inv, active, n_active, nl, dl, do_rep, total, stat_stride;
+};
+BwdWork bwd_work(const uly_plan* pl) {
+  const uly_desc& d = pl->d;
+  BwdWork w;
+  const int64_t nt = static_cast<int64_t>(d.B) * pl->n_kv_tiles;
+  w.stat_stride = static_cast<int64_t>(d.B) * d.Hq * bwd_q_tiles(pl) * kTileRows;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t a = at;
+    at = align256(at + bytes);
+    return a;
+  };
+  w.bits = take(nt * 16);
+  w.active_bits = take(nt * 16);
+  w.active_inv = take(nt * 16);
+  w.active = take(nt * 4);
+  w.n_active = take(static_cast<int64_t>(d.B) * 4);
+  w.nl = take(w.stat_stride * 4 * (d.masked_rows == ULY_ROWS_SELF ? 2 : 1));
+  w.dl = take(w.stat_stride * 4);
+  const bool rep_q = d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX;
+  w.do_rep = take(rep_q ? static_cast<int64_t>(d.B) * d.R * d.Hq * d.D * 2 : 0);
+  w.total = at;
+  return w;
+}
+
+int run_backward(const uly_plan* pl, int fused, const void* const* q, const void* const* k, const void* const* v,
+                 const void* const* o, const float* const* lse, const void* const* dout, const uint8_t* key_mask,
+                 const int32_t* key_ranges, int32_t n_ranges, float scale, void* const* dq, void* const* dk,
+                 void* const* dv, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!pl) return ULY_ERR_INVALID;
+  const uly_desc& d = pl->d;
+  const int P = d.P;
+  int rc;
+  if (d.dtype != ULY_BF16) return ULY_ERR_UNSUPPORTED;
+  const void* const* const lists[9] = {q, k, v, o, dout, const_cast<const void* const*>(dq),
+                                       const_cast<const void* const*>(dk), const_cast<const void* const*>(dv),
+                                       reinterpret_cast<const void* const*>(lse)};
+  for (int i = 0; i < 8; ++i)
+    if ((rc = check_ptrs(lists[i], P))) return rc;
+  if (!lse) return ULY_ERR_INVALID;
+  for (int i = 0; i < P; ++i)
+    if (!lse[i] || (reinterpret_cast<uintptr_t>(lse[i]) & 3u)) return ULY_ERR_INVALID;
+  if (key_mask && key_ranges) return ULY_ERR_INVALID;
+  if (key_ranges && n_ranges < 1) return ULY_ERR_INVALID;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return ULY_ERR_INVALID;
+  const BwdWork w = bwd_work(pl);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
+    return ULY_ERR_INVALID;
+  if ((rc = check_device(pl))) return rc;
+  // launch limits of grid.y and grid.z, and of the row statistics' grid.x
+  if (d.Hq > 65535 || d.B > 65535) return ULY_ERR_UNSUPPORTED;
+
+  const int hq_l = d.Hq / P, hkv_l = d.Hkv / P;
+  const int64_t hq_t = fused ? d.Hq : hq_l, hkv_t = fused ? d.Hkv : hkv_l;  // heads of one tensor
+  static thread_local BwdParams p;  // ~13 KB: keep it off the stack
+  static thread_local Spans spans;
+  memset(&p, 0, sizeof(p));
+  spans.n = 0;
+  p.n_qseg = build_segs(pl, fused, 0, p.qseg);
+  p.n_kseg = build_segs(pl, fused, 1, p.kseg);
+  int acc = 0;
+  for (int i = 0; i < p.n_qseg; ++i) {  // 128-row q tiles
+    p.qseg[i].first = acc;
+    acc += (p.qseg[i].len + kTileRows - 1) / kTileRows;
+  }
+  p.n_q_tiles = acc;
+  p.n_kv_tiles = pl->n_kv_tiles;
+  p.fused = fused;
+  p.P = P;
+  p.B = d.B;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.Hq_l = hq_l;
+  p.Hkv_l = hkv_l;
+  p.G = d.Hq / d.Hkv;
+  p.q_row_stride = hq_t * d.D * 2;
+  p.kv_row_stride = hkv_t * d.D * 2;
+  p.lse_row_stride = hq_t;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  spans.add(workspace, workspace_bytes, true);
+  for (int i = 0; i < P; ++i) {
+    const int64_t rq = fused ? pl->rq_p[i] : pl->nq, rk = fused ? pl->rk_p[i] : pl->nk;
+    p.shard_len[i] = pl->lens[i];
+    p.o[i] = static_cast<const uint8_t*>(o[i]);
+    p.dout[i] = static_cast<const uint8_t*>(dout[i]);
+    p.lse[i] = lse[i];
+    p.dq[i] = static_cast<uint8_t*>(dq[i]);
+    p.dk[i] = static_cast<uint8_t*>(dk[i]);
+    p.dv[i] = static_cast<uint8_t*>(dv[i]);
+    p.q_batch_stride[i] = rq * p.q_row_stride;
+    p.kv_batch_stride[i] = rk * p.kv_row_stride;
+    p.lse_batch_stride[i] = rq * p.lse_row_stride;
+    const int64_t qb = d.B * p.q_batch_stride[i], kb = d.B * p.kv_batch_stride[i];
+    spans.add(q[i], qb, false);
+    spans.add(k[i], kb, false);
+    spans.add(v[i], kb, false);
+    spans.add(o[i], qb, false);
+    spans.add(dout[i], qb, false);
+    spans.add(lse[i], 4 * d.B * p.lse_batch_stride[i], false);
+    spans.add(dq[i], qb, true);
+    spans.add(dk[i], kb, true);
+    spans.add(dv[i], kb, true);
+  }
+  if (spans.clash()) return ULY_ERR_INVALID;
+  for (int i = 0; i < P; ++i) {
+    const int64_t rq = fused ? pl->rq_p[i] : pl->nq, rk = fused ? pl->rk_p[i] : pl->nk;
+    const int hq = static_cast<int>(hq_t), hk = static_cast<int>(hkv_t);
+    if ((rc = encode_map(&p.tq[i], q[i], d.D, hq, rq, d.B, false)) ||
+        (rc = encode_map(&p.tdo[i], dout[i], d.D, hq, rq, d.B, false)) ||
+        (rc = encode_map(&p.tk[i], k[i], d.D, hk, rk, d.B, false)) ||
+        (rc = encode_map(&p.tv[i], v[i], d.D, hk, rk, d.B, false)))
+      return rc;
+  }
+  if (fused && (d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX)) {
+    p.do_rep = ws + w.do_rep;
+    if ((rc = encode_map(&p.tdo_rep, p.do_rep, d.D, d.Hq, d.R, d.B, false))) return rc;
+  }
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.tile_bits = reinterpret_cast<uint4*>(ws + w.bits);
+  p.active_bits = reinterpret_cast<uint4*>(ws + w.active_bits);
+  p.active_inv = reinterpret_cast<uint4*>(ws + w.active_inv);
+  p.active = reinterpret_cast<int32_t*>(ws + w.active);
+  p.n_active = reinterpret_cast<int32_t*>(ws + w.n_active);
+  p.nl = reinterpret_cast<float*>(ws + w.nl);
+  p.dl = reinterpret_cast<float*>(ws + w.dl);
+  p.stat_stride = w.stat_stride;
+  p.masked_rows = d.masked_rows;
+  p.withhold_fill = pl->withhold_fill;
+  p.status = pl->status;
+  p.wait_ns = pl->wait_ns;
+
+  static thread_local TileParams tp;
+  memset(&tp, 0, sizeof(tp));
+  memcpy(tp.kseg, p.kseg, sizeof(tp.kseg));
+  tp.n_kseg = p.n_kseg;
+  tp.n_kv_tiles = p.n_kv_tiles;
+  tp.B = d.B;
+  tp.Nk = static_cast<int32_t>(pl->nk);
+  tp.key_mask = key_mask;
+  tp.key_ranges = key_ranges;
+  tp.n_ranges = key_ranges ? n_ranges : 0;
+  tp.all_tiles = d.masked_rows == ULY_ROWS_SELF;
+  tp.tile_bits = reinterpret_cast<uint4*>(ws + w.bits);
+  tp.active = reinterpret_cast<int32_t*>(ws + w.active);
+  tp.active_bits = reinterpret_cast<uint4*>(ws + w.active_bits);
+  tp.active_inv = reinterpret_cast<uint4*>(ws + w.active_inv);
+  tp.n_active = reinterpret_cast<int32_t*>(ws + w.n_active);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (launch_tiles(tp, s) != cudaSuccess) return ULY_ERR_CUDA;
+  if (launch_attention_backward(p, d.D, s) != cudaSuccess) return ULY_ERR_CUDA;
+  return ULY_OK;
+}
+
+int64_t norm_work(const uly_plan* pl) {
+  return align256((static_cast<int64_t>(pl->sm_count) * kNormCtasPerSm + 2) * pl->d.D * 4);
+}
+
+// Shared by uly_norm_rope (g = nullptr) and its gradient.
+int run_norm(const uly_plan* pl, bool backward, const void* const* const* x, const int64_t* row_stride,
+             const void* const* const* g, const float* const* weight, const float* cos_table, const float* sin_table,
+             int32_t table_batches, int32_t pairs, float eps, void* const* const* y, float* const* dweight,
+             void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!pl) return ULY_ERR_INVALID;
+  const uly_desc& d = pl->d;
+  const int P = d.P;
+  int rc;
+  if (d.dtype != ULY_BF16) return ULY_ERR_UNSUPPORTED;
+  if (pairs != ULY_PAIRS_INTERLEAVED && pairs != ULY_PAIRS_HALF) return ULY_ERR_INVALID;
+  if (!(eps > 0.f) || !(eps < 3.0e38f)) return ULY_ERR_INVALID;
+  if ((cos_table == nullptr) != (sin_table == nullptr) || !aligned16(cos_table) || !aligned16(sin_table))
+    return ULY_ERR_INVALID;
+  if (cos_table && table_batches != 1 && table_batches != d.B) return ULY_ERR_INVALID;
+  if (!x[0] && !x[1]) return ULY_ERR_INVALID;
+  static thread_local NormParams p;
+  static thread_local Spans spans;
+  memset(&p, 0, sizeof(p));
+  spans.n = 0;
+  p.img_off[0] = 0;
+  for (int i = 0; i < P; ++i) p.img_off[i + 1] = p.img_off[i] + pl->lens[i];
+  p.P = P;
+  p.R = d.R;
+  p.mode = d.rep_mode;
+  p.eps = eps;
+  p.cos_table = cos_table;
+  p.sin_table = sin_table;
+  p.table_rows = pl->nk;
+  p.table_batch_stride = table_batches > 1 ? pl->nk * (d.D / 2) : 0;
+  if (cos_table) {
+    const int64_t bytes = static_cast<int64_t>(table_batches) * pl->nk * (d.D / 2) * 4;
+    spans.add(cos_table, bytes, false);
+    spans.add(sin_table, bytes, false);
+  }
+  bool any_dw = false;
+  for (int t = 0; t < 2; ++t) {
+    if ((x[t] == nullptr) != (y[t] == nullptr) || (backward && (x[t] == nullptr) != (g[t] == nullptr)))
+      return ULY_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(weight[t]) & 3u) return ULY_ERR_INVALID;
+    if (backward && dweight[t]) {
+      if (!x[t] || (reinterpret_cast<uintptr_t>(dweight[t]) & 3u)) return ULY_ERR_INVALID;
+      any_dw = true;
+      p.dweight[t] = dweight[t];
+      spans.add(dweight[t], d.D * 4, true);
+    }
+    if (!x[t]) continue;
+    if ((rc = check_ptrs(x[t], P)) || (rc = check_ptrs(const_cast<const void* const*>(y[t]), P)) ||
+        (backward && (rc = check_ptrs(g[t], P))))
+      return rc;
+    const int H = t ? d.Hkv : d.Hq;
+    const int64_t dense = static_cast<int64_t>(H) * d.D, rs = row_stride[t] ? row_stride[t] : dense;
+    if (rs < dense || (rs & 7) || rs > (1LL << 40)) return ULY_ERR_INVALID;
+    p.heads[t] = H;
+    p.row_bytes[t] = rs * 2;
+    p.weight[t] = weight[t];
+    spans.add(weight[t], d.D * 4, false);
+    for (int i = 0; i < P; ++i) {
+      const int64_t rows = t ? pl->rk_p[i] : pl->rq_p[i], n = rows * d.B;
+      p.x[t][i] = static_cast<const uint8_t*>(x[t][i]);
+      p.y[t][i] = static_cast<uint8_t*>(y[t][i]);
+      p.shard_rows[t][i] = static_cast<int32_t>(rows);
+      p.tensor_rows[t][i] = n;
+      p.rows_begin[t][i + 1] = p.rows_begin[t][i] + n;
+      const int pair = t * kMaxRanks + i;
+      spans.add(x[t][i], ((n - 1) * rs + dense) * 2, false, pair);
+      spans.add(y[t][i], n * dense * 2, true, pair);
+      if (backward) {
+        p.g[t][i] = static_cast<const uint8_t*>(g[t][i]);
+        spans.add(g[t][i], n * dense * 2, false, pair);
+      }
+    }
+  }
+  if (backward && any_dw) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < norm_work(pl))
+      return ULY_ERR_INVALID;
+    p.partial = static_cast<float*>(workspace);
+    spans.add(workspace, workspace_bytes, true);
+  }
+  if (spans.clash()) return ULY_ERR_INVALID;
+  if ((rc = check_device(pl))) return rc;
+  if (launch_norm_rope(p, d.D, pairs == ULY_PAIRS_HALF, backward, pl->sm_count, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
+    return ULY_ERR_CUDA;
+  return ULY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int uly_attention_backward(const uly_plan* plan, const void* const* qh, const void* const* kh, const void* const* vh,
+                           const void* const* oh, const float* const* lse, const void* const* doh,
+                           const uint8_t* key_mask, const int32_t* key_ranges, int32_t n_ranges, float scale,
+                           void* const* dqh, void* const* dkh, void* const* dvh, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return run_backward(plan, 0, qh, kh, vh, oh, lse, doh, key_mask, key_ranges, n_ranges, scale, dqh, dkh, dvh,
+                      workspace, workspace_bytes, stream);
+}
+
+int uly_sp_attention_backward(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
+                              const void* const* o, const float* const* lse, const void* const* dout,
+                              const uint8_t* key_mask, const int32_t* key_ranges, int32_t n_ranges, float scale,
+                              void* const* dq, void* const* dk, void* const* dv, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  return run_backward(plan, 1, q, k, v, o, lse, dout, key_mask, key_ranges, n_ranges, scale, dq, dk, dv, workspace,
+                      workspace_bytes, stream);
+}
+
+int64_t uly_attention_backward_workspace(const uly_plan* plan) { return plan ? bwd_work(plan).total : -1; }
+
+int uly_norm_rope(const uly_plan* plan, const void* const* q, const void* const* k, int64_t q_row_stride,
+                  int64_t k_row_stride, const float* q_weight, const float* k_weight, const float* cos_table,
+                  const float* sin_table, int32_t table_batches, int32_t pairs, float eps, void* const* q_out,
+                  void* const* k_out, void* stream) {
+  const void* const* const x[2] = {q, k};
+  void* const* const y[2] = {q_out, k_out};
+  const float* const w[2] = {q_weight, k_weight};
+  const int64_t rs[2] = {q_row_stride, k_row_stride};
+  return run_norm(plan, false, x, rs, nullptr, w, cos_table, sin_table, table_batches, pairs, eps, y, nullptr, nullptr,
+                  0, stream);
+}
+
+int uly_norm_rope_backward(const uly_plan* plan, const void* const* q, const void* const* k, int64_t q_row_stride,
+                           int64_t k_row_stride, const void* const* dq_out, const void* const* dk_out,
+                           const float* q_weight, const float* k_weight, const float* cos_table,
+                           const float* sin_table, int32_t table_batches, int32_t pairs, float eps, void* const* dq,
+                           void* const* dk, float* dq_weight, float* dk_weight, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  const void* const* const x[2] = {q, k};
+  const void* const* const g[2] = {dq_out, dk_out};
+  void* const* const y[2] = {dq, dk};
+  const float* const w[2] = {q_weight, k_weight};
+  float* const dw[2] = {dq_weight, dk_weight};
+  const int64_t rs[2] = {q_row_stride, k_row_stride};
+  return run_norm(plan, true, x, rs, g, w, cos_table, sin_table, table_batches, pairs, eps, y, dw, workspace,
+                  workspace_bytes, stream);
+}
+
+int64_t uly_norm_rope_backward_workspace(const uly_plan* plan) { return plan ? norm_work(plan) : -1; }
 
 }  // extern "C"
 
