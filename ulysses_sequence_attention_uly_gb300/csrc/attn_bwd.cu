@@ -101,31 +101,56 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, ui
     tma_load_4d(dst + pn * BCfg<D>::kPanelBytes, m, bar, pn * 64, head, row, b);
 }
 
+// Shared-memory descriptors (128-byte swizzle; tc.cuh): the upper word is the
+// same for every operand here, the lower one is the start address / 16 and the
+// leading byte offset.  One thread issues every MMA, and what it does between
+// two of them delays the tensor core, so the lower words are a base and a
+// constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_cols(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | ((static_cast<uint32_t>(kTileRows) * 128u >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(blo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+
 // D[tmem] = A B^T of two 128-row tiles in shared memory, both K-major (the
-// sum runs over D)
+// sum runs over D); alo, blo from desc_rows
 template <int D>
-__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t alo, uint32_t blo) {
   using C = BCfg<D>;
-  const uint64_t hi = sdesc_sw128(0, 16, 1024);
-  const uint32_t alo = (a & 0x3FFFFu) >> 4, blo = (b & 0x3FFFFu) >> 4;
 #pragma unroll
   for (int k = 0; k < C::kDSteps; ++k) {
-    const uint32_t off = ((k >> 2) * C::kPanelBytes + (k & 3) * 32) >> 4;
-    mma_bf16_ss(d, hi | (alo + off), hi | (blo + off), C::kIdescS, k > 0);
+    constexpr uint32_t kPanel = C::kPanelBytes >> 4;
+    const uint32_t off = (k >> 2) * kPanel + (k & 3) * 2;
+    mma_ss(d, alo + off, blo + off, C::kIdescS, k > 0);
   }
 }
 
 // D[tmem] (+)= A B with A a 128 x 128 bf16 matrix in TMEM (entries 0..63 of a
 // row in the columns [a, a + 32), 64..127 in [a + 64, a + 96)) and B a
-// 128-row tile in shared memory (MN-major; the sum runs over the rows)
+// 128-row tile in shared memory (MN-major; the sum runs over the rows); blo
+// from desc_cols
 template <int D>
-__device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+__device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t blo, bool acc) {
   using C = BCfg<D>;
-  const uint64_t hi = sdesc_sw128(0, C::kPanelBytes, 1024);
-  const uint32_t blo = (b & 0x3FFFFu) >> 4;
 #pragma unroll
   for (int k = 0; k < C::kRowSteps; ++k)
-    mma_bf16_ts(d, a + 64 * (k >> 2) + 8 * (k & 3), hi | (blo + ((k * 16 * 128) >> 4)), C::kIdescO, acc || k > 0);
+    mma_ts(d, a + 64 * (k >> 2) + 8 * (k & 3), blo + k * 128, C::kIdescO, acc || k > 0);
 }
 
 // Zero the rows of a 128-row tile whose bit in `live` is clear (one warp's
@@ -304,6 +329,85 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
   }
 }
 
+// The 64 entries of a thread's half row, two to a register pair.
+//
+// p = 2^(s sl2 + nl) from the scores at TMEM t, kept in f32 in pr.  NL: the
+// addend is a row's (nl2) or, in shared memory at nl_addr, one per column.
+// MASKED: entries whose bit in w0 (columns 0..31) or w1 (32..63) is clear are
+// 0 whatever the score is.  The masked form is a path of its own, taken by
+// whole warps: a test in the unmasked loop would cut it into pieces that the
+// compiler cannot interleave.
+template <bool COLS, bool MASKED>
+__device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl2, uint32_t nl_addr, uint32_t w0,
+                                           uint32_t w1, uint64_t (&pr)[32]) {
+  uint32_t a[2][32];
+  tmem_ld32(t, a[0]);
+  tmem_ld32(t + 32, a[1]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    uint64_t n[2] = {nl2, nl2};
+    if (COLS) ld_shared_2b64(nl_addr + 16 * k, n[0], n[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * k + e;  // pair: entries 2i, 2i + 1
+      float x0, x1;
+      f2_split(f2_fma(f2(__uint_as_float(a[i >> 4][(2 * i) & 31]), __uint_as_float(a[i >> 4][(2 * i + 1) & 31])), mul,
+                      n[e]),
+               x0, x1);
+      x0 = ex2_approx(x0);
+      x1 = ex2_approx(x1);
+      if (MASKED) {
+        const uint32_t w = (i < 16 ? w0 : w1) >> ((2 * i) & 31);
+        x0 = w & 1u ? x0 : 0.f;
+        x1 = w & 2u ? x1 : 0.f;
+      }
+      pr[i] = f2(x0, x1);
+    }
+  }
+}
+
+// ds = p (dp + ndl), rounded to bf16, from dP at TMEM t; ndl as nl above.
+// `loaded` is called once dP is in registers.
+template <bool COLS, bool MASKED, typename F>
+__device__ __forceinline__ void half_row_ds(uint32_t t, uint64_t dl2, uint32_t dl_addr, uint32_t w0, uint32_t w1,
+                                            const uint64_t (&pr)[32], uint32_t (&pk)[32], F loaded) {
+  uint32_t a[2][32];
+  tmem_ld32(t, a[0]);
+  tmem_ld32(t + 32, a[1]);
+  tmem_wait_ld();
+  loaded();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    uint64_t n[2] = {dl2, dl2};
+    if (COLS) ld_shared_2b64(dl_addr + 16 * k, n[0], n[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * k + e;
+      float x0, x1;
+      f2_split(f2_mul(f2_add(f2(__uint_as_float(a[i >> 4][(2 * i) & 31]), __uint_as_float(a[i >> 4][(2 * i + 1) & 31])),
+                             n[e]),
+                      pr[i]),
+               x0, x1);
+      if (MASKED) {
+        const uint32_t w = (i < 16 ? w0 : w1) >> ((2 * i) & 31);
+        x0 = w & 1u ? x0 : 0.f;
+        x1 = w & 2u ? x1 : 0.f;
+      }
+      pk[i] = pack_bf16x2(x0, x1);
+    }
+  }
+}
+
+__device__ __forceinline__ void pack_half_row(const uint64_t (&pr)[32], uint32_t (&pk)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float x0, x1;
+    f2_split(pr[i], x0, x1);
+    pk[i] = pack_bf16x2(x0, x1);
+  }
+}
+
 struct KvBars {
   uint64_t kv_full;
   uint64_t q_full[2], do_full[2], free[2];
@@ -429,39 +533,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
     }
   } else if (warp == 9) {
     if (lane == 0 && n_it > 0) {
+      const uint32_t dk = desc_rows(sK), dv = desc_rows(sV);
+      uint32_t q_r[2], q_c[2], o_r[2], o_c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q_r[i] = desc_rows(sSt + 2 * i * C::kTileBytes);
+        q_c[i] = desc_cols(sSt + 2 * i * C::kTileBytes);
+        o_r[i] = desc_rows(sSt + (2 * i + 1) * C::kTileBytes);
+        o_c[i] = desc_cols(sSt + (2 * i + 1) * C::kTileBytes);
+      }
       bool ok = mbar_wait(smem_u32(&bars.kv_full), 0, deadline, abort_flag) &&
                 mbar_wait(smem_u32(&bars.q_full[0]), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
-        issue_rows<D>(tS, sK, sSt);
+        issue_rows<D>(tS, dk, q_r[0]);
         mma_commit(smem_u32(&bars.s_full));
         ok = mbar_wait(smem_u32(&bars.do_full[0]), 0, deadline, abort_flag);
         tc_fence_after();
       }
       if (ok) {
-        issue_rows<D>(tDP, sV, sSt + C::kTileBytes);
+        issue_rows<D>(tDP, dv, o_r[0]);
         mma_commit(smem_u32(&bars.dp_full));
       }
-      for (int it = 0; ok && it < n_it; ++it) {
-        const int st = it & 1, nx = st ^ 1;
-        const uint32_t sq = sSt + 2 * st * C::kTileBytes, sqn = sSt + 2 * nx * C::kTileBytes;
-        const bool more = it + 1 < n_it;
-        if (!(ok = mbar_wait(smem_u32(&bars.p_full), it & 1, deadline, abort_flag))) break;
-        tc_fence_after();
-        issue_cols<D>(tDV, tS, sq + C::kTileBytes, it > 0);
-        if (more) {
-          if (!(ok = mbar_wait(smem_u32(&bars.q_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
-          issue_rows<D>(tS, sK, sqn);
-          mma_commit(smem_u32(&bars.s_full));
-        }
-        if (!(ok = mbar_wait(smem_u32(&bars.ds_full), it & 1, deadline, abort_flag))) break;
-        tc_fence_after();
-        issue_cols<D>(tDK, tDP, sq, it > 0);
-        mma_commit(more ? smem_u32(&bars.free[st]) : smem_u32(&bars.done));
-        if (more) {
-          if (!(ok = mbar_wait(smem_u32(&bars.do_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
-          issue_rows<D>(tDP, sV, sqn + C::kTileBytes);
-          mma_commit(smem_u32(&bars.dp_full));
+      for (int it0 = 0; ok && it0 < n_it; it0 += 2) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const int it = it0 + st, nx = st ^ 1;
+          if (!ok || it >= n_it) break;
+          const bool more = it + 1 < n_it;
+          if (!(ok = mbar_wait(smem_u32(&bars.p_full), st, deadline, abort_flag))) break;
+          tc_fence_after();
+          issue_cols<D>(tDV, tS, o_c[st], it > 0);
+          if (more) {
+            if (!(ok = mbar_wait(smem_u32(&bars.q_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
+            issue_rows<D>(tS, dk, q_r[nx]);
+            mma_commit(smem_u32(&bars.s_full));
+          }
+          if (!(ok = mbar_wait(smem_u32(&bars.ds_full), st, deadline, abort_flag))) break;
+          tc_fence_after();
+          issue_cols<D>(tDK, tDP, q_c[st], it > 0);
+          mma_commit(more ? smem_u32(&bars.free[st]) : smem_u32(&bars.done));
+          if (more) {
+            if (!(ok = mbar_wait(smem_u32(&bars.do_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
+            issue_rows<D>(tDP, dv, o_r[nx]);
+            mma_commit(smem_u32(&bars.dp_full));
+          }
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
@@ -506,43 +622,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
         break;
       }
       tc_fence_after();
+      // entries that take part: every query, none for a dead key
+      const uint32_t w0 = dead ? 0u : bits_word(live, 2 * wg), w1 = dead ? 0u : bits_word(live, 2 * wg + 1);
       uint64_t pr[32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t a[32], pk[16];
-        tmem_ld32(mS + 32 * c, a);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint64_t n0, n1;
-          ld_shared_2b64(ss + nl_off + 128 * c + 16 * k, n0, n1);
-          float x0, x1, x2, x3;
-          f2_split(f2_fma(f2(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1])), mul, n0), x0, x1);
-          f2_split(f2_fma(f2(__uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3])), mul, n1), x2, x3);
-          x0 = ex2_approx(x0);
-          x1 = ex2_approx(x1);
-          x2 = ex2_approx(x2);
-          x3 = ex2_approx(x3);
-          if (any_dead) {
-            x0 = dead ? 0.f : x0;
-            x1 = dead ? 0.f : x1;
-            x2 = dead ? 0.f : x2;
-            x3 = dead ? 0.f : x3;
-          }
-          if (fix) {
-            const uint32_t w = bits_word(live, 2 * wg + c) >> (4 * k);
-            x0 = w & 1u ? x0 : 0.f;
-            x1 = w & 2u ? x1 : 0.f;
-            x2 = w & 4u ? x2 : 0.f;
-            x3 = w & 8u ? x3 : 0.f;
-          }
-          pr[16 * c + 2 * k] = f2(x0, x1);
-          pr[16 * c + 2 * k + 1] = f2(x2, x3);
-          pk[2 * k] = pack_bf16x2(x0, x1);
-          pk[2 * k + 1] = pack_bf16x2(x2, x3);
-        }
-        tmem_st16(mS + 16 * c, pk);
-      }
+      uint32_t pk[32];
+      if (!(any_dead || fix))
+        half_row_p<true, false>(mS, mul, 0, ss + nl_off, w0, w1, pr);
+      else
+        half_row_p<true, true>(mS, mul, 0, ss + nl_off, w0, w1, pr);
+      pack_half_row(pr, pk);
+      tmem_st32(mS, pk);
       // (the stage's dO landed: its statistics are read below, and dead rows
       // are zeroed here)
       ok = mbar_wait(smem_u32(&bars.do_full[st]), (it >> 1) & 1, deadline, abort_flag);
@@ -566,39 +655,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t a[32], pk[16];
-        tmem_ld32(mDP + 32 * c, a);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint64_t n0, n1;
-          ld_shared_2b64(ss + 2 * stat + 64 * wg * 4 + 128 * c + 16 * k, n0, n1);
-          float x0, x1, x2, x3;
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1])), n0), pr[16 * c + 2 * k]),
-                   x0, x1);
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3])), n1),
-                          pr[16 * c + 2 * k + 1]),
-                   x2, x3);
-          if (any_dead) {
-            x0 = dead ? 0.f : x0;
-            x1 = dead ? 0.f : x1;
-            x2 = dead ? 0.f : x2;
-            x3 = dead ? 0.f : x3;
-          }
-          if (fix) {
-            const uint32_t w = bits_word(live, 2 * wg + c) >> (4 * k);
-            x0 = w & 1u ? x0 : 0.f;
-            x1 = w & 2u ? x1 : 0.f;
-            x2 = w & 4u ? x2 : 0.f;
-            x3 = w & 8u ? x3 : 0.f;
-          }
-          pk[2 * k] = pack_bf16x2(x0, x1);
-          pk[2 * k + 1] = pack_bf16x2(x2, x3);
-        }
-        tmem_st16(mDP + 16 * c, pk);
-      }
+      const uint32_t dl_addr = ss + 2 * stat + 64 * wg * 4;
+      if (!(any_dead || fix))
+        half_row_ds<true, false>(mDP, 0, dl_addr, w0, w1, pr, pk, [] {});
+      else
+        half_row_ds<true, true>(mDP, 0, dl_addr, w0, w1, pr, pk, [] {});
+      tmem_st32(mDP, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -747,52 +809,62 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
     }
   } else if (warp == 9) {
     if (lane == 0 && n_it > 0) {
+      const uint32_t dq = desc_rows(sQ), ddo = desc_rows(sDO);
+      uint32_t k_r[C::kKSlots], k_c[C::kKSlots], v_r[C::kVSlots];
+#pragma unroll
+      for (int i = 0; i < C::kKSlots; ++i) {
+        k_r[i] = desc_rows(sK + i * C::kTileBytes);
+        k_c[i] = desc_cols(sK + i * C::kTileBytes);
+      }
+#pragma unroll
+      for (int i = 0; i < C::kVSlots; ++i) v_r[i] = desc_rows(sV + i * C::kTileBytes);
       bool ok = mbar_wait(smem_u32(&bars.q_full), 0, deadline, abort_flag) &&
                 mbar_wait(smem_u32(&bars.k_full[0]), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
-        issue_rows<D>(tmem, sQ, sK);
+        issue_rows<D>(tmem, dq, k_r[0]);
         mma_commit(smem_u32(&bars.s_full[0]));
         ok = mbar_wait(smem_u32(&bars.v_full[0]), 0, deadline, abort_flag);
       }
       if (ok) {
-        issue_rows<D>(tDP, sDO, sV);
+        issue_rows<D>(tDP, ddo, v_r[0]);
         mma_commit(smem_u32(&bars.dp_full));
         mma_commit(smem_u32(&bars.v_free[0]));
         if (n_it > 1) {
           ok = mbar_wait(smem_u32(&bars.k_full[1]), 0, deadline, abort_flag);
           if (ok) {
-            issue_rows<D>(tmem + 128, sQ, sK + C::kTileBytes);
+            issue_rows<D>(tmem + 128, dq, k_r[1]);
             mma_commit(smem_u32(&bars.s_full[1]));
           }
         }
       }
-      int ks = 0, ks2 = 2 % C::kKSlots, ph2 = 2 / C::kKSlots;  // slot of K(it); of K(it + 2) and its turn
-      for (int it = 0; ok && it < n_it; ++it) {
-        const int buf = it & 1;
-        if (it + 1 < n_it) {
-          const int vs = (it + 1) % C::kVSlots;
-          if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag) &&
-                     mbar_wait(smem_u32(&bars.v_full[vs]), ((it + 1) / C::kVSlots) & 1, deadline, abort_flag)))
-            break;
+      // unrolled over a turn of both rings, so that every slot is a constant
+      constexpr int kTurn = C::kKSlots * C::kVSlots;
+      static_assert(kTurn % 2 == 0, "S buffers alternate");
+      for (int it0 = 0; ok && it0 < n_it; it0 += kTurn) {
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) {
+          const int it = it0 + u, buf = u & 1, ks = u % C::kKSlots, vs = (u + 1) % C::kVSlots,
+                    ks2 = (u + 2) % C::kKSlots;
+          if (!ok || it >= n_it) break;
+          if (it + 1 < n_it) {
+            if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag) &&
+                       mbar_wait(smem_u32(&bars.v_full[vs]), ((it + 1) / C::kVSlots) & 1, deadline, abort_flag)))
+              break;
+            tc_fence_after();
+            issue_rows<D>(tDP, ddo, v_r[vs]);
+            mma_commit(smem_u32(&bars.dp_full));
+            mma_commit(smem_u32(&bars.v_free[vs]));
+          }
+          if (!(ok = mbar_wait(smem_u32(&bars.ds_full[buf]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
-          issue_rows<D>(tDP, sDO, sV + vs * C::kTileBytes);
-          mma_commit(smem_u32(&bars.dp_full));
-          mma_commit(smem_u32(&bars.v_free[vs]));
-        }
-        if (!(ok = mbar_wait(smem_u32(&bars.ds_full[buf]), (it >> 1) & 1, deadline, abort_flag))) break;
-        tc_fence_after();
-        issue_cols<D>(tDQ, tmem + 128 * buf, sK + ks * C::kTileBytes, it > 0);
-        mma_commit(it + 1 < n_it ? smem_u32(&bars.k_free[ks]) : smem_u32(&bars.done));
-        if (it + 2 < n_it) {
-          if (!(ok = mbar_wait(smem_u32(&bars.k_full[ks2]), ph2 & 1, deadline, abort_flag))) break;
-          issue_rows<D>(tmem + 128 * buf, sQ, sK + ks2 * C::kTileBytes);
-          mma_commit(smem_u32(&bars.s_full[buf]));
-        }
-        if (++ks == C::kKSlots) ks = 0;
-        if (++ks2 == C::kKSlots) {
-          ks2 = 0;
-          ++ph2;
+          issue_cols<D>(tDQ, tmem + 128 * buf, k_c[ks], it > 0);
+          mma_commit(it + 1 < n_it ? smem_u32(&bars.k_free[ks]) : smem_u32(&bars.done));
+          if (it + 2 < n_it) {
+            if (!(ok = mbar_wait(smem_u32(&bars.k_full[ks2]), ((it + 2) / C::kKSlots) & 1, deadline, abort_flag))) break;
+            issue_rows<D>(tmem + 128 * buf, dq, k_r[ks2]);
+            mma_commit(smem_u32(&bars.s_full[buf]));
+          }
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
@@ -836,18 +908,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       }
       tc_fence_after();
       uint64_t pr[32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t a[32];
-        tmem_ld32(mS + 32 * c, a);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x0, x1;
-          f2_split(f2_fma(f2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])), mul, nl2), x0, x1);
-          pr[16 * c + k] = f2(ex2_approx(x0), ex2_approx(x1));
-        }
-      }
+      if (!part)
+        half_row_p<false, false>(mS, mul, nl2, 0, w0, w1, pr);
+      else
+        half_row_p<false, true>(mS, mul, nl2, 0, w0, w1, pr);
       ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -855,30 +919,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       }
       tc_fence_after();
       uint32_t pk[32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t a[32];
-        tmem_ld32(mDP + 32 * c, a);
-        tmem_wait_ld();
-        if (c == 1) {
-          // dP is in registers: the next tile's may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x0, x1;
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])), dl2), pr[16 * c + k]), x0,
-                   x1);
-          if (part) {
-            const uint32_t w = (c ? w1 : w0) >> (2 * k);
-            x0 = w & 1u ? x0 : 0.f;
-            x1 = w & 2u ? x1 : 0.f;
-          }
-          pk[16 * c + k] = pack_bf16x2(x0, x1);
-        }
-      }
+      // (dP is in registers: the next tile's may overwrite it)
+      const auto loaded = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
+      };
+      if (!part)
+        half_row_ds<false, false>(mDP, dl2, 0, w0, w1, pr, pk, loaded);
+      else
+        half_row_ds<false, true>(mDP, dl2, 0, w0, w1, pr, pk, loaded);
       tmem_st32(mS, pk);
       if (part && !self) {
         // keys that are not admitted may hold anything: their rows of K are
