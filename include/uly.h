@@ -437,8 +437,7 @@ int uly_sp_attention_backward(const uly_plan* plan, const void* const* q, const 
                               int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of the two calls above for this plan (about 8 bytes per
- * query row and head, 12 with ULY_ROWS_SELF, and the replicated rows of one
- * q shard), or -1 for a NULL plan. */
+ * query row and head, and the replicated rows of one q shard), or -1 for a NULL plan. */
 int64_t uly_attention_backward_workspace(const uly_plan* plan);
 
 /* ---- pairs that the rotation turns -------------------------------------- */

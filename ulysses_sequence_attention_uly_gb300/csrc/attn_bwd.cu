@@ -57,10 +57,15 @@ struct BCfg {
   static constexpr int kRowSteps = kTileRows / 16;         // MMAs of a product over 128 rows
   static constexpr uint32_t kIdescS = make_idesc(1u, 128, 128, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(1u, 128, D, 0, 1);
-  // dkdv_kernel: K, V and two stages of (Q, dO, row statistics)
-  static constexpr int kStatBytes = 3 * kTileRows * 4;     // -lse (admitted keys, masked keys), -delta
-  static constexpr int kStages = 2;
-  static constexpr int kSmemKv = 1024 + (2 + 2 * kStages) * kTileBytes + kStages * kStatBytes;
+  // dkdv_kernel: K, V, three Q and two dO slots with their row statistics,
+  // barriers.  No static shared memory and no slack: the buffer starts on a
+  // 1024-byte boundary (the kernel checks it), and at D = 128 it is all that a
+  // CTA can have.
+  static constexpr int kQSlots = 3, kOSlots = 2;
+  static constexpr int kStatBytes = kTileRows * 4;         // -lse log2(e) or -delta of a tile's rows
+  static constexpr int kKvBars = (2 + kQSlots + kOSlots) * kTileBytes + (kQSlots + kOSlots) * kStatBytes;
+  static constexpr int kSmemKv = kKvBars + 256;
+  static_assert(kSmemKv <= 227 * 1024, "shared memory of a CTA");
   // dq_kernel: Q, dO, three K and two V slots
   static constexpr int kKSlots = 3, kVSlots = 2;
   static constexpr int kSmemQ = 1024 + (2 + kKSlots + kVSlots) * kTileBytes;
@@ -93,12 +98,14 @@ __device__ __forceinline__ int seg_of(const Seg* segs, int n, int t) {
   return s;
 }
 
-// 128 rows x D of one head to shared memory (128-byte swizzle panels)
-template <int D>
+// 128 rows x D of one head to shared memory, panels of 64 columns one behind
+// the other (the map's fourth dimension), in one instruction
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, uint32_t bar, int head, int row, int b) {
-#pragma unroll
-  for (int pn = 0; pn < BCfg<D>::kPanels; ++pn)
-    tma_load_4d(dst + pn * BCfg<D>::kPanelBytes, m, bar, pn * 64, head, row, b);
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %3, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(b)
+      : "memory");
 }
 
 // Shared-memory descriptors (128-byte swizzle; tc.cuh): the upper word is the
@@ -154,14 +161,17 @@ __device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t blo,
 }
 
 // Zero the rows of a 128-row tile whose bit in `live` is clear (one warp's
-// share: rows [row0, row0 + 16)).
+// share: rows [row0, row0 + 16), four of them at a time).
 template <int D>
 __device__ __forceinline__ void zero_dead_rows(uint32_t tile, const uint4 live, int row0, int lane) {
   const uint32_t w = bits_word(live, row0 >> 5) >> (row0 & 31);
-  for (int r = 0; r < 16; ++r) {
-    if ((w >> r) & 1u) continue;
-    if (lane < 8 * BCfg<D>::kPanels)
-      st_shared_v4(tile + (lane >> 3) * BCfg<D>::kPanelBytes + (row0 + r) * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 4 * k + (lane >> 3);
+    if (!((w >> r) & 1u))
+#pragma unroll
+      for (int pn = 0; pn < BCfg<D>::kPanels; ++pn)
+        st_shared_v4(tile + pn * BCfg<D>::kPanelBytes + (row0 + r) * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
   }
 }
 
@@ -228,10 +238,8 @@ __device__ __forceinline__ void store_rows(const BwdParams& p, uint8_t* const* o
 // Per (batch, q head, 128-row tile of a run): -lse log2(e) and -delta, padded
 // to whole tiles, which the main kernels read in tiles.  A row that takes
 // part in nothing (past its run's end, no admitted key, or zero by the
-// masked-row convention) has -inf, whose exponential is 0.  ULY_ROWS_SELF: the
-// first array holds it for the admitted keys (rows that are admitted keys
-// themselves), the second for the masked keys.  Fused, replicated rows: do is
-// the sum of every shard's copy, since each received the output; the sum is
+// masked-row convention) has -inf, whose exponential is 0.  Fused, replicated
+// rows: do is the sum of every shard's copy, since each received the output; the sum is
 // rounded to bf16 into do_rep (the MMA's operand) and delta uses that value.
 // Bound by memory: o and do are read once.  32 rows x 8 heads a CTA; 16 (D =
 // 128) or 8 lanes share a row, the results go through shared memory so that
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
     const int hh = i / kRows, r = i % kRows, h = h0 + hh;
     if (h >= p.Hq) continue;
     const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + t) * kTileRows + r_lo + r;
-    float nl = -INFINITY, nl2 = -INFINITY, dl = 0.f;
+    float nl = -INFINITY, dl = 0.f;
     const int lrow = row0 + r;
     if (lrow < run.len) {
       const int owner = h / p.Hq_l;
@@ -313,18 +321,11 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
       }
       const bool live = lse != -INFINITY && (own_ok || p.masked_rows != ULY_ROWS_ZERO);
       if (live) {
-        const float v = -lse * 1.4426950408889634f;
-        if (p.masked_rows != ULY_ROWS_SELF)
-          nl = v;
-        else if (own_ok)
-          nl = v;
-        else
-          nl2 = v;
+        nl = -lse * 1.4426950408889634f;
         dl = -s_dl[hh][r];
       }
     }
     p.nl[at] = nl;
-    if (p.masked_rows == ULY_ROWS_SELF) p.nl[p.stat_stride + at] = nl2;
     p.dl[at] = dl;
   }
 }
@@ -337,13 +338,15 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
 // 0 whatever the score is.  The masked form is a path of its own, taken by
 // whole warps: a test in the unmasked loop would cut it into pieces that the
 // compiler cannot interleave.
-template <bool COLS, bool MASKED>
+// `loaded` is called once the scores are in registers.
+template <bool COLS, bool MASKED, typename F>
 __device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl2, uint32_t nl_addr, uint32_t w0,
-                                           uint32_t w1, uint64_t (&pr)[32]) {
+                                           uint32_t w1, uint64_t (&pr)[32], F loaded) {
   uint32_t a[2][32];
   tmem_ld32(t, a[0]);
   tmem_ld32(t + 32, a[1]);
   tmem_wait_ld();
+  loaded();
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     uint64_t n[2] = {nl2, nl2};
@@ -367,16 +370,10 @@ __device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl
   }
 }
 
-// ds = p (dp + ndl), rounded to bf16, from dP at TMEM t; ndl as nl above.
-// `loaded` is called once dP is in registers.
-template <bool COLS, bool MASKED, typename F>
-__device__ __forceinline__ void half_row_ds(uint32_t t, uint64_t dl2, uint32_t dl_addr, uint32_t w0, uint32_t w1,
-                                            const uint64_t (&pr)[32], uint32_t (&pk)[32], F loaded) {
-  uint32_t a[2][32];
-  tmem_ld32(t, a[0]);
-  tmem_ld32(t + 32, a[1]);
-  tmem_wait_ld();
-  loaded();
+// ds = p (dp + ndl), rounded to bf16, from the loaded dP; ndl as nl above.
+template <bool COLS, bool MASKED>
+__device__ __forceinline__ void half_row_ds(const uint32_t (&a)[2][32], uint64_t dl2, uint32_t dl_addr, uint32_t w0,
+                                            uint32_t w1, const uint64_t (&pr)[32], uint32_t (&pk)[32]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     uint64_t n[2] = {dl2, dl2};
@@ -399,41 +396,175 @@ __device__ __forceinline__ void half_row_ds(uint32_t t, uint64_t dl2, uint32_t d
   }
 }
 
-__device__ __forceinline__ void pack_half_row(const uint64_t (&pr)[32], uint32_t (&pk)[32]) {
+// p rounded to bf16 into the 32 TMEM columns from t on
+__device__ __forceinline__ void store_half_row(uint32_t t, const uint64_t (&pr)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float x0, x1;
-    f2_split(pr[i], x0, x1);
-    pk[i] = pack_bf16x2(x0, x1);
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x0, x1;
+      f2_split(pr[16 * c + i], x0, x1);
+      pk[i] = pack_bf16x2(x0, x1);
+    }
+    tmem_st16(t + 16 * c, pk);
   }
 }
 
 struct KvBars {
-  uint64_t kv_full;
-  uint64_t q_full[2], do_full[2], free[2];
-  uint64_t s_full, dp_full;   // S, dP of the tile in TMEM
-  uint64_t p_full, ds_full;   // P, dS stored to TMEM (8 warps)
+  uint64_t kq_full, q1_full;  // K and Q(0); Q(1)
+  uint64_t nl_full[3];        // -lse log2(e) of a tile's rows
+  uint64_t s_full[2];         // S(i) in region i mod 2
+  uint64_t s_go;              // phase i: S(i) read out of TMEM (8 warps); dO(i), -delta (and V) landed
+  uint64_t dp_full;           // phase i: dP(i) in region i mod 2
+  uint64_t ds_full;           // phase i: dS(i) stored (8 warps)
+  uint64_t p_go[2];           // P(i) stored (8 warps), Q(i+2) landed: i mod 2, since a warp may store
+                              // P(i+1) before Q(i+2) is there
+  uint64_t v_done;            // phase i: dV(i), and with it dK(i), complete
   uint64_t done, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
+static_assert(sizeof(KvBars) <= 256, "room for the barriers");
+
+// What the elementwise warps of dkdv_kernel share.
+struct KvWork {
+  KvBars* bars;
+  uint32_t tmem, sQ, sDO, sNl, sDl;
+  int n_it, b;
+  uint64_t deadline;
+};
+
+// The elementwise loop of dkdv_kernel: one thread per key and half of the
+// queries.  MODE 0: every pair of the warp attends.  1: `dead` keys do not.
+// 2: it goes by the queries' own tokens too (ULY_ROWS_ZERO, _SELF).  Loops of
+// their own, so that the common one has no test in it and fits the registers.
+template <int D, int MODE>
+__device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int warp, int lane, bool key_ok, bool dead) {
+  using C = BCfg<D>;
+  KvBars& bars = *k.bars;
+  volatile int* abort_flag = &bars.abort_flag;
+  const int wg = warp >> 2, q4 = warp & 3;
+  const uint32_t off = (static_cast<uint32_t>(q4 * 32) << 16) + 64 * wg;
+  const uint64_t mul = f2(p.scale_log2, p.scale_log2);
+  const bool self = p.masked_rows == ULY_ROWS_SELF, zero_rows = p.masked_rows == ULY_ROWS_ZERO;
+  uint4 live = make_uint4(~0u, ~0u, ~0u, ~0u), live_next = live;
+  int qs = 0, qt = 0;
+  const auto next_live = [&] {  // the queries' own tokens, a tile ahead of their use
+    const Seg& q = p.qseg[qs];
+    if (q.kv_seg >= 0)
+      live_next = __ldg(p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles + p.kseg[q.kv_seg].first + qt);
+    if (++qt * kTileRows >= q.len) {
+      qt = 0;
+      if (++qs == p.n_qseg) qs = 0;
+    }
+  };
+  if (MODE == 2) next_live();
+  int qslot = 0, qturn = 0;
+  for (int it = 0; it < k.n_it; ++it) {
+    const uint32_t mR = k.tmem + off + 128 * (it & 1);
+    const uint32_t nl_addr = k.sNl + qslot * C::kStatBytes + 64 * wg * 4;
+    const uint32_t dl_addr = k.sDl + (it & 1) * C::kStatBytes + 64 * wg * 4;
+    uint32_t w0 = 0u, w1 = 0u;
+    bool masked = MODE == 1;
+    if (MODE == 2) {
+      live = live_next;
+      if (it + 1 < k.n_it) next_live();
+      // queries that attend to the thread's key: those whose own token is
+      // admitted (ULY_ROWS_ZERO), those of the key's own kind (ULY_ROWS_SELF;
+      // past the run's end the statistics exclude)
+      w0 = bits_word(live, 2 * wg);
+      w1 = bits_word(live, 2 * wg + 1);
+      if (self && !key_ok) {
+        w0 = ~w0;
+        w1 = ~w1;
+      }
+      if (dead) w0 = w1 = 0u;
+      masked = __any_sync(0xffffffffu, (w0 & w1) != 0xFFFFFFFFu);
+    } else if (MODE == 1) {
+      w0 = w1 = dead ? 0u : ~0u;
+    }
+    bool ok = mbar_wait(smem_u32(&bars.nl_full[qslot]), qturn & 1, k.deadline, abort_flag) &&
+              mbar_wait(smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1, k.deadline, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint64_t pr[32];
+    const auto s_loaded = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.s_go));
+    };
+    if (MODE == 0 || (MODE == 2 && !masked))
+      half_row_p<true, false>(mR, mul, 0, nl_addr, w0, w1, pr, s_loaded);
+    else
+      half_row_p<true, true>(mR, mul, 0, nl_addr, w0, w1, pr, s_loaded);
+    ok = mbar_wait(smem_u32(&bars.s_go), it & 1, k.deadline, abort_flag) &&
+         mbar_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint32_t a[2][32], pk[32];
+    tmem_ld32(mR, a[0]);
+    tmem_ld32(mR + 32, a[1]);
+    if (MODE == 2 && zero_rows && !bits_full(live)) {
+      // queries that take part in nothing may hold anything: their rows of Q
+      // and dO are zeroed before the sums over queries read them (S and dP
+      // have read them)
+      zero_dead_rows<D>(k.sQ + qslot * C::kTileBytes, live, 16 * warp, lane);
+      zero_dead_rows<D>(k.sDO + (it & 1) * C::kTileBytes, live, 16 * warp, lane);
+      fence_proxy_async_smem();
+    }
+    tmem_wait_ld();
+    if (MODE == 0 || (MODE == 2 && !masked))
+      half_row_ds<true, false>(a, 0, dl_addr, w0, w1, pr, pk);
+    else
+      half_row_ds<true, true>(a, 0, dl_addr, w0, w1, pr, pk);
+    tmem_st32(mR, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full));
+    store_half_row(mR + 32, pr);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.p_go[it & 1]));
+    if (++qslot == C::kQSlots) {
+      qslot = 0;
+      ++qturn;
+    }
+  }
+  if (k.n_it > 0) {
+    const bool ok = mbar_wait(smem_u32(&bars.done), 0, k.deadline, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+  }
+  return true;
+}
 
 // dK and dV of 128 keys of one kv head.
 //   warp 8   TMA: K and V once, then Q, dO and the row statistics of every
-//            128-query tile of every query head of the group (two stages).
+//            128-query tile of every query head of the group.
 //   warp 9   MMA: S = K Q^T and dP = V dO^T (keys are TMEM lanes), dV += P dO
-//            and dK += dS Q with P, dS read from TMEM, in the order
-//              S(0) dP(0) | dV(i) S(i+1) dK(i) dP(i+1) ...
-//            so that two products (~1024 tensor cycles) run while P(i+1) is
-//            computed and two while dS(i+1) is.
-//   warps 0-7: one thread per key and half of the queries: P from S, stored
-//            over S's columns; dS from dP, stored over dP's.
-// TMEM: S [0,128) dP [128,256) dV [256,256+D) dK [256+D,256+2D).
-template <int D>
+//            and dK += dS Q with P and dS read from TMEM.
+//   warps 0-7: P from S, dS from dP.
+// Two query tiles are under way in two TMEM regions of 128 columns.  A region
+// holds in turn a tile's S, then (once S is in registers) its dP, then (once dP
+// is) its dS and P in bf16, half a row's P in the 32 columns behind its dS.
+// Order of the products:
+//   S(0) S(1) dP(0) | dK(i) dP(i+1) dV(i) S(i+2) ...
+// What a step waits for is then only dP(i+1), 512 tensor cycles, after S(i+1)
+// has been read, while P(i+1) is computed; with one region each for S and dP it
+// was two products.  The issuing thread spends about 47 cycles on an MMA (64 on
+// the tensor core), 75 on a commit and 85 on a wait for a barrier that has
+// completed, so the copy of a tile is one more arrival on a barrier that its
+// first reader waits for anyway.  Slots: Q(i) over Q(i-3) once dV(i-3), issued
+// after dK(i-3), is complete; dO(i) over dO(i-2) once dV(i-2) is.
+// TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D).
+template <int D, bool OWN>
 __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_constant__ BwdParams p) {
   using C = BCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ KvBars bars;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  KvBars& bars = *reinterpret_cast<KvBars*>(smem_raw + C::kKvBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int r = hk / p.Hkv_l;  // owning rank
@@ -444,21 +575,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
   const bool any = self || (bits.x | bits.y | bits.z | bits.w) != 0u;
   const int n_it = any ? p.G * p.n_q_tiles : 0;
 
-  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sK = sbase, sV = sbase + C::kTileBytes, sSt = sbase + 2 * C::kTileBytes;  // stage: Q, dO
-  const uint32_t sStat = sSt + 2 * C::kStages * C::kTileBytes;
+  const uint32_t sK = smem_u32(smem_raw), sV = sK + C::kTileBytes, sQ = sK + 2 * C::kTileBytes;
+  const uint32_t sDO = sQ + C::kQSlots * C::kTileBytes, sNl = sDO + C::kOSlots * C::kTileBytes;
+  const uint32_t sDl = sNl + C::kQSlots * C::kStatBytes;
   volatile int* abort_flag = &bars.abort_flag;
+  if (sK & 1023u) {  // (never: the buffer is placed on a 1024-byte boundary)
+    if (tid == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
   if (tid == 0) {
-    mbar_init(smem_u32(&bars.kv_full), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.q_full[i]), 1);
-      mbar_init(smem_u32(&bars.do_full[i]), 1);
-      mbar_init(smem_u32(&bars.free[i]), 1);
-    }
-    mbar_init(smem_u32(&bars.s_full), 1);
+    mbar_init(smem_u32(&bars.kq_full), 1);
+    mbar_init(smem_u32(&bars.q1_full), 1);
+    for (int i = 0; i < C::kQSlots; ++i) mbar_init(smem_u32(&bars.nl_full[i]), 1);
+    mbar_init(smem_u32(&bars.s_full[0]), 1);
+    mbar_init(smem_u32(&bars.s_full[1]), 1);
+    mbar_init(smem_u32(&bars.s_go), 9);
     mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.p_full), 8);
     mbar_init(smem_u32(&bars.ds_full), 8);
+    mbar_init(smem_u32(&bars.p_go[0]), 9);
+    mbar_init(smem_u32(&bars.p_go[1]), 9);
+    mbar_init(smem_u32(&bars.v_done), 1);
     mbar_init(smem_u32(&bars.done), 1);
     mbar_init(smem_u32(&bars.drain), 1);
     bars.abort_flag = 0;
@@ -472,7 +608,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+  const uint32_t tDV = tmem + 256, tDK = tmem + 256 + D;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
 
   if (warp == 8) {
@@ -480,37 +616,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
       const int kvhead = p.fused ? hk : hk % p.Hkv_l;
       const int kmap = run.src < 0 ? r : run.src;
       const int krow = (run.row0 < 0 ? p.shard_len[kmap] : run.row0) + row0;
-      const uint32_t bkv = smem_u32(&bars.kv_full);
-      mbar_arrive_expect_tx(bkv, 2 * C::kTileBytes);
-      load_tile<D>(sK, &p.tk[kmap], bkv, kvhead, krow, b);
-      load_tile<D>(sV, &p.tv[kmap], bkv, kvhead, krow, b);
-      const uint32_t stat = kTileRows * 4;
-      int g = 0, qs = 0, qt = 0, it = 0;  // q head of the group, run, tile inside the run
-      for (; it < n_it; ++it) {
-        const int st = it & 1;
-        if (it >= 2 && !mbar_wait(smem_u32(&bars.free[st]), ((it >> 1) - 1) & 1, deadline, abort_flag)) {
-          bwd_timeout(p, abort_flag);
-          break;
-        }
+      const uint32_t b_sgo = smem_u32(&bars.s_go);
+      // Where tiles come from is worked out ahead, so that their loads follow at
+      // once when a slot is free: mq .. for the next Q, mo .. for the next dO
+      // (the tile before it).
+      int g = 0, qs = 0, qt = 0;  // q head of the group, run, tile inside the run
+      int qhead = 0, qrow = 0, ohead = 0, orow = 0, ohead_n = 0, orow_n = 0;
+      const CUtensorMap *mq = nullptr, *mo = nullptr, *mo_n = nullptr;
+      const float *nl = nullptr, *dl = nullptr, *dl_n = nullptr;
+      const auto next = [&] {
+        mo = mo_n;
+        ohead = ohead_n;
+        orow = orow_n;
+        dl = dl_n;
         const int h = hk * p.G + g;
+        if (g == p.G) return;
         const Seg& q = p.qseg[qs];
         const bool rep = p.fused && q.out_shard < 0;
         const int qmap = q.src < 0 ? r : q.src;
-        const int qhead = p.fused ? h : h % p.Hq_l;
-        const int qrow = (q.row0 < 0 ? p.shard_len[qmap] : q.row0) + qt * kTileRows;
-        const uint32_t bq = smem_u32(&bars.q_full[st]), bd = smem_u32(&bars.do_full[st]);
-        const uint32_t sq = sSt + 2 * st * C::kTileBytes, sd = sq + C::kTileBytes, ss = sStat + st * C::kStatBytes;
+        qhead = p.fused ? h : h % p.Hq_l;
+        qrow = (q.row0 < 0 ? p.shard_len[qmap] : q.row0) + qt * kTileRows;
+        ohead_n = rep ? h : qhead;
+        orow_n = rep ? qt * kTileRows : qrow;
+        mq = &p.tq[qmap];
+        mo_n = rep ? &p.tdo_rep : &p.tdo[qmap];
         const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + q.first + qt) * kTileRows;
-        mbar_arrive_expect_tx(bq, C::kTileBytes + (self ? 2 : 1) * stat);
-        if (it != p.withhold_fill) load_tile<D>(sq, &p.tq[qmap], bq, qhead, qrow, b);
-        bulk_load(ss, p.nl + at, stat, bq);
-        if (self) bulk_load(ss + stat, p.nl + p.stat_stride + at, stat, bq);
-        mbar_arrive_expect_tx(bd, C::kTileBytes + stat);
-        if (rep)
-          load_tile<D>(sd, &p.tdo_rep, bd, h, qt * kTileRows, b);
-        else
-          load_tile<D>(sd, &p.tdo[qmap], bd, qhead, qrow, b);
-        bulk_load(ss + 2 * stat, p.dl + at, stat, bd);
+        nl = p.nl + at;
+        dl_n = p.dl + at;
         if (++qt * kTileRows >= q.len) {
           qt = 0;
           if (++qs == p.n_qseg) {
@@ -518,65 +650,124 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
             ++g;
           }
         }
+      };
+      // Q(it): its slot is free since v_done(it - 3); p_go(it - 4) is complete
+      // for the same reason
+      const auto load_q = [&](int it) {
+        const uint32_t slot = it % C::kQSlots;
+        const uint32_t bq = smem_u32(it == 0 ? &bars.kq_full : it == 1 ? &bars.q1_full : &bars.p_go[it & 1]);
+        const uint32_t bn = smem_u32(&bars.nl_full[slot]);
+        mbar_arrive_expect_tx(bq, (it == 0 ? 2 : 1) * C::kTileBytes);
+        if (it == 0) load_tile(sK, &p.tk[kmap], bq, kvhead, krow, b);
+        if (it != p.withhold_fill) load_tile(sQ + slot * C::kTileBytes, mq, bq, qhead, qrow, b);
+        mbar_arrive_expect_tx(bn, C::kStatBytes);
+        bulk_load(sNl + slot * C::kStatBytes, nl, C::kStatBytes, bn);
+      };
+      // dO(it): its slot is free since v_done(it - 2); that was issued after
+      // dP(it - 1) and so after phase it - 1 of s_go
+      const auto load_o = [&](int it) {
+        const uint32_t slot = it & 1;
+        mbar_arrive_expect_tx(b_sgo, (it == 0 ? 2 : 1) * C::kTileBytes + C::kStatBytes);
+        if (it == 0) load_tile(sV, &p.tv[kmap], b_sgo, kvhead, krow, b);
+        load_tile(sDO + slot * C::kTileBytes, mo, b_sgo, ohead, orow, b);
+        bulk_load(sDl + slot * C::kStatBytes, dl, C::kStatBytes, b_sgo);
+      };
+      bool ok = true;
+      next();
+      load_q(0);
+      next();
+      load_o(0);
+      if (n_it > 1) {
+        load_q(1);
+        next();
+        ok = mbar_wait(b_sgo, 0, deadline, abort_flag);
+        if (ok) load_o(1);
       }
-      if (*abort_flag) {
-        // drain: no copy may land after the CTA has left (a withheld one
-        // never completes and only costs the bound)
-        const uint64_t dl2 = globaltimer_ns() + 100000000ull;
-        volatile int never = 0;
-        for (int f = (it > 2 ? it - 2 : 0); f < it; ++f) {
-          mbar_wait(smem_u32(&bars.q_full[f & 1]), (f >> 1) & 1, dl2, &never);
-          mbar_wait(smem_u32(&bars.do_full[f & 1]), (f >> 1) & 1, dl2, &never);
+      if (ok && n_it > 2) {
+        load_q(2);
+        next();
+        // dO(it) and Q(it + 1) follow v_done(it - 2)
+        for (int it = 2; it < n_it; ++it) {
+          if (!(ok = mbar_wait(smem_u32(&bars.v_done), it & 1, deadline, abort_flag))) break;
+          load_o(it);
+          if (it + 1 < n_it) load_q(it + 1);
+          next();
         }
-        mbar_wait(smem_u32(&bars.kv_full), 0, dl2, &never);
+      }
+      if (ok) {
+        // the last two of p_go have no copy
+        if (n_it > 1) mbar_arrive(smem_u32(&bars.p_go[n_it & 1]));
+        mbar_arrive(smem_u32(&bars.p_go[(n_it - 1) & 1]));
+      } else {
+        bwd_timeout(p, abort_flag);
+        // No copy may land after the CTA has left.  The barriers of the last
+        // ones may lack arrivals for good, so this waits out a time in which
+        // any copy lands.
+        const uint64_t dl2 = globaltimer_ns() + 50000000ull;
+        while (globaltimer_ns() < dl2) {
+        }
       }
     }
   } else if (warp == 9) {
     if (lane == 0 && n_it > 0) {
       const uint32_t dk = desc_rows(sK), dv = desc_rows(sV);
-      uint32_t q_r[2], q_c[2], o_r[2], o_c[2];
+      uint32_t q_r[C::kQSlots], q_c[C::kQSlots], o_r[C::kOSlots], o_c[C::kOSlots];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        q_r[i] = desc_rows(sSt + 2 * i * C::kTileBytes);
-        q_c[i] = desc_cols(sSt + 2 * i * C::kTileBytes);
-        o_r[i] = desc_rows(sSt + (2 * i + 1) * C::kTileBytes);
-        o_c[i] = desc_cols(sSt + (2 * i + 1) * C::kTileBytes);
+      for (int i = 0; i < C::kQSlots; ++i) {
+        q_r[i] = desc_rows(sQ + i * C::kTileBytes);
+        q_c[i] = desc_cols(sQ + i * C::kTileBytes);
       }
-      bool ok = mbar_wait(smem_u32(&bars.kv_full), 0, deadline, abort_flag) &&
-                mbar_wait(smem_u32(&bars.q_full[0]), 0, deadline, abort_flag);
+#pragma unroll
+      for (int i = 0; i < C::kOSlots; ++i) {
+        o_r[i] = desc_rows(sDO + i * C::kTileBytes);
+        o_c[i] = desc_cols(sDO + i * C::kTileBytes);
+      }
+      bool ok = mbar_wait(smem_u32(&bars.kq_full), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
-        issue_rows<D>(tS, dk, q_r[0]);
-        mma_commit(smem_u32(&bars.s_full));
-        ok = mbar_wait(smem_u32(&bars.do_full[0]), 0, deadline, abort_flag);
-        tc_fence_after();
+        issue_rows<D>(tmem, dk, q_r[0]);
+        mma_commit(smem_u32(&bars.s_full[0]));
       }
+      if (ok && n_it > 1) {
+        ok = mbar_wait(smem_u32(&bars.q1_full), 0, deadline, abort_flag);
+        if (ok) {
+          issue_rows<D>(tmem + 128, dk, q_r[1]);
+          mma_commit(smem_u32(&bars.s_full[1]));
+        }
+      }
+      ok = ok && mbar_wait(smem_u32(&bars.s_go), 0, deadline, abort_flag);
+      tc_fence_after();
       if (ok) {
-        issue_rows<D>(tDP, dv, o_r[0]);
+        issue_rows<D>(tmem, dv, o_r[0]);
         mma_commit(smem_u32(&bars.dp_full));
       }
-      for (int it0 = 0; ok && it0 < n_it; it0 += 2) {
+      // unrolled over a turn of the rings, so that every operand is a constant
+      constexpr int kTurn = C::kQSlots * C::kOSlots;
+      static_assert(kTurn % 2 == 0 && C::kOSlots == 2, "regions and phases alternate");
+      for (int it0 = 0; ok && it0 < n_it; it0 += kTurn) {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const int it = it0 + st, nx = st ^ 1;
+        for (int u = 0; u < kTurn; ++u) {
+          const int it = it0 + u;
           if (!ok || it >= n_it) break;
-          const bool more = it + 1 < n_it;
-          if (!(ok = mbar_wait(smem_u32(&bars.p_full), st, deadline, abort_flag))) break;
+          const uint32_t tR = tmem + 128 * (u & 1), tN = tmem + 128 * (~u & 1);
+          if (!(ok = mbar_wait(smem_u32(&bars.ds_full), u & 1, deadline, abort_flag))) break;
           tc_fence_after();
-          issue_cols<D>(tDV, tS, o_c[st], it > 0);
-          if (more) {
-            if (!(ok = mbar_wait(smem_u32(&bars.q_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
-            issue_rows<D>(tS, dk, q_r[nx]);
-            mma_commit(smem_u32(&bars.s_full));
-          }
-          if (!(ok = mbar_wait(smem_u32(&bars.ds_full), st, deadline, abort_flag))) break;
-          tc_fence_after();
-          issue_cols<D>(tDK, tDP, q_c[st], it > 0);
-          mma_commit(more ? smem_u32(&bars.free[st]) : smem_u32(&bars.done));
-          if (more) {
-            if (!(ok = mbar_wait(smem_u32(&bars.do_full[nx]), ((it + 1) >> 1) & 1, deadline, abort_flag))) break;
-            issue_rows<D>(tDP, dv, o_r[nx]);
+          issue_cols<D>(tDK, tR, q_c[u % C::kQSlots], it > 0);
+          if (it + 1 < n_it) {
+            if (!(ok = mbar_wait(smem_u32(&bars.s_go), ~u & 1, deadline, abort_flag))) break;
+            tc_fence_after();
+            issue_rows<D>(tN, dv, o_r[(u + 1) % C::kOSlots]);
             mma_commit(smem_u32(&bars.dp_full));
+          }
+          if (!(ok = mbar_wait(smem_u32(&bars.p_go[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
+          tc_fence_after();
+          issue_cols<D>(tDV, tR + 32, o_c[u % C::kOSlots], it > 0);
+          if (it + 2 < n_it) {
+            mma_commit(smem_u32(&bars.v_done));
+            issue_rows<D>(tR, dk, q_r[(u + 2) % C::kQSlots]);
+            mma_commit(smem_u32(&bars.s_full[u & 1]));
+          } else if (it + 1 == n_it) {
+            mma_commit(smem_u32(&bars.done));
           }
         }
       }
@@ -588,94 +779,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
   } else {
     const int wg = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // key of the tile = TMEM lane
-    const uint32_t off = (static_cast<uint32_t>(q4 * 32) << 16) + 64 * wg;
-    const uint32_t mS = tS + off, mDP = tDP + off;
     const bool key_ok = (bits_word(bits, q4) >> lane) & 1u;
     const bool dead = row0 + row >= run.len || (!self && !key_ok);
-    const bool any_dead = __any_sync(0xffffffffu, dead);
-    const uint32_t stat = kTileRows * 4;
-    const uint32_t nl_off = (self && !key_ok ? stat : 0u) + 64 * wg * 4;
-    const uint64_t mul = f2(p.scale_log2, p.scale_log2);
-    const bool zero_rows = p.masked_rows == ULY_ROWS_ZERO;
-    bool ok = true;
-    int qs = 0, qt = 0;
-    for (int it = 0; it < n_it; ++it) {
-      const int st = it & 1;
-      const uint32_t ss = sStat + st * C::kStatBytes;
-      uint4 live = make_uint4(~0u, ~0u, ~0u, ~0u);
-      if (zero_rows) {
-        // queries that take part in nothing may hold anything: their rows of
-        // Q and dO are zeroed before the sums over queries read them
-        const Seg& q = p.qseg[qs];
-        live = q.kv_seg < 0 ? live
-                            : p.tile_bits[static_cast<int64_t>(b) * p.n_kv_tiles + p.kseg[q.kv_seg].first + qt];
-        if (++qt * kTileRows >= q.len) {
-          qt = 0;
-          if (++qs == p.n_qseg) qs = 0;
-        }
-      }
-      const bool fix = !bits_full(live);
-      ok = mbar_wait(smem_u32(&bars.q_full[st]), (it >> 1) & 1, deadline, abort_flag) &&
-           mbar_wait(smem_u32(&bars.s_full), it & 1, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // entries that take part: every query, none for a dead key
-      const uint32_t w0 = dead ? 0u : bits_word(live, 2 * wg), w1 = dead ? 0u : bits_word(live, 2 * wg + 1);
-      uint64_t pr[32];
-      uint32_t pk[32];
-      if (!(any_dead || fix))
-        half_row_p<true, false>(mS, mul, 0, ss + nl_off, w0, w1, pr);
-      else
-        half_row_p<true, true>(mS, mul, 0, ss + nl_off, w0, w1, pr);
-      pack_half_row(pr, pk);
-      tmem_st32(mS, pk);
-      // (the stage's dO landed: its statistics are read below, and dead rows
-      // are zeroed here)
-      ok = mbar_wait(smem_u32(&bars.do_full[st]), (it >> 1) & 1, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      const uint32_t sq = sSt + 2 * st * C::kTileBytes;
-      if (fix) {
-        zero_dead_rows<D>(sq, live, 16 * warp, lane);
-        zero_dead_rows<D>(sq + C::kTileBytes, live, 16 * warp, lane);
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.p_full));
-      ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t dl_addr = ss + 2 * stat + 64 * wg * 4;
-      if (!(any_dead || fix))
-        half_row_ds<true, false>(mDP, 0, dl_addr, w0, w1, pr, pk, [] {});
-      else
-        half_row_ds<true, true>(mDP, 0, dl_addr, w0, w1, pr, pk, [] {});
-      tmem_st32(mDP, pk);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full));
-    }
-    if (ok && n_it > 0) {
-      ok = mbar_wait(smem_u32(&bars.done), 0, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      tc_fence_after();
-    }
+    const KvWork k = {&bars, tmem, sQ, sDO, sNl, sDl, n_it, b, deadline};
+    bool ok;
+    if constexpr (OWN)
+      ok = kv_loop<D, 2>(p, k, warp, lane, key_ok, dead);
+    else if (__any_sync(0xffffffffu, dead))
+      ok = kv_loop<D, 1>(p, k, warp, lane, key_ok, dead);
+    else
+      ok = kv_loop<D, 0>(p, k, warp, lane, key_ok, dead);
     if (!ok) {
       bwd_timeout(p, abort_flag);
     } else {
       // warps 0-3: dV, warps 4-7: dK; each warp stages and stores its 32 rows
-      const uint32_t stage = sSt + wg * (2 * C::kTileBytes);
+      // (in two slots of Q: every copy into them has been read)
+      const uint32_t stage = sQ + wg * C::kTileBytes;
       stage_rows<D>((wg ? tDK : tDV) + (static_cast<uint32_t>(q4 * 32) << 16), wg ? p.scale : 1.f, stage, row, 0, D,
                     n_it == 0);
       __syncwarp();
@@ -693,7 +812,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
 
 struct QBars {
   uint64_t q_full;
-  uint64_t k_full[3], k_free[3], v_full[2], v_free[2];
+  uint64_t full[3];           // K and V of a tile (K's slot)
   uint64_t s_full[2], dp_full, dp_free, ds_full[2];
   uint64_t done, drain;
   uint32_t tmem_base;
@@ -729,13 +848,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
   volatile int* abort_flag = &bars.abort_flag;
   if (tid == 0) {
     mbar_init(smem_u32(&bars.q_full), 1);
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(smem_u32(&bars.k_full[i]), 1);
-      mbar_init(smem_u32(&bars.k_free[i]), 1);
-    }
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.full[i]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.v_full[i]), 1);
-      mbar_init(smem_u32(&bars.v_free[i]), 1);
       mbar_init(smem_u32(&bars.s_full[i]), 1);
       mbar_init(smem_u32(&bars.ds_full[i]), 8);
     }
@@ -765,45 +879,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       const int qrow = (run.row0 < 0 ? p.shard_len[qmap] : run.row0) + row0;
       const uint32_t bq = smem_u32(&bars.q_full);
       mbar_arrive_expect_tx(bq, 2 * C::kTileBytes);
-      load_tile<D>(sQ, &p.tq[qmap], bq, qhead, qrow, b);
+      load_tile(sQ, &p.tq[qmap], bq, qhead, qrow, b);
       if (rep)
-        load_tile<D>(sDO, &p.tdo_rep, bq, h, row0, b);
+        load_tile(sDO, &p.tdo_rep, bq, h, row0, b);
       else
-        load_tile<D>(sDO, &p.tdo[qmap], bq, qhead, qrow, b);
-      int nk = 0, nv = 0;  // K and V fills issued
-      for (int it = 0; it < n_it; ++it) {
+        load_tile(sDO, &p.tdo[qmap], bq, qhead, qrow, b);
+      // (where a tile comes from is worked out before its slots are free)
+      const CUtensorMap *mk, *mv;
+      int krow;
+      bool good;
+      const auto next = [&](int it) {
         const int e = active[it];
-        const bool good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
+        good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
         const Seg& k = p.kseg[good ? e >> 20 : 0];
         const int kmap = k.src < 0 ? r : k.src;
-        const int krow = (k.row0 < 0 ? p.shard_len[kmap] : k.row0) + (e & 0xFFFFF) * kTileRows;
+        krow = (k.row0 < 0 ? p.shard_len[kmap] : k.row0) + (e & 0xFFFFF) * kTileRows;
+        mk = &p.tk[kmap];
+        mv = &p.tv[kmap];
+      };
+      int it = 0;
+      next(0);
+      for (; it < n_it; ++it) {
         const int ks = it % C::kKSlots, vs = it % C::kVSlots;
-        if (it >= C::kKSlots &&
-            !mbar_wait(smem_u32(&bars.k_free[ks]), (it / C::kKSlots - 1) & 1, deadline, abort_flag)) {
+        // S(it-1) was issued after dQ(it-3) and dP(it-2), the last readers of
+        // the two slots
+        if (it >= 2 && !mbar_wait(smem_u32(&bars.s_full[(it - 1) & 1]), ((it - 1) >> 1) & 1, deadline, abort_flag)) {
           bwd_timeout(p, abort_flag);
           break;
         }
-        const uint32_t bk = smem_u32(&bars.k_full[ks]);
-        mbar_arrive_expect_tx(bk, C::kTileBytes);
-        if (good && it != p.withhold_fill) load_tile<D>(sK + ks * C::kTileBytes, &p.tk[kmap], bk, kvhead, krow, b);
-        ++nk;
-        if (it >= C::kVSlots &&
-            !mbar_wait(smem_u32(&bars.v_free[vs]), (it / C::kVSlots - 1) & 1, deadline, abort_flag)) {
-          bwd_timeout(p, abort_flag);
-          break;
-        }
-        const uint32_t bv = smem_u32(&bars.v_full[vs]);
-        mbar_arrive_expect_tx(bv, C::kTileBytes);
-        if (good) load_tile<D>(sV + vs * C::kTileBytes, &p.tv[kmap], bv, kvhead, krow, b);
-        ++nv;
+        const uint32_t bf = smem_u32(&bars.full[ks]);
+        mbar_arrive_expect_tx(bf, 2 * C::kTileBytes);
+        if (good && it != p.withhold_fill) load_tile(sK + ks * C::kTileBytes, mk, bf, kvhead, krow, b);
+        if (good) load_tile(sV + vs * C::kTileBytes, mv, bf, kvhead, krow, b);
+        if (it + 1 < n_it) next(it + 1);
       }
       if (*abort_flag) {
         const uint64_t dl2 = globaltimer_ns() + 100000000ull;
         volatile int never = 0;
-        for (int f = max(0, nk - C::kKSlots); f < nk; ++f)
-          mbar_wait(smem_u32(&bars.k_full[f % C::kKSlots]), (f / C::kKSlots) & 1, dl2, &never);
-        for (int f = max(0, nv - C::kVSlots); f < nv; ++f)
-          mbar_wait(smem_u32(&bars.v_full[f % C::kVSlots]), (f / C::kVSlots) & 1, dl2, &never);
+        for (int f = max(0, it - C::kKSlots); f < it; ++f)
+          mbar_wait(smem_u32(&bars.full[f % C::kKSlots]), (f / C::kKSlots) & 1, dl2, &never);
         mbar_wait(bq, 0, dl2, &never);
       }
     }
@@ -819,19 +933,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < C::kVSlots; ++i) v_r[i] = desc_rows(sV + i * C::kTileBytes);
       bool ok = mbar_wait(smem_u32(&bars.q_full), 0, deadline, abort_flag) &&
-                mbar_wait(smem_u32(&bars.k_full[0]), 0, deadline, abort_flag);
+                mbar_wait(smem_u32(&bars.full[0]), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
         issue_rows<D>(tmem, dq, k_r[0]);
         mma_commit(smem_u32(&bars.s_full[0]));
-        ok = mbar_wait(smem_u32(&bars.v_full[0]), 0, deadline, abort_flag);
-      }
-      if (ok) {
         issue_rows<D>(tDP, ddo, v_r[0]);
         mma_commit(smem_u32(&bars.dp_full));
-        mma_commit(smem_u32(&bars.v_free[0]));
         if (n_it > 1) {
-          ok = mbar_wait(smem_u32(&bars.k_full[1]), 0, deadline, abort_flag);
+          ok = mbar_wait(smem_u32(&bars.full[1]), 0, deadline, abort_flag);
           if (ok) {
             issue_rows<D>(tmem + 128, dq, k_r[1]);
             mma_commit(smem_u32(&bars.s_full[1]));
@@ -848,22 +958,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
                     ks2 = (u + 2) % C::kKSlots;
           if (!ok || it >= n_it) break;
           if (it + 1 < n_it) {
-            if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag) &&
-                       mbar_wait(smem_u32(&bars.v_full[vs]), ((it + 1) / C::kVSlots) & 1, deadline, abort_flag)))
-              break;
+            if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag))) break;
             tc_fence_after();
             issue_rows<D>(tDP, ddo, v_r[vs]);
             mma_commit(smem_u32(&bars.dp_full));
-            mma_commit(smem_u32(&bars.v_free[vs]));
           }
           if (!(ok = mbar_wait(smem_u32(&bars.ds_full[buf]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_cols<D>(tDQ, tmem + 128 * buf, k_c[ks], it > 0);
-          mma_commit(it + 1 < n_it ? smem_u32(&bars.k_free[ks]) : smem_u32(&bars.done));
           if (it + 2 < n_it) {
-            if (!(ok = mbar_wait(smem_u32(&bars.k_full[ks2]), ((it + 2) / C::kKSlots) & 1, deadline, abort_flag))) break;
+            if (!(ok = mbar_wait(smem_u32(&bars.full[ks2]), ((it + 2) / C::kKSlots) & 1, deadline, abort_flag))) break;
             issue_rows<D>(tmem + 128 * buf, dq, k_r[ks2]);
             mma_commit(smem_u32(&bars.s_full[buf]));
+          } else if (it + 1 == n_it) {
+            mma_commit(smem_u32(&bars.done));
           }
         }
       }
@@ -885,7 +993,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       invert = !((bits_word(qb, q4) >> lane) & 1u);
     }
     const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + t) * kTileRows + row;
-    const float nl = p.nl[(invert ? p.stat_stride : 0) + at], dl = p.dl[at];
+    const float nl = p.nl[at], dl = p.dl[at];
     const bool dead = nl == -INFINITY;
     const bool any_dead = __any_sync(0xffffffffu, dead);
     const uint64_t mul = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), dl2 = f2(dl, dl);
@@ -909,9 +1017,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       tc_fence_after();
       uint64_t pr[32];
       if (!part)
-        half_row_p<false, false>(mS, mul, nl2, 0, w0, w1, pr);
+        half_row_p<false, false>(mS, mul, nl2, 0, w0, w1, pr, [] {});
       else
-        half_row_p<false, true>(mS, mul, nl2, 0, w0, w1, pr);
+        half_row_p<false, true>(mS, mul, nl2, 0, w0, w1, pr, [] {});
       ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -919,16 +1027,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       }
       tc_fence_after();
       uint32_t pk[32];
-      // (dP is in registers: the next tile's may overwrite it)
-      const auto loaded = [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
-      };
+      uint32_t a[2][32];
+      tmem_ld32(mDP, a[0]);
+      tmem_ld32(mDP + 32, a[1]);
+      tmem_wait_ld();
+      // dP is in registers: the next tile's may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
       if (!part)
-        half_row_ds<false, false>(mDP, dl2, 0, w0, w1, pr, pk, loaded);
+        half_row_ds<false, false>(a, dl2, 0, w0, w1, pr, pk);
       else
-        half_row_ds<false, true>(mDP, dl2, 0, w0, w1, pr, pk, loaded);
+        half_row_ds<false, true>(a, dl2, 0, w0, w1, pr, pk);
       tmem_st32(mS, pk);
       if (part && !self) {
         // keys that are not admitted may hold anything: their rows of K are
@@ -977,7 +1087,10 @@ cudaError_t configure() {
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (bit && (configured.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
   using C = BCfg<D>;
-  if ((e = cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemKv)) != cudaSuccess ||
+  if ((e = cudaFuncSetAttribute(dkdv_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemKv)) !=
+          cudaSuccess ||
+      (e = cudaFuncSetAttribute(dkdv_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemKv)) !=
+          cudaSuccess ||
       (e = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemQ)) != cudaSuccess)
     return e;
   configured.fetch_or(bit, std::memory_order_relaxed);
@@ -991,7 +1104,11 @@ cudaError_t launch(const BwdParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   stats_kernel<D><<<dim3(p.n_q_tiles * 4, (p.Hq + 7) / 8, p.B), 256, 0, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dkdv_kernel<D><<<dim3(p.n_kv_tiles, p.Hkv, p.B), kBwdThreads, C::kSmemKv, s>>>(p);
+  const dim3 kv_grid(p.n_kv_tiles, p.Hkv, p.B);
+  if (p.masked_rows == ULY_ROWS_SDPA)
+    dkdv_kernel<D, false><<<kv_grid, kBwdThreads, C::kSmemKv, s>>>(p);
+  else
+    dkdv_kernel<D, true><<<kv_grid, kBwdThreads, C::kSmemKv, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   dq_kernel<D><<<dim3(p.n_q_tiles, p.Hq, p.B), kBwdThreads, C::kSmemQ, s>>>(p);
   return cudaGetLastError();

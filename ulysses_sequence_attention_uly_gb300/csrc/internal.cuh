@@ -229,9 +229,8 @@ struct BwdParams {
   const uint4* active_bits;
   const uint4* active_inv;
   const int32_t* n_active;
-  float* nl;                      // [1 or 2][B][Hq][n_q_tiles * 128]: -lse log2(e) (admitted keys, masked keys)
+  float* nl;                      // [B][Hq][n_q_tiles * 128]: -lse log2(e)
   float* dl;                      // [B][Hq][n_q_tiles * 128]: -delta
-  int64_t stat_stride;            // floats of one such array
   int32_t masked_rows;
   int32_t withhold_fill;
   int32_t* status;

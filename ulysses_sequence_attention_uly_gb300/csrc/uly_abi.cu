@@ -1175,13 +1175,13 @@ int bwd_q_tiles(const uly_plan* pl) {
 // Workspace of the attention's gradient: the tile tables, the row statistics,
 // and (fused) the replicated rows of do summed over the shards.
 struct BwdWork {
-  int64_t bits, active_bits, active_inv, active, n_active, nl, dl, do_rep, total, stat_stride;
+  int64_t bits, active_bits, active_inv, active, n_active, nl, dl, do_rep, total;
 };
 BwdWork bwd_work(const uly_plan* pl) {
   const uly_desc& d = pl->d;
   BwdWork w;
   const int64_t nt = static_cast<int64_t>(d.B) * pl->n_kv_tiles;
-  w.stat_stride = static_cast<int64_t>(d.B) * d.Hq * bwd_q_tiles(pl) * kTileRows;
+  const int64_t stats = static_cast<int64_t>(d.B) * d.Hq * bwd_q_tiles(pl) * kTileRows * 4;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t a = at;
@@ -1193,12 +1193,31 @@ BwdWork bwd_work(const uly_plan* pl) {
   w.active_inv = take(nt * 16);
   w.active = take(nt * 4);
   w.n_active = take(static_cast<int64_t>(d.B) * 4);
-  w.nl = take(w.stat_stride * 4 * (d.masked_rows == ULY_ROWS_SELF ? 2 : 1));
-  w.dl = take(w.stat_stride * 4);
+  w.nl = take(stats);
+  w.dl = take(stats);
   const bool rep_q = d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX;
   w.do_rep = take(rep_q ? static_cast<int64_t>(d.B) * d.R * d.Hq * d.D * 2 : 0);
   w.total = at;
   return w;
+}
+
+// A tensor [B, rows, heads, D] in bf16 as 128-row tiles of one head that land
+// in shared memory as panels of 64 columns (attn_bwd.cu, load_tile): the
+// panels are a dimension of their own, behind the rows.
+int encode_panel_map(CUtensorMap* m, const void* base, int D, int heads, int64_t rows, int B) {
+  auto enc = encode_fn();
+  if (!enc) return ULY_ERR_CUDA;
+  const cuuint64_t row = static_cast<cuuint64_t>(heads) * D * 2;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(D) * 2, row, 128, row * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(kTileRows), static_cast<cuuint32_t>(D / 64), 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         D > 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ULY_OK : ULY_ERR_CUDA;
 }
 
 int run_backward(const uly_plan* pl, int fused, const void* const* q, const void* const* k, const void* const* v,
@@ -1283,15 +1302,15 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   for (int i = 0; i < P; ++i) {
     const int64_t rq = fused ? pl->rq_p[i] : pl->nq, rk = fused ? pl->rk_p[i] : pl->nk;
     const int hq = static_cast<int>(hq_t), hk = static_cast<int>(hkv_t);
-    if ((rc = encode_map(&p.tq[i], q[i], d.D, hq, rq, d.B, false)) ||
-        (rc = encode_map(&p.tdo[i], dout[i], d.D, hq, rq, d.B, false)) ||
-        (rc = encode_map(&p.tk[i], k[i], d.D, hk, rk, d.B, false)) ||
-        (rc = encode_map(&p.tv[i], v[i], d.D, hk, rk, d.B, false)))
+    if ((rc = encode_panel_map(&p.tq[i], q[i], d.D, hq, rq, d.B)) ||
+        (rc = encode_panel_map(&p.tdo[i], dout[i], d.D, hq, rq, d.B)) ||
+        (rc = encode_panel_map(&p.tk[i], k[i], d.D, hk, rk, d.B)) ||
+        (rc = encode_panel_map(&p.tv[i], v[i], d.D, hk, rk, d.B)))
       return rc;
   }
   if (fused && (d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX)) {
     p.do_rep = ws + w.do_rep;
-    if ((rc = encode_map(&p.tdo_rep, p.do_rep, d.D, d.Hq, d.R, d.B, false))) return rc;
+    if ((rc = encode_panel_map(&p.tdo_rep, p.do_rep, d.D, d.Hq, d.R, d.B))) return rc;
   }
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1302,7 +1321,6 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.n_active = reinterpret_cast<int32_t*>(ws + w.n_active);
   p.nl = reinterpret_cast<float*>(ws + w.nl);
   p.dl = reinterpret_cast<float*>(ws + w.dl);
-  p.stat_stride = w.stat_stride;
   p.masked_rows = d.masked_rows;
   p.withhold_fill = pl->withhold_fill;
   p.status = pl->status;
