@@ -814,6 +814,8 @@ struct QBars {
   uint64_t q_full;
   uint64_t full[3];           // K and V of a tile (K's slot)
   uint64_t s_full[2], dp_full, dp_free, ds_full[2];
+  uint64_t k_done[2];         // dQ(i), and with it dP(i+1), complete: i mod 2, as dQ(i+1) does not wait
+                              // for the loads that follow it
   uint64_t done, drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -855,6 +857,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
     }
     mbar_init(smem_u32(&bars.dp_full), 1);
     mbar_init(smem_u32(&bars.dp_free), 8);
+    mbar_init(smem_u32(&bars.k_done[0]), 1);
+    mbar_init(smem_u32(&bars.k_done[1]), 1);
     mbar_init(smem_u32(&bars.done), 1);
     mbar_init(smem_u32(&bars.drain), 1);
     bars.abort_flag = 0;
@@ -901,9 +905,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
       next(0);
       for (; it < n_it; ++it) {
         const int ks = it % C::kKSlots, vs = it % C::kVSlots;
-        // S(it-1) was issued after dQ(it-3) and dP(it-2), the last readers of
-        // the two slots
-        if (it >= 2 && !mbar_wait(smem_u32(&bars.s_full[(it - 1) & 1]), ((it - 1) >> 1) & 1, deadline, abort_flag)) {
+        // the slots' last readers are dQ(it-3) and dP(it-2); S(1) was issued
+        // after dP(0)
+        if (it == 2 ? !mbar_wait(smem_u32(&bars.s_full[1]), 0, deadline, abort_flag)
+                    : it > 2 && !mbar_wait(smem_u32(&bars.k_done[(it - 3) & 1]), ((it - 3) >> 1) & 1, deadline,
+                                           abort_flag)) {
           bwd_timeout(p, abort_flag);
           break;
         }
@@ -967,6 +973,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
           tc_fence_after();
           issue_cols<D>(tDQ, tmem + 128 * buf, k_c[ks], it > 0);
           if (it + 2 < n_it) {
+            if (it + 3 < n_it) mma_commit(smem_u32(&bars.k_done[buf]));
             if (!(ok = mbar_wait(smem_u32(&bars.full[ks2]), ((it + 2) / C::kKSlots) & 1, deadline, abort_flag))) break;
             issue_rows<D>(tmem + 128 * buf, dq, k_r[ks2]);
             mma_commit(smem_u32(&bars.s_full[buf]));
