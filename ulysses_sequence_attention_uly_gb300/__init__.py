@@ -150,6 +150,38 @@ def _want(t, shape, dtypes, what, device):
         raise ValueError("%s: must be contiguous" % what)
 
 
+_TORCH = None
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+_VEC = [ctypes.c_void_p * max(n, 1) for n in range(MAX_RANKS + 1)]
+
+
+def _checked_ptr(t, shape, dtype, what, device):
+    """Address of a dense tensor of that shape and element type on the device;
+    _want says what is wrong with another."""
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        _want(t, shape, (str(dtype),), what, device)
+    return t.data_ptr()
+
+
+def _checked_ptrs(ts, shapes, dtype, what, device):
+    """As _checked_ptr for a list of shards, as a C array."""
+    n = len(shapes)
+    if ts is None or len(ts) != n:
+        raise ValueError("%s: expected %d tensors, got %s" % (what, n, None if ts is None else len(ts)))
+    return _VEC[n](*[_checked_ptr(t, s, dtype, what, device) for t, s in zip(ts, shapes)])
+
+
 def _want_list(ts, shapes, dtypes, what, device):
     if ts is None or len(ts) != len(shapes):
         raise ValueError("%s: expected %d tensors, got %s" % (what, len(shapes), None if ts is None else len(ts)))
@@ -177,39 +209,45 @@ def _want_scales(dtype, q_scale, k_scale, v_scale, Hq, Hkv, device):
         _want(t, (n,), ("torch.float32",), what, device)
 
 
-def _want_rows(ts, shapes, what, device):
-    """bf16 shards whose rows may be more than a row apart (a part of a packed
-    projection); returns the row stride in elements, 0 for dense ones."""
-    import torch
-    if ts is None or len(ts) != len(shapes):
-        raise ValueError("%s: expected %d tensors, got %s" % (what, len(shapes), None if ts is None else len(ts)))
+def _row_ptrs(ts, shapes, what, device):
+    """Addresses of bf16 shards whose rows may be more than a row apart (a part
+    of a packed projection), and the row stride in elements (0 for dense)."""
+    torch = _torch()
+    n = len(shapes)
+    if ts is None or len(ts) != n:
+        raise ValueError("%s: expected %d tensors, got %s" % (what, n, None if ts is None else len(ts)))
     stride = None
-    for i, (t, (B, rows, H, D)) in enumerate(zip(ts, shapes)):
-        w = "%s[%d]" % (what, i)
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.device.index != device:
-            raise ValueError("%s: expected a CUDA tensor on device %d" % (w, device))
-        if t.dtype != torch.bfloat16:
-            raise ValueError("%s: element type %s, expected torch.bfloat16" % (w, t.dtype))
-        if tuple(t.shape) != (B, rows, H, D):
-            raise ValueError("%s: shape %s, expected %s" % (w, tuple(t.shape), (B, rows, H, D)))
+    ptrs = []
+    for i, (t, shape) in enumerate(zip(ts, shapes)):
+        if not isinstance(t, torch.Tensor) or t.get_device() != device or not t.is_cuda:
+            raise ValueError("%s[%d]: expected a CUDA tensor on device %d" % (what, i, device))
+        if t.dtype is not torch.bfloat16:
+            raise ValueError("%s[%d]: element type %s, expected torch.bfloat16" % (what, i, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s[%d]: shape %s, expected %s" % (what, i, tuple(t.shape), tuple(shape)))
+        ptrs.append(t.data_ptr())
+        B, rows, H, D = shape
+        if rows == 1 and B == 1 and H == 1:
+            if t.stride(3) == 1 or D == 1:
+                continue
         sb, sr, sh, sd = t.stride()
         if sd != 1 or (H > 1 and sh != D):
-            raise ValueError("%s: the heads of a row must be contiguous" % w)
+            raise ValueError("%s[%d]: the heads of a row must be contiguous" % (what, i))
         if rows == 1 and B == 1:
             continue  # any stride
         rs = sr if rows > 1 else sb
         if rs < H * D or rs % 8 or (B > 1 and sb != rows * rs):
-            raise ValueError("%s: rows must be a multiple of 8 elements apart, at least %d, and batches rows * that "
-                             "apart" % (w, H * D))
-        if stride not in (None, rs):
-            raise ValueError("%s: the shards' rows must be the same distance apart" % w)
+            raise ValueError("%s[%d]: rows must be a multiple of 8 elements apart, at least %d, and batches rows * "
+                             "that apart" % (what, i, H * D))
+        if stride is not None and stride != rs:
+            raise ValueError("%s: the shards' rows must be the same distance apart" % what)
         stride = rs
-    return stride or 0
+    return _VEC[n](*ptrs), stride or 0
 
 
 def _workspace(ws, nbytes, device, stream):
     """The caller's workspace, checked, or a new one on the call's stream."""
-    import torch
+    torch = _torch()
     if ws is None:
         if stream is None:
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -220,6 +258,11 @@ def _workspace(ws, nbytes, device, stream):
         raise ValueError("workspace: expected a contiguous uint8 tensor of at least %d bytes on device %d"
                          % (nbytes, device))
     return ws
+
+
+def _raw_stream(stream, device):
+    """A stream's handle; by default the device's current one."""
+    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _ptr(t) -> int | None:
@@ -380,31 +423,55 @@ class Plan:
     def test_check_narrow(self, rows: int):
         _check(lib().uly_plan_test_check_narrow(self._h, int(rows)), "uly_plan_test_check_narrow")
 
+    # ---- the tensors' shapes, worked out once
+    def _shapes(self, fused: bool):
+        """(q, k/v, lse) shapes of every shard (fused) or rank."""
+        key = "_shapes_seq" if fused else "_shapes_heads"
+        got = self.__dict__.get(key)
+        if got is None:
+            size = _torch().Size
+            B, D, P = self.B, self.D, self.P
+            if fused:
+                q = [(B, self.shard_rows(p), self.Hq, D) for p in range(P)]
+                k = [(B, self.shard_rows(p, True), self.Hkv, D) for p in range(P)]
+            else:
+                q = [(B, self.heads_rows_q, self.Hq // P, D)] * P
+                k = [(B, self.heads_rows_kv, self.Hkv // P, D)] * P
+            got = ([size(s) for s in q], [size(s) for s in k], [size(s[:3]) for s in q])
+            self.__dict__[key] = got
+        return got
+
+    def _nk(self):
+        n = self.__dict__.get("_heads_rows_kv")
+        if n is None:
+            n = self._heads_rows_kv = self.heads_rows_kv
+        return n
+
     # ---- argument checks against the plan's shape
-    def _check_seq(self, q=None, k=None, v=None, o=None, lse=None, names=("q", "k", "v", "o")):
+    def _check_seq(self, q=None, k=None, v=None, o=None, lse=None):
         B, D, dev, P = self.B, self.D, self.device, self.P
         el = _ELEM[self.dtype]
         if q is not None:
-            _want_list(q, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], el, names[0], dev)
-        for t, what in ((k, names[1]), (v, names[2])):
+            _want_list(q, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], el, "q", dev)
+        for t, what in ((k, "k"), (v, "v")):
             if t is not None:
                 _want_list(t, [(B, self.shard_rows(p, True), self.Hkv, D) for p in range(P)], el, what, dev)
         if o is not None:
-            _want_list(o, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], ("torch.bfloat16",), names[3], dev)
+            _want_list(o, [(B, self.shard_rows(p), self.Hq, D) for p in range(P)], ("torch.bfloat16",), "o", dev)
         if lse is not None:
             _want_list(lse, [(B, self.shard_rows(p), self.Hq) for p in range(P)], ("torch.float32",), "lse", dev)
 
-    def _check_heads(self, qh=None, kh=None, vh=None, oh=None, lse=None, names=("qh", "kh", "vh", "oh")):
+    def _check_heads(self, qh=None, kh=None, vh=None, oh=None, lse=None):
         B, D, dev, P = self.B, self.D, self.device, self.P
         el = _ELEM[self.dtype]
         hq, hkv = self.Hq // P, self.Hkv // P
         if qh is not None:
-            _want_list(qh, [(B, self.heads_rows_q, hq, D)] * P, el, names[0], dev)
-        for t, what in ((kh, names[1]), (vh, names[2])):
+            _want_list(qh, [(B, self.heads_rows_q, hq, D)] * P, el, "qh", dev)
+        for t, what in ((kh, "kh"), (vh, "vh")):
             if t is not None:
                 _want_list(t, [(B, self.heads_rows_kv, hkv, D)] * P, el, what, dev)
         if oh is not None:
-            _want_list(oh, [(B, self.heads_rows_q, hq, D)] * P, ("torch.bfloat16",), names[3], dev)
+            _want_list(oh, [(B, self.heads_rows_q, hq, D)] * P, ("torch.bfloat16",), "oh", dev)
         if lse is not None:
             _want_list(lse, [(B, self.heads_rows_q, hq)] * P, ("torch.float32",), "lse", dev)
 
@@ -485,24 +552,32 @@ class Plan:
         """Bytes of workspace of attention_backward and sp_attention_backward."""
         return int(lib().uly_attention_backward_workspace(self._h))
 
-    def _attn_backward(self, fn, name, q, k, v, o, lse, do, dq, dk, dv, key_mask, key_ranges, scale, workspace,
-                       stream, check):
-        for t, what in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"), (dk, "dk"),
-                        (dv, "dv")):
-            if t is None:
-                raise ValueError("%s: %s is missing" % (name[4:], what))
+    def _attn_backward(self, fn, name, fused, q, k, v, o, lse, do, dq, dk, dv, key_mask, key_ranges, scale,
+                       workspace, stream):
+        torch = _torch()
         if self.dtype != "bf16":
             raise UlyError(ULY_ERR_UNSUPPORTED, name)
-        check(q, k, v, o, lse)
-        check(do, dk, dv, dq, names=("do", "dk", "dv", "dq"))
-        _want_mask(key_mask, key_ranges, self.B, self.heads_rows_kv, self.device)
+        dev, bf16 = self.device, torch.bfloat16
+        qs, ks, ls = self._shapes(fused)
+        ptrs = [_checked_ptrs(t, s, bf16, what, dev)
+                for t, s, what in ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o"), (do, qs, "do"),
+                                   (dq, qs, "dq"), (dk, ks, "dk"), (dv, ks, "dv"))]
+        lse = _checked_ptrs(lse, ls, torch.float32, "lse", dev)
+        if key_mask is not None or key_ranges is not None:
+            _want_mask(key_mask, key_ranges, self.B, self._nk(), dev)
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
-        n_ranges = 0 if key_ranges is None else int(key_ranges.shape[1])
-        workspace = _workspace(workspace, self.attention_backward_workspace(), self.device, stream)
-        _check(fn(self._h, _ptr_array(q), _ptr_array(k), _ptr_array(v), _ptr_array(o), _ptr_array(lse),
-                  _ptr_array(do), _ptr(key_mask), _ptr(key_ranges), n_ranges, ctypes.c_float(scale), _ptr_array(dq),
-                  _ptr_array(dk), _ptr_array(dv), _ptr(workspace), workspace.numel(), _stream(stream)), name)
+        n_ranges = 0 if key_ranges is None else key_ranges.shape[1]
+        nbytes = self.__dict__.get("_bwd_bytes")
+        if nbytes is None:
+            nbytes = self._bwd_bytes = self.attention_backward_workspace()
+        workspace = _workspace(workspace, nbytes, dev, stream)
+        pq, pk, pv, po, pdo, pdq, pdk, pdv = ptrs
+        st = fn(self._h, pq, pk, pv, po, lse, pdo, None if key_mask is None else key_mask.data_ptr(),
+                None if key_ranges is None else key_ranges.data_ptr(), n_ranges, scale, pdq, pdk, pdv,
+                workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+        if st != ULY_OK:
+            raise UlyError(st, name)
 
     def attention_backward(self, qh, kh, vh, oh, lse, doh, dqh, dkh, dvh, key_mask=None, key_ranges=None, scale=None,
                            workspace=None, stream=None):
@@ -510,53 +585,60 @@ class Plan:
         from the forward's inputs, its outputs oh and lse, and doh.  workspace:
         a uint8 tensor of attention_backward_workspace() bytes; by default one
         is allocated on the call's stream."""
-        self._attn_backward(lib().uly_attention_backward, "uly_attention_backward", qh, kh, vh, oh, lse, doh, dqh,
-                            dkh, dvh, key_mask, key_ranges, scale, workspace, stream, self._check_heads)
+        self._attn_backward(lib().uly_attention_backward, "uly_attention_backward", False, qh, kh, vh, oh, lse, doh,
+                            dqh, dkh, dvh, key_mask, key_ranges, scale, workspace, stream)
 
     def sp_attention_backward(self, q, k, v, o, lse, do, dq, dk, dv, key_mask=None, key_ranges=None, scale=None,
                               workspace=None, stream=None):
         """The gradient of sp_attention (uly_sp_attention_backward) on the
         seq-sharded shards.  Replicated rows: the shards' do add up, and the
         gradients go to the copy of the shard that owns the head."""
-        self._attn_backward(lib().uly_sp_attention_backward, "uly_sp_attention_backward", q, k, v, o, lse, do, dq,
-                            dk, dv, key_mask, key_ranges, scale, workspace, stream, self._check_seq)
+        self._attn_backward(lib().uly_sp_attention_backward, "uly_sp_attention_backward", True, q, k, v, o, lse, do,
+                            dq, dk, dv, key_mask, key_ranges, scale, workspace, stream)
 
     # ---- norm and rotation of q and k heads
     def norm_rope_backward_workspace(self) -> int:
         """Bytes of workspace of norm_rope_backward."""
         return int(lib().uly_norm_rope_backward_workspace(self._h))
 
-    def _norm_args(self, q, k, outs, q_weight, k_weight, cos, sin, pairs):
-        """Check one norm_rope call; returns (row strides, table batches, pairs)."""
-        B, D, dev, P = self.B, self.D, self.device, self.P
-        if self.dtype == "bf16":
-            strides = []
-            for x, is_kv, what in ((q, False, "q"), (k, True, "k")):
-                shapes = [(B, self.shard_rows(p, is_kv), self.Hkv if is_kv else self.Hq, D) for p in range(P)]
-                strides.append(0 if x is None else _want_rows(x, shapes, what, dev))
-                for t, name in outs[is_kv]:
-                    if (t is None) != (x is None):
-                        raise ValueError("%s: given or left out with %s" % (name, what))
-                    if t is not None:
-                        _want_list(t, shapes, ("torch.bfloat16",), name, dev)
-        else:
-            strides = [0, 0]  # the C ABI refuses the plan
-        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                _want(w, (D,), ("torch.float32",), what, dev)
+    def _norm_args(self, q, k, dense, q_weight, k_weight, cos, sin, pairs):
+        """Check one norm_rope call; `dense`: pairs of q and k shards with their
+        names.  Returns the C arguments: q, k, their row strides, the dense
+        shards, and the weights, tables, table batches and pairs."""
+        torch = _torch()
+        if self.dtype != "bf16":
+            raise UlyError(ULY_ERR_UNSUPPORTED, "norm_rope")
+        dev, D, f32 = self.device, self.D, torch.float32
+        shapes = self._shapes(True)
+        pq = pk = None
+        rq = rk = 0
+        if q is not None:
+            pq, rq = _row_ptrs(q, shapes[0], "q", dev)
+        if k is not None:
+            pk, rk = _row_ptrs(k, shapes[1], "k", dev)
+        out = []
+        for pair in dense:
+            for x, s, (t, what) in ((q, shapes[0], pair[0]), (k, shapes[1], pair[1])):
+                if (t is None) != (x is None):
+                    raise ValueError("%s: given or left out with %s" % (what, "q" if s is shapes[0] else "k"))
+                out.append(None if t is None else _checked_ptrs(t, s, torch.bfloat16, what, dev))
+        wq = None if q_weight is None else _checked_ptr(q_weight, (D,), f32, "q_weight", dev)
+        wk = None if k_weight is None else _checked_ptr(k_weight, (D,), f32, "k_weight", dev)
         if (cos is None) != (sin is None):
             raise ValueError("cos and sin: both or neither")
-        batches = 1
+        batches, pc, ps = 1, None, None
         if cos is not None:
-            batches = cos.shape[0] if cos.dim() == 3 else 1
-            shape = (self.heads_rows_kv, D // 2) if cos.dim() == 2 else (batches, self.heads_rows_kv, D // 2)
-            if batches not in (1, B):
-                raise ValueError("cos: %d batches, expected 1 or %d" % (batches, B))
-            _want(cos, shape, ("torch.float32",), "cos", dev)
-            _want(sin, shape, ("torch.float32",), "sin", dev)
-        if pairs not in PAIRS:
+            shape = (self._nk(), D // 2)
+            if cos.dim() == 3:
+                batches = cos.shape[0]
+                if batches not in (1, self.B):
+                    raise ValueError("cos: %d batches, expected 1 or %d" % (batches, self.B))
+                shape = (batches,) + shape
+            pc, ps = _checked_ptr(cos, shape, f32, "cos", dev), _checked_ptr(sin, shape, f32, "sin", dev)
+        pr = PAIRS.get(pairs)
+        if pr is None:
             raise ValueError("pairs: %r, expected one of %s" % (pairs, ", ".join(PAIRS)))
-        return strides, batches, PAIRS[pairs]
+        return pq, pk, rq, rk, out, (wq, wk, pc, ps, batches, pr)
 
     def norm_rope(self, q, k, q_out, k_out, q_weight=None, k_weight=None, cos=None, sin=None, pairs="interleaved",
                   eps=1e-6, stream=None):
@@ -565,11 +647,11 @@ class Plan:
         cos, sin: f32 [Nk, D/2] or [B, Nk, D/2] in the global key order.  q and
         k may be parts of a packed projection (rows a fixed stride apart); q
         with q_out, or k with k_out, may be None."""
-        strides, batches, pr = self._norm_args(q, k, (((q_out, "q_out"),), ((k_out, "k_out"),)), q_weight, k_weight,
-                                               cos, sin, pairs)
-        _check(lib().uly_norm_rope(self._h, _ptr_array(q), _ptr_array(k), strides[0], strides[1], _ptr(q_weight),
-                                   _ptr(k_weight), _ptr(cos), _ptr(sin), batches, pr, ctypes.c_float(eps),
-                                   _ptr_array(q_out), _ptr_array(k_out), _stream(stream)), "uly_norm_rope")
+        pq, pk, rq, rk, (oq, ok), rest = self._norm_args(q, k, (((q_out, "q_out"), (k_out, "k_out")),), q_weight,
+                                                         k_weight, cos, sin, pairs)
+        st = lib().uly_norm_rope(self._h, pq, pk, rq, rk, *rest, eps, oq, ok, _raw_stream(stream, self.device))
+        if st != ULY_OK:
+            raise UlyError(st, "uly_norm_rope")
 
     def norm_rope_backward(self, q, k, dq_out, dk_out, dq, dk, q_weight=None, k_weight=None, cos=None, sin=None,
                            dq_weight=None, dk_weight=None, pairs="interleaved", eps=1e-6, workspace=None,
@@ -577,19 +659,23 @@ class Plan:
         """The gradient of norm_rope (uly_norm_rope_backward): dq, dk and, when
         given, dq_weight and dk_weight (f32 [D]) from the gradients dq_out,
         dk_out of its outputs."""
-        outs = (((dq_out, "dq_out"), (dq, "dq")), ((dk_out, "dk_out"), (dk, "dk")))
-        strides, batches, pr = self._norm_args(q, k, outs, q_weight, k_weight, cos, sin, pairs)
-        for w, what in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-            if w is not None:
-                _want(w, (self.D,), ("torch.float32",), what, self.device)
-        if dq_weight is not None or dk_weight is not None or workspace is not None:
-            workspace = _workspace(workspace, self.norm_rope_backward_workspace(), self.device, stream)
-        _check(lib().uly_norm_rope_backward(self._h, _ptr_array(q), _ptr_array(k), strides[0], strides[1],
-                                            _ptr_array(dq_out), _ptr_array(dk_out), _ptr(q_weight), _ptr(k_weight),
-                                            _ptr(cos), _ptr(sin), batches, pr, ctypes.c_float(eps), _ptr_array(dq),
-                                            _ptr_array(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
-                                            0 if workspace is None else workspace.numel(), _stream(stream)),
-               "uly_norm_rope_backward")
+        pq, pk, rq, rk, (gq, gk, oq, ok), rest = self._norm_args(
+            q, k, (((dq_out, "dq_out"), (dk_out, "dk_out")), ((dq, "dq"), (dk, "dk"))), q_weight, k_weight, cos, sin,
+            pairs)
+        f32, dev = _torch().float32, self.device
+        dwq = None if dq_weight is None else _checked_ptr(dq_weight, (self.D,), f32, "dq_weight", dev)
+        dwk = None if dk_weight is None else _checked_ptr(dk_weight, (self.D,), f32, "dk_weight", dev)
+        ws, nbytes = None, 0
+        if dwq is not None or dwk is not None or workspace is not None:
+            nbytes = self.__dict__.get("_norm_bytes")
+            if nbytes is None:
+                nbytes = self._norm_bytes = self.norm_rope_backward_workspace()
+            workspace = _workspace(workspace, nbytes, dev, stream)
+            ws, nbytes = workspace.data_ptr(), workspace.numel()
+        st = lib().uly_norm_rope_backward(self._h, pq, pk, rq, rk, gq, gk, *rest, eps, oq, ok, dwq, dwk, ws, nbytes,
+                                          _raw_stream(stream, dev))
+        if st != ULY_OK:
+            raise UlyError(st, "uly_norm_rope_backward")
 
     def pipelined_attention(self, q, k, v, qh, kh, vh, oh, o, key_mask=None, key_ranges=None, scale=None,
                             head_groups=0, q_scale=None, k_scale=None, v_scale=None, stream=None,
