@@ -179,7 +179,15 @@ def _checked_ptrs(ts, shapes, dtype, what, device):
     n = len(shapes)
     if ts is None or len(ts) != n:
         raise ValueError("%s: expected %d tensors, got %s" % (what, n, None if ts is None else len(ts)))
-    return _VEC[n](*[_checked_ptr(t, s, dtype, what, device) for t, s in zip(ts, shapes)])
+    tensor = _torch().Tensor
+    out = []
+    for i in range(n):
+        t = ts[i]
+        if not (isinstance(t, tensor) and t.dtype is dtype and t.shape == shapes[i] and t.get_device() == device
+                and t.is_contiguous()):
+            _want(t, shapes[i], (str(dtype),), "%s[%d]" % (what, i), device)
+        out.append(t.data_ptr())
+    return _VEC[n](*out)
 
 
 def _want_list(ts, shapes, dtypes, what, device):
@@ -563,19 +571,25 @@ class Plan:
                 for t, s, what in ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o"), (do, qs, "do"),
                                    (dq, qs, "dq"), (dk, ks, "dk"), (dv, ks, "dv"))]
         lse = _checked_ptrs(lse, ls, torch.float32, "lse", dev)
-        if key_mask is not None or key_ranges is not None:
-            _want_mask(key_mask, key_ranges, self.B, self._nk(), dev)
+        pm = pr = None
+        n_ranges = 0
+        if key_ranges is not None:
+            n_ranges = key_ranges.shape[1] if key_ranges.dim() == 3 else 0
+            if n_ranges < 1:
+                _want_mask(None, key_ranges, self.B, 0, dev)
+            pr = _checked_ptr(key_ranges, (self.B, n_ranges, 2), torch.int32, "key_ranges", dev)
+        if key_mask is not None:
+            pm = _checked_ptr(key_mask, (self.B, self._nk()),
+                              torch.bool if key_mask.dtype is torch.bool else torch.uint8, "key_mask", dev)
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
-        n_ranges = 0 if key_ranges is None else key_ranges.shape[1]
         nbytes = self.__dict__.get("_bwd_bytes")
         if nbytes is None:
             nbytes = self._bwd_bytes = self.attention_backward_workspace()
         workspace = _workspace(workspace, nbytes, dev, stream)
         pq, pk, pv, po, pdo, pdq, pdk, pdv = ptrs
-        st = fn(self._h, pq, pk, pv, po, lse, pdo, None if key_mask is None else key_mask.data_ptr(),
-                None if key_ranges is None else key_ranges.data_ptr(), n_ranges, scale, pdq, pdk, pdv,
-                workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+        st = fn(self._h, pq, pk, pv, po, lse, pdo, pm, pr, n_ranges, scale, pdq, pdk, pdv, workspace.data_ptr(),
+                workspace.numel(), _raw_stream(stream, dev))
         if st != ULY_OK:
             raise UlyError(st, name)
 

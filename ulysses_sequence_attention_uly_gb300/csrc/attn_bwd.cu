@@ -12,10 +12,10 @@
 // Two main kernels, each with its sums in TMEM from first to last term, so
 // that no sum passes through memory and none depends on the order in which
 // CTAs run (the results are the same bits on every call):
-//   dkdv_kernel  one CTA per (batch, kv head, 128 keys), over every query
+//   dkdv_cta  one CTA per (batch, kv head, 128 keys), over every query
 //                head of the group and every 128-query tile: four products a
 //                tile pair (S, dP, dV, dK);
-//   dq_kernel    one CTA per (batch, q head, 128 queries), over every 128-key
+//   dq_cta    one CTA per (batch, q head, 128 queries), over every 128-key
 //                tile with an admitted key: three products (S, dP, dQ).
 // One kernel with five products would have to add dQ through f32 atomics in
 // memory, whose order changes the bits; the price of the two is 7/5 of the
@@ -57,18 +57,18 @@ struct BCfg {
   static constexpr int kRowSteps = kTileRows / 16;         // MMAs of a product over 128 rows
   static constexpr uint32_t kIdescS = make_idesc(1u, 128, 128, 0, 0);
   static constexpr uint32_t kIdescO = make_idesc(1u, 128, D, 0, 1);
-  // dkdv_kernel: K, V, three Q and two dO slots with their row statistics,
-  // barriers.  No static shared memory and no slack: the buffer starts on a
-  // 1024-byte boundary (the kernel checks it), and at D = 128 it is all that a
-  // CTA can have.
+  // No static shared memory and no slack: the buffer starts on a 1024-byte
+  // boundary (the kernel checks it), and at D = 128 it is all that a CTA can
+  // have.
+  // dK, dV: K, V, three Q and two dO slots with their row statistics, barriers
   static constexpr int kQSlots = 3, kOSlots = 2;
   static constexpr int kStatBytes = kTileRows * 4;         // -lse log2(e) or -delta of a tile's rows
   static constexpr int kKvBars = (2 + kQSlots + kOSlots) * kTileBytes + (kQSlots + kOSlots) * kStatBytes;
-  static constexpr int kSmemKv = kKvBars + 256;
-  static_assert(kSmemKv <= 227 * 1024, "shared memory of a CTA");
-  // dq_kernel: Q, dO, three K and two V slots
+  // dQ: Q, dO, three K and two V slots, barriers
   static constexpr int kKSlots = 3, kVSlots = 2;
-  static constexpr int kSmemQ = 1024 + (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kQBars = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kSmem = kKvBars + 256;
+  static_assert(kQBars <= kKvBars && kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 constexpr int kBwdThreads = 320;  // 8 warps of elementwise work, a TMA warp, an MMA warp
 
@@ -234,24 +234,112 @@ __device__ __forceinline__ void store_rows(const BwdParams& p, uint8_t* const* o
   }
 }
 
-// ----------------------------------------------------- row statistics --
-// Per (batch, q head, 128-row tile of a run): -lse log2(e) and -delta, padded
-// to whole tiles, which the main kernels read in tiles.  A row that takes
-// part in nothing (past its run's end, no admitted key, or zero by the
-// masked-row convention) has -inf, whose exponential is 0.  Fused, replicated
-// rows: do is the sum of every shard's copy, since each received the output; the sum is
-// rounded to bf16 into do_rep (the MMA's operand) and delta uses that value.
-// Bound by memory: o and do are read once.  32 rows x 8 heads a CTA; 16 (D =
+// ------------------------------------------------------- preparation --
+// Is the key of global index `key` admitted in batch b?
+__device__ __forceinline__ bool admitted(const BwdParams& p, int b, int key) {
+  if (!in_bounds(&g_bwd_violations, key, 1, p.Nk)) return false;
+  if (p.key_mask) return p.key_mask[static_cast<int64_t>(b) * p.Nk + key] != 0;
+  if (!p.key_ranges) return true;
+  const int32_t* rg = p.key_ranges + static_cast<int64_t>(b) * p.n_ranges * 2;
+  for (int q = 0; q < p.n_ranges; ++q)
+    if (key >= rg[2 * q] && key < rg[2 * q + 1]) return true;
+  return false;
+}
+
+// global index of the first key of kv run s
+__device__ __forceinline__ int first_key(const BwdParams& p, int s) {
+  int k = 0;
+  for (int i = 0; i < s; ++i) k += p.kseg[i].len;
+  return k;
+}
+
+constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 16;  // rows of a CTA of prep_kernel
+
+// The kv tile tables of batch b: the admitted keys of every tile, and the list
+// of tiles that a query attends to, in key order.  One CTA, a warp a tile.
+struct TableSmem {
+  uint4 bits[kPrepThreads], inv[kPrepThreads];
+  int32_t packed[kPrepThreads], warp_sum[kPrepThreads / 32];
+};
+__device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSmem& sm) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(b) * p.n_kv_tiles;
+  int base = 0;
+  for (int t0 = 0; t0 < p.n_kv_tiles; t0 += kPrepThreads) {
+    for (int k = warp; k < kPrepThreads && t0 + k < p.n_kv_tiles; k += kPrepThreads / 32) {
+      const int s = seg_of(p.kseg, p.n_kseg, t0 + k), i = t0 + k - p.kseg[s].first;
+      const int key0 = first_key(p, s) + i * kTileRows, n_in = min(kTileRows, p.kseg[s].len - i * kTileRows);
+      uint32_t w[4], in[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = lane + 32 * j;
+        const bool ok = c < n_in && admitted(p, b, key0 + c);
+        w[j] = __ballot_sync(0xffffffffu, ok);
+        in[j] = __ballot_sync(0xffffffffu, c < n_in);
+      }
+      if (lane == 0) {
+        const uint4 wb = make_uint4(w[0], w[1], w[2], w[3]);
+        p.tile_bits[row + t0 + k] = wb;
+        sm.bits[k] = wb;
+        sm.inv[k] = make_uint4(~w[0] & in[0], ~w[1] & in[1], ~w[2] & in[2], ~w[3] & in[3]);
+        sm.packed[k] = (s << 20) | i;
+      }
+    }
+    __syncthreads();
+    const int k = threadIdx.x;
+    bool any = false;
+    if (t0 + k < p.n_kv_tiles) {
+      const uint4 wb = sm.bits[k];
+      any = p.masked_rows == ULY_ROWS_SELF || (wb.x | wb.y | wb.z | wb.w) != 0u;
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, any);
+    if (lane == 0) sm.warp_sum[warp] = __popc(vote);
+    __syncthreads();
+    int slot = base + __popc(vote & ((1u << lane) - 1u));
+    for (int i = 0; i < kPrepThreads / 32; ++i) {
+      if (i < warp) slot += sm.warp_sum[i];
+      base += sm.warp_sum[i];
+    }
+    if (any && in_bounds(&g_bwd_violations, slot, 1, p.n_kv_tiles)) {
+      p.active[row + slot] = sm.packed[k];
+      p.active_bits[row + slot] = sm.bits[k];
+      p.active_inv[row + slot] = sm.inv[k];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.n_active[b] = base;
+}
+
+// The first B CTAs build the kv tile tables.  The others: per (batch, q head,
+// 128-row tile of a run) -lse log2(e) and -delta, padded to whole tiles, which
+// the main kernel reads in tiles.  A row that takes part in nothing (past its
+// run's end, no admitted key, or zero by the masked-row convention) has -inf,
+// whose exponential is 0.  Fused, replicated rows: do is the sum of every
+// shard's copy, since each received the output; the sum is rounded to bf16 into
+// do_rep (the MMA's operand) and delta uses that value.
+// Bound by memory: o and do are read once.  16 rows x 8 heads a CTA; 16 (D =
 // 128) or 8 lanes share a row, the results go through shared memory so that
 // they are written along rows.
 template <int D>
-__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdParams p) {
-  constexpr int kLanes = D / 8, kUnits = 256 / kLanes, kRows = 32, kHeads = 8;
-  __shared__ float s_dl[kHeads][kRows + 1];
-  const int t = blockIdx.x / (kTileRows / kRows), r_lo = (blockIdx.x % (kTileRows / kRows)) * kRows;
-  const int h0 = blockIdx.y * kHeads, b = blockIdx.z;
-  const int s = seg_of(p.qseg, p.n_qseg, t);
-  const Seg run = p.qseg[s];
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ BwdParams p) {
+  constexpr int kLanes = D / 8, kUnits = kPrepThreads / kLanes, kRows = kPrepRows, kHeads = 8;
+  constexpr int kParts = kTileRows / kRows;
+  __shared__ union {
+    TableSmem table;
+    float dl[kHeads][kRows + 1];
+  } sm;
+  if (blockIdx.x < static_cast<uint32_t>(p.B)) {
+    build_tables(p, blockIdx.x, sm.table);
+    return;
+  }
+  uint32_t i0 = blockIdx.x - p.B;
+  const int hg = (p.Hq + kHeads - 1) / kHeads;
+  const int h0 = static_cast<int>(i0 % hg) * kHeads;
+  i0 /= hg;
+  const int t = static_cast<int>(i0 / kParts % p.n_q_tiles), r_lo = static_cast<int>(i0 % kParts) * kRows;
+  const int b = static_cast<int>(i0 / kParts / p.n_q_tiles);
+  const Seg run = p.qseg[seg_of(p.qseg, p.n_qseg, t)];
   const int row0 = (t - run.first) * kTileRows + r_lo;  // first row inside the run
   const int lane = threadIdx.x % kLanes, unit = threadIdx.x / kLanes;
   const bool rep = p.fused && run.out_shard < 0;
@@ -296,10 +384,10 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_dl[hh][r] = sum;
+    if (lane == 0) sm.dl[hh][r] = sum;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * kHeads; i += 256) {
+  for (int i = threadIdx.x; i < kRows * kHeads; i += kPrepThreads) {
     const int hh = i / kRows, r = i % kRows, h = h0 + hh;
     if (h >= p.Hq) continue;
     const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + t) * kTileRows + r_lo + r;
@@ -312,17 +400,13 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ BwdP
       const int64_t li = row * p.lse_row_stride + (p.fused ? h : h % p.Hq_l);
       float lse = -INFINITY;
       if (in_bounds(&g_bwd_violations, li, 1, p.lse_batch_stride[sh])) lse = p.lse[sh][b * p.lse_batch_stride[sh] + li];
-      bool own_ok = true;
-      if (p.masked_rows != ULY_ROWS_SDPA && run.kv_seg >= 0) {
-        const Seg& ks = p.kseg[run.kv_seg];
-        const int c = lrow % kTileRows;
-        const uint4 kb = p.tile_bits[static_cast<int64_t>(b) * p.n_kv_tiles + ks.first + lrow / kTileRows];
-        own_ok = (bits_word(kb, c >> 5) >> (c & 31)) & 1u;
-      }
-      const bool live = lse != -INFINITY && (own_ok || p.masked_rows != ULY_ROWS_ZERO);
+      // (ULY_ROWS_ZERO: a row whose own token is a masked key)
+      const bool zero = p.masked_rows == ULY_ROWS_ZERO && run.kv_seg >= 0 &&
+                        !admitted(p, b, first_key(p, run.kv_seg) + lrow);
+      const bool live = lse != -INFINITY && !zero;
       if (live) {
         nl = -lse * 1.4426950408889634f;
-        dl = -s_dl[hh][r];
+        dl = -sm.dl[hh][r];
       }
     }
     p.nl[at] = nl;
@@ -427,7 +511,7 @@ struct KvBars {
 };
 static_assert(sizeof(KvBars) <= 256, "room for the barriers");
 
-// What the elementwise warps of dkdv_kernel share.
+// What the elementwise warps of dkdv_cta share.
 struct KvWork {
   KvBars* bars;
   uint32_t tmem, sQ, sDO, sNl, sDl;
@@ -435,7 +519,7 @@ struct KvWork {
   uint64_t deadline;
 };
 
-// The elementwise loop of dkdv_kernel: one thread per key and half of the
+// The elementwise loop of dkdv_cta: one thread per key and half of the
 // queries.  MODE 0: every pair of the warp attends.  1: `dead` keys do not.
 // 2: it goes by the queries' own tokens too (ULY_ROWS_ZERO, _SELF).  Loops of
 // their own, so that the common one has no test in it and fits the registers.
@@ -561,12 +645,10 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
 // after dK(i-3), is complete; dO(i) over dO(i-2) once dV(i-2) is.
 // TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D).
 template <int D, bool OWN>
-__global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b) {
   using C = BCfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
   KvBars& bars = *reinterpret_cast<KvBars*>(smem_raw + C::kKvBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int r = hk / p.Hkv_l;  // owning rank
   const Seg run = p.kseg[seg_of(p.kseg, p.n_kseg, t)];
   const int row0 = (t - run.first) * kTileRows;
@@ -579,10 +661,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dkdv_kernel(const __grid_const
   const uint32_t sDO = sQ + C::kQSlots * C::kTileBytes, sNl = sDO + C::kOSlots * C::kTileBytes;
   const uint32_t sDl = sNl + C::kQSlots * C::kStatBytes;
   volatile int* abort_flag = &bars.abort_flag;
-  if (sK & 1023u) {  // (never: the buffer is placed on a 1024-byte boundary)
-    if (tid == 0) atomicOr(p.status, kStatusTimeout);
-    return;
-  }
   if (tid == 0) {
     mbar_init(smem_u32(&bars.kq_full), 1);
     mbar_init(smem_u32(&bars.q1_full), 1);
@@ -832,20 +910,17 @@ struct QBars {
 //            scores are there when this one's are done).
 // TMEM: S0 [0,128) S1 [128,256) dP [256,384) dQ [384,384+D).
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, int t, int h, int b) {
   using C = BCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ QBars bars;
+  QBars& bars = *reinterpret_cast<QBars*>(smem_raw + C::kQBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int r = h / p.Hq_l, hk = h / p.G;
   const Seg run = p.qseg[seg_of(p.qseg, p.n_qseg, t)];
   const int row0 = (t - run.first) * kTileRows;
   const int n_it = p.n_active[b];
   const int32_t* active = p.active + static_cast<int64_t>(b) * p.n_kv_tiles;
 
-  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = sbase, sDO = sbase + C::kTileBytes, sK = sbase + 2 * C::kTileBytes;
+  const uint32_t sQ = smem_u32(smem_raw), sDO = sQ + C::kTileBytes, sK = sQ + 2 * C::kTileBytes;
   const uint32_t sV = sK + C::kKSlots * C::kTileBytes;
   volatile int* abort_flag = &bars.abort_flag;
   if (tid == 0) {
@@ -1083,42 +1158,55 @@ __global__ void __launch_bounds__(kBwdThreads, 1) dq_kernel(const __grid_constan
   }
 }
 
-// The shared-memory limit of a kernel is set once on every device that
-// launches it (setting it twice is harmless).
-template <int D>
-cudaError_t configure() {
+// One launch for both: the CTAs [0, n_kv_ctas) take dK and dV, tile by tile of
+// a head, the following ones dQ.  They need nothing from each other, so that
+// dQ's CTAs fill the SMs that the last ones of dK and dV leave idle.
+template <int D, bool OWN>
+__global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_constant__ BwdParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {  // (never: the buffer is placed on a 1024-byte boundary)
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
+  uint32_t i = blockIdx.x;
+  if (i < p.n_kv_ctas) {
+    const uint32_t t = i % p.n_kv_tiles;
+    i /= p.n_kv_tiles;
+    dkdv_cta<D, OWN>(p, smem_raw, t, i % p.Hkv, i / p.Hkv);
+  } else {
+    i -= p.n_kv_ctas;
+    const uint32_t t = i % p.n_q_tiles;
+    i /= p.n_q_tiles;
+    dq_cta<D>(p, smem_raw, t, i % p.Hq, i / p.Hq);
+  }
+}
+
+template <int D, bool OWN>
+cudaError_t launch_main(const BwdParams& p, unsigned grid, cudaStream_t s) {
+  // the shared-memory limit is set once on every device that launches the
+  // kernel (setting it twice is harmless)
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (bit && (configured.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  using C = BCfg<D>;
-  if ((e = cudaFuncSetAttribute(dkdv_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemKv)) !=
-          cudaSuccess ||
-      (e = cudaFuncSetAttribute(dkdv_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemKv)) !=
-          cudaSuccess ||
-      (e = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemQ)) != cudaSuccess)
-    return e;
-  configured.fetch_or(bit, std::memory_order_relaxed);
-  return cudaSuccess;
+  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(backward_kernel<D, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, BCfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  backward_kernel<D, OWN><<<grid, kBwdThreads, BCfg<D>::kSmem, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const BwdParams& p, cudaStream_t s) {
-  using C = BCfg<D>;
-  cudaError_t e = configure<D>();
+  const unsigned prep = p.B + static_cast<unsigned>(p.n_q_tiles) * (kTileRows / kPrepRows) * ((p.Hq + 7) / 8) * p.B;
+  prep_kernel<D><<<prep, kPrepThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  stats_kernel<D><<<dim3(p.n_q_tiles * 4, (p.Hq + 7) / 8, p.B), 256, 0, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 kv_grid(p.n_kv_tiles, p.Hkv, p.B);
-  if (p.masked_rows == ULY_ROWS_SDPA)
-    dkdv_kernel<D, false><<<kv_grid, kBwdThreads, C::kSmemKv, s>>>(p);
-  else
-    dkdv_kernel<D, true><<<kv_grid, kBwdThreads, C::kSmemKv, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dq_kernel<D><<<dim3(p.n_q_tiles, p.Hq, p.B), kBwdThreads, C::kSmemQ, s>>>(p);
-  return cudaGetLastError();
+  const unsigned grid = p.n_kv_ctas + static_cast<unsigned>(p.n_q_tiles) * p.Hq * p.B;
+  return p.masked_rows == ULY_ROWS_SDPA ? launch_main<D, false>(p, grid, s) : launch_main<D, true>(p, grid, s);
 }
 
 }  // namespace

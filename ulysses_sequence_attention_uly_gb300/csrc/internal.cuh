@@ -224,11 +224,15 @@ struct BwdParams {
   int64_t lse_row_stride;                                           // floats
   int64_t lse_batch_stride[kMaxRanks];                              // floats
   float scale, scale_log2;
-  const uint4* tile_bits;         // tables as in AttnParams
-  const int32_t* active;
-  const uint4* active_bits;
-  const uint4* active_inv;
-  const int32_t* n_active;
+  const uint8_t* key_mask;        // admission as in TileParams
+  const int32_t* key_ranges;
+  int32_t n_ranges, Nk;
+  uint4* tile_bits;               // tables as in AttnParams
+  int32_t* active;
+  uint4* active_bits;
+  uint4* active_inv;
+  int32_t* n_active;
+  uint32_t n_kv_ctas;             // CTAs of dK and dV: n_kv_tiles * Hkv * B
   float* nl;                      // [B][Hq][n_q_tiles * 128]: -lse log2(e)
   float* dl;                      // [B][Hq][n_q_tiles * 128]: -delta
   int32_t masked_rows;

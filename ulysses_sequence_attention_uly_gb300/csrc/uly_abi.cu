@@ -1244,8 +1244,12 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
     return ULY_ERR_INVALID;
   if ((rc = check_device(pl))) return rc;
-  // launch limits of grid.y and grid.z, and of the row statistics' grid.x
-  if (d.Hq > 65535 || d.B > 65535) return ULY_ERR_UNSUPPORTED;
+  // CTAs of the two launches: one for every 128 keys of a kv head and 128
+  // queries of a q head; one for 16 rows of 8 q heads, and one a batch
+  const int64_t q_tiles = bwd_q_tiles(pl), kv_ctas = static_cast<int64_t>(pl->n_kv_tiles) * d.Hkv * d.B;
+  if (kv_ctas + q_tiles * d.Hq * d.B > 0x7FFFFFFF ||
+      q_tiles * (kTileRows / 16) * ((d.Hq + 7) / 8) * d.B + d.B > 0x7FFFFFFF)
+    return ULY_ERR_UNSUPPORTED;
 
   const int hq_l = d.Hq / P, hkv_l = d.Hkv / P;
   const int64_t hq_t = fused ? d.Hq : hq_l, hkv_t = fused ? d.Hkv : hkv_l;  // heads of one tensor
@@ -1260,7 +1264,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
     p.qseg[i].first = acc;
     acc += (p.qseg[i].len + kTileRows - 1) / kTileRows;
   }
-  p.n_q_tiles = acc;
+  p.n_q_tiles = static_cast<int32_t>(q_tiles);
   p.n_kv_tiles = pl->n_kv_tiles;
   p.fused = fused;
   p.P = P;
@@ -1326,24 +1330,12 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.status = pl->status;
   p.wait_ns = pl->wait_ns;
 
-  static thread_local TileParams tp;
-  memset(&tp, 0, sizeof(tp));
-  memcpy(tp.kseg, p.kseg, sizeof(tp.kseg));
-  tp.n_kseg = p.n_kseg;
-  tp.n_kv_tiles = p.n_kv_tiles;
-  tp.B = d.B;
-  tp.Nk = static_cast<int32_t>(pl->nk);
-  tp.key_mask = key_mask;
-  tp.key_ranges = key_ranges;
-  tp.n_ranges = key_ranges ? n_ranges : 0;
-  tp.all_tiles = d.masked_rows == ULY_ROWS_SELF;
-  tp.tile_bits = reinterpret_cast<uint4*>(ws + w.bits);
-  tp.active = reinterpret_cast<int32_t*>(ws + w.active);
-  tp.active_bits = reinterpret_cast<uint4*>(ws + w.active_bits);
-  tp.active_inv = reinterpret_cast<uint4*>(ws + w.active_inv);
-  tp.n_active = reinterpret_cast<int32_t*>(ws + w.n_active);
+  p.key_mask = key_mask;
+  p.key_ranges = key_ranges;
+  p.n_ranges = key_ranges ? n_ranges : 0;
+  p.Nk = static_cast<int32_t>(pl->nk);
+  p.n_kv_ctas = static_cast<uint32_t>(kv_ctas);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_tiles(tp, s) != cudaSuccess) return ULY_ERR_CUDA;
   if (launch_attention_backward(p, d.D, s) != cudaSuccess) return ULY_ERR_CUDA;
   return ULY_OK;
 }
