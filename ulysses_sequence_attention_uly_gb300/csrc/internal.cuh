@@ -267,7 +267,7 @@ struct NormParams {
   int32_t ctas[2];                  // backward: CTAs of q and of k
   float* partial;                   // backward: [ctas][D]
 };
-constexpr int kNormCtasPerSm = 4;
+constexpr int kNormCtasPerSm = 2;  // norm_rope_backward_kernel (norm_rope.cu)
 
 // Pitched copies between host and device buffers of the same row layout,
 // run by SMs (the source or destination is page-locked host memory mapped

@@ -9,12 +9,20 @@
 // both sums over a head, of x^2 and of dn w x, come from the same values, so
 // the gradient needs one reduction step and one pass too.
 //
-// Bound by memory: 4 bytes an element forward, 6 backward.  D / 16 lanes hold
-// a head: lane l has the elements [8l, 8l + 8) and [D/2 + 8l, D/2 + 8l + 8), so
-// that both pairings, (2i, 2i+1) and (i, i + D/2), stay inside a lane and every
-// load and store is 16 bytes.  A warp takes one row and walks its heads, 512 /
-// D at a time, with the row's cosines, sines and the weights in registers.
+// Bound by memory: 4 bytes an element forward, 6 backward.  D / 8 lanes hold a
+// head, eight elements each, so that a lane holds whole pairs: [8l, 8l + 8) for
+// the pairs (2i, 2i+1), and [4l, 4l + 4) with [D/2 + 4l, D/2 + 4l + 4) for the
+// pairs (i, i + D/2).  A warp takes one row and walks its heads, 256 / D at a
+// time and several of these at once, with the row's cosines, sines and the
+// weights in registers.
 // All arithmetic is f32; y and dx are rounded to bf16 once.
+//
+// Measured on q and k of 29328 rows of 40 heads of 128 (GB300, 6797 GB/s
+// copy): forward 180.5 us = 6734 GB/s, backward 290 us = 6262 GB/s with
+// the sum of the weight gradients.  Sixteen elements a lane: 196.9 and 404 us
+// (160 registers: one CTA of the backward kernel on an SM).  Backward, CTAs an
+// SM x head groups in flight: 2 x 4 287 us, 2 x 6 302, 3 x 2 315, 4 x 1 349,
+// 2 x 2 345; three or more CTAs with four groups spill.
 #include "internal.cuh"
 #include "tc.cuh"
 
@@ -36,6 +44,7 @@ uint64_t norm_violations(bool reset) {
 namespace {
 
 constexpr int kNormWarps = 8;
+constexpr int kNormUnroll = 4, kNormBwdUnroll = 4;  // head groups of a warp with loads in flight
 
 struct RowAt {
   int t, shard, b;     // tensor (0 q, 1 k), shard, batch
@@ -63,56 +72,64 @@ __device__ __forceinline__ RowAt decode_row(const NormParams& p, int t, int64_t 
   return a;
 }
 
-template <bool HALF>
-__device__ __forceinline__ void load_tables(const NormParams& p, const RowAt& a, int D, int l, float (&c)[8], float (&s)[8]) {
-  const int half = D / 2;
-  if (!p.cos_table || !in_bounds(&g_norm_violations, a.table, 1, p.table_rows)) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[j] = 1.f;
-      s[j] = 0.f;
-    }
-    return;
-  }
-  const int64_t at = a.b * p.table_batch_stride + static_cast<int64_t>(a.table) * half;
-  const int i0 = HALF ? 8 * l : 4 * l, i1 = HALF ? 8 * l + 4 : half / 2 + 4 * l;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(p.cos_table + at + i0));
-  const float4 c1 = __ldg(reinterpret_cast<const float4*>(p.cos_table + at + i1));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(p.sin_table + at + i0));
-  const float4 s1 = __ldg(reinterpret_cast<const float4*>(p.sin_table + at + i1));
-  c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-  s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+// the lane's four cosines and sines
+template <int D, bool HALF>
+__device__ __forceinline__ void load_tables(const NormParams& p, const RowAt& a, int l, float4& c, float4& s) {
+  c = make_float4(1.f, 1.f, 1.f, 1.f);
+  s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!p.cos_table || !in_bounds(&g_norm_violations, a.table, 1, p.table_rows)) return;
+  const int64_t at = a.b * p.table_batch_stride + static_cast<int64_t>(a.table) * (D / 2) + 4 * l;
+  c = __ldg(reinterpret_cast<const float4*>(p.cos_table + at));
+  s = __ldg(reinterpret_cast<const float4*>(p.sin_table + at));
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int D, int l, float (&v)[16]) {
+// index of the lane's element j
+template <int D, bool HALF>
+__device__ __forceinline__ int element(int l, int j) {
+  return HALF ? (j < 4 ? 4 * l + j : D / 2 + 4 * l + j - 4) : 8 * l + j;
+}
+
+template <int D, bool HALF>
+__device__ __forceinline__ void load_weights(const float* w, int l, float (&v)[8]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = 1.f;
-  if (!w) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = __ldg(w + 8 * l + j);
-    v[8 + j] = __ldg(w + D / 2 + 8 * l + j);
+  for (int j = 0; j < 8; ++j) v[j] = w ? __ldg(w + element<D, HALF>(l, j)) : 1.f;
+}
+
+// the lane's eight elements of the head at p (which includes the lane's offset)
+template <int D, bool HALF>
+__device__ __forceinline__ uint4 load_head(const uint8_t* p) {
+  if (!HALF) return *reinterpret_cast<const uint4*>(p);
+  const uint2 lo = *reinterpret_cast<const uint2*>(p), hi = *reinterpret_cast<const uint2*>(p + D);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+template <int D, bool HALF>
+__device__ __forceinline__ void store_head(uint8_t* p, const float (&v)[8]) {
+  const uint4 r = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7]));
+  if (!HALF) {
+    *reinterpret_cast<uint4*>(p) = r;
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(r.x, r.y);
+    *reinterpret_cast<uint2*>(p + D) = make_uint2(r.z, r.w);
   }
 }
 
-__device__ __forceinline__ void unpack(const uint4 lo, const uint4 hi, float (&v)[16]) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ void unpack(const uint4 x, float (&v)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 4; ++k) {
     v[2 * k] = __uint_as_float(w[k] << 16);
     v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
 
-// y = R v (sign = 1) or R^T v (sign = -1) of the lane's eight pairs
+// v = R v (sign = 1) or R^T v (sign = -1) of the lane's four pairs
 template <bool HALF>
-__device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], const float (&s)[8], float sign) {
+__device__ __forceinline__ void rotate(float (&v)[8], const float4 c4, const float4 s4, float sign) {
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int a = HALF ? j : 2 * j, b = HALF ? 8 + j : 2 * j + 1;
+  for (int j = 0; j < 4; ++j) {
+    const int a = HALF ? j : 2 * j, b = HALF ? 4 + j : 2 * j + 1;
     const float x = v[a], y = v[b], sj = sign * s[j];
     v[a] = fmaf(x, c[j], -(y * sj));
     v[b] = fmaf(x, sj, y * c[j]);
@@ -122,7 +139,7 @@ __device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], cons
 // Forward.  A warp's task: heads [h0, h0 + heads_task) of one row.
 template <int D, bool HALF>
 __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes of a head, heads of a warp pass
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes of a head, heads of a warp at once
   const int lane = threadIdx.x & 31, l = lane % kLanes, hs = lane / kLanes;
   int64_t task = static_cast<int64_t>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5);
   if (task >= p.tasks_begin[2]) return;
@@ -133,41 +150,37 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_kernel(const __grid
   const int h_hi = min(h_lo + p.task_heads, p.heads[t]);
   const RowAt a = decode_row(p, t, i);
   if (!in_bounds(&g_norm_violations, a.row, 1, p.tensor_rows[t][a.shard])) return;
-  float c[8], s[8], w[16];
-  load_tables<HALF>(p, a, D, l, c, s);
-  load_weights(p.weight[t], D, l, w);
-  const uint8_t* x = p.x[t][a.shard] + a.row * p.row_bytes[t] + 16 * l;
-  uint8_t* y = p.y[t][a.shard] + a.row * (static_cast<int64_t>(p.heads[t]) * D * 2) + 16 * l;
-  constexpr int kUnroll = 4;
+  float4 c, s;
+  float w[8];
+  load_tables<D, HALF>(p, a, l, c, s);
+  load_weights<D, HALF>(p.weight[t], l, w);
+  const int off = (HALF ? 8 : 16) * l;
+  const uint8_t* x = p.x[t][a.shard] + a.row * p.row_bytes[t] + off;
+  uint8_t* y = p.y[t][a.shard] + a.row * (static_cast<int64_t>(p.heads[t]) * D * 2) + off;
+  constexpr int kUnroll = kNormUnroll;
   for (int h0 = h_lo; h0 < h_hi; h0 += kUnroll * kHeads) {
-    uint4 lo[kUnroll], hi[kUnroll];
+    uint4 in[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kHeads + hs;
-      lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < h_hi) {
-        lo[u] = *reinterpret_cast<const uint4*>(x + h * (D * 2));
-        hi[u] = *reinterpret_cast<const uint4*>(x + h * (D * 2) + D);
-      }
+      in[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < h_hi) in[u] = load_head<D, HALF>(x + h * (D * 2));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kHeads + hs;
-      float v[16];
-      unpack(lo[u], hi[u], v);
+      float v[8];
+      unpack(in[u], v);
       float sq = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sq = fmaf(v[j], v[j], sq);
+      for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
       const float rstd = rsqrtf(sq * (1.f / D) + p.eps);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = v[j] * rstd * w[j];
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * w[j];
       rotate<HALF>(v, c, s, 1.f);
-      if (h < h_hi) {
-        *reinterpret_cast<uint4*>(y + h * (D * 2)) = pack8(v);
-        *reinterpret_cast<uint4*>(y + h * (D * 2) + D) = pack8(v + 8);
-      }
+      if (h < h_hi) store_head<D, HALF>(y + h * (D * 2), v);
     }
   }
 }
@@ -178,17 +191,19 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_kernel(const __grid
 // weight_grad_kernel adds up in a fixed order: the result does not depend on
 // which CTA finishes first.
 template <int D, bool HALF>
-__global__ void __launch_bounds__(32 * kNormWarps) norm_rope_backward_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+__global__ void __launch_bounds__(32 * kNormWarps, kNormCtasPerSm)
+    norm_rope_backward_kernel(const __grid_constant__ NormParams p) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
   __shared__ float sums[kNormWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes, hs = lane / kLanes;
   const int t = blockIdx.x >= p.ctas[0];
   const int cta = blockIdx.x - (t ? p.ctas[0] : 0);
-  float w[16], dw[16];
-  load_weights(p.weight[t], D, l, w);
+  float w[8], dw[8];
+  load_weights<D, HALF>(p.weight[t], l, w);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) dw[j] = 0.f;
+  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
   const int64_t dense = static_cast<int64_t>(p.heads[t]) * D * 2;
+  const int off = (HALF ? 8 : 16) * l;
   for (int64_t task = static_cast<int64_t>(cta) * kNormWarps + warp; task < p.tasks_begin[t + 1] - p.tasks_begin[t];
        task += static_cast<int64_t>(p.ctas[t]) * kNormWarps) {
     const int64_t i = task / p.task_parts[t];
@@ -196,35 +211,33 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_backward_kernel(con
     const int h_hi = min(h_lo + p.task_heads, p.heads[t]);
     const RowAt a = decode_row(p, t, i);
     if (!in_bounds(&g_norm_violations, a.row, 1, p.tensor_rows[t][a.shard])) continue;
-    float c[8], s[8];
-    load_tables<HALF>(p, a, D, l, c, s);
-    const uint8_t* x = p.x[t][a.shard] + a.row * p.row_bytes[t] + 16 * l;
-    const uint8_t* g = p.g[t][a.shard] + a.row * dense + 16 * l;
-    uint8_t* y = p.y[t][a.shard] + a.row * dense + 16 * l;
-    constexpr int kUnroll = 2;
+    float4 c, s;
+    load_tables<D, HALF>(p, a, l, c, s);
+    const uint8_t* x = p.x[t][a.shard] + a.row * p.row_bytes[t] + off;
+    const uint8_t* g = p.g[t][a.shard] + a.row * dense + off;
+    uint8_t* y = p.y[t][a.shard] + a.row * dense + off;
+    constexpr int kUnroll = kNormBwdUnroll;
     for (int h0 = h_lo; h0 < h_hi; h0 += kUnroll * kHeads) {
-      uint4 xlo[kUnroll], xhi[kUnroll], glo[kUnroll], ghi[kUnroll];
+      uint4 xi[kUnroll], gi[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = h0 + u * kHeads + hs;
-        xlo[u] = xhi[u] = glo[u] = ghi[u] = make_uint4(0u, 0u, 0u, 0u);
+        xi[u] = gi[u] = make_uint4(0u, 0u, 0u, 0u);
         if (h < h_hi) {
-          xlo[u] = *reinterpret_cast<const uint4*>(x + h * (D * 2));
-          xhi[u] = *reinterpret_cast<const uint4*>(x + h * (D * 2) + D);
-          glo[u] = *reinterpret_cast<const uint4*>(g + h * (D * 2));
-          ghi[u] = *reinterpret_cast<const uint4*>(g + h * (D * 2) + D);
+          xi[u] = load_head<D, HALF>(x + h * (D * 2));
+          gi[u] = load_head<D, HALF>(g + h * (D * 2));
         }
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = h0 + u * kHeads + hs;
-        float v[16], dn[16];
-        unpack(xlo[u], xhi[u], v);
-        unpack(glo[u], ghi[u], dn);
+        float v[8], dn[8];
+        unpack(xi[u], v);
+        unpack(gi[u], dn);
         rotate<HALF>(dn, c, s, -1.f);
         float sq = 0.f, dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           sq = fmaf(v[j], v[j], sq);
           dot = fmaf(dn[j] * w[j], v[j], dot);
         }
@@ -236,24 +249,21 @@ __global__ void __launch_bounds__(32 * kNormWarps) norm_rope_backward_kernel(con
         const float rstd = rsqrtf(sq * (1.f / D) + p.eps);
         const float mean = dot * rstd * (1.f / D);  // of dn w z
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
           const float z = v[j] * rstd;
           dw[j] = fmaf(dn[j], z, dw[j]);
           v[j] = rstd * (dn[j] * w[j] - z * mean);
         }
-        if (h < h_hi) {
-          *reinterpret_cast<uint4*>(y + h * (D * 2)) = pack8(v);
-          *reinterpret_cast<uint4*>(y + h * (D * 2) + D) = pack8(v + 8);
-        }
+        if (h < h_hi) store_head<D, HALF>(y + h * (D * 2), v);
       }
     }
   }
   if (!p.partial) return;  // no weight gradient wanted
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
 #pragma unroll
     for (int o = kLanes; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
-    if (hs == 0) sums[warp][(j < 8 ? 0 : D / 2) + 8 * l + (j & 7)] = dw[j];
+    if (hs == 0) sums[warp][element<D, HALF>(l, j)] = dw[j];
   }
   __syncthreads();
   if (threadIdx.x < D) {
@@ -286,9 +296,9 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partial,
 }
 
 // Heads of a task: a whole row's, unless there are too few rows for every
-// SM's warps; then one pass's (512 / D heads) each.
+// SM's warps; then one pass's (256 / D heads) each.
 void split_tasks(NormParams& p, int D, int sm_count) {
-  const int pass = 512 / D;
+  const int pass = 256 / D;
   const int64_t rows = p.rows_begin[0][p.P] + p.rows_begin[1][p.P];
   const int most = p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1];
   p.task_heads = rows < static_cast<int64_t>(sm_count) * kNormWarps * 4 ? pass : (most + pass - 1) / pass * pass;
