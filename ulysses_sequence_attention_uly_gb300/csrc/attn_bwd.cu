@@ -72,6 +72,11 @@ struct BCfg {
 };
 constexpr int kBwdThreads = 320;  // 8 warps of elementwise work, a TMA warp, an MMA warp
 
+// barrier 1 of a CTA: the TMA warp arrives (its barriers are initialised) and
+// goes on, the others wait
+__device__ __forceinline__ void ready_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kBwdThreads) : "memory"); }
+__device__ __forceinline__ void ready_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kBwdThreads) : "memory"); }
+
 __device__ __forceinline__ void bwd_timeout(const BwdParams& p, volatile int* abort_flag) {
   *abort_flag = 1;
   atomicOr(p.status, kStatusTimeout);
@@ -414,18 +419,43 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
   }
 }
 
-// The 64 entries of a thread's half row, two to a register pair.
+// A thread works on 64 entries of a tile's row, two to a register pair.
 //
-// p = 2^(s sl2 + nl) from the scores at TMEM t, kept in f32 in pr.  NL: the
-// addend is a row's (nl2) or, in shared memory at nl_addr, one per column.
-// MASKED: entries whose bit in w0 (columns 0..31) or w1 (32..63) is clear are
-// 0 whatever the score is.  The masked form is a path of its own, taken by
-// whole warps: a test in the unmasked loop would cut it into pieces that the
-// compiler cannot interleave.
-// `loaded` is called once the scores are in registers.
-template <bool COLS, bool MASKED, typename F>
-__device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl2, uint32_t nl_addr, uint32_t w0,
-                                           uint32_t w1, uint64_t (&pr)[32], F loaded) {
+// Entries that do not attend are cleared in the packed bf16 pairs, so that
+// neither an infinity nor a NaN in a masked place gets through and the f32
+// arithmetic is the same for all.  A mask word's even and odd bits are first
+// drawn apart within each half (bit 2i + e of a half to bit 8e + i), so that
+// one shift puts the two bits of two pairs at the tops of bytes and one byte
+// permutation, which can repeat a byte's top bit, makes a pair's mask.
+__device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
+  uint32_t t = (x ^ (x >> 1)) & 0x22222222u;
+  x ^= t ^ (t << 1);
+  t = (x ^ (x >> 2)) & 0x0C0C0C0Cu;
+  x ^= t ^ (t << 2);
+  t = (x ^ (x >> 4)) & 0x00F000F0u;
+  return x ^ t ^ (t << 4);
+}
+// the mask of pair i (0..31) from the two words' pair_bits
+template <int I>
+__device__ __forceinline__ uint32_t pair_mask(uint32_t u0, uint32_t u1) {
+  uint32_t m;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(m) : "r"((I < 16 ? u0 : u1) << (7 - (I & 7))), "n"((I & 8) ? 0xBBAA : 0x9988));
+  return m;
+}
+template <int N, int I = 0>
+__device__ __forceinline__ void mask_pairs(uint32_t (&pk)[N], uint32_t u0, uint32_t u1) {
+  if constexpr (I < N) {
+    pk[I] &= pair_mask<I>(u0, u1);
+    mask_pairs<N, I + 1>(pk, u0, u1);
+  }
+}
+
+// p = 2^(s sl2 + nl) from the scores at TMEM t, kept in f32 in pr.  COLS: the
+// addend is one per column, in shared memory at nl_addr; otherwise the row's,
+// nl2.  `loaded` is called once the scores are in registers.
+template <bool COLS, typename F>
+__device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl2, uint32_t nl_addr,
+                                           uint64_t (&pr)[32], F loaded) {
   uint32_t a[2][32];
   tmem_ld32(t, a[0]);
   tmem_ld32(t + 32, a[1]);
@@ -442,22 +472,15 @@ __device__ __forceinline__ void half_row_p(uint32_t t, uint64_t mul, uint64_t nl
       f2_split(f2_fma(f2(__uint_as_float(a[i >> 4][(2 * i) & 31]), __uint_as_float(a[i >> 4][(2 * i + 1) & 31])), mul,
                       n[e]),
                x0, x1);
-      x0 = ex2_approx(x0);
-      x1 = ex2_approx(x1);
-      if (MASKED) {
-        const uint32_t w = (i < 16 ? w0 : w1) >> ((2 * i) & 31);
-        x0 = w & 1u ? x0 : 0.f;
-        x1 = w & 2u ? x1 : 0.f;
-      }
-      pr[i] = f2(x0, x1);
+      pr[i] = f2(ex2_approx(x0), ex2_approx(x1));
     }
   }
 }
 
 // ds = p (dp + ndl), rounded to bf16, from the loaded dP; ndl as nl above.
-template <bool COLS, bool MASKED>
-__device__ __forceinline__ void half_row_ds(const uint32_t (&a)[2][32], uint64_t dl2, uint32_t dl_addr, uint32_t w0,
-                                            uint32_t w1, const uint64_t (&pr)[32], uint32_t (&pk)[32]) {
+template <bool COLS>
+__device__ __forceinline__ void half_row_ds(const uint32_t (&a)[2][32], uint64_t dl2, uint32_t dl_addr,
+                                            const uint64_t (&pr)[32], uint32_t (&pk)[32]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     uint64_t n[2] = {dl2, dl2};
@@ -470,29 +493,23 @@ __device__ __forceinline__ void half_row_ds(const uint32_t (&a)[2][32], uint64_t
                              n[e]),
                       pr[i]),
                x0, x1);
-      if (MASKED) {
-        const uint32_t w = (i < 16 ? w0 : w1) >> ((2 * i) & 31);
-        x0 = w & 1u ? x0 : 0.f;
-        x1 = w & 2u ? x1 : 0.f;
-      }
       pk[i] = pack_bf16x2(x0, x1);
     }
   }
 }
 
-// p rounded to bf16 into the 32 TMEM columns from t on
-__device__ __forceinline__ void store_half_row(uint32_t t, const uint64_t (&pr)[32]) {
+// p rounded to bf16, 32 entries to the 16 TMEM columns from t on
+template <bool MASKED, int C>
+__device__ __forceinline__ void store_p(uint32_t t, const uint64_t (&pr)[32], uint32_t u) {
+  uint32_t pk[16];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x0, x1;
-      f2_split(pr[16 * c + i], x0, x1);
-      pk[i] = pack_bf16x2(x0, x1);
-    }
-    tmem_st16(t + 16 * c, pk);
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    f2_split(pr[16 * C + i], x0, x1);
+    pk[i] = pack_bf16x2(x0, x1);
   }
+  if (MASKED) mask_pairs(pk, u, u);
+  tmem_st16(t + 16 * C, pk);
 }
 
 struct KvBars {
@@ -549,7 +566,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     const uint32_t mR = k.tmem + off + 128 * (it & 1);
     const uint32_t nl_addr = k.sNl + qslot * C::kStatBytes + 64 * wg * 4;
     const uint32_t dl_addr = k.sDl + (it & 1) * C::kStatBytes + 64 * wg * 4;
-    uint32_t w0 = 0u, w1 = 0u;
+    uint32_t u0 = 0u, u1 = 0u;
     bool masked = MODE == 1;
     if (MODE == 2) {
       live = live_next;
@@ -557,16 +574,18 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
       // queries that attend to the thread's key: those whose own token is
       // admitted (ULY_ROWS_ZERO), those of the key's own kind (ULY_ROWS_SELF;
       // past the run's end the statistics exclude)
-      w0 = bits_word(live, 2 * wg);
-      w1 = bits_word(live, 2 * wg + 1);
+      u0 = bits_word(live, 2 * wg);
+      u1 = bits_word(live, 2 * wg + 1);
       if (self && !key_ok) {
-        w0 = ~w0;
-        w1 = ~w1;
+        u0 = ~u0;
+        u1 = ~u1;
       }
-      if (dead) w0 = w1 = 0u;
-      masked = __any_sync(0xffffffffu, (w0 & w1) != 0xFFFFFFFFu);
+      if (dead) u0 = u1 = 0u;
+      masked = __any_sync(0xffffffffu, (u0 & u1) != 0xFFFFFFFFu);
+      u0 = pair_bits(u0);
+      u1 = pair_bits(u1);
     } else if (MODE == 1) {
-      w0 = w1 = dead ? 0u : ~0u;
+      u0 = u1 = dead ? 0u : ~0u;
     }
     bool ok = mbar_wait(smem_u32(&bars.nl_full[qslot]), qturn & 1, k.deadline, abort_flag) &&
               mbar_wait(smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1, k.deadline, abort_flag);
@@ -578,10 +597,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.s_go));
     };
-    if (MODE == 0 || (MODE == 2 && !masked))
-      half_row_p<true, false>(mR, mul, 0, nl_addr, w0, w1, pr, s_loaded);
-    else
-      half_row_p<true, true>(mR, mul, 0, nl_addr, w0, w1, pr, s_loaded);
+    half_row_p<true>(mR, mul, 0, nl_addr, pr, s_loaded);
     ok = mbar_wait(smem_u32(&bars.s_go), it & 1, k.deadline, abort_flag) &&
          mbar_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -598,16 +614,25 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
       fence_proxy_async_smem();
     }
     tmem_wait_ld();
-    if (MODE == 0 || (MODE == 2 && !masked))
-      half_row_ds<true, false>(a, 0, dl_addr, w0, w1, pr, pk);
-    else
-      half_row_ds<true, true>(a, 0, dl_addr, w0, w1, pr, pk);
+    half_row_ds<true>(a, 0, dl_addr, pr, pk);
+    if (MODE == 1) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) pk[i] &= u0;
+    } else if (MODE == 2 && masked) {
+      mask_pairs(pk, u0, u1);
+    }
     tmem_st32(mR, pk);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full));
-    store_half_row(mR + 32, pr);
+    if (MODE == 0 || (MODE == 2 && !masked)) {
+      store_p<false, 0>(mR + 32, pr, 0u);
+      store_p<false, 1>(mR + 32, pr, 0u);
+    } else {
+      store_p<true, 0>(mR + 32, pr, u0);
+      store_p<true, 1>(mR + 32, pr, u1);
+    }
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -648,7 +673,7 @@ template <int D, bool OWN>
 __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b) {
   using C = BCfg<D>;
   KvBars& bars = *reinterpret_cast<KvBars*>(smem_raw + C::kKvBars);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = hk / p.Hkv_l;  // owning rank
   const Seg run = p.kseg[seg_of(p.kseg, p.n_kseg, t)];
   const int row0 = (t - run.first) * kTileRows;
@@ -661,35 +686,28 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   const uint32_t sDO = sQ + C::kQSlots * C::kTileBytes, sNl = sDO + C::kOSlots * C::kTileBytes;
   const uint32_t sDl = sNl + C::kQSlots * C::kStatBytes;
   volatile int* abort_flag = &bars.abort_flag;
-  if (tid == 0) {
-    mbar_init(smem_u32(&bars.kq_full), 1);
-    mbar_init(smem_u32(&bars.q1_full), 1);
-    for (int i = 0; i < C::kQSlots; ++i) mbar_init(smem_u32(&bars.nl_full[i]), 1);
-    mbar_init(smem_u32(&bars.s_full[0]), 1);
-    mbar_init(smem_u32(&bars.s_full[1]), 1);
-    mbar_init(smem_u32(&bars.s_go), 9);
-    mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.ds_full), 8);
-    mbar_init(smem_u32(&bars.p_go[0]), 9);
-    mbar_init(smem_u32(&bars.p_go[1]), 9);
-    mbar_init(smem_u32(&bars.v_done), 1);
-    mbar_init(smem_u32(&bars.done), 1);
-    mbar_init(smem_u32(&bars.drain), 1);
-    bars.abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&bars.tmem_base), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars.tmem_base;
-  const uint32_t tDV = tmem + 256, tDK = tmem + 256 + D;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
 
   if (warp == 8) {
+    if (lane == 0) {
+      mbar_init(smem_u32(&bars.kq_full), 1);
+      mbar_init(smem_u32(&bars.q1_full), 1);
+      for (int i = 0; i < C::kQSlots; ++i) mbar_init(smem_u32(&bars.nl_full[i]), 1);
+      mbar_init(smem_u32(&bars.s_full[0]), 1);
+      mbar_init(smem_u32(&bars.s_full[1]), 1);
+      mbar_init(smem_u32(&bars.s_go), 9);
+      mbar_init(smem_u32(&bars.dp_full), 1);
+      mbar_init(smem_u32(&bars.ds_full), 8);
+      mbar_init(smem_u32(&bars.p_go[0]), 9);
+      mbar_init(smem_u32(&bars.p_go[1]), 9);
+      mbar_init(smem_u32(&bars.v_done), 1);
+      mbar_init(smem_u32(&bars.done), 1);
+      mbar_init(smem_u32(&bars.drain), 1);
+      bars.abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    ready_arrive();
     if (lane == 0 && n_it > 0) {
       const int kvhead = p.fused ? hk : hk % p.Hkv_l;
       const int kmap = run.src < 0 ? r : run.src;
@@ -787,6 +805,12 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       }
     }
   } else if (warp == 9) {
+    tmem_alloc(smem_u32(&bars.tmem_base), 512);
+    tmem_relinquish();
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base, tDV = tmem + 256, tDK = tmem + 256 + D;
     if (lane == 0 && n_it > 0) {
       const uint32_t dk = desc_rows(sK), dv = desc_rows(sV);
       uint32_t q_r[C::kQSlots], q_c[C::kQSlots], o_r[C::kOSlots], o_c[C::kOSlots];
@@ -855,6 +879,10 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       if (!mbar_wait(smem_u32(&bars.drain), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
     }
   } else {
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base, tDV = tmem + 256, tDK = tmem + 256 + D;
     const int wg = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // key of the tile = TMEM lane
     const bool key_ok = (bits_word(bits, q4) >> lane) & 1u;
@@ -884,7 +912,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(bars.tmem_base, 512);
   }
 }
 
@@ -913,7 +941,7 @@ template <int D>
 __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, int t, int h, int b) {
   using C = BCfg<D>;
   QBars& bars = *reinterpret_cast<QBars*>(smem_raw + C::kQBars);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = h / p.Hq_l, hk = h / p.G;
   const Seg run = p.qseg[seg_of(p.qseg, p.n_qseg, t)];
   const int row0 = (t - run.first) * kTileRows;
@@ -923,34 +951,26 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   const uint32_t sQ = smem_u32(smem_raw), sDO = sQ + C::kTileBytes, sK = sQ + 2 * C::kTileBytes;
   const uint32_t sV = sK + C::kKSlots * C::kTileBytes;
   volatile int* abort_flag = &bars.abort_flag;
-  if (tid == 0) {
-    mbar_init(smem_u32(&bars.q_full), 1);
-    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.full[i]), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.s_full[i]), 1);
-      mbar_init(smem_u32(&bars.ds_full[i]), 8);
-    }
-    mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.dp_free), 8);
-    mbar_init(smem_u32(&bars.k_done[0]), 1);
-    mbar_init(smem_u32(&bars.k_done[1]), 1);
-    mbar_init(smem_u32(&bars.done), 1);
-    mbar_init(smem_u32(&bars.drain), 1);
-    bars.abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&bars.tmem_base), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars.tmem_base;
-  const uint32_t tDP = tmem + 256, tDQ = tmem + 384;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
 
   if (warp == 8) {
+    if (lane == 0) {
+      mbar_init(smem_u32(&bars.q_full), 1);
+      for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.full[i]), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&bars.s_full[i]), 1);
+        mbar_init(smem_u32(&bars.ds_full[i]), 8);
+        mbar_init(smem_u32(&bars.k_done[i]), 1);
+      }
+      mbar_init(smem_u32(&bars.dp_full), 1);
+      mbar_init(smem_u32(&bars.dp_free), 8);
+      mbar_init(smem_u32(&bars.done), 1);
+      mbar_init(smem_u32(&bars.drain), 1);
+      bars.abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    ready_arrive();
     if (lane == 0 && n_it > 0) {
       const bool rep = p.fused && run.out_shard < 0;
       const int qmap = run.src < 0 ? r : run.src;
@@ -1003,6 +1023,12 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       }
     }
   } else if (warp == 9) {
+    tmem_alloc(smem_u32(&bars.tmem_base), 512);
+    tmem_relinquish();
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base, tDP = tmem + 256, tDQ = tmem + 384;
     if (lane == 0 && n_it > 0) {
       const uint32_t dq = desc_rows(sQ), ddo = desc_rows(sDO);
       uint32_t k_r[C::kKSlots], k_c[C::kKSlots], v_r[C::kVSlots];
@@ -1063,6 +1089,10 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       if (!mbar_wait(smem_u32(&bars.drain), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
     }
   } else {
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base, tDP = tmem + 256, tDQ = tmem + 384;
     const int wg = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // query of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -1090,7 +1120,6 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       if (it + 1 < n_it) bits_next = __ldg(row_bits + it + 1);
       // some entry of the warp is not admitted
       const bool part = any_dead || __any_sync(0xffffffffu, !bits_full(bits));
-      const uint32_t w0 = dead ? 0u : bits_word(bits, 2 * wg), w1 = dead ? 0u : bits_word(bits, 2 * wg + 1);
       ok = mbar_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -1098,10 +1127,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       }
       tc_fence_after();
       uint64_t pr[32];
-      if (!part)
-        half_row_p<false, false>(mS, mul, nl2, 0, w0, w1, pr, [] {});
-      else
-        half_row_p<false, true>(mS, mul, nl2, 0, w0, w1, pr, [] {});
+      half_row_p<false>(mS, mul, nl2, 0, pr, [] {});
       ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -1117,10 +1143,9 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
-      if (!part)
-        half_row_ds<false, false>(a, dl2, 0, w0, w1, pr, pk);
-      else
-        half_row_ds<false, true>(a, dl2, 0, w0, w1, pr, pk);
+      half_row_ds<false>(a, dl2, 0, pr, pk);
+      if (part)
+        mask_pairs(pk, pair_bits(dead ? 0u : bits_word(bits, 2 * wg)), pair_bits(dead ? 0u : bits_word(bits, 2 * wg + 1)));
       tmem_st32(mS, pk);
       if (part && !self) {
         // keys that are not admitted may hold anything: their rows of K are
@@ -1154,7 +1179,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(bars.tmem_base, 512);
   }
 }
 
