@@ -540,6 +540,8 @@ struct KvWork {
 // queries.  MODE 0: every pair of the warp attends.  1: `dead` keys do not.
 // 2: it goes by the queries' own tokens too (ULY_ROWS_ZERO, _SELF).  Loops of
 // their own, so that the common one has no test in it and fits the registers.
+// (A test that jumps over a tile's masking costs more in instruction fetches
+// than the masking.)
 template <int D, int MODE>
 __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int warp, int lane, bool key_ok, bool dead) {
   using C = BCfg<D>;
@@ -550,15 +552,14 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
   const uint64_t mul = f2(p.scale_log2, p.scale_log2);
   const bool self = p.masked_rows == ULY_ROWS_SELF, zero_rows = p.masked_rows == ULY_ROWS_ZERO;
   uint4 live = make_uint4(~0u, ~0u, ~0u, ~0u), live_next = live;
-  int qs = 0, qt = 0;
-  const auto next_live = [&] {  // the queries' own tokens, a tile ahead of their use
-    const Seg& q = p.qseg[qs];
-    if (q.kv_seg >= 0)
-      live_next = __ldg(p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles + p.kseg[q.kv_seg].first + qt);
-    if (++qt * kTileRows >= q.len) {
-      qt = 0;
-      if (++qs == p.n_qseg) qs = 0;
-    }
+  // The queries' own tokens, a tile ahead of their use.  The q runs are kv runs
+  // of the same tokens, in order, so their kv tiles follow one another.
+  const uint4* own = p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles +
+                     (MODE == 2 && p.qseg[0].kv_seg >= 0 ? p.kseg[p.qseg[0].kv_seg].first : 0);
+  int own_tile = 0;
+  const auto next_live = [&] {
+    live_next = __ldg(own + own_tile);
+    if (++own_tile == p.n_q_tiles) own_tile = 0;
   };
   if (MODE == 2) next_live();
   int qslot = 0, qturn = 0;
@@ -567,7 +568,6 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     const uint32_t nl_addr = k.sNl + qslot * C::kStatBytes + 64 * wg * 4;
     const uint32_t dl_addr = k.sDl + (it & 1) * C::kStatBytes + 64 * wg * 4;
     uint32_t u0 = 0u, u1 = 0u;
-    bool masked = MODE == 1;
     if (MODE == 2) {
       live = live_next;
       if (it + 1 < k.n_it) next_live();
@@ -581,7 +581,6 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
         u1 = ~u1;
       }
       if (dead) u0 = u1 = 0u;
-      masked = __any_sync(0xffffffffu, (u0 & u1) != 0xFFFFFFFFu);
       u0 = pair_bits(u0);
       u1 = pair_bits(u1);
     } else if (MODE == 1) {
@@ -618,7 +617,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     if (MODE == 1) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) pk[i] &= u0;
-    } else if (MODE == 2 && masked) {
+    } else if (MODE == 2) {
       mask_pairs(pk, u0, u1);
     }
     tmem_st32(mR, pk);
@@ -626,7 +625,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full));
-    if (MODE == 0 || (MODE == 2 && !masked)) {
+    if (MODE == 0) {
       store_p<false, 0>(mR + 32, pr, 0u);
       store_p<false, 1>(mR + 32, pr, 0u);
     } else {
