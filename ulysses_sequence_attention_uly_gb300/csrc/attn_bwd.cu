@@ -262,15 +262,19 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 16;  // rows of a CTA of prep_kernel
 
 // The kv tile tables of batch b: the admitted keys of every tile, and the list
-// of tiles that a query attends to, in key order.  One CTA, a warp a tile.
+// of tiles that a query attends to: those whose 128 keys are all admitted from
+// the front, in key order, and the others from the back, so that dQ's loop over
+// the former needs no masks (ULY_ROWS_SELF: all from the back).  One CTA, a
+// warp a tile.
 struct TableSmem {
   uint4 bits[kPrepThreads], inv[kPrepThreads];
-  int32_t packed[kPrepThreads], warp_sum[kPrepThreads / 32];
+  int32_t packed[kPrepThreads];
+  int2 warp_sum[kPrepThreads / 32];
 };
 __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSmem& sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(b) * p.n_kv_tiles;
-  int base = 0;
+  int n_full = 0, n_part = 0;
   for (int t0 = 0; t0 < p.n_kv_tiles; t0 += kPrepThreads) {
     for (int k = warp; k < kPrepThreads && t0 + k < p.n_kv_tiles; k += kPrepThreads / 32) {
       const int s = seg_of(p.kseg, p.n_kseg, t0 + k), i = t0 + k - p.kseg[s].first;
@@ -293,19 +297,27 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
     }
     __syncthreads();
     const int k = threadIdx.x;
-    bool any = false;
+    bool any = false, full = false;
     if (t0 + k < p.n_kv_tiles) {
       const uint4 wb = sm.bits[k];
-      any = p.masked_rows == ULY_ROWS_SELF || (wb.x | wb.y | wb.z | wb.w) != 0u;
+      const bool self = p.masked_rows == ULY_ROWS_SELF;
+      any = self || (wb.x | wb.y | wb.z | wb.w) != 0u;
+      full = !self && bits_full(wb);
     }
-    const uint32_t vote = __ballot_sync(0xffffffffu, any);
-    if (lane == 0) sm.warp_sum[warp] = __popc(vote);
+    const uint32_t vf = __ballot_sync(0xffffffffu, full), vp = __ballot_sync(0xffffffffu, any && !full);
+    if (lane == 0) sm.warp_sum[warp] = make_int2(__popc(vf), __popc(vp));
     __syncthreads();
-    int slot = base + __popc(vote & ((1u << lane) - 1u));
+    const uint32_t below = (1u << lane) - 1u;
+    int front = n_full + __popc(vf & below), back = n_part + __popc(vp & below);
     for (int i = 0; i < kPrepThreads / 32; ++i) {
-      if (i < warp) slot += sm.warp_sum[i];
-      base += sm.warp_sum[i];
+      if (i < warp) {
+        front += sm.warp_sum[i].x;
+        back += sm.warp_sum[i].y;
+      }
+      n_full += sm.warp_sum[i].x;
+      n_part += sm.warp_sum[i].y;
     }
+    const int slot = full ? front : p.n_kv_tiles - 1 - back;
     if (any && in_bounds(&g_bwd_violations, slot, 1, p.n_kv_tiles)) {
       p.active[row + slot] = sm.packed[k];
       p.active_bits[row + slot] = sm.bits[k];
@@ -313,7 +325,10 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) p.n_active[b] = base;
+  if (threadIdx.x == 0) {
+    p.n_active[b] = n_full + n_part;
+    p.n_full[b] = n_full;
+  }
 }
 
 // The first B CTAs build the kv tile tables.  The others: per (batch, q head,
@@ -926,6 +941,81 @@ struct QBars {
   int abort_flag;
 };
 
+// slot in the tile list of the it'th tile of dQ's loop
+__device__ __forceinline__ int listed(const BwdParams& p, int it, int n_full) {
+  return it < n_full ? it : p.n_kv_tiles - 1 - (it - n_full);
+}
+
+// What the elementwise warps of dq_cta share.
+struct QWork {
+  QBars* bars;
+  uint32_t tmem, sK;
+  int n_it, n_full, b;
+  uint64_t deadline;
+};
+
+// The elementwise loop of dq_cta over the tiles [it0, it1): one thread per
+// query and half of the keys.  MASKED: keys that are not admitted, and dead
+// rows.
+template <int D, bool MASKED>
+__device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int warp, int lane, int it0, int it1, float nl,
+                                       float dl, bool dead, const uint4* row_bits) {
+  using C = BCfg<D>;
+  QBars& bars = *k.bars;
+  volatile int* abort_flag = &bars.abort_flag;
+  const int wg = warp >> 2, q4 = warp & 3;
+  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  const uint32_t mDP = k.tmem + 256 + lane_off + 64 * wg;
+  const uint64_t mul = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), dl2 = f2(dl, dl);
+  const uint4* tile_bits = p.active_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles;
+  const bool zero_keys = p.masked_rows != ULY_ROWS_SELF;
+  uint4 bits_next = make_uint4(0u, 0u, 0u, 0u), keys_next = bits_next;
+  if (MASKED && it0 < it1) {
+    bits_next = __ldg(row_bits + listed(p, it0, k.n_full));
+    keys_next = __ldg(tile_bits + listed(p, it0, k.n_full));
+  }
+  for (int it = it0; it < it1; ++it) {
+    const int buf = it & 1;
+    const uint32_t mS = k.tmem + lane_off + 128 * buf + 64 * wg;
+    const uint4 bits = bits_next, keys = keys_next;
+    if (MASKED && it + 1 < it1) {
+      bits_next = __ldg(row_bits + listed(p, it + 1, k.n_full));
+      keys_next = __ldg(tile_bits + listed(p, it + 1, k.n_full));
+    }
+    bool ok = mbar_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint64_t pr[32];
+    half_row_p<false>(mS, mul, nl2, 0, pr, [] {});
+    ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    uint32_t a[2][32], pk[32];
+    tmem_ld32(mDP, a[0]);
+    tmem_ld32(mDP + 32, a[1]);
+    tmem_wait_ld();
+    // dP is in registers: the next tile's may overwrite it
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
+    half_row_ds<false>(a, dl2, 0, pr, pk);
+    if (MASKED)
+      mask_pairs(pk, pair_bits(dead ? 0u : bits_word(bits, 2 * wg)), pair_bits(dead ? 0u : bits_word(bits, 2 * wg + 1)));
+    tmem_st32(mS, pk);
+    if (MASKED && zero_keys) {
+      // keys that are not admitted may hold anything: their rows of K are
+      // zeroed before the sum over keys reads them (S has read them)
+      zero_dead_rows<D>(k.sK + (it % C::kKSlots) * C::kTileBytes, keys, 16 * warp, lane);
+      fence_proxy_async_smem();
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[buf]));
+  }
+  return true;
+}
+
 // dQ of 128 queries of one q head.
 //   warp 8   TMA: Q and dO once, K (three slots) and V (two) of every kv tile
 //            with an admitted key.
@@ -944,7 +1034,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   const int r = h / p.Hq_l, hk = h / p.G;
   const Seg run = p.qseg[seg_of(p.qseg, p.n_qseg, t)];
   const int row0 = (t - run.first) * kTileRows;
-  const int n_it = p.n_active[b];
+  const int n_it = p.n_active[b], n_full = p.n_full[b];
   const int32_t* active = p.active + static_cast<int64_t>(b) * p.n_kv_tiles;
 
   const uint32_t sQ = smem_u32(smem_raw), sDO = sQ + C::kTileBytes, sK = sQ + 2 * C::kTileBytes;
@@ -987,7 +1077,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       int krow;
       bool good;
       const auto next = [&](int it) {
-        const int e = active[it];
+        const int e = active[listed(p, it, n_full)];
         good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
         const Seg& k = p.kseg[good ? e >> 20 : 0];
         const int kmap = k.src < 0 ? r : k.src;
@@ -1095,7 +1185,6 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     const int wg = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // query of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t mDP = tDP + lane_off + 64 * wg;
     const bool self = p.masked_rows == ULY_ROWS_SELF;
     // a masked row under ULY_ROWS_SELF attends to the masked keys
     bool invert = false;
@@ -1106,59 +1195,13 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + t) * kTileRows + row;
     const float nl = p.nl[at], dl = p.dl[at];
     const bool dead = nl == -INFINITY;
-    const bool any_dead = __any_sync(0xffffffffu, dead);
-    const uint64_t mul = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), dl2 = f2(dl, dl);
     const uint4* row_bits = (invert ? p.active_inv : p.active_bits) + static_cast<int64_t>(b) * p.n_kv_tiles;
-    uint4 bits_next = n_it > 0 ? __ldg(row_bits) : make_uint4(0u, 0u, 0u, 0u);
-    bool ok = true;
-    int ks = 0;
-    for (int it = 0; it < n_it; ++it) {
-      const int buf = it & 1;
-      const uint32_t mS = tmem + lane_off + 128 * buf + 64 * wg;
-      const uint4 bits = bits_next;
-      if (it + 1 < n_it) bits_next = __ldg(row_bits + it + 1);
-      // some entry of the warp is not admitted
-      const bool part = any_dead || __any_sync(0xffffffffu, !bits_full(bits));
-      ok = mbar_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint64_t pr[32];
-      half_row_p<false>(mS, mul, nl2, 0, pr, [] {});
-      ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, deadline, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t pk[32];
-      uint32_t a[2][32];
-      tmem_ld32(mDP, a[0]);
-      tmem_ld32(mDP + 32, a[1]);
-      tmem_wait_ld();
-      // dP is in registers: the next tile's may overwrite it
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
-      half_row_ds<false>(a, dl2, 0, pr, pk);
-      if (part)
-        mask_pairs(pk, pair_bits(dead ? 0u : bits_word(bits, 2 * wg)), pair_bits(dead ? 0u : bits_word(bits, 2 * wg + 1)));
-      tmem_st32(mS, pk);
-      if (part && !self) {
-        // keys that are not admitted may hold anything: their rows of K are
-        // zeroed before the sum over keys reads them (S has read them)
-        zero_dead_rows<D>(sK + ks * C::kTileBytes, __ldg(p.active_bits + static_cast<int64_t>(b) * p.n_kv_tiles + it),
-                          16 * warp, lane);
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[buf]));
-      if (++ks == C::kKSlots) ks = 0;
-    }
+    const QWork k = {&bars, tmem, sK, n_it, n_full, b, deadline};
+    // the tiles without masks, then the others; all of them with masks where a
+    // row of the warp takes part in nothing
+    const int plain = __any_sync(0xffffffffu, dead) ? 0 : n_full;
+    bool ok = q_loop<D, false>(p, k, warp, lane, 0, plain, nl, dl, dead, row_bits) &&
+              q_loop<D, true>(p, k, warp, lane, plain, n_it, nl, dl, dead, row_bits);
     if (ok && n_it > 0) {
       ok = mbar_wait(smem_u32(&bars.done), 0, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) ok = false;

@@ -227,11 +227,13 @@ struct BwdParams {
   const uint8_t* key_mask;        // admission as in TileParams
   const int32_t* key_ranges;
   int32_t n_ranges, Nk;
-  uint4* tile_bits;               // tables as in AttnParams
+  uint4* tile_bits;               // tables as in AttnParams, the list in another order
   int32_t* active;
   uint4* active_bits;
   uint4* active_inv;
   int32_t* n_active;
+  int32_t* n_full;                // [B]: the list's tiles whose keys are all admitted, listed from its front;
+                                  // the others are listed from its back
   uint32_t n_kv_ctas;             // CTAs of dK and dV: n_kv_tiles * Hkv * B
   float* nl;                      // [B][Hq][n_q_tiles * 128]: -lse log2(e)
   float* dl;                      // [B][Hq][n_q_tiles * 128]: -delta

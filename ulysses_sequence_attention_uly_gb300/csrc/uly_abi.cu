@@ -1175,7 +1175,7 @@ int bwd_q_tiles(const uly_plan* pl) {
 // Workspace of the attention's gradient: the tile tables, the row statistics,
 // and (fused) the replicated rows of do summed over the shards.
 struct BwdWork {
-  int64_t bits, active_bits, active_inv, active, n_active, nl, dl, do_rep, total;
+  int64_t bits, active_bits, active_inv, active, n_active, n_full, nl, dl, do_rep, total;
 };
 BwdWork bwd_work(const uly_plan* pl) {
   const uly_desc& d = pl->d;
@@ -1193,6 +1193,7 @@ BwdWork bwd_work(const uly_plan* pl) {
   w.active_inv = take(nt * 16);
   w.active = take(nt * 4);
   w.n_active = take(static_cast<int64_t>(d.B) * 4);
+  w.n_full = take(static_cast<int64_t>(d.B) * 4);
   w.nl = take(stats);
   w.dl = take(stats);
   const bool rep_q = d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX;
@@ -1323,6 +1324,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.active_inv = reinterpret_cast<uint4*>(ws + w.active_inv);
   p.active = reinterpret_cast<int32_t*>(ws + w.active);
   p.n_active = reinterpret_cast<int32_t*>(ws + w.n_active);
+  p.n_full = reinterpret_cast<int32_t*>(ws + w.n_full);
   p.nl = reinterpret_cast<float*>(ws + w.nl);
   p.dl = reinterpret_cast<float*>(ws + w.dl);
   p.masked_rows = d.masked_rows;
