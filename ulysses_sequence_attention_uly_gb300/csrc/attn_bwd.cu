@@ -82,6 +82,27 @@ __device__ __forceinline__ void bwd_timeout(const BwdParams& p, volatile int* ab
   atomicOr(p.status, kStatusTimeout);
 }
 
+// As mbar_wait in as little code as possible, for the elementwise loops: a jump
+// over a long loop costs them instruction fetches, several times a tile.
+__device__ __forceinline__ bool ew_wait(uint32_t bar, uint32_t parity, uint64_t deadline_ns, volatile int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 r;\n\t.reg .b64 t;\n"
+      "EW_LOOP_%=:\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra EW_DONE_%=;\n\t"
+      "ld.volatile.shared.b32 r, [%3];\n\t"
+      "setp.ne.b32 q, r, 0;\n\t"
+      "@q bra EW_DONE_%=;\n\t"
+      "mov.u64 t, %%globaltimer;\n\t"
+      "setp.gt.u64 q, t, %4;\n\t"
+      "@!q bra EW_LOOP_%=;\n"
+      "EW_DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity), "r"(smem_u32(const_cast<int*>(abort_flag))), "l"(deadline_ns) : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ uint32_t bits_word(const uint4 b, int w) {
   return w == 0 ? b.x : w == 1 ? b.y : w == 2 ? b.z : b.w;
 }
@@ -601,8 +622,8 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     } else if (MODE == 1) {
       u0 = u1 = dead ? 0u : ~0u;
     }
-    bool ok = mbar_wait(smem_u32(&bars.nl_full[qslot]), qturn & 1, k.deadline, abort_flag) &&
-              mbar_wait(smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1, k.deadline, abort_flag);
+    bool ok = ew_wait(smem_u32(&bars.nl_full[qslot]), qturn & 1, k.deadline, abort_flag) &
+              ew_wait(smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
     uint64_t pr[32];
@@ -612,8 +633,8 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
       if (lane == 0) mbar_arrive(smem_u32(&bars.s_go));
     };
     half_row_p<true>(mR, mul, 0, nl_addr, pr, s_loaded);
-    ok = mbar_wait(smem_u32(&bars.s_go), it & 1, k.deadline, abort_flag) &&
-         mbar_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
+    ok = ew_wait(smem_u32(&bars.s_go), it & 1, k.deadline, abort_flag) &
+         ew_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
     uint32_t a[2][32], pk[32];
@@ -657,7 +678,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     }
   }
   if (k.n_it > 0) {
-    const bool ok = mbar_wait(smem_u32(&bars.done), 0, k.deadline, abort_flag);
+    const bool ok = ew_wait(smem_u32(&bars.done), 0, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
   }
@@ -982,12 +1003,12 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
       bits_next = __ldg(row_bits + listed(p, it + 1, k.n_full));
       keys_next = __ldg(tile_bits + listed(p, it + 1, k.n_full));
     }
-    bool ok = mbar_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
+    bool ok = ew_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
     uint64_t pr[32];
     half_row_p<false>(mS, mul, nl2, 0, pr, [] {});
-    ok = mbar_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
+    ok = ew_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
     uint32_t a[2][32], pk[32];
