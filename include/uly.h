@@ -424,7 +424,7 @@ int uly_attention_backward(const uly_plan* plan, const void* const* qh, const vo
  * seq-sharded dq, dk, dv, with no staging copy.  It is the gradient of the
  * call as a function of the P shards:
  *  - the replicated rows' output reaches every shard, so their output gradient
- *    is the sum of the shards' dout (formed in f32, rounded to bf16);
+ *    is the sum of the shards' dout (in f32, as two bf16 operands);
  *  - the owner of a head (rank h / (Hq/P), k/v: h / (Hkv/P)) reads the
  *    replicated rows of its own shard, so its copies of dq, dk, dv hold that
  *    head's gradient and the other shards' copies hold zero.  The gradient of
@@ -437,7 +437,7 @@ int uly_sp_attention_backward(const uly_plan* plan, const void* const* q, const 
                               int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of the two calls above for this plan (about 8 bytes per
- * query row and head, and the replicated rows of one q shard), or -1 for a NULL plan. */
+ * query row and head, and the replicated rows of one q shard twice), or -1 for a NULL plan. */
 int64_t uly_attention_backward_workspace(const uly_plan* plan);
 
 /* ---- pairs that the rotation turns -------------------------------------- */

@@ -154,7 +154,8 @@ def reference(c, d, scale=None):
     the output.  r64 stands for the 32-bit arithmetic: sums of up to 2^14 terms
     (2^-24 each, added pairwise or in order by the MMA in chunks of 16) and the
     exponential's argument, |s| up to about 60: together below 2^-13.  Fused,
-    replicated rows: the sum of the shards' do is rounded once more."""
+    replicated rows: the sum of the shards' do enters as two bf16 parts, off by
+    u^2."""
     scale = 1.0 / math.sqrt(c.D) if scale is None else scale
     u, r = 2.0 ** -8, 2.0 ** -13
     shards = [[x.double().requires_grad_() for x in d[n]] for n in "qkv"]
@@ -179,7 +180,7 @@ def reference(c, d, scale=None):
             if c.rep_q:
                 sl = slice(c.n, None) if c.mode == "suffix" else slice(0, c.rep_q)
                 tot[:, sl] += rr
-                rep_u[:, sl] = u
+                rep_u[:, sl] = u * u
         G = c.Hq // c.Hkv
         kk, vv = k.repeat_interleave(G, 2), v.repeat_interleave(G, 2)
         tr = tot.abs() * (1 + 0 * rep_u)

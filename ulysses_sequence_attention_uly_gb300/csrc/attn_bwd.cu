@@ -9,21 +9,23 @@
 //   dQ_n  = scale sum_m dS_nm k_m
 // dK and dV also sum over the G query heads of a kv head.
 //
-// Two main kernels, each with its sums in TMEM from first to last term, so
-// that no sum passes through memory and none depends on the order in which
-// CTAs run (the results are the same bits on every call):
-//   dkdv_cta  one CTA per (batch, kv head, 128 keys), over every query
-//                head of the group and every 128-query tile: four products a
-//                tile pair (S, dP, dV, dK);
-//   dq_cta    one CTA per (batch, q head, 128 queries), over every 128-key
-//                tile with an admitted key: three products (S, dP, dQ).
-// One kernel with five products would have to add dQ through f32 atomics in
+// Two kinds of CTA in one launch, each with its sums in TMEM from first to last
+// term, so that no sum passes through memory and none depends on the order in
+// which CTAs run (the results are the same bits on every call):
+//   dkdv_cta  one for a (batch, kv head, 128 keys), over every query head of the
+//             group and every 128-query tile: four products a tile pair (S, dP,
+//             dV, dK);
+//   dq_cta    one for a (batch, q head, 128 queries), over every 128-key tile
+//             with an admitted key: three products (S, dP, dQ).
+// With five products in one, dQ would have to be added through f32 atomics in
 // memory, whose order changes the bits; the price of the two is 7/5 of the
 // tensor work.
 //
-// Rounding: P, dS and (replicated rows of the fused call) the sum of the
-// shards' do are rounded to bf16, since they are operands of bf16 MMAs; dS is
-// formed from the f32 P, every sum is f32, the outputs are rounded once.
+// Rounding: P and dS are rounded to bf16, since they are operands of bf16 MMAs;
+// dS is formed from the f32 P, every sum is f32, the outputs are rounded once.
+// Replicated rows of the fused call, whose do is the sum over the shards: that
+// sum enters as two bf16 parts, the products being linear in do, so these
+// rows' tiles are gone through twice.
 //
 // Every mbarrier wait is bounded, as in attn.cu.
 #include <atomic>
@@ -279,6 +281,23 @@ __device__ __forceinline__ int first_key(const BwdParams& p, int s) {
   return k;
 }
 
+// sum over eight bf16 pairs of products
+__device__ __forceinline__ float dot8(const uint4 a, const uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
+    s = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
+// first row of tile i of the replicated run in dl_lo
+__device__ __forceinline__ int64_t lo_at(const BwdParams& p, int b, int h, int i) {
+  return ((static_cast<int64_t>(b) * p.Hq + h) * p.n_lo + i) * kTileRows;
+}
+
 constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 16;  // rows of a CTA of prep_kernel
 
@@ -357,8 +376,8 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
 // the main kernel reads in tiles.  A row that takes part in nothing (past its
 // run's end, no admitted key, or zero by the masked-row convention) has -inf,
 // whose exponential is 0.  Fused, replicated rows: do is the sum of every
-// shard's copy, since each received the output; the sum is rounded to bf16 into
-// do_rep (the MMA's operand) and delta uses that value.
+// shard's copy, since each received the output, written as two bf16 operands
+// (do_hi, do_lo) with a delta each.
 // Bound by memory: o and do are read once.  16 rows x 8 heads a CTA; 16 (D =
 // 128) or 8 lanes share a row, the results go through shared memory so that
 // they are written along rows.
@@ -368,7 +387,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
   constexpr int kParts = kTileRows / kRows;
   __shared__ union {
     TableSmem table;
-    float dl[kHeads][kRows + 1];
+    struct {
+      float hi[kHeads][kRows + 1], lo[kHeads][kRows + 1];
+    } dl;
   } sm;
   if (blockIdx.x < static_cast<uint32_t>(p.B)) {
     build_tables(p, blockIdx.x, sm.table);
@@ -387,7 +408,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 #pragma unroll 4
   for (int i = unit; i < kRows * kHeads; i += kUnits) {
     const int r = i / kHeads, hh = i % kHeads, h = h0 + hh;
-    float sum = 0.f;
+    float sum = 0.f, sum_lo = 0.f;
     if (h < p.Hq && row0 + r < run.len) {
       const int owner = h / p.Hq_l;
       const int sh = p.fused ? (rep ? owner : run.out_shard) : owner;
@@ -395,7 +416,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
       const int64_t row = (run.out_row0 < 0 ? p.shard_len[sh] : run.out_row0) + row0 + r;
       if (in_bounds(&g_bwd_violations, row * p.q_row_stride, p.q_row_stride, p.q_batch_stride[sh])) {
         const uint4 ov = *reinterpret_cast<const uint4*>(p.o[sh] + b * p.q_batch_stride[sh] + row * p.q_row_stride + col);
-        uint4 dv;
+        uint4 dv, dlo = make_uint4(0u, 0u, 0u, 0u);
         if (!rep) {
           dv = *reinterpret_cast<const uint4*>(p.dout[sh] + b * p.q_batch_stride[sh] + row * p.q_row_stride + col);
         } else {
@@ -410,29 +431,40 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
               acc[2 * k + 1] += __uint_as_float(xw[k] & 0xFFFF0000u);
             }
           }
-          dv = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                          pack_bf16x2(acc[6], acc[7]));
-          *reinterpret_cast<uint4*>(p.do_rep + ((static_cast<int64_t>(b) * run.len + row0 + r) * p.Hq + h) * D * 2 +
-                                    lane * 16) = dv;
-        }
-        const uint32_t *ow = reinterpret_cast<const uint32_t*>(&ov), *dw = reinterpret_cast<const uint32_t*>(&dv);
+          // the sum as two bf16 values, whose own sum is off by at most 2^-17
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sum = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(dw[k] << 16), sum);
-          sum = fmaf(__uint_as_float(ow[k] & 0xFFFF0000u), __uint_as_float(dw[k] & 0xFFFF0000u), sum);
+          for (int k = 0; k < 4; ++k) {
+            hi[k] = pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
+            lo[k] = pack_bf16x2(acc[2 * k] - __uint_as_float(hi[k] << 16),
+                                acc[2 * k + 1] - __uint_as_float(hi[k] & 0xFFFF0000u));
+          }
+          dv = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          dlo = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const int64_t at = ((static_cast<int64_t>(b) * run.len + row0 + r) * p.Hq + h) * D * 2 + lane * 16;
+          *reinterpret_cast<uint4*>(p.do_hi + at) = dv;
+          if (p.n_lo) *reinterpret_cast<uint4*>(p.do_lo + at) = dlo;
         }
+        sum = dot8(ov, dv);
+        if (rep) sum_lo = dot8(ov, dlo);
       }
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sm.dl[hh][r] = sum;
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, o);
+    }
+    if (lane == 0) {
+      sm.dl.hi[hh][r] = sum;
+      sm.dl.lo[hh][r] = sum_lo;
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * kHeads; i += kPrepThreads) {
     const int hh = i / kRows, r = i % kRows, h = h0 + hh;
     if (h >= p.Hq) continue;
     const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + t) * kTileRows + r_lo + r;
-    float nl = -INFINITY, dl = 0.f;
+    float nl = -INFINITY, dl = 0.f, dl_lo = 0.f;
     const int lrow = row0 + r;
     if (lrow < run.len) {
       const int owner = h / p.Hq_l;
@@ -447,11 +479,13 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
       const bool live = lse != -INFINITY && !zero;
       if (live) {
         nl = -lse * 1.4426950408889634f;
-        dl = -sm.dl[hh][r];
+        dl = -sm.dl.hi[hh][r];
+        dl_lo = -sm.dl.lo[hh][r];
       }
     }
     p.nl[at] = nl;
     p.dl[at] = dl;
+    if (rep && p.n_lo) p.dl_lo[lo_at(p, b, h, t - run.first) + r_lo + r] = dl_lo;
   }
 }
 
@@ -592,10 +626,11 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
   // of the same tokens, in order, so their kv tiles follow one another.
   const uint4* own = p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles +
                      (MODE == 2 && p.qseg[0].kv_seg >= 0 ? p.kseg[p.qseg[0].kv_seg].first : 0);
+  const int rep_tile = p.qseg[p.rep_qseg].first;  // (the replicated run's once more, with do_lo)
   int own_tile = 0;
   const auto next_live = [&] {
-    live_next = __ldg(own + own_tile);
-    if (++own_tile == p.n_q_tiles) own_tile = 0;
+    live_next = __ldg(own + (own_tile < p.n_q_tiles ? own_tile : rep_tile + own_tile - p.n_q_tiles));
+    if (++own_tile == p.n_q_tiles + p.n_lo) own_tile = 0;
   };
   if (MODE == 2) next_live();
   int qslot = 0, qturn = 0;
@@ -715,7 +750,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   const uint4 bits = p.tile_bits[static_cast<int64_t>(b) * p.n_kv_tiles + t];
   const bool self = p.masked_rows == ULY_ROWS_SELF;
   const bool any = self || (bits.x | bits.y | bits.z | bits.w) != 0u;
-  const int n_it = any ? p.G * p.n_q_tiles : 0;
+  const int n_it = any ? p.G * (p.n_q_tiles + p.n_lo) : 0;
 
   const uint32_t sK = smem_u32(smem_raw), sV = sK + C::kTileBytes, sQ = sK + 2 * C::kTileBytes;
   const uint32_t sDO = sQ + C::kQSlots * C::kTileBytes, sNl = sDO + C::kOSlots * C::kTileBytes;
@@ -751,7 +786,10 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       // Where tiles come from is worked out ahead, so that their loads follow at
       // once when a slot is free: mq .. for the next Q, mo .. for the next dO
       // (the tile before it).
+      // A head's tiles: every run's, then the replicated run's again with do_lo
+      // (run n_qseg here).
       int g = 0, qs = 0, qt = 0;  // q head of the group, run, tile inside the run
+      const int n_runs = p.n_qseg + (p.n_lo ? 1 : 0);
       int qhead = 0, qrow = 0, ohead = 0, orow = 0, ohead_n = 0, orow_n = 0;
       const CUtensorMap *mq = nullptr, *mo = nullptr, *mo_n = nullptr;
       const float *nl = nullptr, *dl = nullptr, *dl_n = nullptr;
@@ -762,7 +800,8 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         dl = dl_n;
         const int h = hk * p.G + g;
         if (g == p.G) return;
-        const Seg& q = p.qseg[qs];
+        const bool lo = qs == p.n_qseg;
+        const Seg& q = p.qseg[lo ? p.rep_qseg : qs];
         const bool rep = p.fused && q.out_shard < 0;
         const int qmap = q.src < 0 ? r : q.src;
         qhead = p.fused ? h : h % p.Hq_l;
@@ -770,13 +809,13 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         ohead_n = rep ? h : qhead;
         orow_n = rep ? qt * kTileRows : qrow;
         mq = &p.tq[qmap];
-        mo_n = rep ? &p.tdo_rep : &p.tdo[qmap];
+        mo_n = rep ? (lo ? &p.tdo_lo : &p.tdo_hi) : &p.tdo[qmap];
         const int64_t at = ((static_cast<int64_t>(b) * p.Hq + h) * p.n_q_tiles + q.first + qt) * kTileRows;
         nl = p.nl + at;
-        dl_n = p.dl + at;
+        dl_n = lo ? p.dl_lo + lo_at(p, b, h, qt) : p.dl + at;
         if (++qt * kTileRows >= q.len) {
           qt = 0;
-          if (++qs == p.n_qseg) {
+          if (++qs == n_runs) {
             qs = 0;
             ++g;
           }
@@ -952,7 +991,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
 }
 
 struct QBars {
-  uint64_t q_full;
+  uint64_t q_full, lo_full;   // Q and dO; do_lo in dO's place
   uint64_t full[3];           // K and V of a tile (K's slot)
   uint64_t s_full[2], dp_full, dp_free, ds_full[2];
   uint64_t k_done[2];         // dQ(i), and with it dP(i+1), complete: i mod 2, as dQ(i+1) does not wait
@@ -975,12 +1014,13 @@ struct QWork {
   uint64_t deadline;
 };
 
-// The elementwise loop of dq_cta over the tiles [it0, it1): one thread per
+// The elementwise loop of dq_cta over the tiles [it0, it1) (base: 0, or the
+// number of tiles when they are gone through again): one thread per
 // query and half of the keys.  MASKED: keys that are not admitted, and dead
 // rows.
 template <int D, bool MASKED>
-__device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int warp, int lane, int it0, int it1, float nl,
-                                       float dl, bool dead, const uint4* row_bits) {
+__device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int warp, int lane, int base, int it0, int it1,
+                                       float nl, float dl, bool dead, const uint4* row_bits) {
   using C = BCfg<D>;
   QBars& bars = *k.bars;
   volatile int* abort_flag = &bars.abort_flag;
@@ -995,13 +1035,13 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
     bits_next = __ldg(row_bits + listed(p, it0, k.n_full));
     keys_next = __ldg(tile_bits + listed(p, it0, k.n_full));
   }
-  for (int it = it0; it < it1; ++it) {
-    const int buf = it & 1;
+  for (int j = it0; j < it1; ++j) {
+    const int it = base + j, buf = it & 1;
     const uint32_t mS = k.tmem + lane_off + 128 * buf + 64 * wg;
     const uint4 bits = bits_next, keys = keys_next;
-    if (MASKED && it + 1 < it1) {
-      bits_next = __ldg(row_bits + listed(p, it + 1, k.n_full));
-      keys_next = __ldg(tile_bits + listed(p, it + 1, k.n_full));
+    if (MASKED && j + 1 < it1) {
+      bits_next = __ldg(row_bits + listed(p, j + 1, k.n_full));
+      keys_next = __ldg(tile_bits + listed(p, j + 1, k.n_full));
     }
     bool ok = ew_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -1055,7 +1095,9 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   const int r = h / p.Hq_l, hk = h / p.G;
   const Seg run = p.qseg[seg_of(p.qseg, p.n_qseg, t)];
   const int row0 = (t - run.first) * kTileRows;
-  const int n_it = p.n_active[b], n_full = p.n_full[b];
+  // replicated rows of the fused call: every tile with do_hi, then with do_lo
+  const bool rep = p.fused && run.out_shard < 0, twice = rep && p.n_lo > 0;
+  const int n = p.n_active[b], n_full = p.n_full[b], n_it = twice ? 2 * n : n;
   const int32_t* active = p.active + static_cast<int64_t>(b) * p.n_kv_tiles;
 
   const uint32_t sQ = smem_u32(smem_raw), sDO = sQ + C::kTileBytes, sK = sQ + 2 * C::kTileBytes;
@@ -1066,6 +1108,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   if (warp == 8) {
     if (lane == 0) {
       mbar_init(smem_u32(&bars.q_full), 1);
+      mbar_init(smem_u32(&bars.lo_full), 1);
       for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.full[i]), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&bars.s_full[i]), 1);
@@ -1082,7 +1125,6 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     __syncwarp();
     ready_arrive();
     if (lane == 0 && n_it > 0) {
-      const bool rep = p.fused && run.out_shard < 0;
       const int qmap = run.src < 0 ? r : run.src;
       const int qhead = p.fused ? h : h % p.Hq_l, kvhead = p.fused ? hk : hk % p.Hkv_l;
       const int qrow = (run.row0 < 0 ? p.shard_len[qmap] : run.row0) + row0;
@@ -1090,7 +1132,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       mbar_arrive_expect_tx(bq, 2 * C::kTileBytes);
       load_tile(sQ, &p.tq[qmap], bq, qhead, qrow, b);
       if (rep)
-        load_tile(sDO, &p.tdo_rep, bq, h, row0, b);
+        load_tile(sDO, &p.tdo_hi, bq, h, row0, b);
       else
         load_tile(sDO, &p.tdo[qmap], bq, qhead, qrow, b);
       // (where a tile comes from is worked out before its slots are free)
@@ -1098,7 +1140,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       int krow;
       bool good;
       const auto next = [&](int it) {
-        const int e = active[listed(p, it, n_full)];
+        const int e = active[listed(p, it < n ? it : it - n, n_full)];
         good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
         const Seg& k = p.kseg[good ? e >> 20 : 0];
         const int kmap = k.src < 0 ? r : k.src;
@@ -1122,6 +1164,18 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         mbar_arrive_expect_tx(bf, 2 * C::kTileBytes);
         if (good && it != p.withhold_fill) load_tile(sK + ks * C::kTileBytes, mk, bf, kvhead, krow, b);
         if (good) load_tile(sV + vs * C::kTileBytes, mv, bf, kvhead, krow, b);
+        if (twice && it == n) {
+          // do_lo over do_hi once dP(n - 1) is complete (dP(n - 2) is: the
+          // waits above; dP(n) waits for this copy)
+          if (!mbar_wait(smem_u32(&bars.dp_full), (n - 1) & 1, deadline, abort_flag)) {
+            bwd_timeout(p, abort_flag);
+            ++it;
+            break;
+          }
+          const uint32_t bl = smem_u32(&bars.lo_full);
+          mbar_arrive_expect_tx(bl, C::kTileBytes);
+          load_tile(sDO, &p.tdo_lo, bl, h, row0, b);
+        }
         if (it + 1 < n_it) next(it + 1);
       }
       if (*abort_flag) {
@@ -1130,6 +1184,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         for (int f = max(0, it - C::kKSlots); f < it; ++f)
           mbar_wait(smem_u32(&bars.full[f % C::kKSlots]), (f / C::kKSlots) & 1, dl2, &never);
         mbar_wait(bq, 0, dl2, &never);
+        if (twice && it > n) mbar_wait(smem_u32(&bars.lo_full), 0, dl2, &never);
       }
     }
   } else if (warp == 9) {
@@ -1176,6 +1231,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
           if (!ok || it >= n_it) break;
           if (it + 1 < n_it) {
             if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag))) break;
+            if (twice && it + 1 == n && !(ok = mbar_wait(smem_u32(&bars.lo_full), 0, deadline, abort_flag))) break;
             tc_fence_after();
             issue_rows<D>(tDP, ddo, v_r[vs]);
             mma_commit(smem_u32(&bars.dp_full));
@@ -1202,7 +1258,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     tc_fence_before();
     ready_wait();
     tc_fence_after();
-    const uint32_t tmem = bars.tmem_base, tDP = tmem + 256, tDQ = tmem + 384;
+    const uint32_t tmem = bars.tmem_base, tDQ = tmem + 384;
     const int wg = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // query of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -1221,8 +1277,12 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     // the tiles without masks, then the others; all of them with masks where a
     // row of the warp takes part in nothing
     const int plain = __any_sync(0xffffffffu, dead) ? 0 : n_full;
-    bool ok = q_loop<D, false>(p, k, warp, lane, 0, plain, nl, dl, dead, row_bits) &&
-              q_loop<D, true>(p, k, warp, lane, plain, n_it, nl, dl, dead, row_bits);
+    bool ok = true;
+    for (int base = 0; ok && base < n_it; base += n) {
+      const float d = base == 0 ? dl : p.dl_lo[lo_at(p, b, h, row0 / kTileRows) + row];
+      ok = q_loop<D, false>(p, k, warp, lane, base, 0, plain, nl, d, dead, row_bits) &&
+           q_loop<D, true>(p, k, warp, lane, base, plain, n, nl, d, dead, row_bits);
+    }
     if (ok && n_it > 0) {
       ok = mbar_wait(smem_u32(&bars.done), 0, deadline, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
@@ -1246,9 +1306,8 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   }
 }
 
-// One launch for both: the CTAs [0, n_kv_ctas) take dK and dV, tile by tile of
-// a head, the following ones dQ.  They need nothing from each other, so that
-// dQ's CTAs fill the SMs that the last ones of dK and dV leave idle.
+// One launch for both kinds of CTA: they need nothing from each other, so that
+// dQ's fill the SMs that the last ones of dK and dV leave idle.
 template <int D, bool OWN>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_constant__ BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1256,15 +1315,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_c
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
+  // longest first: dQ of tiles that are gone through twice, dK and dV, dQ
   uint32_t i = blockIdx.x;
-  if (i < p.n_kv_ctas) {
+  const uint32_t n_lo = p.n_lo, n_twice = n_lo * p.Hq * p.B, lo0 = p.qseg[p.rep_qseg].first;
+  if (i >= n_twice && i - n_twice < p.n_kv_ctas) {
+    i -= n_twice;
     const uint32_t t = i % p.n_kv_tiles;
     i /= p.n_kv_tiles;
     dkdv_cta<D, OWN>(p, smem_raw, t, i % p.Hkv, i / p.Hkv);
   } else {
-    i -= p.n_kv_ctas;
-    const uint32_t t = i % p.n_q_tiles;
-    i /= p.n_q_tiles;
+    uint32_t n, t;  // tiles of this kind, and which
+    if (i < n_twice) {
+      n = n_lo;
+      t = lo0 + i % n;
+    } else {
+      i -= n_twice + p.n_kv_ctas;
+      n = p.n_q_tiles - n_lo;
+      t = i % n;
+      if (t >= lo0) t += n_lo;
+    }
+    i /= n;
     dq_cta<D>(p, smem_raw, t, i % p.Hq, i / p.Hq);
   }
 }

@@ -206,14 +206,14 @@ struct BwdParams {
   CUtensorMap tk[kMaxRanks];
   CUtensorMap tv[kMaxRanks];
   CUtensorMap tdo[kMaxRanks];
-  CUtensorMap tdo_rep;            // fused: replicated rows of do, summed over the shards
+  CUtensorMap tdo_hi, tdo_lo;     // fused: replicated rows of do, summed over the shards, in two bf16 parts
   const uint8_t* o[kMaxRanks];
   const uint8_t* dout[kMaxRanks];
   const float* lse[kMaxRanks];
   uint8_t* dq[kMaxRanks];
   uint8_t* dk[kMaxRanks];
   uint8_t* dv[kMaxRanks];
-  uint8_t* do_rep;                // [B][R][Hq][D] bf16
+  uint8_t *do_hi, *do_lo;         // [B][R][Hq][D] bf16 each
   Seg qseg[kMaxSegs];             // `first`: first 128-row tile, for q and kv alike
   Seg kseg[kMaxSegs];             // out_row0 / out_shard: where dk, dv rows go
   int32_t n_qseg, n_kseg, n_q_tiles, n_kv_tiles;
@@ -236,7 +236,10 @@ struct BwdParams {
                                   // the others are listed from its back
   uint32_t n_kv_ctas;             // CTAs of dK and dV: n_kv_tiles * Hkv * B
   float* nl;                      // [B][Hq][n_q_tiles * 128]: -lse log2(e)
-  float* dl;                      // [B][Hq][n_q_tiles * 128]: -delta
+  float* dl;                      // [B][Hq][n_q_tiles * 128]: -delta (of do_hi)
+  float* dl_lo;                   // [B][Hq][n_lo * 128]: -delta of do_lo
+  int32_t n_lo;                   // tiles of the replicated run that do_lo adds (0: no replicated q rows, or one shard)
+  int32_t rep_qseg;               // its index in qseg
   int32_t masked_rows;
   int32_t withhold_fill;
   int32_t* status;

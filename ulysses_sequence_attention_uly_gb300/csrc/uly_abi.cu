@@ -1173,9 +1173,10 @@ int bwd_q_tiles(const uly_plan* pl) {
 }
 
 // Workspace of the attention's gradient: the tile tables, the row statistics,
-// and (fused) the replicated rows of do summed over the shards.
+// and (fused) the replicated rows of do summed over the shards, in two parts.
 struct BwdWork {
-  int64_t bits, active_bits, active_inv, active, n_active, n_full, nl, dl, do_rep, total;
+  int64_t bits, active_bits, active_inv, active, n_active, n_full, nl, dl, dl_lo, do_hi, do_lo, total;
+  int32_t n_lo;  // tiles of the replicated q run that are gone through twice
 };
 BwdWork bwd_work(const uly_plan* pl) {
   const uly_desc& d = pl->d;
@@ -1197,7 +1198,11 @@ BwdWork bwd_work(const uly_plan* pl) {
   w.nl = take(stats);
   w.dl = take(stats);
   const bool rep_q = d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX;
-  w.do_rep = take(rep_q ? static_cast<int64_t>(d.B) * d.R * d.Hq * d.D * 2 : 0);
+  w.n_lo = rep_q && d.P > 1 ? (d.R + kTileRows - 1) / kTileRows : 0;
+  const int64_t rep_bytes = rep_q ? static_cast<int64_t>(d.B) * d.R * d.Hq * d.D * 2 : 0;
+  w.dl_lo = take(static_cast<int64_t>(d.B) * d.Hq * w.n_lo * kTileRows * 4);
+  w.do_hi = take(rep_bytes);
+  w.do_lo = take(w.n_lo ? rep_bytes : 0);
   w.total = at;
   return w;
 }
@@ -1248,7 +1253,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   // CTAs of the two launches: one for every 128 keys of a kv head and 128
   // queries of a q head; one for 16 rows of 8 q heads, and one a batch
   const int64_t q_tiles = bwd_q_tiles(pl), kv_ctas = static_cast<int64_t>(pl->n_kv_tiles) * d.Hkv * d.B;
-  if (kv_ctas + q_tiles * d.Hq * d.B > 0x7FFFFFFF ||
+  if (kv_ctas + q_tiles * d.Hq * d.B > 0x7FFFFFFF || 2 * q_tiles * (d.Hq / d.Hkv) > 0x7FFFFFFF ||
       q_tiles * (kTileRows / 16) * ((d.Hq + 7) / 8) * d.B + d.B > 0x7FFFFFFF)
     return ULY_ERR_UNSUPPORTED;
 
@@ -1314,8 +1319,15 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
       return rc;
   }
   if (fused && (d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX)) {
-    p.do_rep = ws + w.do_rep;
-    if ((rc = encode_panel_map(&p.tdo_rep, p.do_rep, d.D, d.Hq, d.R, d.B))) return rc;
+    p.do_hi = ws + w.do_hi;
+    p.do_lo = ws + w.do_lo;
+    p.dl_lo = reinterpret_cast<float*>(ws + w.dl_lo);
+    p.n_lo = w.n_lo;
+    for (int i = 0; i < p.n_qseg; ++i)
+      if (p.qseg[i].out_shard < 0) p.rep_qseg = i;
+    if ((rc = encode_panel_map(&p.tdo_hi, p.do_hi, d.D, d.Hq, d.R, d.B)) ||
+        (p.n_lo && (rc = encode_panel_map(&p.tdo_lo, p.do_lo, d.D, d.Hq, d.R, d.B))))
+      return rc;
   }
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
