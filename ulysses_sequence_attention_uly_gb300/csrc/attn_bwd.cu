@@ -30,7 +30,7 @@
 // Every mbarrier wait is bounded, as in attn.cu.
 #include <atomic>
 
-#include "internal.cuh"
+#include "grad.cuh"
 #include "tc.cuh"
 
 namespace uly {

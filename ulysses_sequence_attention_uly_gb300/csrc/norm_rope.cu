@@ -23,7 +23,7 @@
 // (160 registers: one CTA of the backward kernel on an SM).  Backward, CTAs an
 // SM x head groups in flight: 2 x 4 287 us, 2 x 6 302, 3 x 2 315, 4 x 1 349,
 // 2 x 2 345; three or more CTAs with four groups spill.
-#include "internal.cuh"
+#include "grad.cuh"
 #include "tc.cuh"
 
 namespace uly {

@@ -7,7 +7,7 @@
 
 #include <cudaTypedefs.h>
 
-#include "internal.cuh"
+#include "grad.cuh"
 
 using namespace uly;
 
