@@ -102,6 +102,38 @@ def test_staged(c):
         R.check(x, want, bound, n)
 
 
+# few tiles, of long loops: shared by two or four CTAs each
+SPLIT = [
+    R.Case("one-head", 1, (2000,), 0, "none", 1, 1, 128),
+    R.Case("one-head-ranges", 1, (1100,), 0, "none", 1, 1, 64, mask="ranges"),
+    R.Case("shared-kv", 1, (1025,), 0, "none", 4, 1, 128, mask="random"),
+    R.Case("shared-kv-prefix", 1, (700, 260), 140, "prefix", 8, 2, 128, mask="ranges"),
+    R.Case("suffix-zero", 2, (1000,), 200, "suffix", 2, 1, 64, rows="zero", mask="random"),
+    R.Case("self", 1, (900,), 129, "prefix", 4, 1, 128, rows="self", mask="random"),
+    R.Case("kv-prefix-self", 1, (600, 600), 70, "kv_prefix", 4, 2, 64, rows="self", mask="ranges"),
+    R.Case("few-keys", 1, (1500,), 0, "none", 4, 1, 128, mask="tail"),
+    R.Case("no-key", 1, (1500,), 0, "none", 2, 1, 128, mask="none"),
+    R.Case("two-parts", 1, (2048,), 0, "none", 8, 2, 128),
+]
+
+
+@pytest.mark.parametrize("c", SPLIT, ids=ids)
+def test_few_tiles(c):
+    """Right, and the same bits on every call; nothing behind the rows written."""
+    import torch
+    d = R.inputs(c, 21)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    g = run_fused(c, plan, d, ref)
+    assert plan.sync_status() == 0
+    for n, x in zip(("dq", "dk", "dv"), g):
+        R.check(x, ref[n], ref["e_" + n], n)
+    for _ in range(3):
+        again = run_fused(c, plan, d, ref)
+        for x, y in zip(sum(g, []), sum(again, [])):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("c", [CASES[6], CASES[13]], ids=ids)
 def test_against_differences(c):
     """<gradient, direction> against the difference quotient of <o, do> in 64

@@ -74,6 +74,11 @@ struct BCfg {
 };
 constexpr int kBwdThreads = 320;  // 8 warps of elementwise work, a TMA warp, an MMA warp
 
+// first of n iterations that are part k of `parts`
+__device__ __forceinline__ int share(int n, int k, int parts) {
+  return static_cast<int>(static_cast<int64_t>(n) * k / parts);
+}
+
 // barrier 1 of a CTA: the TMA warp arrives (its barriers are initialised) and
 // goes on, the others wait
 __device__ __forceinline__ void ready_arrive() { asm volatile("bar.arrive 1, %0;" ::"n"(kBwdThreads) : "memory"); }
@@ -258,6 +263,90 @@ __device__ __forceinline__ void store_rows(const BwdParams& p, uint8_t* const* o
       if (!zero)
         v = ld_shared_v4(stage + i * 2 * D + ((static_cast<uint32_t>(ch) ^ static_cast<uint32_t>(i & (kChunks - 1))) << 4));
       *reinterpret_cast<uint4*>(base + off) = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------- split --
+// Where there are too few tiles for the SMs, a tile's loop is shared by the
+// CTAs of a cluster, a part of the iterations each.  Each leaves its f32 sums
+// in its shared memory, and each adds up a share of the rows of all of them in
+// the order of the CTAs: the same bits on every call.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// address of 16-byte piece c of row r of an f32 matrix [][D]
+template <int D>
+__device__ __forceinline__ uint32_t f32_at(uint32_t base, int r, int c) {
+  constexpr int kPieces = D / 4;
+  return base + static_cast<uint32_t>(r * kPieces + (c ^ (r & (kPieces - 1)))) * 16u;
+}
+
+// piece c of row r of the matrix in the shared memory of CTA `rank` of the cluster
+template <int D>
+__device__ __forceinline__ float4 ld_peer(uint32_t base, int r, int c, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(f32_at<D>(base, r, c)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// the thread's row of an f32 accumulator in TMEM, columns [c_lo, c_hi), to
+// shared memory
+template <int D>
+__device__ __forceinline__ void keep_rows(uint32_t t, uint32_t base, int row, int c_lo, int c_hi, bool zero) {
+  for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+    uint32_t o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0u;
+    if (!zero) {
+      tmem_ld32(t + c0, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      st_shared_v4(f32_at<D>(base, row, c0 / 4 + k), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+  }
+}
+
+// This CTA's share of the rows of a matrix at `base`: the sum over the
+// cluster's CTAs, times mul, to the output tensors as store_rows writes them.
+template <int D>
+__device__ __forceinline__ void join_rows(const BwdParams& p, uint8_t* const* out, const int64_t* batch_stride,
+                                          int64_t row_stride, const Seg& run, int row0, int head, int owner, int b,
+                                          uint32_t base, float mul, int part) {
+  constexpr int kPieces = D / 4, kSets = 8;
+  const int log = p.parts >> 1, rows = kTileRows >> log;  // (parts: 2 or 4)
+  const int n = min(rows, run.len - row0 - part * rows) * kPieces, lane_off = head * D * 2;
+  if (!in_bounds(&g_bwd_violations, lane_off, D * 2, row_stride)) return;
+  const bool all = p.fused && run.out_shard < 0;
+  const int lo = all ? 0 : (p.fused ? run.out_shard : owner), hi = all ? p.P : lo + 1;
+  for (int sh = lo; sh < hi; ++sh) {
+    const int64_t r0 = (run.out_row0 < 0 ? p.shard_len[sh] : run.out_row0) + row0 + part * rows;
+    if (n > 0 && !in_bounds(&g_bwd_violations, r0 * row_stride, n / kPieces * row_stride, batch_stride[sh])) continue;
+    uint8_t* dst = out[sh] + b * batch_stride[sh] + r0 * row_stride + lane_off;
+    const bool zero = all && sh != owner;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kBwdThreads * (kSets >> log)) {
+      float4 u[kSets];
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) {
+        const int i = min(i0 + (s >> log) * kBwdThreads, n - 1);
+        u[s] = ld_peer<D>(base, part * rows + i / kPieces, i % kPieces, s & (p.parts - 1));
+      }
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) {
+        const int i = i0 + (s >> log) * kBwdThreads;
+        if (s & (p.parts - 1)) u[s] = make_float4(u[s - 1].x + u[s].x, u[s - 1].y + u[s].y, u[s - 1].z + u[s].z, u[s - 1].w + u[s].w);
+        if ((s & (p.parts - 1)) == p.parts - 1 && i < n) {
+          const uint2 w = make_uint2(pack_bf16x2(u[s].x * mul, u[s].y * mul), pack_bf16x2(u[s].z * mul, u[s].w * mul));
+          *reinterpret_cast<uint2*>(dst + i / kPieces * row_stride + i % kPieces * 8) = zero ? make_uint2(0u, 0u) : w;
+        }
+      }
     }
   }
 }
@@ -602,7 +691,7 @@ static_assert(sizeof(KvBars) <= 256, "room for the barriers");
 struct KvWork {
   KvBars* bars;
   uint32_t tmem, sQ, sDO, sNl, sDl;
-  int n_it, b;
+  int n_it, b, first_tile;  // of the head's tiles
   uint64_t deadline;
 };
 
@@ -627,7 +716,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
   const uint4* own = p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles +
                      (MODE == 2 && p.qseg[0].kv_seg >= 0 ? p.kseg[p.qseg[0].kv_seg].first : 0);
   const int rep_tile = p.qseg[p.rep_qseg].first;  // (the replicated run's once more, with do_lo)
-  int own_tile = 0;
+  int own_tile = k.first_tile;
   const auto next_live = [&] {
     live_next = __ldg(own + (own_tile < p.n_q_tiles ? own_tile : rep_tile + own_tile - p.n_q_tiles));
     if (++own_tile == p.n_q_tiles + p.n_lo) own_tile = 0;
@@ -739,8 +828,8 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
 // first reader waits for anyway.  Slots: Q(i) over Q(i-3) once dV(i-3), issued
 // after dK(i-3), is complete; dO(i) over dO(i-2) once dV(i-2) is.
 // TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D).
-template <int D, bool OWN>
-__device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b) {
+template <int D, bool OWN, bool SPLIT>
+__device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b, int part) {
   using C = BCfg<D>;
   KvBars& bars = *reinterpret_cast<KvBars*>(smem_raw + C::kKvBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -750,7 +839,10 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   const uint4 bits = p.tile_bits[static_cast<int64_t>(b) * p.n_kv_tiles + t];
   const bool self = p.masked_rows == ULY_ROWS_SELF;
   const bool any = self || (bits.x | bits.y | bits.z | bits.w) != 0u;
-  const int n_it = any ? p.G * (p.n_q_tiles + p.n_lo) : 0;
+  const int n_all = any ? p.G * (p.n_q_tiles + p.n_lo) : 0;
+  // SPLIT: this CTA's share of them
+  const int it_lo = SPLIT ? share(n_all, part, p.parts) : 0;
+  const int n_it = SPLIT ? share(n_all, part + 1, p.parts) - it_lo : n_all;
 
   const uint32_t sK = smem_u32(smem_raw), sV = sK + C::kTileBytes, sQ = sK + 2 * C::kTileBytes;
   const uint32_t sDO = sQ + C::kQSlots * C::kTileBytes, sNl = sDO + C::kOSlots * C::kTileBytes;
@@ -790,6 +882,12 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       // (run n_qseg here).
       int g = 0, qs = 0, qt = 0;  // q head of the group, run, tile inside the run
       const int n_runs = p.n_qseg + (p.n_lo ? 1 : 0);
+      if (SPLIT) {
+        g = it_lo / (p.n_q_tiles + p.n_lo);
+        const int i = it_lo % (p.n_q_tiles + p.n_lo);
+        qs = i < p.n_q_tiles ? seg_of(p.qseg, p.n_qseg, i) : p.n_qseg;
+        qt = i - (i < p.n_q_tiles ? p.qseg[qs].first : p.n_q_tiles);
+      }
       int qhead = 0, qrow = 0, ohead = 0, orow = 0, ohead_n = 0, orow_n = 0;
       const CUtensorMap *mq = nullptr, *mo = nullptr, *mo_n = nullptr;
       const float *nl = nullptr, *dl = nullptr, *dl_n = nullptr;
@@ -961,7 +1059,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
     const int row = q4 * 32 + lane;  // key of the tile = TMEM lane
     const bool key_ok = (bits_word(bits, q4) >> lane) & 1u;
     const bool dead = row0 + row >= run.len || (!self && !key_ok);
-    const KvWork k = {&bars, tmem, sQ, sDO, sNl, sDl, n_it, b, deadline};
+    const KvWork k = {&bars, tmem, sQ, sDO, sNl, sDl, n_it, b, n_it > 0 ? it_lo % (p.n_q_tiles + p.n_lo) : 0, deadline};
     bool ok;
     if constexpr (OWN)
       ok = kv_loop<D, 2>(p, k, warp, lane, key_ok, dead);
@@ -971,6 +1069,11 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       ok = kv_loop<D, 0>(p, k, warp, lane, key_ok, dead);
     if (!ok) {
       bwd_timeout(p, abort_flag);
+    } else if (SPLIT) {
+      // warps 0-3: dV, warps 4-7: dK, in f32 from the buffer's start on (every
+      // copy into it has been read)
+      keep_rows<D>((wg ? tDK : tDV) + (static_cast<uint32_t>(q4 * 32) << 16), sK + wg * (kTileRows * D * 4), row, 0, D,
+                   n_it == 0);
     } else {
       // warps 0-3: dV, warps 4-7: dK; each warp stages and stores its 32 rows
       // (in two slots of Q: every copy into them has been read)
@@ -987,6 +1090,14 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(bars.tmem_base, 512);
+  }
+  if (SPLIT) {
+    cluster_sync();
+    const int head = p.fused ? hk : hk % p.Hkv_l;
+    for (int m = 0; m < 2; ++m)
+      join_rows<D>(p, m ? p.dk : p.dv, p.kv_batch_stride, p.kv_row_stride, run, row0, head, r, b,
+                   sK + m * (kTileRows * D * 4), m ? p.scale : 1.f, part);
+    cluster_sync();  // no CTA leaves while another reads its sums
   }
 }
 
@@ -1010,7 +1121,7 @@ __device__ __forceinline__ int listed(const BwdParams& p, int it, int n_full) {
 struct QWork {
   QBars* bars;
   uint32_t tmem, sK;
-  int n_it, n_full, b;
+  int n_it, n_full, b, j_lo;  // j_lo: first tile of the list
   uint64_t deadline;
 };
 
@@ -1032,16 +1143,16 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
   const bool zero_keys = p.masked_rows != ULY_ROWS_SELF;
   uint4 bits_next = make_uint4(0u, 0u, 0u, 0u), keys_next = bits_next;
   if (MASKED && it0 < it1) {
-    bits_next = __ldg(row_bits + listed(p, it0, k.n_full));
-    keys_next = __ldg(tile_bits + listed(p, it0, k.n_full));
+    bits_next = __ldg(row_bits + listed(p, k.j_lo + it0, k.n_full));
+    keys_next = __ldg(tile_bits + listed(p, k.j_lo + it0, k.n_full));
   }
   for (int j = it0; j < it1; ++j) {
     const int it = base + j, buf = it & 1;
     const uint32_t mS = k.tmem + lane_off + 128 * buf + 64 * wg;
     const uint4 bits = bits_next, keys = keys_next;
     if (MASKED && j + 1 < it1) {
-      bits_next = __ldg(row_bits + listed(p, j + 1, k.n_full));
-      keys_next = __ldg(tile_bits + listed(p, j + 1, k.n_full));
+      bits_next = __ldg(row_bits + listed(p, k.j_lo + j + 1, k.n_full));
+      keys_next = __ldg(tile_bits + listed(p, k.j_lo + j + 1, k.n_full));
     }
     bool ok = ew_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -1087,8 +1198,8 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
 //            stored over S's columns (two S buffers, so that the next tile's
 //            scores are there when this one's are done).
 // TMEM: S0 [0,128) S1 [128,256) dP [256,384) dQ [384,384+D).
-template <int D>
-__device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, int t, int h, int b) {
+template <int D, bool SPLIT>
+__device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, int t, int h, int b, int part) {
   using C = BCfg<D>;
   QBars& bars = *reinterpret_cast<QBars*>(smem_raw + C::kQBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1097,7 +1208,11 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   const int row0 = (t - run.first) * kTileRows;
   // replicated rows of the fused call: every tile with do_hi, then with do_lo
   const bool rep = p.fused && run.out_shard < 0, twice = rep && p.n_lo > 0;
-  const int n = p.n_active[b], n_full = p.n_full[b], n_it = twice ? 2 * n : n;
+  const int n_all = p.n_active[b], n_full = p.n_full[b];
+  // SPLIT: this CTA's share of the list
+  const int j_lo = SPLIT ? share(n_all, part, p.parts) : 0;
+  const int n = SPLIT ? share(n_all, part + 1, p.parts) - j_lo : n_all;
+  const int n_it = twice ? 2 * n : n;
   const int32_t* active = p.active + static_cast<int64_t>(b) * p.n_kv_tiles;
 
   const uint32_t sQ = smem_u32(smem_raw), sDO = sQ + C::kTileBytes, sK = sQ + 2 * C::kTileBytes;
@@ -1140,7 +1255,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       int krow;
       bool good;
       const auto next = [&](int it) {
-        const int e = active[listed(p, it < n ? it : it - n, n_full)];
+        const int e = active[listed(p, j_lo + (it < n ? it : it - n), n_full)];
         good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
         const Seg& k = p.kseg[good ? e >> 20 : 0];
         const int kmap = k.src < 0 ? r : k.src;
@@ -1273,10 +1388,10 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     const float nl = p.nl[at], dl = p.dl[at];
     const bool dead = nl == -INFINITY;
     const uint4* row_bits = (invert ? p.active_inv : p.active_bits) + static_cast<int64_t>(b) * p.n_kv_tiles;
-    const QWork k = {&bars, tmem, sK, n_it, n_full, b, deadline};
+    const QWork k = {&bars, tmem, sK, n_it, n_full, b, j_lo, deadline};
     // the tiles without masks, then the others; all of them with masks where a
     // row of the warp takes part in nothing
-    const int plain = __any_sync(0xffffffffu, dead) ? 0 : n_full;
+    const int plain = __any_sync(0xffffffffu, dead) ? 0 : min(max(n_full - j_lo, 0), n);
     bool ok = true;
     for (int base = 0; ok && base < n_it; base += n) {
       const float d = base == 0 ? dl : p.dl_lo[lo_at(p, b, h, row0 / kTileRows) + row];
@@ -1290,6 +1405,8 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     }
     if (!ok) {
       bwd_timeout(p, abort_flag);
+    } else if (SPLIT) {
+      keep_rows<D>(tDQ + lane_off, sQ, row, wg * (D / 2), (wg + 1) * (D / 2), n_it == 0);
     } else {
       // warps 0-3: the first half of the columns, warps 4-7 the second
       stage_rows<D>(tDQ + lane_off, p.scale, sQ, row, wg * (D / 2), (wg + 1) * (D / 2), n_it == 0);
@@ -1304,11 +1421,16 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     tc_fence_after();
     tmem_dealloc(bars.tmem_base, 512);
   }
+  if (SPLIT) {
+    cluster_sync();
+    join_rows<D>(p, p.dq, p.q_batch_stride, p.q_row_stride, run, row0, p.fused ? h : h % p.Hq_l, r, b, sQ, p.scale, part);
+    cluster_sync();
+  }
 }
 
 // One launch for both kinds of CTA: they need nothing from each other, so that
 // dQ's fill the SMs that the last ones of dK and dV leave idle.
-template <int D, bool OWN>
+template <int D, bool OWN, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_constant__ BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {  // (never: the buffer is placed on a 1024-byte boundary)
@@ -1316,13 +1438,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_c
     return;
   }
   // longest first: dQ of tiles that are gone through twice, dK and dV, dQ
-  uint32_t i = blockIdx.x;
+  uint32_t i = blockIdx.x, part = 0;
+  if (SPLIT) {
+    part = i % p.parts;
+    i /= p.parts;
+  }
   const uint32_t n_lo = p.n_lo, n_twice = n_lo * p.Hq * p.B, lo0 = p.qseg[p.rep_qseg].first;
   if (i >= n_twice && i - n_twice < p.n_kv_ctas) {
     i -= n_twice;
     const uint32_t t = i % p.n_kv_tiles;
     i /= p.n_kv_tiles;
-    dkdv_cta<D, OWN>(p, smem_raw, t, i % p.Hkv, i / p.Hkv);
+    dkdv_cta<D, OWN, SPLIT>(p, smem_raw, t, i % p.Hkv, i / p.Hkv, part);
   } else {
     uint32_t n, t;  // tiles of this kind, and which
     if (i < n_twice) {
@@ -1335,11 +1461,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_c
       if (t >= lo0) t += n_lo;
     }
     i /= n;
-    dq_cta<D>(p, smem_raw, t, i % p.Hq, i / p.Hq);
+    dq_cta<D, SPLIT>(p, smem_raw, t, i % p.Hq, i / p.Hq, part);
   }
 }
 
-template <int D, bool OWN>
+template <int D, bool OWN, bool SPLIT>
 cudaError_t launch_main(const BwdParams& p, unsigned grid, cudaStream_t s) {
   // the shared-memory limit is set once on every device that launches the
   // kernel (setting it twice is harmless)
@@ -1349,12 +1475,28 @@ cudaError_t launch_main(const BwdParams& p, unsigned grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(backward_kernel<D, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, BCfg<D>::kSmem);
+    e = cudaFuncSetAttribute(backward_kernel<D, OWN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             BCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  backward_kernel<D, OWN><<<grid, kBwdThreads, BCfg<D>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  if (!SPLIT) {
+    backward_kernel<D, OWN, SPLIT><<<grid, kBwdThreads, BCfg<D>::kSmem, s>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid * p.parts);
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = BCfg<D>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.parts;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, backward_kernel<D, OWN, SPLIT>, p);
 }
 
 template <int D>
@@ -1364,7 +1506,9 @@ cudaError_t launch(const BwdParams& p, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid = p.n_kv_ctas + static_cast<unsigned>(p.n_q_tiles) * p.Hq * p.B;
-  return p.masked_rows == ULY_ROWS_SDPA ? launch_main<D, false>(p, grid, s) : launch_main<D, true>(p, grid, s);
+  const bool own = p.masked_rows != ULY_ROWS_SDPA;
+  if (p.parts > 1) return own ? launch_main<D, true, true>(p, grid, s) : launch_main<D, false, true>(p, grid, s);
+  return own ? launch_main<D, true, false>(p, grid, s) : launch_main<D, false, false>(p, grid, s);
 }
 
 }  // namespace

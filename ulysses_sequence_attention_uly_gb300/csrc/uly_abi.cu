@@ -1226,6 +1226,37 @@ int encode_panel_map(CUtensorMap* m, const void* base, int D, int heads, int64_t
   return r == CUDA_SUCCESS ? ULY_OK : ULY_ERR_CUDA;
 }
 
+// CTAs that share a tile's loop (1, 2 or 4).  Times in hundreds of cycles, as
+// measured: a step takes a dK/dV CTA 26 (20 for 64-wide heads) and a dQ CTA 20
+// (15), and what surrounds a CTA's loop 110, with the joining of the sums 205
+// (165).
+// A split takes the longest CTA's time, or where there are more CTAs than SMs
+// the work shared out and half a CTA that ends alone; clusters of four leave a
+// twentieth of the SMs out.  Measured, one call without and with the split it
+// gets: 1 head of 1024 rows 16.5 / 13.6 us, of 4096 rows 46.9 / 32.8; 4 q heads
+// on one kv head, 1024 rows 46.3 / 22.9, 8192 rows 327 / 297; the other side: 2
+// heads of 4096 rows 47.3 unsplit, 57.5 in pairs, 8 heads of 1024 17.0 and 28.9.
+int pick_parts(int D, int64_t kv_units, int64_t kv_steps, int64_t q_units, int64_t q_steps, bool twice, int sms) {
+  const int64_t kv = kv_steps * (D == 128 ? 26 : 20), q = q_steps * (D == 128 ? 20 : 15);
+  int best = 1;
+  int64_t least = 0;
+  for (int s = 1; s <= 4; s *= 2) {
+    const int64_t around = s == 1 ? 110 : D == 128 ? 205 : 165, n = s == 4 ? sms - sms / 20 : sms;
+    const int64_t kv_cta = kv / s + around, q_cta = (twice ? 2 * q : q) / s + around;
+    int64_t time = kv_cta > q_cta ? kv_cta : q_cta;
+    if ((kv_units + q_units) * s > n) {
+      const int64_t all = (kv_units * (kv + s * around) + q_units * (q + s * around)) / n;
+      const int64_t shared = all + (kv_cta < q_cta ? kv_cta : q_cta) / 2;
+      if (shared > time) time = shared;
+    }
+    if (s == 1 || time * 20 < least * 19) {  // (for less than a twentieth: as it was)
+      best = s;
+      least = time;
+    }
+  }
+  return best;
+}
+
 int run_backward(const uly_plan* pl, int fused, const void* const* q, const void* const* k, const void* const* v,
                  const void* const* o, const float* const* lse, const void* const* dout, const uint8_t* key_mask,
                  const int32_t* key_ranges, int32_t n_ranges, float scale, void* const* dq, void* const* dk,
@@ -1253,7 +1284,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   // CTAs of the two launches: one for every 128 keys of a kv head and 128
   // queries of a q head; one for 16 rows of 8 q heads, and one a batch
   const int64_t q_tiles = bwd_q_tiles(pl), kv_ctas = static_cast<int64_t>(pl->n_kv_tiles) * d.Hkv * d.B;
-  if (kv_ctas + q_tiles * d.Hq * d.B > 0x7FFFFFFF || 2 * q_tiles * (d.Hq / d.Hkv) > 0x7FFFFFFF ||
+  if (kv_ctas + q_tiles * d.Hq * d.B > 0x0FFFFFFF || 2 * q_tiles * (d.Hq / d.Hkv) > 0x7FFFFFFF ||
       q_tiles * (kTileRows / 16) * ((d.Hq + 7) / 8) * d.B + d.B > 0x7FFFFFFF)
     return ULY_ERR_UNSUPPORTED;
 
@@ -1349,6 +1380,8 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.n_ranges = key_ranges ? n_ranges : 0;
   p.Nk = static_cast<int32_t>(pl->nk);
   p.n_kv_ctas = static_cast<uint32_t>(kv_ctas);
+  p.parts = pick_parts(d.D, kv_ctas, static_cast<int64_t>(p.G) * (q_tiles + p.n_lo),
+                       (q_tiles + p.n_lo) * d.Hq * d.B, p.n_kv_tiles, p.n_lo > 0, pl->sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_attention_backward(p, d.D, s) != cudaSuccess) return ULY_ERR_CUDA;
   return ULY_OK;
