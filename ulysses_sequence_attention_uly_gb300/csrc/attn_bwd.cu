@@ -72,7 +72,7 @@ struct BCfg {
   static constexpr int kSmem = kKvBars + 256;
   static_assert(kQBars <= kKvBars && kSmem <= 227 * 1024, "shared memory of a CTA");
 };
-constexpr int kBwdThreads = 320;  // 8 warps of elementwise work, a TMA warp, an MMA warp
+constexpr int kBwdThreads = 352;  // 8 warps of elementwise work, a TMA warp, two MMA warps
 
 // first of n iterations that are part k of `parts`
 __device__ __forceinline__ int share(int n, int k, int parts) {
@@ -677,11 +677,11 @@ struct KvBars {
   uint64_t s_full[2];         // S(i) in region i mod 2
   uint64_t s_go;              // phase i: S(i) read out of TMEM (8 warps); dO(i), -delta (and V) landed
   uint64_t dp_full;           // phase i: dP(i) in region i mod 2
-  uint64_t ds_full;           // phase i: dS(i) stored (8 warps)
+  uint64_t ds_full[2];        // dS(i) stored (8 warps): i mod 2, as dP(i+1) does not wait for dK(i)
   uint64_t p_go[2];           // P(i) stored (8 warps), Q(i+2) landed: i mod 2, since a warp may store
                               // P(i+1) before Q(i+2) is there
-  uint64_t v_done;            // phase i: dV(i), and with it dK(i), complete
-  uint64_t done, drain;
+  uint64_t v_done[2];         // dV(i), and with it dK(i), complete: i mod 2, as dV(i+1) does not wait for S(i+2)
+  uint64_t done, drain[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -784,7 +784,7 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full));
+    if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[it & 1]));
     if (MODE == 0) {
       store_p<false, 0>(mR + 32, pr, 0u);
       store_p<false, 1>(mR + 32, pr, 0u);
@@ -812,21 +812,22 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
 // dK and dV of 128 keys of one kv head.
 //   warp 8   TMA: K and V once, then Q, dO and the row statistics of every
 //            128-query tile of every query head of the group.
-//   warp 9   MMA: S = K Q^T and dP = V dO^T (keys are TMEM lanes), dV += P dO
-//            and dK += dS Q with P and dS read from TMEM.
+//   warp 9   MMA: S = K Q^T (keys are TMEM lanes), dK += dS Q and dV += P do
+//            with dS and P read from TMEM, in the order
+//              S(0) S(1) | dK(i) dV(i) S(i+2) ...
+//   warp 10  MMA: dP(i) = V dO^T, as soon as S(i) is in registers.
 //   warps 0-7: P from S, dS from dP.
 // Two query tiles are under way in two TMEM regions of 128 columns.  A region
 // holds in turn a tile's S, then (once S is in registers) its dP, then (once dP
 // is) its dS and P in bf16, half a row's P in the 32 columns behind its dS.
-// Order of the products:
-//   S(0) S(1) dP(0) | dK(i) dP(i+1) dV(i) S(i+2) ...
-// What a step waits for is then only dP(i+1), 512 tensor cycles, after S(i+1)
-// has been read, while P(i+1) is computed; with one region each for S and dP it
-// was two products.  The issuing thread spends about 47 cycles on an MMA (64 on
-// the tensor core), 75 on a commit and 85 on a wait for a barrier that has
-// completed, so the copy of a tile is one more arrival on a barrier that its
-// first reader waits for anyway.  Slots: Q(i) over Q(i-3) once dV(i-3), issued
-// after dK(i-3), is complete; dO(i) over dO(i-2) once dV(i-2) is.
+// A thread spends about 47 cycles on issuing an MMA (64 on the tensor core for
+// 128-wide heads, 32 for the sums of 64-wide ones), 75 on a commit and 85 on a
+// wait for a barrier that has completed.  So there are two of them: one thread
+// for all four products, 578 us, two 537 (8 heads of 8192 rows; 64-wide 459 and
+// 408); S on the second thread, which then waits for dV(i), 625.  And the copy
+// of a tile is one more arrival on a barrier that its first reader waits for
+// anyway.  Slots: Q(i) over Q(i-3) once dV(i-3), issued after dK(i-3), is
+// complete; dO(i) over dO(i-2) once dV(i-2) is.
 // TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D).
 template <int D, bool OWN, bool SPLIT>
 __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b, int part) {
@@ -859,12 +860,13 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       mbar_init(smem_u32(&bars.s_full[1]), 1);
       mbar_init(smem_u32(&bars.s_go), 9);
       mbar_init(smem_u32(&bars.dp_full), 1);
-      mbar_init(smem_u32(&bars.ds_full), 8);
-      mbar_init(smem_u32(&bars.p_go[0]), 9);
-      mbar_init(smem_u32(&bars.p_go[1]), 9);
-      mbar_init(smem_u32(&bars.v_done), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&bars.ds_full[i]), 8);
+        mbar_init(smem_u32(&bars.p_go[i]), 9);
+        mbar_init(smem_u32(&bars.v_done[i]), 1);
+        mbar_init(smem_u32(&bars.drain[i]), 1);
+      }
       mbar_init(smem_u32(&bars.done), 1);
-      mbar_init(smem_u32(&bars.drain), 1);
       bars.abort_flag = 0;
       fence_mbar_init();
     }
@@ -931,8 +933,8 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         mbar_arrive_expect_tx(bn, C::kStatBytes);
         bulk_load(sNl + slot * C::kStatBytes, nl, C::kStatBytes, bn);
       };
-      // dO(it): its slot is free since v_done(it - 2); that was issued after
-      // dP(it - 1) and so after phase it - 1 of s_go
+      // dO(it): its slot is free since v_done(it - 2); phase it - 1 of s_go is
+      // complete
       const auto load_o = [&](int it) {
         const uint32_t slot = it & 1;
         mbar_arrive_expect_tx(b_sgo, (it == 0 ? 2 : 1) * C::kTileBytes + C::kStatBytes);
@@ -954,9 +956,11 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       if (ok && n_it > 2) {
         load_q(2);
         next();
-        // dO(it) and Q(it + 1) follow v_done(it - 2)
+        // dO(it) and Q(it + 1) follow v_done(it - 2) and s_go(it - 1)
         for (int it = 2; it < n_it; ++it) {
-          if (!(ok = mbar_wait(smem_u32(&bars.v_done), it & 1, deadline, abort_flag))) break;
+          if (!(ok = mbar_wait(smem_u32(&bars.v_done[it & 1]), ((it - 2) >> 1) & 1, deadline, abort_flag) &&
+                     mbar_wait(b_sgo, ~it & 1, deadline, abort_flag)))
+            break;
           load_o(it);
           if (it + 1 < n_it) load_q(it + 1);
           next();
@@ -984,18 +988,15 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
     tc_fence_after();
     const uint32_t tmem = bars.tmem_base, tDV = tmem + 256, tDK = tmem + 256 + D;
     if (lane == 0 && n_it > 0) {
-      const uint32_t dk = desc_rows(sK), dv = desc_rows(sV);
-      uint32_t q_r[C::kQSlots], q_c[C::kQSlots], o_r[C::kOSlots], o_c[C::kOSlots];
+      uint32_t q_c[C::kQSlots], o_c[C::kOSlots];
 #pragma unroll
-      for (int i = 0; i < C::kQSlots; ++i) {
-        q_r[i] = desc_rows(sQ + i * C::kTileBytes);
-        q_c[i] = desc_cols(sQ + i * C::kTileBytes);
-      }
+      for (int i = 0; i < C::kQSlots; ++i) q_c[i] = desc_cols(sQ + i * C::kTileBytes);
 #pragma unroll
-      for (int i = 0; i < C::kOSlots; ++i) {
-        o_r[i] = desc_rows(sDO + i * C::kTileBytes);
-        o_c[i] = desc_cols(sDO + i * C::kTileBytes);
-      }
+      for (int i = 0; i < C::kOSlots; ++i) o_c[i] = desc_cols(sDO + i * C::kTileBytes);
+      const uint32_t dk = desc_rows(sK);
+      uint32_t q_r[C::kQSlots];
+#pragma unroll
+      for (int i = 0; i < C::kQSlots; ++i) q_r[i] = desc_rows(sQ + i * C::kTileBytes);
       bool ok = mbar_wait(smem_u32(&bars.kq_full), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
@@ -1009,12 +1010,6 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
           mma_commit(smem_u32(&bars.s_full[1]));
         }
       }
-      ok = ok && mbar_wait(smem_u32(&bars.s_go), 0, deadline, abort_flag);
-      tc_fence_after();
-      if (ok) {
-        issue_rows<D>(tmem, dv, o_r[0]);
-        mma_commit(smem_u32(&bars.dp_full));
-      }
       // unrolled over a turn of the rings, so that every operand is a constant
       constexpr int kTurn = C::kQSlots * C::kOSlots;
       static_assert(kTurn % 2 == 0 && C::kOSlots == 2, "regions and phases alternate");
@@ -1023,32 +1018,58 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         for (int u = 0; u < kTurn; ++u) {
           const int it = it0 + u;
           if (!ok || it >= n_it) break;
-          const uint32_t tR = tmem + 128 * (u & 1), tN = tmem + 128 * (~u & 1);
-          if (!(ok = mbar_wait(smem_u32(&bars.ds_full), u & 1, deadline, abort_flag))) break;
+          const uint32_t tR = tmem + 128 * (u & 1);
+          if (!(ok = mbar_wait(smem_u32(&bars.ds_full[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_cols<D>(tDK, tR, q_c[u % C::kQSlots], it > 0);
-          if (it + 1 < n_it) {
-            if (!(ok = mbar_wait(smem_u32(&bars.s_go), ~u & 1, deadline, abort_flag))) break;
-            tc_fence_after();
-            issue_rows<D>(tN, dv, o_r[(u + 1) % C::kOSlots]);
-            mma_commit(smem_u32(&bars.dp_full));
-          }
           if (!(ok = mbar_wait(smem_u32(&bars.p_go[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_cols<D>(tDV, tR + 32, o_c[u % C::kOSlots], it > 0);
           if (it + 2 < n_it) {
-            mma_commit(smem_u32(&bars.v_done));
+            mma_commit(smem_u32(&bars.v_done[u & 1]));
             issue_rows<D>(tR, dk, q_r[(u + 2) % C::kQSlots]);
             mma_commit(smem_u32(&bars.s_full[u & 1]));
-          } else if (it + 1 == n_it) {
+          } else if (it + 1 == n_it)
             mma_commit(smem_u32(&bars.done));
-          }
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain));
+      mma_commit(smem_u32(&bars.drain[0]));
       volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      if (!mbar_wait(smem_u32(&bars.drain[0]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+    }
+  } else if (warp == 10) {
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+    if (lane == 0 && n_it > 0) {
+      const uint32_t dv = desc_rows(sV);
+      uint32_t o_r[C::kOSlots];
+#pragma unroll
+      for (int i = 0; i < C::kOSlots; ++i) o_r[i] = desc_rows(sDO + i * C::kTileBytes);
+      bool ok = true;
+      ok = ok && mbar_wait(smem_u32(&bars.s_go), 0, deadline, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        issue_rows<D>(tmem, dv, o_r[0]);
+        mma_commit(smem_u32(&bars.dp_full));
+      }
+      for (int it0 = 0; ok && it0 + 1 < n_it; it0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int it = it0 + u;
+          if (!ok || it + 1 >= n_it) break;
+          if (!(ok = mbar_wait(smem_u32(&bars.s_go), ~u & 1, deadline, abort_flag))) break;
+          tc_fence_after();
+          issue_rows<D>(tmem + 128 * (~u & 1), dv, o_r[~u & 1]);
+          mma_commit(smem_u32(&bars.dp_full));
+        }
+      }
+      if (!ok) bwd_timeout(p, abort_flag);
+      mma_commit(smem_u32(&bars.drain[1]));
+      volatile int never = 0;
+      if (!mbar_wait(smem_u32(&bars.drain[1]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
     }
   } else {
     tc_fence_before();
@@ -1105,9 +1126,9 @@ struct QBars {
   uint64_t q_full, lo_full;   // Q and dO; do_lo in dO's place
   uint64_t full[3];           // K and V of a tile (K's slot)
   uint64_t s_full[2], dp_full, dp_free, ds_full[2];
-  uint64_t k_done[2];         // dQ(i), and with it dP(i+1), complete: i mod 2, as dQ(i+1) does not wait
-                              // for the loads that follow it
-  uint64_t done, drain;
+  uint64_t v_free[2];         // dP(i) complete
+  uint64_t k_done[2];         // dQ(i) complete: i mod 2, as dQ(i+1) does not wait for S(i+2)
+  uint64_t done, drain[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -1191,9 +1212,9 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
 // dQ of 128 queries of one q head.
 //   warp 8   TMA: Q and dO once, K (three slots) and V (two) of every kv tile
 //            with an admitted key.
-//   warp 9   MMA: S = Q K^T, dP = dO V^T (queries are TMEM lanes), dQ += dS K
-//            with dS read from TMEM, in the order
-//              S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2) ...
+//   warp 9   MMA: S = Q K^T (queries are TMEM lanes), dQ += dS K with dS read
+//            from TMEM, in the order  S(0) S(1) | dQ(j) S(j+2) ...
+//   warp 10  MMA: dP(j) = dO V^T, as soon as dP(j-1) is in registers.
 //   warps 0-7: one thread per query and half of the keys: dS from S and dP,
 //            stored over S's columns (two S buffers, so that the next tile's
 //            scores are there when this one's are done).
@@ -1229,11 +1250,12 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         mbar_init(smem_u32(&bars.s_full[i]), 1);
         mbar_init(smem_u32(&bars.ds_full[i]), 8);
         mbar_init(smem_u32(&bars.k_done[i]), 1);
+        mbar_init(smem_u32(&bars.v_free[i]), 1);
+        mbar_init(smem_u32(&bars.drain[i]), 1);
       }
       mbar_init(smem_u32(&bars.dp_full), 1);
       mbar_init(smem_u32(&bars.dp_free), 8);
       mbar_init(smem_u32(&bars.done), 1);
-      mbar_init(smem_u32(&bars.drain), 1);
       bars.abort_flag = 0;
       fence_mbar_init();
     }
@@ -1267,11 +1289,9 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       next(0);
       for (; it < n_it; ++it) {
         const int ks = it % C::kKSlots, vs = it % C::kVSlots;
-        // the slots' last readers are dQ(it-3) and dP(it-2); S(1) was issued
-        // after dP(0)
-        if (it == 2 ? !mbar_wait(smem_u32(&bars.s_full[1]), 0, deadline, abort_flag)
-                    : it > 2 && !mbar_wait(smem_u32(&bars.k_done[(it - 3) & 1]), ((it - 3) >> 1) & 1, deadline,
-                                           abort_flag)) {
+        // the slots' last readers are dQ(it-3) and dP(it-2)
+        if ((it >= 2 && !mbar_wait(smem_u32(&bars.v_free[it & 1]), ((it - 2) >> 1) & 1, deadline, abort_flag)) ||
+            (it >= 3 && !mbar_wait(smem_u32(&bars.k_done[(it - 3) & 1]), ((it - 3) >> 1) & 1, deadline, abort_flag))) {
           bwd_timeout(p, abort_flag);
           break;
         }
@@ -1282,7 +1302,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         if (twice && it == n) {
           // do_lo over do_hi once dP(n - 1) is complete (dP(n - 2) is: the
           // waits above; dP(n) waits for this copy)
-          if (!mbar_wait(smem_u32(&bars.dp_full), (n - 1) & 1, deadline, abort_flag)) {
+          if (!mbar_wait(smem_u32(&bars.v_free[(n - 1) & 1]), ((n - 1) >> 1) & 1, deadline, abort_flag)) {
             bwd_timeout(p, abort_flag);
             ++it;
             break;
@@ -1308,25 +1328,21 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     tc_fence_before();
     ready_wait();
     tc_fence_after();
-    const uint32_t tmem = bars.tmem_base, tDP = tmem + 256, tDQ = tmem + 384;
+    const uint32_t tmem = bars.tmem_base, tDQ = tmem + 384;
     if (lane == 0 && n_it > 0) {
-      const uint32_t dq = desc_rows(sQ), ddo = desc_rows(sDO);
-      uint32_t k_r[C::kKSlots], k_c[C::kKSlots], v_r[C::kVSlots];
+      uint32_t k_c[C::kKSlots];
 #pragma unroll
-      for (int i = 0; i < C::kKSlots; ++i) {
-        k_r[i] = desc_rows(sK + i * C::kTileBytes);
-        k_c[i] = desc_cols(sK + i * C::kTileBytes);
-      }
+      for (int i = 0; i < C::kKSlots; ++i) k_c[i] = desc_cols(sK + i * C::kTileBytes);
+      const uint32_t dq = desc_rows(sQ);
+      uint32_t k_r[C::kKSlots];
 #pragma unroll
-      for (int i = 0; i < C::kVSlots; ++i) v_r[i] = desc_rows(sV + i * C::kTileBytes);
+      for (int i = 0; i < C::kKSlots; ++i) k_r[i] = desc_rows(sK + i * C::kTileBytes);
       bool ok = mbar_wait(smem_u32(&bars.q_full), 0, deadline, abort_flag) &&
                 mbar_wait(smem_u32(&bars.full[0]), 0, deadline, abort_flag);
       tc_fence_after();
       if (ok) {
         issue_rows<D>(tmem, dq, k_r[0]);
         mma_commit(smem_u32(&bars.s_full[0]));
-        issue_rows<D>(tDP, ddo, v_r[0]);
-        mma_commit(smem_u32(&bars.dp_full));
         if (n_it > 1) {
           ok = mbar_wait(smem_u32(&bars.full[1]), 0, deadline, abort_flag);
           if (ok) {
@@ -1341,33 +1357,68 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       for (int it0 = 0; ok && it0 < n_it; it0 += kTurn) {
 #pragma unroll
         for (int u = 0; u < kTurn; ++u) {
-          const int it = it0 + u, buf = u & 1, ks = u % C::kKSlots, vs = (u + 1) % C::kVSlots,
-                    ks2 = (u + 2) % C::kKSlots;
+          const int it = it0 + u, buf = u & 1;
           if (!ok || it >= n_it) break;
-          if (it + 1 < n_it) {
-            if (!(ok = mbar_wait(smem_u32(&bars.dp_free), it & 1, deadline, abort_flag))) break;
-            if (twice && it + 1 == n && !(ok = mbar_wait(smem_u32(&bars.lo_full), 0, deadline, abort_flag))) break;
-            tc_fence_after();
-            issue_rows<D>(tDP, ddo, v_r[vs]);
-            mma_commit(smem_u32(&bars.dp_full));
-          }
           if (!(ok = mbar_wait(smem_u32(&bars.ds_full[buf]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
-          issue_cols<D>(tDQ, tmem + 128 * buf, k_c[ks], it > 0);
+          issue_cols<D>(tDQ, tmem + 128 * buf, k_c[u % C::kKSlots], it > 0);
           if (it + 2 < n_it) {
+            const int ks2 = (u + 2) % C::kKSlots;
             if (it + 3 < n_it) mma_commit(smem_u32(&bars.k_done[buf]));
             if (!(ok = mbar_wait(smem_u32(&bars.full[ks2]), ((it + 2) / C::kKSlots) & 1, deadline, abort_flag))) break;
             issue_rows<D>(tmem + 128 * buf, dq, k_r[ks2]);
             mma_commit(smem_u32(&bars.s_full[buf]));
-          } else if (it + 1 == n_it) {
+          } else if (it + 1 == n_it)
             mma_commit(smem_u32(&bars.done));
+        }
+      }
+      if (!ok) bwd_timeout(p, abort_flag);
+      mma_commit(smem_u32(&bars.drain[0]));
+      volatile int never = 0;
+      if (!mbar_wait(smem_u32(&bars.drain[0]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+    }
+  } else if (warp == 10) {
+    tc_fence_before();
+    ready_wait();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base, tDP = tmem + 256;
+    if (lane == 0 && n_it > 0) {
+      const uint32_t ddo = desc_rows(sDO);
+      uint32_t v_r[C::kVSlots];
+#pragma unroll
+      for (int i = 0; i < C::kVSlots; ++i) v_r[i] = desc_rows(sV + i * C::kTileBytes);
+      bool ok = mbar_wait(smem_u32(&bars.q_full), 0, deadline, abort_flag) &&
+                mbar_wait(smem_u32(&bars.full[0]), 0, deadline, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        issue_rows<D>(tDP, ddo, v_r[0]);
+        mma_commit(smem_u32(&bars.dp_full));
+        mma_commit(smem_u32(&bars.v_free[0]));
+      }
+      int slot = 1, turn = 0;  // of tile it + 1
+      for (int it0 = 0; ok && it0 + 1 < n_it; it0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int it = it0 + u;
+          if (!ok || it + 1 >= n_it) break;
+          if (!(ok = mbar_wait(smem_u32(&bars.dp_free), u, deadline, abort_flag) &&
+                     mbar_wait(smem_u32(&bars.full[slot]), turn & 1, deadline, abort_flag)))
+            break;
+          if (twice && it + 1 == n && !(ok = mbar_wait(smem_u32(&bars.lo_full), 0, deadline, abort_flag))) break;
+          tc_fence_after();
+          issue_rows<D>(tDP, ddo, v_r[~u & 1]);
+          mma_commit(smem_u32(&bars.dp_full));
+          mma_commit(smem_u32(&bars.v_free[~u & 1]));
+          if (++slot == C::kKSlots) {
+            slot = 0;
+            ++turn;
           }
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain));
+      mma_commit(smem_u32(&bars.drain[1]));
       volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      if (!mbar_wait(smem_u32(&bars.drain[1]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
     }
   } else {
     tc_fence_before();
