@@ -1230,12 +1230,13 @@ int encode_panel_map(CUtensorMap* m, const void* base, int D, int heads, int64_t
 // measured: a step takes a dK/dV CTA 26 (20 for 64-wide heads) and a dQ CTA 20
 // (15), and what surrounds a CTA's loop 110, with the joining of the sums 205
 // (165).
-// A split takes the longest CTA's time, or where there are more CTAs than SMs
-// the work shared out and half a CTA that ends alone; clusters of four leave a
-// twentieth of the SMs out.  Measured, one call without and with the split it
-// gets: 1 head of 1024 rows 16.5 / 13.6 us, of 4096 rows 46.9 / 32.8; 4 q heads
-// on one kv head, 1024 rows 46.3 / 22.9, 8192 rows 327 / 297; the other side: 2
-// heads of 4096 rows 47.3 unsplit, 57.5 in pairs, 8 heads of 1024 17.0 and 28.9.
+// A split takes the longest CTA's time; where there are more CTAs than SMs, the
+// rounds of the dK/dV CTAs, which come first, or the work shared out and half a
+// CTA that ends alone.  Clusters of four leave a twentieth of the SMs out.
+// Measured, one call without and with the split it gets: 1 head of 1024 rows
+// 15.7 / 13.5 us, of 4096 rows 45.0 / 31.1; 4 q heads on one kv head, 1024 rows
+// 44.8 / 21.9, 8192 rows 320 / 279; the other side: 2 heads of 4096 rows 45.8
+// unsplit, 53.2 in pairs, 8 heads of 1024 rows 16.6 and 27.7.
 int pick_parts(int D, int64_t kv_units, int64_t kv_steps, int64_t q_units, int64_t q_steps, bool twice, int sms) {
   const int64_t kv = kv_steps * (D == 128 ? 26 : 20), q = q_steps * (D == 128 ? 20 : 15);
   int best = 1;
@@ -1247,7 +1248,9 @@ int pick_parts(int D, int64_t kv_units, int64_t kv_steps, int64_t q_units, int64
     if ((kv_units + q_units) * s > n) {
       const int64_t all = (kv_units * (kv + s * around) + q_units * (q + s * around)) / n;
       const int64_t shared = all + (kv_cta < q_cta ? kv_cta : q_cta) / 2;
+      const int64_t rounds = (kv_units * s + n - 1) / n * kv_cta;
       if (shared > time) time = shared;
+      if (rounds > time) time = rounds;
     }
     if (s == 1 || time * 20 < least * 19) {  // (for less than a twentieth: as it was)
       best = s;
