@@ -46,6 +46,11 @@ def test_binding_refuses_before_any_call():
             call(q, k, k, q, lse, q, q, k, k)
         with pytest.raises(ValueError):
             call(q, k, k, q, None, q, q, k, k)
+        for bad in ([1], q[0]):  # neither is a mask or ranges on a GPU
+            with pytest.raises(ValueError):
+                call(q, k, k, q, lse, q, q, k, k, key_mask=bad)
+            with pytest.raises(ValueError):
+                call(q, k, k, q, lse, q, q, k, k, key_ranges=bad)
     with pytest.raises(ValueError):
         p.norm_rope(q, k, q, k)
     with pytest.raises(ValueError):

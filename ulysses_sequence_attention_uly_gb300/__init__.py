@@ -574,13 +574,16 @@ class Plan:
         pm = pr = None
         n_ranges = 0
         if key_ranges is not None:
+            if not isinstance(key_ranges, torch.Tensor):
+                raise ValueError("key_ranges: expected a CUDA tensor on device %d" % dev)
             n_ranges = key_ranges.shape[1] if key_ranges.dim() == 3 else 0
             if n_ranges < 1:
                 _want_mask(None, key_ranges, self.B, 0, dev)
             pr = _checked_ptr(key_ranges, (self.B, n_ranges, 2), torch.int32, "key_ranges", dev)
         if key_mask is not None:
             pm = _checked_ptr(key_mask, (self.B, self._nk()),
-                              torch.bool if key_mask.dtype is torch.bool else torch.uint8, "key_mask", dev)
+                              torch.bool if getattr(key_mask, "dtype", None) is torch.bool else torch.uint8,
+                              "key_mask", dev)
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
         nbytes = self.__dict__.get("_bwd_bytes")
