@@ -193,19 +193,22 @@ __device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t blo,
     mma_ts(d, a + 64 * (k >> 2) + 8 * (k & 3), blo + k * 128, C::kIdescO, acc || k > 0);
 }
 
-// Zero the rows of a 128-row tile whose bit in `live` is clear (one warp's
-// share: rows [row0, row0 + 16), four of them at a time).
+// Zero the rows of a 128-row tile whose bit in `live` is clear: one warp's
+// share, rows [row0, row0 + 16) (four of them at a time), bits 0..15.
 template <int D>
-__device__ __forceinline__ void zero_dead_rows(uint32_t tile, const uint4 live, int row0, int lane) {
-  const uint32_t w = bits_word(live, row0 >> 5) >> (row0 & 31);
+__device__ __forceinline__ void zero_dead_rows(uint32_t tile, uint32_t live, int row0, int lane) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = 4 * k + (lane >> 3);
-    if (!((w >> r) & 1u))
+    if (!((live >> r) & 1u))
 #pragma unroll
       for (int pn = 0; pn < BCfg<D>::kPanels; ++pn)
         st_shared_v4(tile + pn * BCfg<D>::kPanelBytes + (row0 + r) * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
   }
+}
+// that share of warp `warp`, from the two words of its half of the tile's bits
+__device__ __forceinline__ uint32_t warp_rows(const uint2 half, int warp) {
+  return ((warp & 2 ? half.y : half.x) >> (16 * (warp & 1))) & 0xFFFFu;
 }
 
 // A 128 x D f32 accumulator in TMEM -> bf16 rows in the shared-memory buffer
@@ -677,6 +680,7 @@ struct KvBars {
   uint64_t s_full[2];         // S(i) in region i mod 2
   uint64_t s_go;              // phase i: S(i) read out of TMEM (8 warps); dO(i), -delta (and V) landed
   uint64_t dp_full;           // phase i: dP(i) in region i mod 2
+  uint64_t dp_issued;         // phase i: dP(i) issued
   uint64_t ds_full[2];        // dS(i) stored (8 warps): i mod 2, as dP(i+1) does not wait for dK(i)
   uint64_t p_go[2];           // P(i) stored (8 warps), Q(i+2) landed: i mod 2, since a warp may store
                               // P(i+1) before Q(i+2) is there
@@ -710,15 +714,17 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
   const uint32_t off = (static_cast<uint32_t>(q4 * 32) << 16) + 64 * wg;
   const uint64_t mul = f2(p.scale_log2, p.scale_log2);
   const bool self = p.masked_rows == ULY_ROWS_SELF, zero_rows = p.masked_rows == ULY_ROWS_ZERO;
-  uint4 live = make_uint4(~0u, ~0u, ~0u, ~0u), live_next = live;
+  uint2 live_next = make_uint2(0u, 0u);
   // The queries' own tokens, a tile ahead of their use.  The q runs are kv runs
   // of the same tokens, in order, so their kv tiles follow one another.
-  const uint4* own = p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles +
-                     (MODE == 2 && p.qseg[0].kv_seg >= 0 ? p.kseg[p.qseg[0].kv_seg].first : 0);
+  const uint2* own = reinterpret_cast<const uint2*>(
+                         p.tile_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles +
+                         (MODE == 2 && p.qseg[0].kv_seg >= 0 ? p.kseg[p.qseg[0].kv_seg].first : 0)) +
+                     wg;  // (the warp's half of a tile's bits)
   const int rep_tile = p.qseg[p.rep_qseg].first;  // (the replicated run's once more, with do_lo)
   int own_tile = k.first_tile;
   const auto next_live = [&] {
-    live_next = __ldg(own + (own_tile < p.n_q_tiles ? own_tile : rep_tile + own_tile - p.n_q_tiles));
+    live_next = __ldg(own + 2 * (own_tile < p.n_q_tiles ? own_tile : rep_tile + own_tile - p.n_q_tiles));
     if (++own_tile == p.n_q_tiles + p.n_lo) own_tile = 0;
   };
   if (MODE == 2) next_live();
@@ -727,15 +733,16 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     const uint32_t mR = k.tmem + off + 128 * (it & 1);
     const uint32_t nl_addr = k.sNl + qslot * C::kStatBytes + 64 * wg * 4;
     const uint32_t dl_addr = k.sDl + (it & 1) * C::kStatBytes + 64 * wg * 4;
-    uint32_t u0 = 0u, u1 = 0u;
+    uint32_t u0 = 0u, u1 = 0u, rows = 0xFFFFu;
     if (MODE == 2) {
-      live = live_next;
+      const uint2 live = live_next;
+      rows = warp_rows(live, warp);
       if (it + 1 < k.n_it) next_live();
       // queries that attend to the thread's key: those whose own token is
       // admitted (ULY_ROWS_ZERO), those of the key's own kind (ULY_ROWS_SELF;
       // past the run's end the statistics exclude)
-      u0 = bits_word(live, 2 * wg);
-      u1 = bits_word(live, 2 * wg + 1);
+      u0 = live.x;
+      u1 = live.y;
       if (self && !key_ok) {
         u0 = ~u0;
         u1 = ~u1;
@@ -764,12 +771,12 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     uint32_t a[2][32], pk[32];
     tmem_ld32(mR, a[0]);
     tmem_ld32(mR + 32, a[1]);
-    if (MODE == 2 && zero_rows && !bits_full(live)) {
+    if (MODE == 2 && zero_rows && rows != 0xFFFFu) {
       // queries that take part in nothing may hold anything: their rows of Q
       // and dO are zeroed before the sums over queries read them (S and dP
       // have read them)
-      zero_dead_rows<D>(k.sQ + qslot * C::kTileBytes, live, 16 * warp, lane);
-      zero_dead_rows<D>(k.sDO + (it & 1) * C::kTileBytes, live, 16 * warp, lane);
+      zero_dead_rows<D>(k.sQ + qslot * C::kTileBytes, rows, 16 * warp, lane);
+      zero_dead_rows<D>(k.sDO + (it & 1) * C::kTileBytes, rows, 16 * warp, lane);
       fence_proxy_async_smem();
     }
     tmem_wait_ld();
@@ -815,7 +822,9 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
 //   warp 9   MMA: S = K Q^T (keys are TMEM lanes), dK += dS Q and dV += P do
 //            with dS and P read from TMEM, in the order
 //              S(0) S(1) | dK(i) dV(i) S(i+2) ...
-//   warp 10  MMA: dP(i) = V dO^T, as soon as S(i) is in registers.
+//   warp 10  MMA: dP(i) = V dO^T, as soon as S(i) is in registers.  Where the
+//            tile has masks, so that the elementwise work is what everything
+//            waits for, dV(i - 1) and S(i + 1) come after it.
 //   warps 0-7: P from S, dS from dP.
 // Two query tiles are under way in two TMEM regions of 128 columns.  A region
 // holds in turn a tile's S, then (once S is in registers) its dP, then (once dP
@@ -860,6 +869,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       mbar_init(smem_u32(&bars.s_full[1]), 1);
       mbar_init(smem_u32(&bars.s_go), 9);
       mbar_init(smem_u32(&bars.dp_full), 1);
+      mbar_init(smem_u32(&bars.dp_issued), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&bars.ds_full[i]), 8);
         mbar_init(smem_u32(&bars.p_go[i]), 9);
@@ -993,6 +1003,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       for (int i = 0; i < C::kQSlots; ++i) q_c[i] = desc_cols(sQ + i * C::kTileBytes);
 #pragma unroll
       for (int i = 0; i < C::kOSlots; ++i) o_c[i] = desc_cols(sDO + i * C::kTileBytes);
+      const bool ordered = OWN || run.len - row0 < kTileRows || !bits_full(bits);
       const uint32_t dk = desc_rows(sK);
       uint32_t q_r[C::kQSlots];
 #pragma unroll
@@ -1022,6 +1033,9 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
           if (!(ok = mbar_wait(smem_u32(&bars.ds_full[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_cols<D>(tDK, tR, q_c[u % C::kQSlots], it > 0);
+          // (measured, 12 heads on 4 of 2304 rows: by the queries' own masks 99 us
+          // without this order and 89 with it, no masks 80 and 83)
+          if (ordered && it + 1 < n_it && !(ok = mbar_wait(smem_u32(&bars.dp_issued), ~u & 1, deadline, abort_flag))) break;
           if (!(ok = mbar_wait(smem_u32(&bars.p_go[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_cols<D>(tDV, tR + 32, o_c[u % C::kOSlots], it > 0);
@@ -1053,6 +1067,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
       tc_fence_after();
       if (ok) {
         issue_rows<D>(tmem, dv, o_r[0]);
+        mbar_arrive(smem_u32(&bars.dp_issued));
         mma_commit(smem_u32(&bars.dp_full));
       }
       for (int it0 = 0; ok && it0 + 1 < n_it; it0 += 2) {
@@ -1063,6 +1078,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
           if (!(ok = mbar_wait(smem_u32(&bars.s_go), ~u & 1, deadline, abort_flag))) break;
           tc_fence_after();
           issue_rows<D>(tmem + 128 * (~u & 1), dv, o_r[~u & 1]);
+          mbar_arrive(smem_u32(&bars.dp_issued));
           mma_commit(smem_u32(&bars.dp_full));
         }
       }
@@ -1160,20 +1176,21 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const uint32_t mDP = k.tmem + 256 + lane_off + 64 * wg;
   const uint64_t mul = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), dl2 = f2(dl, dl);
-  const uint4* tile_bits = p.active_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles;
+  const uint2* tile_bits = reinterpret_cast<const uint2*>(p.active_bits + static_cast<int64_t>(k.b) * p.n_kv_tiles) + wg;
+  const uint2* half_bits = reinterpret_cast<const uint2*>(row_bits) + wg;
   const bool zero_keys = p.masked_rows != ULY_ROWS_SELF;
-  uint4 bits_next = make_uint4(0u, 0u, 0u, 0u), keys_next = bits_next;
+  uint2 bits_next = make_uint2(0u, 0u), keys_next = bits_next;
   if (MASKED && it0 < it1) {
-    bits_next = __ldg(row_bits + listed(p, k.j_lo + it0, k.n_full));
-    keys_next = __ldg(tile_bits + listed(p, k.j_lo + it0, k.n_full));
+    bits_next = __ldg(half_bits + 2 * listed(p, k.j_lo + it0, k.n_full));
+    keys_next = __ldg(tile_bits + 2 * listed(p, k.j_lo + it0, k.n_full));
   }
   for (int j = it0; j < it1; ++j) {
     const int it = base + j, buf = it & 1;
     const uint32_t mS = k.tmem + lane_off + 128 * buf + 64 * wg;
-    const uint4 bits = bits_next, keys = keys_next;
+    const uint2 bits = bits_next, keys = keys_next;
     if (MASKED && j + 1 < it1) {
-      bits_next = __ldg(row_bits + listed(p, k.j_lo + j + 1, k.n_full));
-      keys_next = __ldg(tile_bits + listed(p, k.j_lo + j + 1, k.n_full));
+      bits_next = __ldg(half_bits + 2 * listed(p, k.j_lo + j + 1, k.n_full));
+      keys_next = __ldg(tile_bits + 2 * listed(p, k.j_lo + j + 1, k.n_full));
     }
     bool ok = ew_wait(smem_u32(&bars.s_full[buf]), (it >> 1) & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -1193,12 +1210,12 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
     if (lane == 0) mbar_arrive(smem_u32(&bars.dp_free));
     half_row_ds<false>(a, dl2, 0, pr, pk);
     if (MASKED)
-      mask_pairs(pk, pair_bits(dead ? 0u : bits_word(bits, 2 * wg)), pair_bits(dead ? 0u : bits_word(bits, 2 * wg + 1)));
+      mask_pairs(pk, pair_bits(dead ? 0u : bits.x), pair_bits(dead ? 0u : bits.y));
     tmem_st32(mS, pk);
     if (MASKED && zero_keys) {
       // keys that are not admitted may hold anything: their rows of K are
       // zeroed before the sum over keys reads them (S has read them)
-      zero_dead_rows<D>(k.sK + (it % C::kKSlots) * C::kTileBytes, keys, 16 * warp, lane);
+      zero_dead_rows<D>(k.sK + (it % C::kKSlots) * C::kTileBytes, warp_rows(keys, warp), 16 * warp, lane);
       fence_proxy_async_smem();
     }
     tmem_wait_st();
