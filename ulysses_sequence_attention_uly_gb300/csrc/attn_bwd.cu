@@ -21,6 +21,14 @@
 // memory, whose order changes the bits; the price of the two is 7/5 of the
 // tensor work.
 //
+// Bound by the tensor cores where loops are long and D is 128 (8 heads of 8192
+// rows: 537 us, 1792 TFLOP/s of the seven products, 94% of 1912 measured with
+// one large matrix product; larger calls run into the power limit: 40 heads of
+// 27792 rows 31.4 ms, 1745 TFLOP/s, which is what a matrix product sustains).
+// With 64-wide heads, or masks, by the elementwise work and the issue of MMAs:
+// 408 us, 1180 TFLOP/s.  Short loops, by what surrounds them: about 5.5 us a
+// CTA, of which 2.5 pass before its first scores are there.
+//
 // Rounding: P and dS are rounded to bf16, since they are operands of bf16 MMAs;
 // dS is formed from the f32 P, every sum is f32, the outputs are rounded once.
 // Replicated rows of the fused call, whose do is the sum over the shards: that
@@ -470,9 +478,11 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
 // whose exponential is 0.  Fused, replicated rows: do is the sum of every
 // shard's copy, since each received the output, written as two bf16 operands
 // (do_hi, do_lo) with a delta each.
-// Bound by memory: o and do are read once.  16 rows x 8 heads a CTA; 16 (D =
-// 128) or 8 lanes share a row, the results go through shared memory so that
-// they are written along rows.
+// Bound by memory: o and do are read once (40 heads of 27792 rows of 128, 616
+// MB with the summed rows: 121 us, 5.1 TB/s; small calls 6 to 10 us, the
+// longest of its dependent steps).  16 rows x 8 heads a CTA; 16 (D = 128) or 8
+// lanes share a row, the results go through shared memory so that they are
+// written along rows.
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ BwdParams p) {
   constexpr int kLanes = D / 8, kUnits = kPrepThreads / kLanes, kRows = kPrepRows, kHeads = 8;
@@ -1235,6 +1245,8 @@ __device__ __forceinline__ bool q_loop(const BwdParams& p, const QWork& k, int w
 //   warps 0-7: one thread per query and half of the keys: dS from S and dP,
 //            stored over S's columns (two S buffers, so that the next tile's
 //            scores are there when this one's are done).
+// A step takes about 1900 cycles at D = 128 (1536 of them on the tensor core;
+// dK/dV 2450 of 2048), 1350 with 64-wide heads.
 // TMEM: S0 [0,128) S1 [128,256) dP [256,384) dQ [384,384+D).
 template <int D, bool SPLIT>
 __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, int t, int h, int b, int part) {
@@ -1497,7 +1509,8 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
 }
 
 // One launch for both kinds of CTA: they need nothing from each other, so that
-// dQ's fill the SMs that the last ones of dK and dV leave idle.
+// dQ's fill the SMs that the last ones of dK and dV leave idle (8 heads of 8192
+// rows: 649 us in two launches, 580 in one).
 template <int D, bool OWN, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const __grid_constant__ BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
