@@ -134,6 +134,51 @@ def test_few_tiles(c):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("c", [R.Case("rounds", 2, (900,), 0, "none", 24, 8, 64, rows="zero", mask="random"),
+                               R.Case("rounds-text", 1, (800, 801), 150, "prefix", 16, 16, 128, mask="ranges")], ids=ids)
+def test_more_ctas_than_sms(c):
+    d = R.inputs(c, 22)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    g = run_fused(c, plan, d, ref)
+    assert plan.sync_status() == 0
+    for n, x in zip(("dq", "dk", "dv"), g):
+        R.check(x, ref[n], ref["e_" + n], n)
+
+
+def test_few_tiles_at_once_and_in_graphs():
+    """Calls whose CTAs work in clusters, several under way at once on streams of
+    their own and replayed from graphs: the bits of a call alone."""
+    import torch
+    live = []
+    for i, c in enumerate((SPLIT[0], SPLIT[3], SPLIT[5], SPLIT[9])):
+        d = R.inputs(c, 30 + i)
+        ref = R.reference(c, d)
+        plan = R.plan_of(c)
+        want = run_fused(c, plan, d, ref)
+        torch.cuda.synchronize()
+        s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        ws = torch.empty(plan.attention_backward_workspace(), dtype=torch.uint8, device="cuda")
+        got = [outputs(d[n]) for n in "qkv"]
+        with torch.cuda.graph(graph, stream=s):
+            plan.sp_attention_backward(d["q"], d["k"], d["v"], ref["o"], ref["lse"], d["do"], *got, scale=ref["scale"],
+                                       workspace=ws, **mask_args(c, d["mask"], "mask"))
+        live.append((c, plan, d, ref, want, s, graph, got, torch.cuda.Stream()))
+    eager = []
+    for _ in range(4):
+        for c, plan, d, ref, want, s, graph, got, s2 in live:
+            with torch.cuda.stream(s):
+                graph.replay()
+            with torch.cuda.stream(s2):
+                eager.append((want, run_fused(c, plan, d, ref)))
+    torch.cuda.synchronize()
+    for c, plan, *_ in live:
+        assert plan.sync_status() == 0
+    for want, got in eager + [(x[4], x[7]) for x in live]:
+        for x, y in zip(sum(want, []), sum(got, [])):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
 @pytest.mark.parametrize("c", [CASES[6], CASES[13]], ids=ids)
 def test_against_differences(c):
     """<gradient, direction> against the difference quotient of <o, do> in 64
@@ -341,6 +386,29 @@ def test_withheld_load_times_out():
     plan.test_withhold_fill(2)
     run_fused(c, plan, d, ref)
     assert plan.sync_status() == uly.ULY_ERR_TIMEOUT
+    plan.test_withhold_fill(-1)
+    plan.set_wait_limit(4_000_000_000)
+    g = run_fused(c, plan, d, ref)
+    torch.cuda.synchronize()
+    assert plan.sync_status() == 0
+    for n, x in zip(("dq", "dk", "dv"), g):
+        R.check(x, ref[n], ref["e_" + n], n)
+
+
+def test_withheld_load_of_unsplit_tiles_times_out():
+    """The same where every tile has a CTA of its own, with masks by the queries'
+    own tokens and replicated rows."""
+    import torch
+    import ulysses_sequence_attention_uly_gb300 as uly
+    c = R.Case("withheld", 2, (500, 431), 140, "suffix", 16, 8, 64, rows="zero", mask="random")
+    d = R.inputs(c, 14)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    for fill in (0, 1, 3):
+        plan.set_wait_limit(20_000_000)
+        plan.test_withhold_fill(fill)
+        run_fused(c, plan, d, ref)
+        assert plan.sync_status() == uly.ULY_ERR_TIMEOUT
     plan.test_withhold_fill(-1)
     plan.set_wait_limit(4_000_000_000)
     g = run_fused(c, plan, d, ref)
