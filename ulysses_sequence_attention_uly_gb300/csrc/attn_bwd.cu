@@ -399,7 +399,6 @@ __device__ __forceinline__ int64_t lo_at(const BwdParams& p, int b, int h, int i
 }
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepRows = 16;  // rows of a CTA of prep_kernel
 
 // The kv tile tables of batch b: the admitted keys of every tile, and the list
 // of tiles that a query attends to: those whose 128 keys are all admitted from
@@ -415,10 +414,18 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(b) * p.n_kv_tiles;
   int n_full = 0, n_part = 0;
+  // the run of the warp's tile, and the keys before it
+  int s = 0, seg_first = 0, seg_len = p.kseg[0].len, seg_end = p.n_kseg > 1 ? p.kseg[1].first : p.n_kv_tiles, key_base = 0;
   for (int t0 = 0; t0 < p.n_kv_tiles; t0 += kPrepThreads) {
     for (int k = warp; k < kPrepThreads && t0 + k < p.n_kv_tiles; k += kPrepThreads / 32) {
-      const int s = seg_of(p.kseg, p.n_kseg, t0 + k), i = t0 + k - p.kseg[s].first;
-      const int key0 = first_key(p, s) + i * kTileRows, n_in = min(kTileRows, p.kseg[s].len - i * kTileRows);
+      while (t0 + k >= seg_end) {
+        key_base += seg_len;
+        ++s;
+        seg_first = p.kseg[s].first;
+        seg_len = p.kseg[s].len;
+        seg_end = s + 1 < p.n_kseg ? p.kseg[s + 1].first : p.n_kv_tiles;
+      }
+      const int i = t0 + k - seg_first, key0 = key_base + i * kTileRows, n_in = min(kTileRows, seg_len - i * kTileRows);
       uint32_t w[4], in[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -478,14 +485,14 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
 // whose exponential is 0.  Fused, replicated rows: do is the sum of every
 // shard's copy, since each received the output, written as two bf16 operands
 // (do_hi, do_lo) with a delta each.
-// Bound by memory: o and do are read once (40 heads of 27792 rows of 128, 616
-// MB with the summed rows: 121 us, 5.1 TB/s; small calls 6 to 10 us, the
-// longest of its dependent steps).  16 rows x 8 heads a CTA; 16 (D = 128) or 8
-// lanes share a row, the results go through shared memory so that they are
-// written along rows.
-template <int D>
+// Bound by memory: o and do are read once (40 heads of 29328 rows of 128, 616
+// MB with the summed rows: 114 us, 5.4 TB/s; small calls 4 to 8 us, the longest
+// of its dependent steps).  ROWS rows x 8 heads a CTA; 16 (D = 128) or 8 lanes
+// share a row, the results go through shared memory so that they are written
+// along rows.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ BwdParams p) {
-  constexpr int kLanes = D / 8, kUnits = kPrepThreads / kLanes, kRows = kPrepRows, kHeads = 8;
+  constexpr int kLanes = D / 8, kUnits = kPrepThreads / kLanes, kRows = ROWS, kHeads = 8;
   constexpr int kParts = kTileRows / kRows;
   __shared__ union {
     TableSmem table;
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
   const int row0 = (t - run.first) * kTileRows + r_lo;  // first row inside the run
   const int lane = threadIdx.x % kLanes, unit = threadIdx.x / kLanes;
   const bool rep = p.fused && run.out_shard < 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = unit; i < kRows * kHeads; i += kUnits) {
     const int r = i / kHeads, hh = i % kHeads, h = h0 + hh;
     float sum = 0.f, sum_lo = 0.f;
@@ -1582,8 +1589,14 @@ cudaError_t launch_main(const BwdParams& p, unsigned grid, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch(const BwdParams& p, cudaStream_t s) {
-  const unsigned prep = p.B + static_cast<unsigned>(p.n_q_tiles) * (kTileRows / kPrepRows) * ((p.Hq + 7) / 8) * p.B;
-  prep_kernel<D><<<prep, kPrepThreads, 0, s>>>(p);
+  // 16 rows a CTA of the preparation, 8 where an SM would get less than two of
+  // these (8 heads of 2048 rows: 6.3 us with 16, 4.6 with 8; 40 heads of 29328
+  // rows 114 and 123)
+  const unsigned prep = static_cast<unsigned>(p.n_q_tiles) * ((p.Hq + 7) / 8) * p.B, n16 = prep * (kTileRows / 16);
+  if (n16 < 2u * static_cast<unsigned>(p.sms))
+    prep_kernel<D, 8><<<p.B + prep * (kTileRows / 8), kPrepThreads, 0, s>>>(p);
+  else
+    prep_kernel<D, 16><<<p.B + n16, kPrepThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid = p.n_kv_ctas + static_cast<unsigned>(p.n_q_tiles) * p.Hq * p.B;

@@ -49,6 +49,7 @@ struct BwdParams {
   float* dl_lo;                   // [B][Hq][n_lo * 128]: -delta of do_lo
   int32_t n_lo;                   // tiles of the replicated run that do_lo adds (0: no replicated q rows, or one shard)
   int32_t rep_qseg;               // its index in qseg
+  int32_t sms;                    // SMs of the device
   int32_t parts;                  // CTAs that share a tile's loop (a cluster): 1, 2 or 4
   int32_t masked_rows;
   int32_t withhold_fill;

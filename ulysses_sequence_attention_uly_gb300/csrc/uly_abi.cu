@@ -1383,6 +1383,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.n_ranges = key_ranges ? n_ranges : 0;
   p.Nk = static_cast<int32_t>(pl->nk);
   p.n_kv_ctas = static_cast<uint32_t>(kv_ctas);
+  p.sms = pl->sm_count;
   p.parts = pick_parts(d.D, kv_ctas, static_cast<int64_t>(p.G) * (q_tiles + p.n_lo),
                        (q_tiles + p.n_lo) * d.Hq * d.B, p.n_kv_tiles, p.n_lo > 0, pl->sm_count);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
