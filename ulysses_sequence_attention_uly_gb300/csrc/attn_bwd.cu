@@ -72,6 +72,12 @@ struct BCfg {
   // have.
   // dK, dV: K, V, three Q and two dO slots with their row statistics, barriers
   static constexpr int kQSlots = 3, kOSlots = 2;
+  // dK, dV: a tile's P has columns of TMEM to itself, which 64-wide heads leave
+  // free, and is stored while dP is computed (8 heads of 8192 rows 413 -> 406
+  // us, 12 on 4 of 2300 rows 69.8 -> 65.9); not where the queries' own tokens
+  // mask (78.6 -> 81.9: it takes registers that the masks need)
+  template <bool OWN>
+  static constexpr bool kOwnP = D == 64 && !OWN;
   static constexpr int kStatBytes = kTileRows * 4;         // -lse log2(e) or -delta of a tile's rows
   static constexpr int kKvBars = (2 + kQSlots + kOSlots) * kTileBytes + (kQSlots + kOSlots) * kStatBytes;
   // dQ: Q, dO, three K and two V slots, barriers
@@ -190,15 +196,15 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint32_t alo, uint32_t bl
 }
 
 // D[tmem] (+)= A B with A a 128 x 128 bf16 matrix in TMEM (entries 0..63 of a
-// row in the columns [a, a + 32), 64..127 in [a + 64, a + 96)) and B a
+// row in the columns [a, a + 32), 64..127 in [a + HALF, a + HALF + 32)) and B a
 // 128-row tile in shared memory (MN-major; the sum runs over the rows); blo
 // from desc_cols
-template <int D>
+template <int D, int HALF = 64>
 __device__ __forceinline__ void issue_cols(uint32_t d, uint32_t a, uint32_t blo, bool acc) {
   using C = BCfg<D>;
 #pragma unroll
   for (int k = 0; k < C::kRowSteps; ++k)
-    mma_ts(d, a + 64 * (k >> 2) + 8 * (k & 3), blo + k * 128, C::kIdescO, acc || k > 0);
+    mma_ts(d, a + HALF * (k >> 2) + 8 * (k & 3), blo + k * 128, C::kIdescO, acc || k > 0);
 }
 
 // Zero the rows of a 128-row tile whose bit in `live` is clear: one warp's
@@ -781,6 +787,12 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
       if (lane == 0) mbar_arrive(smem_u32(&bars.s_go));
     };
     half_row_p<true>(mR, mul, 0, nl_addr, pr, s_loaded);
+    constexpr bool kOwnP = C::template kOwnP<MODE == 2>;
+    const uint32_t mP = kOwnP ? k.tmem + 384 + (static_cast<uint32_t>(q4 * 32) << 16) + 64 * (it & 1) + 32 * wg : mR + 32;
+    if (kOwnP) {
+      store_p<MODE != 0, 0>(mP, pr, u0);
+      store_p<MODE != 0, 1>(mP, pr, u1);
+    }
     ok = ew_wait(smem_u32(&bars.s_go), it & 1, k.deadline, abort_flag) &
          ew_wait(smem_u32(&bars.dp_full), it & 1, k.deadline, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -809,16 +821,13 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[it & 1]));
-    if (MODE == 0) {
-      store_p<false, 0>(mR + 32, pr, 0u);
-      store_p<false, 1>(mR + 32, pr, 0u);
-    } else {
-      store_p<true, 0>(mR + 32, pr, u0);
-      store_p<true, 1>(mR + 32, pr, u1);
+    if (!kOwnP) {
+      store_p<MODE != 0, 0>(mP, pr, u0);
+      store_p<MODE != 0, 1>(mP, pr, u1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
     }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.p_go[it & 1]));
     if (++qslot == C::kQSlots) {
       qslot = 0;
@@ -854,7 +863,8 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
 // of a tile is one more arrival on a barrier that its first reader waits for
 // anyway.  Slots: Q(i) over Q(i-3) once dV(i-3), issued after dK(i-3), is
 // complete; dO(i) over dO(i-2) once dV(i-2) is.
-// TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D).
+// TMEM: regions [0,128) [128,256), dV [256,256+D), dK [256+D,256+2D); 64-wide
+// heads: P of the two tiles [384,448) [448,512).
 template <int D, bool OWN, bool SPLIT>
 __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, int t, int hk, int b, int part) {
   using C = BCfg<D>;
@@ -1055,7 +1065,10 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
           if (ordered && it + 1 < n_it && !(ok = mbar_wait(smem_u32(&bars.dp_issued), ~u & 1, deadline, abort_flag))) break;
           if (!(ok = mbar_wait(smem_u32(&bars.p_go[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
-          issue_cols<D>(tDV, tR + 32, o_c[u % C::kOSlots], it > 0);
+          if constexpr (C::template kOwnP<OWN>)
+            issue_cols<D, 32>(tDV, tmem + 384 + 64 * (u & 1), o_c[u % C::kOSlots], it > 0);
+          else
+            issue_cols<D>(tDV, tR + 32, o_c[u % C::kOSlots], it > 0);
           if (it + 2 < n_it) {
             mma_commit(smem_u32(&bars.v_done[u & 1]));
             issue_rows<D>(tR, dk, q_r[(u + 2) % C::kQSlots]);
