@@ -26,7 +26,7 @@
 // one large matrix product; larger calls run into the power limit: 40 heads of
 // 27792 rows 31.4 ms, 1745 TFLOP/s, which is what a matrix product sustains).
 // With 64-wide heads, or masks, by the elementwise work and the issue of MMAs:
-// 408 us, 1180 TFLOP/s.  Short loops, by what surrounds them: about 5.5 us a
+// 406 us, 1185 TFLOP/s.  Short loops, by what surrounds them: about 5.5 us a
 // CTA, of which 2.5 pass before its first scores are there.
 //
 // Rounding: P and dS are rounded to bf16, since they are operands of bf16 MMAs;
