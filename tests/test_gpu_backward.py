@@ -146,6 +146,25 @@ def test_more_ctas_than_sms(c):
         R.check(x, ref[n], ref["e_" + n], n)
 
 
+@pytest.mark.parametrize("mode", ["prefix", "kv_prefix"])
+def test_conventions_are_one_without_a_mask(mode):
+    """No mask, no masked row: every convention gives the same bits, right ones."""
+    import torch
+    got = []
+    for rows in ("sdpa", "zero", "self"):
+        c = R.Case("no-mask", 1, (300, 211), 140, mode, 4, 2, 64, rows=rows)
+        d = R.inputs(c, 24)
+        ref = R.reference(c, d)
+        plan = R.plan_of(c)
+        got.append(sum(run_fused(c, plan, d, ref), []))
+        assert plan.sync_status() == 0
+        for n, x in zip(("dq", "dk", "dv"), (got[-1][:2], got[-1][2:4], got[-1][4:])):
+            R.check(x, ref[n], ref["e_" + n], n)
+    for other in got[1:]:
+        for x, y in zip(got[0], other):
+            assert torch.equal(x, y)
+
+
 def test_few_tiles_at_once_and_in_graphs():
     """Calls whose CTAs work in clusters, several under way at once on streams of
     their own and replayed from graphs: the bits of a call alone."""

@@ -157,9 +157,8 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, ui
 
 // Shared-memory descriptors (128-byte swizzle; tc.cuh): the upper word is the
 // same for every operand here, the lower one is the start address / 16 and the
-// leading byte offset.  One thread issues every MMA, and what it does between
-// two of them delays the tensor core, so the lower words are a base and a
-// constant.
+// leading byte offset.  What an issuing thread does between two MMAs delays the
+// tensor core, so the lower words are a base and a constant.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_cols(uint32_t addr) {
@@ -288,7 +287,11 @@ __device__ __forceinline__ void store_rows(const BwdParams& p, uint8_t* const* o
 // Where there are too few tiles for the SMs, a tile's loop is shared by the
 // CTAs of a cluster, a part of the iterations each.  Each leaves its f32 sums
 // in its shared memory, and each adds up a share of the rows of all of them in
-// the order of the CTAs: the same bits on every call.
+// the order of the CTAs: the same bits on every call.  A read of another CTA's
+// shared memory takes hundreds of cycles, so eight of a lane's are under way,
+// along the rows.  All of it, the launch in clusters included, costs a call 3
+// to 5 us (128-wide heads; reads of two pieces in turn 2 us more, writes to the
+// CTA that adds up 4 more).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -358,7 +361,8 @@ __device__ __forceinline__ void join_rows(const BwdParams& p, uint8_t* const* ou
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
         const int i = i0 + (s >> log) * kBwdThreads;
-        if (s & (p.parts - 1)) u[s] = make_float4(u[s - 1].x + u[s].x, u[s - 1].y + u[s].y, u[s - 1].z + u[s].z, u[s - 1].w + u[s].w);
+        if (s & (p.parts - 1))
+          u[s] = make_float4(u[s - 1].x + u[s].x, u[s - 1].y + u[s].y, u[s - 1].z + u[s].z, u[s - 1].w + u[s].w);
         if ((s & (p.parts - 1)) == p.parts - 1 && i < n) {
           const uint2 w = make_uint2(pack_bf16x2(u[s].x * mul, u[s].y * mul), pack_bf16x2(u[s].z * mul, u[s].w * mul));
           *reinterpret_cast<uint2*>(dst + i / kPieces * row_stride + i % kPieces * 8) = zero ? make_uint2(0u, 0u) : w;
@@ -421,7 +425,8 @@ __device__ __forceinline__ void build_tables(const BwdParams& p, int b, TableSme
   const int64_t row = static_cast<int64_t>(b) * p.n_kv_tiles;
   int n_full = 0, n_part = 0;
   // the run of the warp's tile, and the keys before it
-  int s = 0, seg_first = 0, seg_len = p.kseg[0].len, seg_end = p.n_kseg > 1 ? p.kseg[1].first : p.n_kv_tiles, key_base = 0;
+  int s = 0, seg_first = 0, seg_len = p.kseg[0].len, key_base = 0;
+  int seg_end = p.n_kseg > 1 ? p.kseg[1].first : p.n_kv_tiles;
   for (int t0 = 0; t0 < p.n_kv_tiles; t0 += kPrepThreads) {
     for (int k = warp; k < kPrepThreads && t0 + k < p.n_kv_tiles; k += kPrepThreads / 32) {
       while (t0 + k >= seg_end) {
@@ -788,7 +793,8 @@ __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int
     };
     half_row_p<true>(mR, mul, 0, nl_addr, pr, s_loaded);
     constexpr bool kOwnP = C::template kOwnP<MODE == 2>;
-    const uint32_t mP = kOwnP ? k.tmem + 384 + (static_cast<uint32_t>(q4 * 32) << 16) + 64 * (it & 1) + 32 * wg : mR + 32;
+    const uint32_t mP =
+        kOwnP ? k.tmem + 384 + (static_cast<uint32_t>(q4 * 32) << 16) + 64 * (it & 1) + 32 * wg : mR + 32;
     if (kOwnP) {
       store_p<MODE != 0, 0>(mP, pr, u0);
       store_p<MODE != 0, 1>(mP, pr, u1);
@@ -1062,7 +1068,9 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
           issue_cols<D>(tDK, tR, q_c[u % C::kQSlots], it > 0);
           // (measured, 12 heads on 4 of 2304 rows: by the queries' own masks 99 us
           // without this order and 89 with it, no masks 80 and 83)
-          if (ordered && it + 1 < n_it && !(ok = mbar_wait(smem_u32(&bars.dp_issued), ~u & 1, deadline, abort_flag))) break;
+          if (ordered && it + 1 < n_it &&
+              !(ok = mbar_wait(smem_u32(&bars.dp_issued), ~u & 1, deadline, abort_flag)))
+            break;
           if (!(ok = mbar_wait(smem_u32(&bars.p_go[u & 1]), (it >> 1) & 1, deadline, abort_flag))) break;
           tc_fence_after();
           if constexpr (C::template kOwnP<OWN>)

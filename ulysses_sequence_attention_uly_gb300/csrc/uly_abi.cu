@@ -1373,7 +1373,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.n_full = reinterpret_cast<int32_t*>(ws + w.n_full);
   p.nl = reinterpret_cast<float*>(ws + w.nl);
   p.dl = reinterpret_cast<float*>(ws + w.dl);
-  p.masked_rows = d.masked_rows;
+  p.masked_rows = key_mask || key_ranges ? d.masked_rows : ULY_ROWS_SDPA;  // (without a mask all are the same)
   p.withhold_fill = pl->withhold_fill;
   p.status = pl->status;
   p.wait_ns = pl->wait_ns;
