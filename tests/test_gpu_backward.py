@@ -270,6 +270,45 @@ def test_masked_places_hold_anything(c, fill):
             assert torch.equal(x.view(torch.int16), y.view(torch.int16))
 
 
+# the last tile of a shard's image rows ends inside the tile (and, in suffix mode, before the shard's text rows)
+COPIES = [
+    R.Case("suffix", 1, (300, 77), 140, "suffix", 4, 2, 128, mask="ranges"),
+    R.Case("suffix-d64", 2, (45, 257, 130), 33, "suffix", 6, 3, 64),
+    R.Case("suffix-zero", 1, (300, 77), 140, "suffix", 4, 4, 64, rows="zero", mask="random"),
+    R.Case("suffix-self", 2, (300, 77), 140, "suffix", 4, 2, 128, rows="self", mask="random"),
+    R.Case("suffix-self-d64", 1, (200, 333), 70, "suffix", 4, 4, 64, rows="self", mask="ranges"),
+    R.Case("suffix-few-tiles", 1, (900, 701), 129, "suffix", 2, 2, 128, rows="self", mask="random"),
+    R.Case("suffix-many-tiles", 2, (500, 631), 60, "suffix", 16, 16, 64),
+    R.Case("prefix", 1, (300, 77), 140, "prefix", 4, 2, 128, rows="self", mask="random"),
+    R.Case("kv-prefix", 2, (300, 77), 140, "kv_prefix", 4, 2, 64, mask="ranges"),
+]
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3.0e38])
+@pytest.mark.parametrize("c", COPIES, ids=ids)
+def test_copies_that_are_not_read_hold_anything(c, fill):
+    """A shard's copies of the replicated rows of heads that another rank owns
+    are not read (do's apart): they change no bit of the result."""
+    import torch
+    d = R.inputs(c, 25)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    want = run_fused(c, plan, d, ref)
+    for n, x in zip(("dq", "dk", "dv"), want):
+        R.check(x, ref[n], ref["e_" + n], n)
+    for ts, rep_rows in ((d["q"], c.rep_q), (d["k"], c.R), (d["v"], c.R), (ref["o"], c.rep_q), (ref["lse"], c.rep_q)):
+        per = ts[0].shape[2] // c.P
+        for p, t in enumerate(ts):
+            rep, _ = R._parts(c, t, p, rep_rows)
+            rep[:, :, :p * per] = fill
+            rep[:, :, (p + 1) * per:] = fill
+    got = run_fused(c, plan, d, ref)
+    assert plan.sync_status() == 0
+    for a, b in zip(got, want):
+        for x, y in zip(a, b):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
 def test_writes_nothing_else():
     """Outputs inside larger buffers: the memory around them stays as it was."""
     import torch

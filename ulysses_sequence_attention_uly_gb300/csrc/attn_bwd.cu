@@ -145,6 +145,12 @@ __device__ __forceinline__ int seg_of(const Seg* segs, int n, int t) {
   return s;
 }
 
+// tensor map of run s for the heads of rank r, and the run's first row in it
+__device__ __forceinline__ int map_of(const Seg& s, int r) { return s.src < 0 ? r - 1 - s.src : s.src; }
+__device__ __forceinline__ int first_row(const BwdParams& p, const Seg& s, int r) {
+  return s.row0 < 0 ? p.shard_len[r] : s.row0;
+}
+
 // 128 rows x D of one head to shared memory, panels of 64 columns one behind
 // the other (the map's fourth dimension), in one instruction
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, uint32_t bar, int head, int row, int b) {
@@ -917,8 +923,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
     ready_arrive();
     if (lane == 0 && n_it > 0) {
       const int kvhead = p.fused ? hk : hk % p.Hkv_l;
-      const int kmap = run.src < 0 ? r : run.src;
-      const int krow = (run.row0 < 0 ? p.shard_len[kmap] : run.row0) + row0;
+      const int kmap = map_of(run, r), krow = first_row(p, run, r) + row0;
       const uint32_t b_sgo = smem_u32(&bars.s_go);
       // Where tiles come from is worked out ahead, so that their loads follow at
       // once when a slot is free: mq .. for the next Q, mo .. for the next dO
@@ -946,9 +951,9 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         const bool lo = qs == p.n_qseg;
         const Seg& q = p.qseg[lo ? p.rep_qseg : qs];
         const bool rep = p.fused && q.out_shard < 0;
-        const int qmap = q.src < 0 ? r : q.src;
+        const int qmap = map_of(q, r);
         qhead = p.fused ? h : h % p.Hq_l;
-        qrow = (q.row0 < 0 ? p.shard_len[qmap] : q.row0) + qt * kTileRows;
+        qrow = first_row(p, q, r) + qt * kTileRows;
         ohead_n = rep ? h : qhead;
         orow_n = rep ? qt * kTileRows : qrow;
         mq = &p.tq[qmap];
@@ -1319,9 +1324,9 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
     __syncwarp();
     ready_arrive();
     if (lane == 0 && n_it > 0) {
-      const int qmap = run.src < 0 ? r : run.src;
+      const int qmap = map_of(run, r);
       const int qhead = p.fused ? h : h % p.Hq_l, kvhead = p.fused ? hk : hk % p.Hkv_l;
-      const int qrow = (run.row0 < 0 ? p.shard_len[qmap] : run.row0) + row0;
+      const int qrow = first_row(p, run, r) + row0;
       const uint32_t bq = smem_u32(&bars.q_full);
       mbar_arrive_expect_tx(bq, 2 * C::kTileBytes);
       load_tile(sQ, &p.tq[qmap], bq, qhead, qrow, b);
@@ -1337,8 +1342,8 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         const int e = active[listed(p, j_lo + (it < n ? it : it - n), n_full)];
         good = in_bounds(&g_bwd_violations, e >> 20, 1, p.n_kseg);
         const Seg& k = p.kseg[good ? e >> 20 : 0];
-        const int kmap = k.src < 0 ? r : k.src;
-        krow = (k.row0 < 0 ? p.shard_len[kmap] : k.row0) + (e & 0xFFFFF) * kTileRows;
+        const int kmap = map_of(k, r);
+        krow = first_row(p, k, r) + (e & 0xFFFFF) * kTileRows;
         mk = &p.tk[kmap];
         mv = &p.tv[kmap];
       };

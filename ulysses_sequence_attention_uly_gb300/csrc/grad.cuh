@@ -11,10 +11,14 @@ uint64_t norm_violations(bool reset);
 // The gradient of the attention (attn_bwd.cu).  q tensors (q, o, do, dq) share
 // their shape, as do k/v tensors (k, v, dk, dv).
 struct BwdParams {
-  CUtensorMap tq[kMaxRanks];
-  CUtensorMap tk[kMaxRanks];
-  CUtensorMap tv[kMaxRanks];
-  CUtensorMap tdo[kMaxRanks];
+  // [p]: shard p (fused) or rank p's tensor.  Fused, replicated suffix: [p] ends
+  // with the shard's image rows, and [kMaxRanks + p], of the whole shard, is for
+  // the replicated rows, so that a tile at the end of the image rows is filled
+  // with zeros there and not with copies that are not read.
+  CUtensorMap tq[2 * kMaxRanks];
+  CUtensorMap tk[2 * kMaxRanks];
+  CUtensorMap tv[2 * kMaxRanks];
+  CUtensorMap tdo[kMaxRanks];     // (replicated rows: tdo_hi, tdo_lo)
   CUtensorMap tdo_hi, tdo_lo;     // fused: replicated rows of do, summed over the shards, in two bf16 parts
   const uint8_t* o[kMaxRanks];
   const uint8_t* dout[kMaxRanks];
@@ -23,8 +27,10 @@ struct BwdParams {
   uint8_t* dk[kMaxRanks];
   uint8_t* dv[kMaxRanks];
   uint8_t *do_hi, *do_lo;         // [B][R][Hq][D] bf16 each
-  Seg qseg[kMaxSegs];             // `first`: first 128-row tile, for q and kv alike
-  Seg kseg[kMaxSegs];             // out_row0 / out_shard: where dk, dv rows go
+  // `first`: first 128-row tile, for q and kv alike; `src` < 0: map -1 - src +
+  // the rank that owns the head; kseg's out_row0 / out_shard: where dk, dv rows go
+  Seg qseg[kMaxSegs];
+  Seg kseg[kMaxSegs];
   int32_t n_qseg, n_kseg, n_q_tiles, n_kv_tiles;
   int32_t fused, P, B, Hq, Hkv, Hq_l, Hkv_l, G;
   int32_t shard_len[kMaxRanks];   // image rows of each shard

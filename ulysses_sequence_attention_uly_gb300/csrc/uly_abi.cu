@@ -1207,16 +1207,17 @@ BwdWork bwd_work(const uly_plan* pl) {
   return w;
 }
 
-// A tensor [B, rows, heads, D] in bf16 as 128-row tiles of one head that land
-// in shared memory as panels of 64 columns (attn_bwd.cu, load_tile): the
-// panels are a dimension of their own, behind the rows.
-int encode_panel_map(CUtensorMap* m, const void* base, int D, int heads, int64_t rows, int B) {
+// The first `rows` rows of every batch of a tensor [B, all_rows, heads, D] in
+// bf16 as 128-row tiles of one head that land in shared memory as panels of 64
+// columns (attn_bwd.cu, load_tile): the panels are a dimension of their own,
+// behind the rows.
+int encode_panel_map(CUtensorMap* m, const void* base, int D, int heads, int64_t all_rows, int64_t rows, int B) {
   auto enc = encode_fn();
   if (!enc) return ULY_ERR_CUDA;
   const cuuint64_t row = static_cast<cuuint64_t>(heads) * D * 2;
   cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[4] = {static_cast<cuuint64_t>(D) * 2, row, 128, row * static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(D) * 2, row, 128, row * static_cast<cuuint64_t>(all_rows)};
   cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(kTileRows), static_cast<cuuint32_t>(D / 64), 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
@@ -1293,12 +1294,16 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
 
   const int hq_l = d.Hq / P, hkv_l = d.Hkv / P;
   const int64_t hq_t = fused ? d.Hq : hq_l, hkv_t = fused ? d.Hkv : hkv_l;  // heads of one tensor
-  static thread_local BwdParams p;  // ~13 KB: keep it off the stack
+  static thread_local BwdParams p;  // ~19 KB: keep it off the stack
   static thread_local Spans spans;
   memset(&p, 0, sizeof(p));
   spans.n = 0;
   p.n_qseg = build_segs(pl, fused, 0, p.qseg);
   p.n_kseg = build_segs(pl, fused, 1, p.kseg);
+  // (a replicated suffix of the fused call has maps of its own, see below)
+  for (Seg* s : {p.qseg, p.kseg})
+    for (int i = 0; i < kMaxSegs; ++i)
+      if (s[i].row0 < 0) s[i].src = -1 - kMaxRanks;
   int acc = 0;
   for (int i = 0; i < p.n_qseg; ++i) {  // 128-row q tiles
     p.qseg[i].first = acc;
@@ -1343,13 +1348,22 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
     spans.add(dv[i], kb, true);
   }
   if (spans.clash()) return ULY_ERR_INVALID;
+  // A shard's tensor in one map, except where its replicated rows come last: a
+  // tile at the end of the image rows must not reach into them, since a shard's
+  // copies of other ranks' heads are not read and may hold anything.
+  const bool tail = fused && d.rep_mode == ULY_REP_SUFFIX;
   for (int i = 0; i < P; ++i) {
     const int64_t rq = fused ? pl->rq_p[i] : pl->nq, rk = fused ? pl->rk_p[i] : pl->nk;
+    const int64_t len = pl->lens[i], nq = tail ? len : rq, nk = tail ? len : rk;
     const int hq = static_cast<int>(hq_t), hk = static_cast<int>(hkv_t);
-    if ((rc = encode_panel_map(&p.tq[i], q[i], d.D, hq, rq, d.B)) ||
-        (rc = encode_panel_map(&p.tdo[i], dout[i], d.D, hq, rq, d.B)) ||
-        (rc = encode_panel_map(&p.tk[i], k[i], d.D, hk, rk, d.B)) ||
-        (rc = encode_panel_map(&p.tv[i], v[i], d.D, hk, rk, d.B)))
+    if ((rc = encode_panel_map(&p.tq[i], q[i], d.D, hq, rq, nq, d.B)) ||
+        (rc = encode_panel_map(&p.tdo[i], dout[i], d.D, hq, rq, nq, d.B)) ||
+        (rc = encode_panel_map(&p.tk[i], k[i], d.D, hk, rk, nk, d.B)) ||
+        (rc = encode_panel_map(&p.tv[i], v[i], d.D, hk, rk, nk, d.B)))
+      return rc;
+    if (tail && ((rc = encode_panel_map(&p.tq[kMaxRanks + i], q[i], d.D, hq, rq, rq, d.B)) ||
+                 (rc = encode_panel_map(&p.tk[kMaxRanks + i], k[i], d.D, hk, rk, rk, d.B)) ||
+                 (rc = encode_panel_map(&p.tv[kMaxRanks + i], v[i], d.D, hk, rk, rk, d.B))))
       return rc;
   }
   if (fused && (d.rep_mode == ULY_REP_PREFIX || d.rep_mode == ULY_REP_SUFFIX)) {
@@ -1359,8 +1373,8 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
     p.n_lo = w.n_lo;
     for (int i = 0; i < p.n_qseg; ++i)
       if (p.qseg[i].out_shard < 0) p.rep_qseg = i;
-    if ((rc = encode_panel_map(&p.tdo_hi, p.do_hi, d.D, d.Hq, d.R, d.B)) ||
-        (p.n_lo && (rc = encode_panel_map(&p.tdo_lo, p.do_lo, d.D, d.Hq, d.R, d.B))))
+    if ((rc = encode_panel_map(&p.tdo_hi, p.do_hi, d.D, d.Hq, d.R, d.R, d.B)) ||
+        (p.n_lo && (rc = encode_panel_map(&p.tdo_lo, p.do_lo, d.D, d.Hq, d.R, d.R, d.B))))
       return rc;
   }
   p.scale = scale;
