@@ -523,3 +523,31 @@ def test_refusals():
     # nothing was written
     torch.cuda.synchronize()
     assert all(torch.isnan(x).all() for t in g for x in t)
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_masks_inside_written_memory_are_refused(fused):
+    """A mask or ranges inside the workspace or an output would be overwritten
+    while the call still reads them."""
+    import torch
+    import ulysses_sequence_attention_uly_gb300 as uly
+    c = CASES[6]
+    d = R.inputs(c, 15)
+    plan = R.plan_of(c)
+    shape = (lambda n: d[n]) if fused else (lambda n: heads(c, R.to_global(c, d[n], n in "kv")))  # noqa: E731
+    q, k, v, do = (shape(n) for n in ("q", "k", "v", "do"))
+    lse = [torch.zeros(x.shape[:3], device="cuda") for x in q]
+    g = [outputs(x) for x in (q, k, v)]
+    n = plan.attention_backward_workspace()
+    ws = torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+    call = plan.sp_attention_backward if fused else plan.attention_backward
+    for t in (ws, g[0][0], g[1][1], g[2][0]):
+        b = t.view(-1).view(torch.uint8)
+        for kw in ({"key_mask": b[:c.B * c.nk].view(c.B, c.nk)},
+                   {"key_mask": b[-c.B * c.nk:].view(c.B, c.nk)},
+                   {"key_ranges": b[256:256 + c.B * 24].view(torch.int32).view(c.B, 3, 2)}):
+            with pytest.raises(uly.UlyError) as e:
+                call(q, k, v, q, lse, do, *g, workspace=ws, **kw)
+            assert e.value.status == uly.ULY_ERR_INVALID
+    torch.cuda.synchronize()
+    assert (ws == 0x55).all() and all(torch.isnan(x).all() for t in g for x in t)

@@ -1324,6 +1324,8 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   p.lse_row_stride = hq_t;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   spans.add(workspace, workspace_bytes, true);
+  spans.add(key_mask, d.B * pl->nk, false);
+  spans.add(key_ranges, static_cast<int64_t>(d.B) * n_ranges * 8, false);
   for (int i = 0; i < P; ++i) {
     const int64_t rq = fused ? pl->rq_p[i] : pl->nq, rk = fused ? pl->rk_p[i] : pl->nk;
     p.shard_len[i] = pl->lens[i];
