@@ -551,3 +551,23 @@ def test_masks_inside_written_memory_are_refused(fused):
             assert e.value.status == uly.ULY_ERR_INVALID
     torch.cuda.synchronize()
     assert (ws == 0x55).all() and all(torch.isnan(x).all() for t in g for x in t)
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_misaligned_ranges_are_refused(fused):
+    """Through the C ABI (the binding's tensors are aligned): ranges that are not
+    on a 4-byte boundary would fault when they are read."""
+    import torch
+    import ulysses_sequence_attention_uly_gb300 as uly
+    c = CASES[0]
+    plan = R.plan_of(c)
+    x = [torch.zeros((c.B, c.n, c.Hq, c.D), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    lse = torch.zeros((c.B, c.n, c.Hq), device="cuda")
+    rg = torch.zeros(6, dtype=torch.int32, device="cuda")
+    n = plan.attention_backward_workspace()
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    fn = uly.lib().uly_sp_attention_backward if fused else uly.lib().uly_attention_backward
+    q, k, v, o, do, dq, dk, dv, l = (uly._ptr_array([t]) for t in x + [lse])
+    for off in (1, 2, 3):
+        assert fn(plan._h, q, k, v, o, l, do, None, rg.data_ptr() + off, 2, 0.1, dq, dk, dv, ws.data_ptr(), n,
+                  None) == uly.ULY_ERR_INVALID

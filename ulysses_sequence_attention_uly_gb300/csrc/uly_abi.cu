@@ -1279,7 +1279,7 @@ int run_backward(const uly_plan* pl, int fused, const void* const* q, const void
   for (int i = 0; i < P; ++i)
     if (!lse[i] || (reinterpret_cast<uintptr_t>(lse[i]) & 3u)) return ULY_ERR_INVALID;
   if (key_mask && key_ranges) return ULY_ERR_INVALID;
-  if (key_ranges && n_ranges < 1) return ULY_ERR_INVALID;
+  if (key_ranges && (n_ranges < 1 || (reinterpret_cast<uintptr_t>(key_ranges) & 3u))) return ULY_ERR_INVALID;
   if (!(scale > 0.f) || !(scale < 3.0e38f)) return ULY_ERR_INVALID;
   const BwdWork w = bwd_work(pl);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
