@@ -57,6 +57,17 @@ def test_binding_refuses_before_any_call():
         p.norm_rope_backward(q, k, q, k, q, k)
 
 
+@pytest.mark.parametrize("bad", [[1.0], 1.0, "cos"])
+def test_tables_that_are_no_tensors_are_refused(bad):
+    p = _Shape()
+    good = torch.zeros((16, 32))
+    for cos, sin in ((bad, good), (bad, bad), (good, bad)):
+        with pytest.raises(ValueError):
+            p.norm_rope(None, None, None, None, cos=cos, sin=sin)
+        with pytest.raises(ValueError):
+            p.norm_rope_backward(None, None, None, None, None, None, cos=cos, sin=sin)
+
+
 @pytest.mark.parametrize("c", [R.Case("prefix", 1, (5, 4), 3, "prefix", 4, 2, 8, mask="ranges"),
                                R.Case("suffix-self", 2, (6, 3), 2, "suffix", 2, 2, 8, rows="self", mask="random"),
                                R.Case("kv-zero", 1, (7, 5), 4, "kv_prefix", 4, 2, 8, rows="zero", mask="random")],

@@ -646,7 +646,7 @@ class Plan:
         batches, pc, ps = 1, None, None
         if cos is not None:
             shape = (self._nk(), D // 2)
-            if cos.dim() == 3:
+            if isinstance(cos, torch.Tensor) and cos.dim() == 3:
                 batches = cos.shape[0]
                 if batches not in (1, self.B):
                     raise ValueError("cos: %d batches, expected 1 or %d" % (batches, self.B))
