@@ -571,3 +571,32 @@ def test_misaligned_ranges_are_refused(fused):
     for off in (1, 2, 3):
         assert fn(plan._h, q, k, v, o, l, do, None, rg.data_ptr() + off, 2, 0.1, dq, dk, dv, ws.data_ptr(), n,
                   None) == uly.ULY_ERR_INVALID
+
+
+@pytest.mark.parametrize("c", [R.Case("plain", 1, (1500,), 0, "none", 8, 8, 128),
+                               R.Case("suffix", 1, (700, 461), 140, "suffix", 8, 4, 128, mask="random"),
+                               R.Case("zero-d64", 1, (700, 500), 0, "none", 8, 8, 64, rows="zero", mask="random"),
+                               R.Case("plain-d64", 1, (1500,), 0, "none", 12, 4, 64),
+                               R.Case("shared", 1, (1500,), 0, "none", 4, 1, 128),
+                               R.Case("shared-self", 1, (700, 700), 60, "prefix", 2, 2, 64, rows="self", mask="random")],
+                         ids=ids)
+def test_any_wait_limit(c):
+    """However short the limit of a wait is (the hardware waits a while of its own
+    before the clock is read), the call ends with ULY_ERR_TIMEOUT or is right, and
+    the next one is right."""
+    import torch
+    import ulysses_sequence_attention_uly_gb300 as uly
+    d = R.inputs(c, 16)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    want = run_fused(c, plan, d, ref)
+    assert plan.sync_status() == 0
+    same = lambda g: all(torch.equal(x, y) for a, b in zip(g, want) for x, y in zip(a, b))  # noqa: E731
+    for ns in (1, 1500, 4000, 8000, 12000, 16000, 24000):
+        plan.set_wait_limit(ns)
+        got = run_fused(c, plan, d, ref)
+        status = plan.sync_status()
+        assert status in (uly.ULY_ERR_TIMEOUT, uly.ULY_OK), (ns, status)
+        assert status == uly.ULY_ERR_TIMEOUT or same(got)
+        plan.set_wait_limit(4_000_000_000)
+        assert same(run_fused(c, plan, d, ref)) and plan.sync_status() == 0

@@ -103,6 +103,25 @@ __device__ __forceinline__ void bwd_timeout(const BwdParams& p, volatile int* ab
   atomicOr(p.status, kStatusTimeout);
 }
 
+// What is in flight when a CTA gives up ends in its shared memory or TMEM, which
+// the next CTA gets, so it is waited for whatever the plan's limit: the products
+// on their barrier (a limit that is never reached), the copies by time, since
+// the barriers that they arrive on may lack other arrivals for good.
+constexpr uint64_t kDrainNs = 100000000ull, kCopiesNs = 50000000ull;
+
+__device__ __forceinline__ void drain_products(const BwdParams& p, uint64_t* bar, volatile int* abort_flag) {
+  mma_commit(smem_u32(bar));
+  volatile int never = 0;
+  if (!mbar_wait(smem_u32(bar), 0, globaltimer_ns() + kDrainNs, &never)) bwd_timeout(p, abort_flag);
+}
+// (by one warp, once every thread of the CTA has come past its last copy)
+__device__ __forceinline__ void drain_copies(volatile int* abort_flag) {
+  if (!*abort_flag) return;
+  const uint64_t until = globaltimer_ns() + kCopiesNs;
+  while (globaltimer_ns() < until) {
+  }
+}
+
 // As mbar_wait in as little code as possible, for the elementwise loops: a jump
 // over a long loop costs them instruction fetches, several times a tile.
 __device__ __forceinline__ bool ew_wait(uint32_t bar, uint32_t parity, uint64_t deadline_ns, volatile int* abort_flag) {
@@ -1020,12 +1039,6 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         mbar_arrive(smem_u32(&bars.p_go[(n_it - 1) & 1]));
       } else {
         bwd_timeout(p, abort_flag);
-        // No copy may land after the CTA has left.  The barriers of the last
-        // ones may lack arrivals for good, so this waits out a time in which
-        // any copy lands.
-        const uint64_t dl2 = globaltimer_ns() + 50000000ull;
-        while (globaltimer_ns() < dl2) {
-        }
       }
     }
   } else if (warp == 9) {
@@ -1091,9 +1104,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain[0]));
-      volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain[0]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      drain_products(p, &bars.drain[0], abort_flag);
     }
   } else if (warp == 10) {
     tc_fence_before();
@@ -1126,9 +1137,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain[1]));
-      volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain[1]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      drain_products(p, &bars.drain[1], abort_flag);
     }
   } else {
     tc_fence_before();
@@ -1148,6 +1157,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
     else
       ok = kv_loop<D, 0>(p, k, warp, lane, key_ok, dead);
     if (!ok) {
+      tmem_wait_st();  // (P may be on its way)
       bwd_timeout(p, abort_flag);
     } else if (SPLIT) {
       // warps 0-3: dV, warps 4-7: dK, in f32 from the buffer's start on (every
@@ -1167,6 +1177,7 @@ __device__ __forceinline__ void dkdv_cta(const BwdParams& p, uint8_t* smem_raw, 
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 8) drain_copies(abort_flag);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(bars.tmem_base, 512);
@@ -1347,9 +1358,8 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         mk = &p.tk[kmap];
         mv = &p.tv[kmap];
       };
-      int it = 0;
       next(0);
-      for (; it < n_it; ++it) {
+      for (int it = 0; it < n_it; ++it) {
         const int ks = it % C::kKSlots, vs = it % C::kVSlots;
         // the slots' last readers are dQ(it-3) and dP(it-2)
         if ((it >= 2 && !mbar_wait(smem_u32(&bars.v_free[it & 1]), ((it - 2) >> 1) & 1, deadline, abort_flag)) ||
@@ -1366,7 +1376,6 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
           // waits above; dP(n) waits for this copy)
           if (!mbar_wait(smem_u32(&bars.v_free[(n - 1) & 1]), ((n - 1) >> 1) & 1, deadline, abort_flag)) {
             bwd_timeout(p, abort_flag);
-            ++it;
             break;
           }
           const uint32_t bl = smem_u32(&bars.lo_full);
@@ -1374,14 +1383,6 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
           load_tile(sDO, &p.tdo_lo, bl, h, row0, b);
         }
         if (it + 1 < n_it) next(it + 1);
-      }
-      if (*abort_flag) {
-        const uint64_t dl2 = globaltimer_ns() + 100000000ull;
-        volatile int never = 0;
-        for (int f = max(0, it - C::kKSlots); f < it; ++f)
-          mbar_wait(smem_u32(&bars.full[f % C::kKSlots]), (f / C::kKSlots) & 1, dl2, &never);
-        mbar_wait(bq, 0, dl2, &never);
-        if (twice && it > n) mbar_wait(smem_u32(&bars.lo_full), 0, dl2, &never);
       }
     }
   } else if (warp == 9) {
@@ -1435,9 +1436,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain[0]));
-      volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain[0]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      drain_products(p, &bars.drain[0], abort_flag);
     }
   } else if (warp == 10) {
     tc_fence_before();
@@ -1478,9 +1477,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
         }
       }
       if (!ok) bwd_timeout(p, abort_flag);
-      mma_commit(smem_u32(&bars.drain[1]));
-      volatile int never = 0;
-      if (!mbar_wait(smem_u32(&bars.drain[1]), 0, globaltimer_ns() + p.wait_ns, &never)) bwd_timeout(p, abort_flag);
+      drain_products(p, &bars.drain[1], abort_flag);
     }
   } else {
     tc_fence_before();
@@ -1517,6 +1514,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
       tc_fence_after();
     }
     if (!ok) {
+      tmem_wait_st();  // (P may be on its way)
       bwd_timeout(p, abort_flag);
     } else if (SPLIT) {
       keep_rows<D>(tDQ + lane_off, sQ, row, wg * (D / 2), (wg + 1) * (D / 2), n_it == 0);
@@ -1530,6 +1528,7 @@ __device__ __forceinline__ void dq_cta(const BwdParams& p, uint8_t* smem_raw, in
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 8) drain_copies(abort_flag);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(bars.tmem_base, 512);
