@@ -600,3 +600,48 @@ def test_any_wait_limit(c):
         assert status == uly.ULY_ERR_TIMEOUT or same(got)
         plan.set_wait_limit(4_000_000_000)
         assert same(run_fused(c, plan, d, ref)) and plan.sync_status() == 0
+
+
+# one tile of queries and many of keys: only a dQ CTA has a load of that number; one tile with admitted keys and many of
+# queries: only a dK/dV CTA has.  With 16 heads every tile has a CTA of its own, with one head four share it.
+WITHHELD = [
+    (R.Case("dq", 1, (20,), 1500, "kv_prefix", 16, 16, 128), (1, 5, 12), "dq"),
+    (R.Case("dq-d64", 2, (30,), 1400, "kv_prefix", 16, 16, 64, mask="random"), (1, 2, 10), "dq"),
+    (R.Case("dq-twice", 1, (7, 7), 100, "suffix", 64, 64, 128), (4, 5), "dq"),
+    (R.Case("dq-split", 1, (20,), 1500, "kv_prefix", 1, 1, 128), (1, 2), "dq"),
+    (R.Case("dq-split-d64", 1, (20,), 2100, "kv_prefix", 1, 1, 64, rows="self", mask="random"), (1, 3), "dq"),
+    (R.Case("dkdv", 1, (1500,), 0, "none", 16, 16, 128, mask="tail"), (1, 2, 11), "dkdv"),
+    (R.Case("dkdv-own", 1, (1500,), 0, "none", 16, 16, 64, rows="zero", mask="tail"), (1, 3, 10), "dkdv"),
+    (R.Case("dkdv-split", 1, (1500,), 0, "none", 1, 1, 128, mask="tail"), (1, 2), "dkdv"),
+    (R.Case("dkdv-split-d64", 1, (2000,), 0, "none", 1, 1, 64, mask="tail"), (1, 2, 3), "dkdv"),
+]
+
+
+@pytest.mark.parametrize("c, fills, kind", WITHHELD, ids=[x[0].name for x in WITHHELD])
+def test_withheld_load_of_one_kind_times_out(c, fills, kind):
+    """A tile that never arrives in dQ's CTAs alone, and in dK's and dV's alone,
+    ends in ULY_ERR_TIMEOUT; the other kind's outputs and the next call are right."""
+    import torch
+    import ulysses_sequence_attention_uly_gb300 as uly
+    d = R.inputs(c, 17)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    want = run_fused(c, plan, d, ref)
+    assert plan.sync_status() == 0
+    for n, x in zip(("dq", "dk", "dv"), want):
+        R.check(x, ref[n], ref["e_" + n], n)
+    for fill in fills:
+        plan.set_wait_limit(20_000_000)
+        plan.test_withhold_fill(fill)
+        got = run_fused(c, plan, d, ref)
+        assert plan.sync_status() == uly.ULY_ERR_TIMEOUT
+        for a, b in zip(got[1:], want[1:]) if kind == "dq" else zip(got[:1], want[:1]):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+        plan.test_withhold_fill(-1)
+        plan.set_wait_limit(4_000_000_000)
+        again = run_fused(c, plan, d, ref)
+        assert plan.sync_status() == 0
+        for a, b in zip(again, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
