@@ -349,3 +349,43 @@ def test_training_step(c):
         assert math.sqrt(num / den) <= 6 * 2.0 ** -8, (i, math.sqrt(num / den))
     for a, b in zip(got[3 * c.P:], want[3 * c.P:]):
         assert float((a.double() - b).norm() / b.norm()) <= 6 * 2.0 ** -8
+
+
+# rows enough for a warp to take a whole row: several turns of its loop over the heads, the last one partly filled
+WHOLE_ROWS = [
+    (R.Case("33-11-heads", 2, (1300,), 0, "none", 33, 11, 128), "interleaved", False, 2, True, True),
+    (R.Case("18-6-heads-half", 1, (1400, 1300), 33, "suffix", 18, 6, 128), "half", False, 1, True, True),
+    (R.Case("9-3-heads", 1, (2500,), 7, "kv_prefix", 9, 3, 128), "half", False, 1, True, True),
+    (R.Case("21-7-heads-64", 1, (2600,), 0, "none", 21, 7, 64), "interleaved", False, 1, True, True),
+    (R.Case("39-13-heads-64-packed", 3, (900,), 0, "none", 39, 13, 64), "half", True, 3, True, True),
+    (R.Case("20-20-heads-64", 1, (1200, 1301), 50, "prefix", 20, 20, 64), "interleaved", False, 1, True, True),
+]
+
+
+@pytest.mark.parametrize("case", WHOLE_ROWS, ids=ids)
+def test_whole_rows(case):
+    """Outputs, gradients and the weights' gradients where tasks are whole rows;
+    in place, the same bits."""
+    import torch
+    c, d = case[0], make(case, 11)
+    plan = R.plan_of(c)
+    rows = c.B * sum(R.shard_rows(c, p, kv) for p in range(c.P) for kv in (False, True))
+    assert rows >= 32 * torch.cuda.get_device_properties(0).multi_processor_count
+    qo, ko = run(plan, d)
+    dq, dk, dw = run_backward(plan, d)
+    for t, out, grad, w in (("q", qo, dq, dw[0]), ("k", ko, dk, dw[1])):
+        total = bound = 0
+        for p in range(c.P):
+            within(out[p], *reference(c, d, t, p, False), "%s[%d]" % (t, p))
+            gx, e, gw, e_w = reference(c, d, t, p, True)
+            within(grad[p], gx, e, "d%s[%d]" % (t, p))
+            total, bound = total + gw, bound + e_w
+        within(w, total, bound, "dw" + t)
+    x2, g2 = ({t: [x.clone() for x in d[n + t]] for t in "qk"} for n in ("", "g"))
+    x2 = {t: [x.contiguous() for x in x2[t]] for t in "qk"}
+    w2 = [torch.empty(c.D, device="cuda") for _ in "qk"]
+    plan.norm_rope_backward(x2["q"], x2["k"], g2["q"], g2["k"], g2["q"], g2["k"], d["wq"], d["wk"], d["cos"], d["sin"],
+                            *w2, pairs=d["pairs"], eps=EPS)
+    plan.norm_rope(x2["q"], x2["k"], x2["q"], x2["k"], d["wq"], d["wk"], d["cos"], d["sin"], pairs=d["pairs"], eps=EPS)
+    for a, b in zip(dq + dk + dw + qo + ko, g2["q"] + g2["k"] + w2 + x2["q"] + x2["k"]):
+        assert torch.equal(a, b)
