@@ -645,3 +645,26 @@ def test_withheld_load_of_one_kind_times_out(c, fills, kind):
         for a, b in zip(again, want):
             for x, y in zip(a, b):
                 assert torch.equal(x, y)
+
+
+# more key tiles than one turn of the tile tables' loop takes (256), few queries
+LONG_KEYS = [
+    R.Case("sdpa-ranges", 2, (70,), 40000, "kv_prefix", 4, 2, 64, mask="ranges"),
+    R.Case("zero-random", 1, (130, 20), 70000, "kv_prefix", 2, 2, 128, rows="zero", mask="random"),
+    R.Case("self-random", 1, (200,), 33000, "kv_prefix", 2, 1, 128, rows="self", mask="random"),
+    R.Case("self-ranges", 1, (90, 61), 66001, "kv_prefix", 2, 2, 64, rows="self", mask="ranges"),
+    R.Case("all", 1, (50,), 33100, "kv_prefix", 2, 2, 128),
+    R.Case("tail", 1, (300,), 99000, "kv_prefix", 1, 1, 64, mask="tail"),
+    R.Case("none", 1, (20,), 40000, "kv_prefix", 1, 1, 128, mask="none"),
+]
+
+
+@pytest.mark.parametrize("c", LONG_KEYS, ids=ids)
+def test_long_key_lists(c):
+    d = R.inputs(c, 18)
+    ref = R.reference(c, d)
+    plan = R.plan_of(c)
+    g = run_fused(c, plan, d, ref, "ranges" if c.mask == "ranges" else "mask")
+    assert plan.sync_status() == 0
+    for n, x in zip(("dq", "dk", "dv"), g):
+        R.check(x, ref[n], ref["e_" + n], n)
