@@ -141,7 +141,9 @@ int64_t uly_plan_shard_rows(const uly_plan* plan, int32_t shard, int32_t is_kv);
 void uly_plan_destroy(uly_plan* plan);
 
 /* Limit, in nanoseconds, of every device-side wait (default 4e9).  A wait
- * that expires makes the kernel record ULY_ERR_TIMEOUT and return. */
+ * that expires makes the kernel record ULY_ERR_TIMEOUT and return.  (The
+ * hardware waits a while by itself before the clock is read, so that limits of
+ * microseconds do not expire in a call that makes progress.) */
 int uly_plan_set_wait_limit(uly_plan* plan, uint64_t ns);
 
 /* Failure-detection test hook: when fill >= 0, the attention kernels' TMA
@@ -244,6 +246,9 @@ int uly_to_seq(const uly_plan* plan, const void* const* oh, void* const* o, void
  * bf16 shard outputs o[p] [B, Rq, Hq, D], with no staging copy.  Arguments
  * as in uly_attention; lse, when given, is per shard f32 [B, Rq, Hq]
  * (replicated rows' values reach every shard, like their outputs).
+ * ULY_REP_SUFFIX: v has to be finite in every shard's copy of every head of the
+ * replicated rows, also where another rank owns the head (the rows behind a
+ * shard's image rows are multiplied by zero, not left out).
  * The call enqueues work only (no host synchronisation), so it may be
  * captured into a CUDA graph; the graph keeps the pointers, so replays read
  * the buffers' current values.  Make the first call for a plan outside a
@@ -408,7 +413,8 @@ int uly_ring_attention(uly_plan* plan, const void* const* qh, const void* const*
  *   the caller; its contents mean nothing before and after the call.  The call
  *   uses no other scratch of the plan, so calls with one plan may overlap on
  *   the GPU, also with its forward calls, when their workspaces differ.
- * Outputs and workspace must not overlap each other or any input.
+ * Outputs and workspace must not overlap each other or any input, the mask and
+ * the ranges included.
  * bf16 plans only: ULY_ERR_UNSUPPORTED for e4m3.  ULY_ERR_INVALID for NULL,
  * misaligned or overlapping pointers, a workspace that is too small, a NULL lse
  * and as uly_attention.  The call may be captured into a CUDA graph (not the
@@ -429,7 +435,8 @@ int uly_attention_backward(const uly_plan* plan, const void* const* qh, const vo
  *    replicated rows of its own shard, so its copies of dq, dk, dv hold that
  *    head's gradient and the other shards' copies hold zero.  The gradient of
  *    text rows that all shards share is the sum over the copies.
- *  - of o and lse in replicated rows the owner's copy is read. */
+ *  - of q, k, v, o and lse in replicated rows the owner's copy is read; what the
+ *    other shards' copies hold for that head does not matter, NaN included. */
 int uly_sp_attention_backward(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
                               const void* const* o, const float* const* lse, const void* const* dout,
                               const uint8_t* key_mask, const int32_t* key_ranges, int32_t n_ranges, float scale,

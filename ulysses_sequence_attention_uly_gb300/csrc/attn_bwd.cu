@@ -17,16 +17,16 @@
 //             dV, dK);
 //   dq_cta    one for a (batch, q head, 128 queries), over every 128-key tile
 //             with an admitted key: three products (S, dP, dQ).
-// With five products in one, dQ would have to be added through f32 atomics in
-// memory, whose order changes the bits; the price of the two is 7/5 of the
-// tensor work.
+// With five products in one, dQ would have to be added up in memory, by atomics
+// whose order changes the bits or by CTAs in turn; the price of the two is 7/5
+// of the tensor work.
 //
 // Bound by the tensor cores where loops are long and D is 128 (8 heads of 8192
 // rows: 537 us, 1792 TFLOP/s of the seven products, 94% of 1912 measured with
 // one large matrix product; larger calls run into the power limit: 40 heads of
 // 27792 rows 31.4 ms, 1745 TFLOP/s, which is what a matrix product sustains).
 // With 64-wide heads, or masks, by the elementwise work and the issue of MMAs:
-// 406 us, 1185 TFLOP/s.  Short loops, by what surrounds them: about 5.5 us a
+// 406 us, 1185 TFLOP/s (tensor pipe active 49% of cycles, issue slots 39%).  Short loops, by what surrounds them: about 5.5 us a
 // CTA, of which 2.5 pass before its first scores are there.
 //
 // Rounding: P and dS are rounded to bf16, since they are operands of bf16 MMAs;
@@ -122,8 +122,9 @@ __device__ __forceinline__ void drain_copies(volatile int* abort_flag) {
   }
 }
 
-// As mbar_wait in as little code as possible, for the elementwise loops: a jump
-// over a long loop costs them instruction fetches, several times a tile.
+// As mbar_wait in as little code as possible, for the elementwise loops, which
+// jump over it several times a tile (8 heads of 8192 rows of 64: 488 us with
+// mbar_wait, 481 with this, when it was taken).
 __device__ __forceinline__ bool ew_wait(uint32_t bar, uint32_t parity, uint64_t deadline_ns, volatile int* abort_flag) {
   uint32_t ok;
   asm volatile(
@@ -755,9 +756,10 @@ struct KvWork {
 // The elementwise loop of dkdv_cta: one thread per key and half of the
 // queries.  MODE 0: every pair of the warp attends.  1: `dead` keys do not.
 // 2: it goes by the queries' own tokens too (ULY_ROWS_ZERO, _SELF).  Loops of
-// their own, so that the common one has no test in it and fits the registers.
-// (A test that jumps over a tile's masking costs more in instruction fetches
-// than the masking.)
+// their own, so that the common one has no test in it and all but fits the
+// registers (at D = 128 up to 8 bytes are spilled).  (A test that jumps over
+// a tile's masking costs more than the masking: 64-wide heads, scattered mask,
+// 177 us with it and 157 without, when it was taken.)
 template <int D, int MODE>
 __device__ __forceinline__ bool kv_loop(const BwdParams& p, const KvWork& k, int warp, int lane, bool key_ok, bool dead) {
   using C = BCfg<D>;
