@@ -668,3 +668,44 @@ def test_long_key_lists(c):
     assert plan.sync_status() == 0
     for n, x in zip(("dq", "dk", "dv"), g):
         R.check(x, ref[n], ref["e_" + n], n)
+
+
+def test_two_threads_one_plan():
+    """Gradient calls of one plan from two threads at once, each on a stream and
+    with tensors of its own, beside norm_rope calls: the bits of calls alone."""
+    import threading
+
+    import torch
+    c = R.Case("threads", 2, (300, 77), 140, "suffix", 4, 2, 128, rows="zero", mask="random")
+    plan = R.plan_of(c)
+    jobs = []
+    for seed in (40, 41):
+        d = R.inputs(c, seed)
+        ref = R.reference(c, d)
+        nq, nk = outputs(d["q"]), outputs(d["k"])
+        plan.norm_rope(d["q"], d["k"], nq, nk)
+        jobs.append((d, ref, run_fused(c, plan, d, ref), nq + nk))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(d, ref, want, norm):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    g = run_fused(c, plan, d, ref)
+                    nq, nk = outputs(d["q"]), outputs(d["k"])
+                    plan.norm_rope(d["q"], d["k"], nq, nk)
+                    s.synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(sum(g, []) + nq + nk, sum(want, []) + norm)):
+                        wrong.append("other bits")
+        except Exception as e:  # noqa: BLE001 - reported below
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+    assert plan.sync_status() == 0
