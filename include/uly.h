@@ -15,7 +15,14 @@
  *   uly_norm_rope     the RMS norm of the q and k heads and the rotation by
  *                     position, on the shards, before the exchange,
  *   uly_*_backward    the gradients of the attention (staged and fused) and
- *                     of uly_norm_rope.
+ *                     of uly_norm_rope;
+ *
+ * and, for sequences that are generated token by token:
+ *
+ *   uly_sp_prompt_attention  causal attention over packed sequences of
+ *                     different lengths, on the shards,
+ *   uly_cache_append  k and v rows of new tokens into an 8-bit paged cache,
+ *   uly_cache_attention  attention of the newest tokens over that cache.
  *
  * Sources (web pages, cited by title and section):
  *  [cp]   flashdreams core/attention/cp.py, ContextParallelAttention.
@@ -503,6 +510,119 @@ int uly_norm_rope_backward(const uly_plan* plan, const void* const* q, const voi
 
 /* Bytes of workspace of uly_norm_rope_backward, or -1 for a NULL plan. */
 int64_t uly_norm_rope_backward_workspace(const uly_plan* plan);
+
+/* Causal attention over packed sequences (whole prompts of different lengths)
+ * on the seq-sharded shards.  The plan's gathered rows (P * S_l, or the sum of
+ * an uneven plan's shards) are a row budget that any number of sequences share:
+ * sequence s holds the rows [seq_starts[s], seq_starts[s + 1]) of the global row
+ * order, wherever the shards' ends lie, and its row i attends to its rows j <= i:
+ *     o_i = sum_j softmax_j(scale <q_i, k_j>) v_j        (bf16, rounded once)
+ * q head h uses kv head h / (Hq/Hkv); q, k, v, o are shards as in
+ * uly_sp_attention, lse (may be NULL) f32 [1, rows, Hq] per shard: the natural
+ * logarithm of the sum of the row's exponentials.
+ *   seq_starts: device int32 [n_seqs + 1], non-decreasing, within [0, rows]
+ *     (values outside are clamped; sequences that overlap give undefined
+ *     outputs).  A sequence may be empty.  o and lse of rows before the first
+ *     and behind the last sequence are left as they were.
+ *   k and v of a sequence's own rows have to be finite; rows of other sequences
+ *     and of none may hold anything, NaN included.
+ *   workspace: device memory of at least
+ *     uly_sp_prompt_attention_workspace(plan, n_seqs) bytes, 256-byte aligned,
+ *     owned by the caller; its contents mean nothing before and after the call.
+ *     Calls with one plan may overlap on the GPU when their workspaces differ.
+ * The same bits on every call.  n_seqs = 0 does nothing.  May be captured into a
+ * CUDA graph (not the first call on a device); a replay reads the sequences'
+ * bounds that are then in seq_starts.
+ * Plans with B = 1, ULY_REP_NONE and bf16 only: ULY_ERR_UNSUPPORTED otherwise,
+ * and for more than 65536 sequences.  ULY_ERR_INVALID for NULL, misaligned or
+ * overlapping pointers, a workspace that is too small, a bad scale, n_seqs < 0. */
+int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
+                            const int32_t* seq_starts, int32_t n_seqs, float scale, void* const* o,
+                            float* const* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of uly_sp_prompt_attention for n_seqs sequences (36 bytes a
+ * sequence and 16 for 128 rows, about), or -1 for a NULL plan or n_seqs < 0. */
+int64_t uly_sp_prompt_attention_workspace(const uly_plan* plan, int32_t n_seqs);
+
+/* ---- 8-bit paged cache --------------------------------------------------
+ * k and v of past tokens as e4m3 codes in pages of page_rows tokens, with one
+ * scale for each page and head: token at slot t of page g has
+ *     k[h][:] = k_scale[g][h] * k_pages[g][h][t][:]        and v alike.
+ * H are the k/v heads of one rank (or all of them).  All memory is the
+ * caller's.  Which page holds which tokens is in a table, device int32 [n_seqs,
+ * table_width]: tokens [i * page_rows, (i + 1) * page_rows) of sequence s are in
+ * page table[s][i]; entries that no token needs may hold anything. */
+typedef struct uly_cache {
+  void* k_pages;       /* device e4m3 [n_pages, H, page_rows, D], 16-byte aligned */
+  void* v_pages;
+  float* k_scale;      /* device f32 [n_pages, H]; positive, between 2^-60 and 2^120 */
+  float* v_scale;
+  int32_t n_pages;
+  int32_t page_rows;   /* 16, 32, 64 or 128 */
+  int32_t H;
+  int32_t D;           /* 64 or 128 */
+} uly_cache;
+
+/* New tokens' k and v rows into the cache.  Rows [starts[s], starts[s + 1]) of k
+ * and v (bf16 [n_rows, H, D]) are the newest tokens of sequence s, which has
+ * lens[s] tokens with them: they take its positions lens[s] - (starts[s + 1] -
+ * starts[s]) to lens[s] - 1.
+ *   The scale of a page and head is the least power of two s >= 2^-60 with
+ * |x| <= 448 s for the values that it has to hold; codes are round(x / s) to
+ * e4m3.  A page that holds tokens before the call keeps its scale, or gets the
+ * larger one that the new values need; its old codes are then brought to it (a
+ * shift of their exponents: exact except where a code becomes subnormal).  A
+ * page whose slot 0 is written starts anew: its scale before the call does not
+ * matter.  Slots that no token takes are left as they were.
+ *   k_row_stride, v_row_stride: elements between consecutive rows, a multiple of
+ *     8 and at least H * D (k and v parts of a packed projection are read in
+ *     place); 0 = dense.
+ *   starts: device int32 [n_seqs + 1], non-decreasing, within [0, n_rows]
+ *     (clamped); rows of no sequence are not read.  lens: device int32 [n_seqs].
+ *     A row whose position is negative or past the table's width, or whose page
+ *     is outside [0, n_pages), is dropped.
+ *   A page may take new rows of one sequence only.  Values have to be finite (a
+ *   NaN stays a NaN; an infinity takes the precision of its page and head).
+ * Works on the current device; no workspace; may be captured into a CUDA graph.
+ * ULY_ERR_INVALID for NULL, misaligned or overlapping pointers, bad strides or
+ * sizes; ULY_ERR_UNSUPPORTED for other page sizes or D, more than 65535 heads,
+ * 65536 sequences or 2^27 rows. */
+int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64_t k_row_stride,
+                     int64_t v_row_stride, int64_t n_rows, const int32_t* starts, const int32_t* lens,
+                     const int32_t* table, int32_t n_seqs, int32_t table_width, void* stream);
+
+/* Attention of the newest tokens of every sequence over its cache, the newest
+ * ones included (uly_cache_append comes first).  Rows [starts[s], starts[s + 1])
+ * of q (bf16 [n_rows, Hq, D]) are the last tokens of sequence s, which has
+ * lens[s] tokens: the row at position i attends to the positions j <= i, with
+ * k and v as the cache holds them:
+ *     o = sum_j softmax_j(scale <q, k_j>) v_j            (bf16, rounded once)
+ * q head h uses cache head h / (Hq / H).  One row a sequence is plain
+ * generation; a few are a guess that is checked, or the end of a prompt.
+ *   o: bf16 [n_rows, Hq, D]; lse: NULL or f32 [n_rows, Hq] (natural log-sum-exp).
+ *     A row that has no key (lens[s] = 0, a position below zero) gets 0 and
+ *     -inf; rows of no sequence are left as they were.
+ *   Tokens in a page outside [0, n_pages) do not take part.  Codes behind a
+ *     sequence's last token may be anything, NaN included; those of its tokens,
+ *     and the scales, have to be finite.
+ *   q_row_stride: as in uly_cache_append.  starts, lens, table: as there.
+ *   workspace: device memory of at least uly_cache_attention_workspace(...)
+ *     bytes, 256-byte aligned, owned by the caller; its contents mean nothing
+ *     before and after the call.
+ * P (after the exponential) is rounded to f16 and q to f16 with a power of two
+ * taken out of each row; everything else is f32.  The same bits on every call
+ * on a device.  Works on the current device; may be captured into a CUDA graph;
+ * a replay reads starts, lens and the table anew.
+ * Errors as uly_cache_append, and ULY_ERR_INVALID for Hq % H, a bad scale or a
+ * workspace that is too small. */
+int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_stride, int32_t Hq, int64_t n_rows,
+                        const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t n_seqs,
+                        int32_t table_width, float scale, void* o, float* lse, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of uly_cache_attention on the current device, or -1 for a
+ * bad argument. */
+int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs);
 
 /* Allocation-free fused attention.  The source pages have no counterpart:
  * this entry point exists for callers that cannot call cudaMalloc -- an

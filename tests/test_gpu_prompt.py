@@ -1,0 +1,179 @@
+"""Causal attention over packed prompts on the shards (uly_sp_prompt_attention)
+against 64 bits: lengths around the tiles' ends, sequences across shards, empty
+and single-row ones, rows of no sequence, every kind of head group."""
+import pytest
+import torch
+
+from tests import _serve as R
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    R.Prompt("one row", (1,), (1,), 1, 1, 64),
+    R.Prompt("short", (17,), (17,), 4, 2, 64),
+    R.Prompt("a tile", (128,), (128,), 2, 1, 128),
+    R.Prompt("past a tile", (129,), (129,), 2, 2, 128),
+    R.Prompt("two tiles", (256,), (256,), 3, 1, 128),
+    R.Prompt("past two tiles", (257,), (257,), 1, 1, 128),
+    R.Prompt("tile ends", (1500,), (127, 128, 129, 255, 256, 257, 1), 4, 2, 128, first=100),
+    R.Prompt("single rows", (700,), (1,) * 300 + (0,) * 7 + (1,) * 200, 4, 1, 64, first=3),
+    R.Prompt("four shards", (300,) * 4, (1000, 0, 1, 199), 8, 4, 128),
+    R.Prompt("uneven shards", (333, 1, 77, 500), (410, 2, 400), 4, 4, 64, first=50),
+    R.Prompt("shards of a row", (1,) * 16, (5, 9), 16, 16, 64, first=1),
+    R.Prompt("tiny shards", (3, 200, 5, 130), (330,), 4, 4, 128, first=2),
+    R.Prompt("odd group", (600,), (77, 300, 223), 6, 2, 128),
+    R.Prompt("group of five", (400,), (399,), 5, 1, 64),
+    R.Prompt("group of eight", (520,), (130, 390), 16, 2, 128),
+    R.Prompt("long rows", (2000, 1300), (3200,), 4, 2, 128, first=7, std=0.7),
+    R.Prompt("long rows, odd group", (2000, 1300), (3200,), 6, 2, 64, first=7),
+    R.Prompt("peaked", (512,), (512,), 4, 2, 128, std=4.0),
+    R.Prompt("no rows", (64,), (0, 0), 2, 2, 64, first=9),
+]
+
+
+def run(c, d, plan=None, **kw):
+    plan = plan or R.plan_of(c)
+    plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"], **kw)
+    torch.cuda.synchronize()
+    assert plan.sync_status() == 0
+    return plan
+
+
+@pytest.mark.parametrize("c", CASES, ids=lambda c: c.name)
+def test_against_64_bits(c):
+    d = R.prompt_inputs(c, 1)
+    run(c, d)
+    R.check_prompt(c, d, d["o"], d["lse"])
+
+
+@pytest.mark.parametrize("c", CASES[6:12:2], ids=lambda c: c.name)
+def test_scale_and_no_lse(c):
+    d = R.prompt_inputs(c, 2)
+    plan = R.plan_of(c)
+    plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], scale=0.031)
+    torch.cuda.synchronize()
+    R.check_prompt(c, d, d["o"], None, scale=0.031)
+
+
+def test_more_sequences_than_threads():
+    lens = tuple((i * 7) % 4 for i in range(2500))
+    c = R.Prompt("many", (2200, 2000), lens, 2, 2, 64, first=11)
+    d = R.prompt_inputs(c, 3)
+    run(c, d)
+    R.check_prompt(c, d, d["o"], d["lse"])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 3)])
+def test_what_other_rows_hold_does_not_matter(Hq, Hkv):
+    """Rows of no sequence, and of a neighbour, may hold NaN and infinities."""
+    c = R.Prompt("neighbours", (200, 300), (100, 90, 230), Hq, Hkv, 128, first=20) if Hkv % 2 == 0 else \
+        R.Prompt("neighbours", (500,), (100, 90, 230), Hq, Hkv, 128, first=20)
+    clean = R.prompt_inputs(c, 4)
+    want, _, _, _ = R.prompt_reference(c, clean)
+    run(c, clean)
+    d = R.prompt_inputs(c, 4)
+    flat = {n: torch.cat(d[n], 1) for n in "qkv"}
+    for n, bad in zip("qkv", (float("nan"), float("inf"), float("nan"))):
+        flat[n][:, :20] = bad
+        flat[n][:, 120:210] = bad  # the middle sequence
+        flat[n][:, 440:] = -bad
+        d[n] = [x.contiguous() for x in flat[n].split(list(c.shards), 1)]
+    run(c, d)
+    a, b = (torch.cat(x["o"], 1)[0] for x in (clean, d))
+    for lo, hi in ((0, 120), (210, 500)):
+        assert torch.equal(a[lo:hi].view(torch.int16), b[lo:hi].view(torch.int16))
+
+
+def test_the_same_bits_every_time_and_between_shard_counts():
+    c = R.Prompt("again", (256,) * 4, (300, 256, 1, 467), 8, 4, 128)
+    d = R.prompt_inputs(c, 5)
+    plan = run(c, d)
+    first = [x.clone() for x in d["o"]]
+    for _ in range(5):
+        run(c, d, plan)
+        for x, y in zip(first, d["o"]):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def test_plain_attention_of_the_last_row():
+    """A sequence's last row sees what the framework's attention without a mask sees."""
+    c = R.Prompt("last", (300,), (300,), 4, 2, 128)
+    d = R.prompt_inputs(c, 6)
+    plan = run(c, d)
+    o = [torch.empty_like(x) for x in d["q"]]
+    plan.sp_attention(d["q"], d["k"], d["v"], o)
+    torch.cuda.synchronize()
+    diff = (o[0][0, -1].double() - d["o"][0][0, -1].double()).abs()
+    # each is off by a rounding of the probabilities and one of the output
+    assert float(diff.max()) <= 4 * 2.0 ** -8 * float(d["v"][0].abs().max())
+
+
+def test_streams_workspaces_and_graph():
+    c = R.Prompt("graph", (500, 400), (123, 456, 200), 4, 2, 128, first=30)
+    d = R.prompt_inputs(c, 7)
+    plan = run(c, d)  # outside a capture
+    side = torch.cuda.Stream()
+    # two calls at once on two streams, their workspaces their own
+    e = R.prompt_inputs(c, 8)
+    ws = [torch.empty(plan.prompt_attention_workspace(3), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"], workspace=ws[0])
+        plan.prompt_attention(e["q"], e["k"], e["v"], e["o"], e["starts"], lse=e["lse"], workspace=ws[1], stream=side)
+    torch.cuda.synchronize()
+    R.check_prompt(c, d, d["o"], d["lse"])
+    R.check_prompt(c, e, e["o"], e["lse"])
+    # replayed with other sequences in the same tensor
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"], workspace=ws[0])
+    for seqs, first in (((1, 799, 2), 0), ((0, 300, 0), 128)):
+        other = R.Prompt("other", c.shards, seqs, c.Hq, c.Hkv, c.D, first=first)
+        for n in ("o", "lse"):
+            for x in d[n]:
+                x.fill_(7.0)
+        d["starts"].copy_(torch.tensor(other.bounds, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        R.check_prompt(other, d, d["o"], d["lse"])
+
+
+def test_sequence_bounds_are_clamped():
+    c = R.Prompt("clamped", (200, 100), (300,), 4, 2, 64)
+    d = R.prompt_inputs(c, 9)
+    d["starts"] = torch.tensor([-5, 120, 1 << 30], dtype=torch.int32, device="cuda")
+    run(c, d)
+    as_is = R.Prompt("clamped", (200, 100), (120, 180), 4, 2, 64)
+    R.check_prompt(as_is, d, d["o"], d["lse"])
+
+
+def test_refusals():
+    import ulysses_sequence_attention_uly_gb300 as uly
+    c = R.Prompt("refused", (64, 64), (100,), 4, 2, 64)
+    d = R.prompt_inputs(c, 10)
+    plan = R.plan_of(c)
+    ok = dict(q=d["q"], k=d["k"], v=d["v"], o=d["o"], seq_starts=d["starts"], lse=d["lse"])
+    need = plan.prompt_attention_workspace(1)
+    for change in (dict(q=d["q"][:1]), dict(k=d["q"]), dict(o=[x.float() for x in d["o"]]), dict(lse=d["lse"][:1]),
+                   dict(seq_starts=d["starts"].long()), dict(seq_starts=d["starts"].cpu()), dict(seq_starts=[0, 1]),
+                   dict(seq_starts=d["starts"][:0]), dict(v=[x.transpose(1, 2) for x in d["v"]]),
+                   dict(workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            plan.prompt_attention(**{**ok, **change})
+    for change in (dict(o=d["q"]), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                   dict(workspace=torch.empty(need + 256, dtype=torch.uint8, device="cuda")[1:])):
+        with pytest.raises(uly.UlyError) as e:
+            plan.prompt_attention(**{**ok, **change})
+        assert e.value.status == uly.ULY_ERR_INVALID
+    for other in (uly.Plan(2, 2, 64, 0, "none", 4, 2, 64), uly.Plan(1, 2, 64, 8, "prefix", 4, 2, 64)):
+        q, k = ([torch.zeros((other.B, other.shard_rows(p, kv), h, 64), dtype=torch.bfloat16, device="cuda")
+                 for p in range(2)] for kv, h in ((False, 4), (True, 2)))
+        with pytest.raises(uly.UlyError) as e:
+            other.prompt_attention(q, k, k, [torch.empty_like(x) for x in q], d["starts"])
+        assert e.value.status == uly.ULY_ERR_UNSUPPORTED
+    with pytest.raises(uly.UlyError) as e:
+        uly.Plan(1, 2, 64, 0, "none", 4, 2, 128, dtype="e4m3").prompt_attention(**ok)
+    assert e.value.status == uly.ULY_ERR_UNSUPPORTED
+    plan.prompt_attention(**{**ok, "seq_starts": d["starts"][:1]})  # no sequence: nothing happens
+    torch.cuda.synchronize()
+    assert all((x == 7.0).all() for x in d["o"])

@@ -35,7 +35,9 @@ EXPORTS = ("uly_plan_create", "uly_plan_destroy", "uly_plan_set_wait_limit", "ul
            "uly_plan_shard_rows", "uly_sp_attention_host", "uly_checked_violations",
            "uly_plan_test_check_narrow", "uly_attention_merge", "uly_noalloc_sync_status", "uly_ring_attention",
            "uly_attention_backward", "uly_sp_attention_backward", "uly_attention_backward_workspace",
-           "uly_norm_rope", "uly_norm_rope_backward", "uly_norm_rope_backward_workspace")
+           "uly_norm_rope", "uly_norm_rope_backward", "uly_norm_rope_backward_workspace",
+           "uly_sp_prompt_attention", "uly_sp_prompt_attention_workspace", "uly_cache_append",
+           "uly_cache_attention", "uly_cache_attention_workspace")
 
 
 class UlyError(RuntimeError):
@@ -47,6 +49,11 @@ class UlyError(RuntimeError):
 class _Desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "P", "S_l", "R", "rep_mode", "Hq", "Hkv", "D", "dtype", "masked_rows")]
+
+
+class _CacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale")] + \
+        [(n, ctypes.c_int32) for n in ("n_pages", "page_rows", "H", "D")]
 
 
 _lib = None
@@ -110,6 +117,15 @@ def lib():
                                              ctypes.c_float, vpp, vpp, vp, vp, vp, i64, vp]
         L.uly_norm_rope_backward_workspace.argtypes = [vp]
         L.uly_norm_rope_backward_workspace.restype = i64
+        L.uly_sp_prompt_attention.argtypes = [vp, vpp, vpp, vpp, vp, i32, ctypes.c_float, vpp, vpp, vp, i64, vp]
+        L.uly_sp_prompt_attention_workspace.argtypes = [vp, i32]
+        L.uly_sp_prompt_attention_workspace.restype = i64
+        cache = ctypes.POINTER(_CacheDesc)
+        L.uly_cache_append.argtypes = [cache, vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, vp]
+        L.uly_cache_attention.argtypes = [cache, vp, i64, i32, i64, vp, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp,
+                                          i64, vp]
+        L.uly_cache_attention_workspace.argtypes = [cache, i32, i64, i32]
+        L.uly_cache_attention_workspace.restype = i64
         L.uly_device_sm_count.argtypes = [ctypes.c_int]
         L.uly_device_sm_count.restype = i32
         L.uly_checked_violations.argtypes = [i32]
@@ -266,6 +282,35 @@ def _workspace(ws, nbytes, device, stream):
         raise ValueError("workspace: expected a contiguous uint8 tensor of at least %d bytes on device %d"
                          % (nbytes, device))
     return ws
+
+
+def _vector_len(t, what, device):
+    """Length (at least 1) of an int32 vector on the device."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != 1 or t.shape[0] < 1:
+        raise ValueError("%s: expected an int32 vector on device %d" % (what, device))
+    _checked_ptr(t, t.shape, _torch().int32, what, device)
+    return t.shape[0]
+
+
+def _token_rows(t, H, D, what, device):
+    """Rows, address and row stride in elements (0 for dense) of bf16 [rows, H,
+    D], whose rows may be more than a row apart (a part of a packed projection)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
+        raise ValueError("%s: expected a CUDA tensor on device %d" % (what, device))
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError("%s: %s %s, expected torch.bfloat16 (rows, %d, %d)" % (what, t.dtype, tuple(t.shape), H, D))
+    rows = t.shape[0]
+    if rows == 0:
+        return 0, t.data_ptr(), 0
+    sr, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
+        raise ValueError("%s: the heads of a row must be contiguous" % what)
+    if rows == 1:
+        return 1, t.data_ptr(), 0  # any stride
+    if sr < H * D or sr % 8:
+        raise ValueError("%s: rows must be a multiple of 8 elements apart, at least %d" % (what, H * D))
+    return rows, t.data_ptr(), sr
 
 
 def _raw_stream(stream, device):
@@ -694,6 +739,36 @@ class Plan:
         if st != ULY_OK:
             raise UlyError(st, "uly_norm_rope_backward")
 
+    # ---- packed prompts
+    def prompt_attention_workspace(self, n_seqs: int) -> int:
+        """Bytes of workspace of prompt_attention for n_seqs sequences."""
+        return int(lib().uly_sp_prompt_attention_workspace(self._h, n_seqs))
+
+    def prompt_attention(self, q, k, v, o, seq_starts, scale=None, lse=None, workspace=None, stream=None):
+        """Causal attention over packed sequences on the seq-sharded shards
+        (uly_sp_prompt_attention): sequence s holds the rows [seq_starts[s],
+        seq_starts[s + 1]) of the global row order.  seq_starts: int32
+        [n_seqs + 1] on the plan's device; rows of no sequence stay as they are
+        in o and lse.  workspace: a uint8 tensor of
+        prompt_attention_workspace(n_seqs) bytes; by default one is allocated on
+        the call's stream."""
+        torch = _torch()
+        if self.dtype != "bf16":
+            raise UlyError(ULY_ERR_UNSUPPORTED, "uly_sp_prompt_attention")
+        dev, bf16 = self.device, torch.bfloat16
+        qs, ks, ls = self._shapes(True)
+        pq, pk, pv, po = (_checked_ptrs(t, s, bf16, what, dev)
+                          for t, s, what in ((q, qs, "q"), (k, ks, "k"), (v, ks, "v"), (o, qs, "o")))
+        pl = None if lse is None else _checked_ptrs(lse, ls, torch.float32, "lse", dev)
+        n_seqs = _vector_len(seq_starts, "seq_starts", dev) - 1
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.D)
+        workspace = _workspace(workspace, self.prompt_attention_workspace(n_seqs), dev, stream)
+        st = lib().uly_sp_prompt_attention(self._h, pq, pk, pv, seq_starts.data_ptr(), n_seqs, scale, po, pl,
+                                           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+        if st != ULY_OK:
+            raise UlyError(st, "uly_sp_prompt_attention")
+
     def pipelined_attention(self, q, k, v, qh, kh, vh, oh, o, key_mask=None, key_ranges=None, scale=None,
                             head_groups=0, q_scale=None, k_scale=None, v_scale=None, stream=None,
                             copy_stream=None):
@@ -748,3 +823,95 @@ class Plan:
 
     def sync_status(self, stream=None) -> int:
         return int(lib().uly_sync_status(self._h, _stream(stream)))
+
+
+class Cache:
+    """An 8-bit paged cache of k and v (include/uly.h, uly_cache) over the
+    caller's tensors: k_pages, v_pages e4m3 (or uint8) [n_pages, H, page_rows, D]
+    and k_scale, v_scale f32 [n_pages, H].  `starts` (int32 [n_seqs + 1]), `lens`
+    (int32 [n_seqs]) and `table` (int32 [n_seqs, width]) are those of
+    uly_cache_append and uly_cache_attention."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale):
+        torch = _torch()
+        if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda or k_pages.dim() != 4:
+            raise ValueError("k_pages: expected a CUDA tensor [n_pages, H, page_rows, D]")
+        dev = self.device = k_pages.get_device()
+        n, H, rows, D = self.shape = tuple(k_pages.shape)
+        _want(k_pages, self.shape, _ELEM["e4m3"], "k_pages", dev)
+        _want(v_pages, self.shape, _ELEM["e4m3"], "v_pages", dev)
+        _want(k_scale, (n, H), ("torch.float32",), "k_scale", dev)
+        _want(v_scale, (n, H), ("torch.float32",), "v_scale", dev)
+        self.tensors = (k_pages, v_pages, k_scale, v_scale)
+        self._d = _CacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, rows,
+                             H, D)
+        self._work = {}
+
+    def _sequences(self, starts, lens, table):
+        dev, i32 = self.device, _torch().int32
+        n = _vector_len(starts, "starts", dev) - 1
+        _checked_ptr(lens, (n,), i32, "lens", dev)
+        if not isinstance(table, _torch().Tensor) or table.dim() != 2 or table.shape[1] < 1:
+            raise ValueError("table: expected an int32 tensor [%d, width >= 1]" % n)
+        _checked_ptr(table, (n, table.shape[1]), i32, "table", dev)
+        return n, table.shape[1]
+
+    def _call(self, fn, name, *args):
+        """fn on the cache's device."""
+        torch = _torch()
+        if torch.cuda.current_device() == self.device:
+            st = fn(self._d, *args)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(self._d, *args)
+        if st != ULY_OK:
+            raise UlyError(st, name)
+
+    def append(self, k, v, starts, lens, table, stream=None):
+        """The rows of new tokens (bf16 [rows, H, D], parts of a packed
+        projection allowed) into the cache (uly_cache_append); lens counts them
+        already."""
+        n, width = self._sequences(starts, lens, table)
+        _, H, _, D = self.shape
+        rows, pk, sk = _token_rows(k, H, D, "k", self.device)
+        vrows, pv, sv = _token_rows(v, H, D, "v", self.device)
+        if rows != vrows:
+            raise ValueError("v: %d rows, expected %d" % (vrows, rows))
+        if rows and n:
+            self._call(lib().uly_cache_append, "uly_cache_append", pk, pv, sk, sv, rows, starts.data_ptr(),
+                       lens.data_ptr(), table.data_ptr(), n, width, _raw_stream(stream, self.device))
+
+    def attention_workspace(self, Hq: int, n_rows: int, n_seqs: int) -> int:
+        """Bytes of workspace of attention."""
+        with _torch().cuda.device(self.device):
+            return int(lib().uly_cache_attention_workspace(self._d, Hq, n_rows, n_seqs))
+
+    def attention(self, q, o, starts, lens, table, scale=None, lse=None, workspace=None, stream=None):
+        """Attention of the newest tokens (q, o bf16 [rows, Hq, D]) over the cache
+        (uly_cache_attention).  lse: f32 [rows, Hq] or None.  workspace: a uint8
+        tensor of attention_workspace(Hq, rows, n_seqs) bytes; by default one is
+        allocated on the call's stream."""
+        torch = _torch()
+        n, width = self._sequences(starts, lens, table)
+        _, H, _, D = self.shape
+        dev = self.device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % H:
+            raise ValueError("q: expected bfloat16 [rows, a multiple of %d heads, %d]" % (H, D))
+        Hq = q.shape[1]
+        rows, pq, sq = _token_rows(q, Hq, D, "q", dev)
+        po = _checked_ptr(o, q.shape, torch.bfloat16, "o", dev)
+        pl = None if lse is None else _checked_ptr(lse, (rows, Hq), torch.float32, "lse", dev)
+        if not rows or not n:
+            return
+        if scale is None:
+            scale = 1.0 / math.sqrt(D)
+        key = (Hq, rows, n)
+        nbytes = self._work.get(key)
+        if nbytes is None:
+            if len(self._work) > 256:
+                self._work.clear()
+            nbytes = self._work[key] = self.attention_workspace(*key)
+        workspace = _workspace(workspace, nbytes, dev, stream)
+        self._call(lib().uly_cache_attention, "uly_cache_attention", pq, sq, Hq, rows, starts.data_ptr(),
+                   lens.data_ptr(), table.data_ptr(), n, width, scale, po, pl, workspace.data_ptr(),
+                   workspace.numel(), _raw_stream(stream, dev))

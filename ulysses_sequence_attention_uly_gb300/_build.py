@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libuly.so")
 LIB_CHECKED = os.path.join(OUT, "libuly_checked.so")
-UNITS = ("layout.cu", "attn.cu", "attn_bwd.cu", "norm_rope.cu", "uly_abi.cu")
+UNITS = ("layout.cu", "attn.cu", "attn_bwd.cu", "norm_rope.cu", "prompt.cu", "cache.cu", "uly_abi.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 _lock = threading.Lock()

@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include "grad.cuh"
+#include "serve.cuh"
 
 using namespace uly;
 
@@ -693,8 +694,8 @@ int uly_plan_test_check_narrow(uly_plan* plan, int32_t rows) {
 int64_t uly_checked_violations(int32_t reset) {
   if (!kChecked) return -1;
   if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-  const uint64_t n[4] = {layout_violations(reset != 0), attn_violations(reset != 0), bwd_violations(reset != 0),
-                         norm_violations(reset != 0)};
+  const uint64_t n[6] = {layout_violations(reset != 0), attn_violations(reset != 0), bwd_violations(reset != 0),
+                         norm_violations(reset != 0), prompt_violations(reset != 0), cache_violations(reset != 0)};
   uint64_t sum = 0;
   for (uint64_t v : n) {
     if (v == ~0ull) return -1;
@@ -1724,3 +1725,186 @@ extern "C" int uly_noalloc_sync_status(void* stream) {
   }
   return ULY_OK;
 }
+
+// ------------------------------------------------------------------------
+// Causal attention over packed prompts, and the 8-bit cache.  These calls
+// keep nothing between them: their scratch is the caller's workspace.
+namespace {
+
+constexpr int kMaxSeqs = 65536;
+constexpr int64_t kMaxRows = 1LL << 27;
+
+bool misaligned(const void* p, uintptr_t to) { return !p || (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+int64_t prompt_work(const uly_plan* pl, int32_t n_seqs) { return 256; }
+
+// Rows of H heads that may be more than a row apart: bytes between rows, and of
+// all of them; 0 for a bad stride.
+int64_t row_step(int64_t stride, int64_t dense) {
+  if (!stride) return dense * 2;
+  return stride < dense || (stride & 7) || stride > (1LL << 40) ? 0 : stride * 2;
+}
+
+int64_t rows_bytes(int64_t rows, int64_t step, int64_t dense) { return rows > 0 ? (rows - 1) * step + dense * 2 : 0; }
+
+// What the two cache calls check and fill in alike.
+int setup_cache(const uly_cache* cache, int64_t n_rows, const int32_t* starts, const int32_t* lens,
+                const int32_t* table, int32_t n_seqs, int32_t table_width, CacheParams& c, Spans& spans, bool write) {
+  if (!cache) return ULY_ERR_INVALID;
+  const uly_cache& a = *cache;
+  if (a.n_pages < 1 || a.page_rows < 1 || a.H < 1 || a.D < 1 || n_rows < 0 || n_seqs < 0 || table_width < 1)
+    return ULY_ERR_INVALID;
+  if ((a.D != 64 && a.D != 128) ||
+      (a.page_rows != 16 && a.page_rows != 32 && a.page_rows != 64 && a.page_rows != 128) || a.H > 65535 ||
+      n_seqs > kMaxSeqs || n_rows > kMaxRows)
+    return ULY_ERR_UNSUPPORTED;
+  if (misaligned(a.k_pages, 16) || misaligned(a.v_pages, 16) || misaligned(a.k_scale, 4) ||
+      misaligned(a.v_scale, 4) || misaligned(starts, 4) || misaligned(lens, 4) || misaligned(table, 4))
+    return ULY_ERR_INVALID;
+  c.k_pages = static_cast<uint8_t*>(a.k_pages);
+  c.v_pages = static_cast<uint8_t*>(a.v_pages);
+  c.k_scale = a.k_scale;
+  c.v_scale = a.v_scale;
+  c.n_pages = a.n_pages;
+  c.page_rows = a.page_rows;
+  c.page_shift = a.page_rows == 16 ? 4 : a.page_rows == 32 ? 5 : a.page_rows == 64 ? 6 : 7;
+  c.H = a.H;
+  c.starts = starts;
+  c.lens = lens;
+  c.table = table;
+  c.n_seqs = n_seqs;
+  c.table_width = table_width;
+  c.n_rows = static_cast<int32_t>(n_rows);
+  const int64_t blocks = static_cast<int64_t>(a.n_pages) * a.H;
+  spans.n = 0;
+  spans.add(a.k_pages, blocks * a.page_rows * a.D, write);
+  spans.add(a.v_pages, blocks * a.page_rows * a.D, write);
+  spans.add(a.k_scale, blocks * 4, write);
+  spans.add(a.v_scale, blocks * 4, write);
+  spans.add(starts, (static_cast<int64_t>(n_seqs) + 1) * 4, false);
+  spans.add(lens, static_cast<int64_t>(n_seqs) * 4, false);
+  spans.add(table, static_cast<int64_t>(n_seqs) * table_width * 4, false);
+  return ULY_OK;
+}
+
+int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) { return 256; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t uly_sp_prompt_attention_workspace(const uly_plan* plan, int32_t n_seqs) {
+  return plan && n_seqs >= 0 ? prompt_work(plan, n_seqs) : -1;
+}
+
+int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
+                            const int32_t* seq_starts, int32_t n_seqs, float scale, void* const* o,
+                            float* const* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!plan) return ULY_ERR_INVALID;
+  const uly_desc& d = plan->d;
+  const int P = d.P;
+  int rc;
+  if (d.B != 1 || d.rep_mode != ULY_REP_NONE || d.dtype != ULY_BF16 || n_seqs > kMaxSeqs) return ULY_ERR_UNSUPPORTED;
+  if ((rc = check_ptrs(q, P)) || (rc = check_ptrs(k, P)) || (rc = check_ptrs(v, P)) ||
+      (rc = check_ptrs(const_cast<const void* const*>(o), P)))
+    return rc;
+  if (lse)
+    for (int i = 0; i < P; ++i)
+      if (misaligned(lse[i], 4)) return ULY_ERR_INVALID;
+  if (n_seqs < 0 || misaligned(seq_starts, 4)) return ULY_ERR_INVALID;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return ULY_ERR_INVALID;
+  if (misaligned(workspace, 256) || workspace_bytes < prompt_work(plan, n_seqs)) return ULY_ERR_INVALID;
+  if ((rc = check_device(plan))) return rc;
+
+  static thread_local PromptParams p;
+  static thread_local Spans spans;
+  memset(&p, 0, sizeof(p));
+  spans.n = 0;
+  spans.add(workspace, workspace_bytes, true);
+  spans.add(seq_starts, (static_cast<int64_t>(n_seqs) + 1) * 4, false);
+  for (int i = 0; i < P; ++i) {
+    const int64_t rows = plan->lens[i], qb = rows * d.Hq * d.D * 2, kb = rows * d.Hkv * d.D * 2;
+    p.shard_begin[i + 1] = p.shard_begin[i] + plan->lens[i];
+    p.q[i] = static_cast<const uint8_t*>(q[i]);
+    p.k[i] = static_cast<const uint8_t*>(k[i]);
+    p.v[i] = static_cast<const uint8_t*>(v[i]);
+    p.out[i] = static_cast<uint8_t*>(o[i]);
+    p.lse[i] = lse ? lse[i] : nullptr;
+    spans.add(q[i], qb, false);
+    spans.add(k[i], kb, false);
+    spans.add(v[i], kb, false);
+    spans.add(o[i], qb, true);
+    spans.add(p.lse[i], rows * d.Hq * 4, true);
+  }
+  if (spans.clash()) return ULY_ERR_INVALID;
+  if (!n_seqs) return ULY_OK;
+  p.P = P;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.G = d.Hq / d.Hkv;
+  p.n_seqs = n_seqs;
+  p.lse_out = lse != nullptr;
+  p.seq_starts = seq_starts;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return launch_prompt(p, d.D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
+}
+
+int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64_t k_row_stride,
+                     int64_t v_row_stride, int64_t n_rows, const int32_t* starts, const int32_t* lens,
+                     const int32_t* table, int32_t n_seqs, int32_t table_width, void* stream) {
+  AppendParams p = {};
+  static thread_local Spans spans;
+  const int rc = setup_cache(cache, n_rows, starts, lens, table, n_seqs, table_width, p.c, spans, true);
+  if (rc) return rc;
+  const int64_t dense = static_cast<int64_t>(cache->H) * cache->D;
+  const void* const x[2] = {k, v};
+  const int64_t strides[2] = {k_row_stride, v_row_stride};
+  for (int t = 0; t < 2; ++t) {
+    if (misaligned(x[t], 16) || !(p.row_bytes[t] = row_step(strides[t], dense))) return ULY_ERR_INVALID;
+    p.x[t] = static_cast<const uint8_t*>(x[t]);
+    spans.add(x[t], rows_bytes(n_rows, p.row_bytes[t], dense), false);
+  }
+  if (spans.clash()) return ULY_ERR_INVALID;
+  if (!n_rows || !n_seqs) return ULY_OK;
+  // a CTA for every row where that is few CTAs or where most rows lead a page
+  // (a few tokens a sequence); else one for every page_rows rows
+  p.group = n_rows * cache->H * 2 <= 4096 || n_rows < 8LL * n_seqs ? 1 : cache->page_rows;
+  return launch_cache_append(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
+}
+
+int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
+  if (!cache || Hq < 1 || cache->H < 1 || Hq % cache->H || n_rows < 0 || n_seqs < 0) return -1;
+  return cached_work(cache, Hq, n_rows, n_seqs);
+}
+
+int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_stride, int32_t Hq, int64_t n_rows,
+                        const int32_t* starts, const int32_t* lens, const int32_t* table, int32_t n_seqs,
+                        int32_t table_width, float scale, void* o, float* lse, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  CachedParams p = {};
+  static thread_local Spans spans;
+  const int rc = setup_cache(cache, n_rows, starts, lens, table, n_seqs, table_width, p.c, spans, false);
+  if (rc) return rc;
+  if (Hq < 1 || Hq % cache->H || !(scale > 0.f) || !(scale < 3.0e38f)) return ULY_ERR_INVALID;
+  if (Hq > 65535) return ULY_ERR_UNSUPPORTED;
+  const int64_t dense = static_cast<int64_t>(Hq) * cache->D;
+  if (misaligned(q, 16) || misaligned(o, 16) || (lse && misaligned(lse, 4)) ||
+      !(p.q_row_bytes = row_step(q_row_stride, dense)))
+    return ULY_ERR_INVALID;
+  if (misaligned(workspace, 256) || workspace_bytes < cached_work(cache, Hq, n_rows, n_seqs)) return ULY_ERR_INVALID;
+  spans.add(q, rows_bytes(n_rows, p.q_row_bytes, dense), false);
+  spans.add(o, n_rows * dense * 2, true);
+  spans.add(lse, n_rows * Hq * 4, true);
+  spans.add(workspace, workspace_bytes, true);
+  if (spans.clash()) return ULY_ERR_INVALID;
+  if (!n_rows || !n_seqs) return ULY_OK;
+  p.q = static_cast<const uint8_t*>(q);
+  p.Hq = Hq;
+  p.G = Hq / cache->H;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = static_cast<uint8_t*>(o);
+  p.lse = lse;
+  return launch_cache_attention(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
+}
+
+}  // extern "C"
