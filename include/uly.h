@@ -158,6 +158,7 @@ int uly_plan_set_wait_limit(uly_plan* plan, uint64_t ns);
  * K_0, V_0, K_1, V_1, ...), so the consumer's bounded wait expires and the
  * call reports ULY_ERR_TIMEOUT through uly_sync_status (nothing hangs or
  * faults; the kernels drain and free TMEM).  -1 (the default) disables it.
+ * (uly_sp_prompt_attention's too, counted over all that a CTA works on.)
  * The backward kernels withhold the load of that number of each CTA's moving
  * tiles (Q for dk and dv, K for dq).  Outputs of a call made with the hook set
  * are undefined. */
@@ -521,8 +522,8 @@ int64_t uly_norm_rope_backward_workspace(const uly_plan* plan);
  * uly_sp_attention, lse (may be NULL) f32 [1, rows, Hq] per shard: the natural
  * logarithm of the sum of the row's exponentials.
  *   seq_starts: device int32 [n_seqs + 1], non-decreasing, within [0, rows]
- *     (values outside are clamped; sequences that overlap give undefined
- *     outputs).  A sequence may be empty.  o and lse of rows before the first
+ *     (values outside are clamped, and one below an earlier one counts as that
+ *     one).  A sequence may be empty.  o and lse of rows before the first
  *     and behind the last sequence are left as they were.
  *   k and v of a sequence's own rows have to be finite; rows of other sequences
  *     and of none may hold anything, NaN included.

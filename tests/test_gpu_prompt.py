@@ -147,6 +147,41 @@ def test_sequence_bounds_are_clamped():
     R.check_prompt(as_is, d, d["o"], d["lse"])
 
 
+def test_a_start_below_an_earlier_one_counts_as_that_one():
+    c = R.Prompt("falling", (200, 100), (300,), 4, 2, 64)
+    d = R.prompt_inputs(c, 11)
+    d["starts"] = torch.tensor([10, 150, 50, 40, 290, 0, 7], dtype=torch.int32, device="cuda")
+    run(c, d)
+    as_is = R.Prompt("falling", (200, 100), (140, 0, 0, 140, 0, 0), 4, 2, 64, first=10)
+    R.check_prompt(as_is, d, d["o"], d["lse"])
+    # past a thousand sequences, too
+    starts = [(i * 37) % 200 for i in range(2500)] + [250]
+    d = R.prompt_inputs(c, 12)
+    d["starts"] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    run(c, d)
+    top = torch.tensor(starts).cummax(0).values.tolist()
+    as_is = R.Prompt("falling", (200, 100), tuple(b - a for a, b in zip(top, top[1:])), 4, 2, 64, first=top[0])
+    R.check_prompt(as_is, d, d["o"], d["lse"])
+
+
+@pytest.mark.parametrize("fill", [0, 1, 3, 4])
+def test_a_withheld_load_times_out_and_the_next_call_is_right(fill):
+    from ulysses_sequence_attention_uly_gb300 import ULY_ERR_TIMEOUT
+    c = R.Prompt("withheld", (700, 500), (900, 300), 4, 2, 128)
+    d = R.prompt_inputs(c, 13)
+    plan = R.plan_of(c)
+    plan.set_wait_limit(20_000_000)
+    plan.test_withhold_fill(fill)
+    plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"])
+    assert plan.sync_status() == ULY_ERR_TIMEOUT
+    plan.test_withhold_fill(-1)
+    for n in ("o", "lse"):
+        for x in d[n]:
+            x.fill_(7.0)
+    run(c, d, plan)
+    R.check_prompt(c, d, d["o"], d["lse"])
+
+
 def test_refusals():
     import ulysses_sequence_attention_uly_gb300 as uly
     c = R.Prompt("refused", (64, 64), (100,), 4, 2, 64)

@@ -1,8 +1,38 @@
-// prompt.cu -- causal attention over packed sequences on the seq-sharded shards.
+// prompt.cu -- causal attention over packed sequences on the seq-sharded shards
+// (tcgen05 + TMEM + TMA).
 //
 // For row i of a sequence: softmax over its rows j <= i of scale * q_i.k_j,
 // times v_j; q head h uses kv head h / (Hq/Hkv).
-#include <cuda_bf16.h>
+//
+// tables_kernel cuts the sequences into runs (a sequence's rows in one shard)
+// and the runs into units of query rows, those with most keys first.  The
+// attention kernel is persistent, one CTA an SM; an item is a unit and a head
+// (pair), taken from a counter, so that a CTA that is done early takes more.
+//
+// An item has two 128-row query tiles that walk the same keys: one tile of two
+// q heads of a kv head where the group is even, else two tiles of one head
+// (then the first ends a key tile before the second).  Key tiles are 128 rows
+// from a run's first row on, as are query tiles, so that only a tile's last key
+// tile is cut by the diagonal and only a run's last one is short.
+//   warp 8      TMA producer: takes items, loads Q tiles, and K and V tiles
+//               through a ring of slots, in groups (V_s-1, K_s) of one step
+//               each; it goes on to the next item while this one is finished.
+//   warp 9      one thread issues the MMAs, in the order
+//                 PV0(s) S0(s+1) PV1(s) S1(s+1)
+//               where step s + 1 may be the first of the next item: the tensor
+//               core has the next item's scores done by the time the softmax
+//               warps have stored this item's output.
+//   warps 0-7   softmax of the two tiles, one thread a row, as in attn.cu: log2
+//               domain, a lazily raised reference maximum, P in bf16 over S in
+//               TMEM.  The epilogue stages its rows in shared memory of its own,
+//               so that Q's slot is free for the next item.
+// Rows of V behind a run's end (another sequence's, or nothing's) are zeroed in
+// shared memory before P V: their P is 0, but 0 times a NaN is not.
+// TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D).
+//
+// The arithmetic of an item does not depend on which CTA takes it: the same
+// bits on every call.  Every wait is bounded, as in attn.cu.
+#include <atomic>
 
 #include "serve.cuh"
 #include "tc.cuh"
@@ -22,69 +52,718 @@ uint64_t prompt_violations(bool reset) {
   return v;
 }
 
-// One warp per row and q head; the lanes share the head's elements.
+namespace {
+
+constexpr int kItems = 4;  // items under way between the roles of a CTA
+
 template <int D>
-__global__ void __launch_bounds__(256) prompt_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int E = D / 32;  // elements a lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int N = p.shard_begin[p.P];
-  if (h >= p.Hq) return;
-  // the last sequence that begins at or before the row
-  int lo = 0, hi = p.n_seqs;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (min(max(p.seq_starts[mid + 1], 0), N) > row)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  if (lo >= p.n_seqs) return;
-  const int first = min(max(p.seq_starts[lo], 0), N);
-  if (row < first) return;
-  int sh = 0;
-  while (row >= p.shard_begin[sh + 1]) ++sh;
-  const int64_t q_row = static_cast<int64_t>(p.Hq) * D * 2, kv_row = static_cast<int64_t>(p.Hkv) * D * 2;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q[sh] + (row - p.shard_begin[sh]) * q_row) + h * D;
-  float qf[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = __bfloat162float(q[lane + 32 * e]);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  int ks = 0;
-  for (int j = first; j <= row; ++j) {
-    while (j >= p.shard_begin[ks + 1]) ++ks;
-    const int64_t off = (j - p.shard_begin[ks]) * kv_row + (h / p.G) * D * 2;
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k[ks] + off);
-    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v[ks] + off);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += qf[e] * __bfloat162float(k[lane + 32 * e]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * __bfloat162float(v[lane + 32 * e]);
-  }
-  const int64_t orow = row - p.shard_begin[sh];
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out[sh] + orow * q_row) + h * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16(o[e] / l);
-  if (lane == 0 && p.lse_out) p.lse[sh][orow * p.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
+struct PCfg {
+  static constexpr int kPanelBytes = kTileRows * 128;
+  static constexpr int kTileBytes = D / 64 * kPanelBytes;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kHalf = kSlots / 2;  // groups in the ring
+  static constexpr int kQkSteps = D / 16;
+  static constexpr int kPvSteps = 8;
+  static constexpr uint32_t kIdescS = make_idesc(1, 128, 128, 0, 0);
+  static constexpr uint32_t kIdescO = make_idesc(1, 128, D, 0, 1);
+  static constexpr int kStageBytes = 32 * 128;  // a warp's 32 rows, 64 columns at a time
+  static constexpr int kSmem = 1024 + (2 + kSlots) * kTileBytes + 8 * kStageBytes;
+  static constexpr int kThreads = 320;
+  static_assert(kSmem + 1024 <= 232448, "shared memory");
+};
+
+struct Item {
+  int32_t run;      // -1: no more
+  int32_t tile;     // first q tile (128 rows) inside the run
+  int32_t head;     // first q head
+  int32_t n[2];     // key tiles of the two q tiles (0: no such tile)
+  int32_t shard, row0, len, first_run;
+  int32_t pad[3];
+};
+
+struct PBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[4], empty[4];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t drain;
+  Item item[kItems];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(0), "r"(0)
+      : "memory");
 }
 
+// wait for the launch before this one in the stream (a programmatic dependency)
+__device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---------------------------------------------------------------- tables --
+// Exclusive sum over the block's 1024 threads; *total receives the whole.
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* shared, uint64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) shared[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t w = shared[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    shared[lane] = w;
+  }
+  __syncthreads();
+  const uint64_t before = warp ? shared[warp - 1] : 0;
+  *total = shared[31];
+  __syncthreads();
+  return before + x - v;
+}
+
+// Largest of the values (none negative) up to this thread's.
+__device__ __forceinline__ int block_max(int v, uint64_t* shared64) {
+  int* const shared = reinterpret_cast<int*>(shared64);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v = max(v, y);
+  }
+  if (lane == 31) shared[warp] = v;
+  __syncthreads();
+  const int before = __reduce_max_sync(0xffffffffu, lane < warp ? shared[lane] : 0);
+  __syncthreads();
+  return max(v, before);
+}
+
+__device__ __forceinline__ int units_of(int len, int pair) {
+  return pair ? (len + kTileRows - 1) / kTileRows : (len + 2 * kTileRows - 1) / (2 * kTileRows);
+}
+
+// One CTA: runs and units of all sequences.  The units are put in order of
+// their key tiles (counting sort, largest first; which of two alike comes first
+// is chance and changes nothing).
+__global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ uint64_t sums[32];
+  __shared__ int32_t run_unit_s[kSortBuckets];
+  __shared__ int32_t bucket[kSortBuckets];
+  __shared__ int32_t last_end;
+  let_next_launch_start();
+  const PromptTables& t = p.t;
+  const int tid = threadIdx.x, N = p.shard_begin[p.P];
+  int n_runs = 0, n_units = 0, reached = 0;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 1024) {
+    // rows [a, b) of sequence s.  A start below an earlier one counts as that
+    // one, so that no row is in two sequences and the tables hold them all.
+    const int s = s0 + tid;
+    const int start = s < p.n_seqs ? min(max(p.seq_starts[s], 0), N) : 0;
+    const int end = s < p.n_seqs ? min(max(p.seq_starts[s + 1], 0), N) : 0;
+    const int a = max(block_max(start, sums), reached), b = s < p.n_seqs ? max(a, end) : a;
+    if (tid == 1023) last_end = b;
+    int runs = 0, units = 0;
+    for (int i = 0; i < p.P; ++i) {
+      const int len = min(b, p.shard_begin[i + 1]) - max(a, p.shard_begin[i]);
+      if (len > 0) {
+        ++runs;
+        units += units_of(len, p.pair);
+      }
+    }
+    uint64_t total;
+    const uint64_t before = block_sum((static_cast<uint64_t>(runs) << 32) | static_cast<uint32_t>(units), sums, &total);
+    int r = n_runs + static_cast<int>(before >> 32), u = n_units + static_cast<int>(before & 0xFFFFFFFFu);
+    const int first = r;
+    int kv = 0;
+    for (int i = 0; i < p.P; ++i) {
+      const int lo = max(a, p.shard_begin[i]), len = min(b, p.shard_begin[i + 1]) - lo;
+      if (len <= 0 || !in_bounds(&g_prompt_violations, r, 1, t.max_runs)) continue;
+      t.runs[r] = PromptRun{i, lo - p.shard_begin[i], len, first};
+      t.run_unit[r] = u;
+      if (r < kSortBuckets) run_unit_s[r] = u;
+      t.run_kv[r] = kv;
+      kv += (len + kTileRows - 1) / kTileRows;
+      u += units_of(len, p.pair);
+      ++r;
+    }
+    n_runs += static_cast<int>(total >> 32);
+    n_units += static_cast<int>(total & 0xFFFFFFFFu);
+    reached = last_end;
+  }
+  for (int i = tid; i < kSortBuckets; i += 1024) bucket[i] = 0;
+  __syncthreads();
+  const int32_t* const run_unit = n_runs <= kSortBuckets ? run_unit_s : t.run_unit;
+  // unit i of the sequences' order: its run (the last that begins at or before it)
+  auto unit = [&](int i) {
+    int lo = 0, hi = n_runs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (run_unit[mid] <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int len = t.runs[lo].len, tiles = (len + kTileRows - 1) / kTileRows;
+    const int tile = (i - run_unit[lo]) * (p.pair ? 1 : 2);
+    const int last = p.pair ? tile : min(tile + 1, tiles - 1);
+    return PromptUnit{lo, tile, t.run_kv[lo] + last + 1, 0};
+  };
+  for (int i = tid; i < n_units; i += 1024)
+    atomicAdd(&bucket[kSortBuckets - 1 - min(unit(i).n_kv >> p.sort_shift, kSortBuckets - 1)], 1);
+  __syncthreads();
+  const int c0 = bucket[2 * tid], c1 = bucket[2 * tid + 1];
+  uint64_t total;
+  const int at = static_cast<int>(block_sum(static_cast<uint64_t>(c0 + c1), sums, &total));
+  bucket[2 * tid] = at;
+  bucket[2 * tid + 1] = at + c0;
+  __syncthreads();
+  for (int i = tid; i < n_units; i += 1024) {
+    const PromptUnit u = unit(i);
+    const int place = atomicAdd(&bucket[kSortBuckets - 1 - min(u.n_kv >> p.sort_shift, kSortBuckets - 1)], 1);
+    if (in_bounds(&g_prompt_violations, place, 1, t.max_units)) t.units[place] = u;
+  }
+  if (tid == 0) {
+    t.head[0] = n_units;
+    t.head[1] = p.grid;  // (CTA b's first item is item b)
+  }
+}
+
+// ------------------------------------------------------------- attention --
+__device__ __forceinline__ void record_timeout(const PromptParams& p, volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(p.status, kStatusTimeout);
+}
+
+// The scores of columns from `limit` on become -inf.
+__device__ __forceinline__ void mask_from(uint32_t (&a)[4][32], int limit) {
+  const uint32_t ninf = __float_as_uint(-INFINITY);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (32 * c + k >= limit) a[c][k] = ninf;
+}
+
+__device__ __forceinline__ float row_max(const uint32_t (&a)[4][32]) {
+  float m[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    m[c] = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) m[c] = max3f(m[c], __uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1]));
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// p = 2^(s * sl2 + neg) for the 32-score chunks [C0, C1) of a row, in bf16 to
+// TMEM at tP as the A operand of P V; returns the sum of the f32 values.
+template <int C0, int C1>
+__device__ __forceinline__ float exp_store(const uint32_t (&a)[4][32], float sl2, float neg, uint32_t tP) {
+  const uint64_t mul = f2(sl2, sl2), add = f2(neg, neg);
+  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+  for (int c = C0; c < C1; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float x0, x1;
+      f2_split(f2_fma(f2(__uint_as_float(a[c][2 * q]), __uint_as_float(a[c][2 * q + 1])), mul, add), x0, x1);
+      const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+      acc[q & 3] = f2_add(acc[q & 3], f2(e0, e1));
+      pk[q] = pack_bf16x2(e0, e1);
+    }
+    tmem_st16(tP + 16 * c, pk);
+  }
+  float s0, s1;
+  f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+  return s0 + s1;
+}
+
+// Key tiles of an item in order: the runs of its sequence from the first on.
+struct KeyTiles {
+  const PromptRun* runs;
+  int run, tile, left;  // left: rows of the run from this tile on
+  int shard, row0;
+  __device__ __forceinline__ void begin(const PromptTables& t, const Item& it) {
+    runs = t.runs;
+    run = it.first_run;
+    enter();
+  }
+  __device__ __forceinline__ void enter() {
+    const int4 v = *reinterpret_cast<const int4*>(runs + run);
+    shard = v.x;
+    row0 = v.y;
+    left = v.z;
+    tile = 0;
+  }
+  // (not after the item's last tile: there may be no run behind it)
+  __device__ __forceinline__ void next() {
+    if (left > kTileRows) {
+      left -= kTileRows;
+      row0 += kTileRows;
+    } else {
+      ++run;
+      enter();
+    }
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV, int n_items,
+                                         uint64_t deadline) {
+  using C = PCfg<D>;
+  volatile int* abort_flag = &bars.abort_flag;
+  bool ok = true;
+  int g = 0;                // groups issued (= steps begun)
+  int n_q[2] = {0, 0};      // Q tiles loaded
+  int v_shard = 0, v_row = 0, v_head = 0;
+  // group g: V of step g - 1 and K of step g
+  auto group = [&](bool has_k, int shard, int row, int head) {
+    const int bi = g % C::kHalf;
+    if (g >= C::kHalf && !mbar_wait(smem_u32(&bars.empty[bi]), (g / C::kHalf - 1) & 1, deadline, abort_flag))
+      return false;
+    const uint32_t bf = smem_u32(&bars.full[bi]);
+    mbar_arrive_expect_tx(bf, (g > 0 && has_k ? 2 : 1) * C::kTileBytes);
+    if (g > 0 && 2 * g - 1 != p.withhold_fill)
+      tma_load_tile(sKV + (2 * g - 1) % C::kSlots * C::kTileBytes, &p.tv[v_shard], bf, v_head, v_row);
+    if (has_k && 2 * g != p.withhold_fill)
+      tma_load_tile(sKV + 2 * g % C::kSlots * C::kTileBytes, &p.tk[shard], bf, head, row);
+    v_shard = shard;
+    v_row = row;
+    v_head = head;
+    ++g;
+    return true;
+  };
+  int idx = blockIdx.x;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % kItems;
+    if (k >= kItems &&
+        !(ok = mbar_wait(smem_u32(&bars.item_empty[slot]), (k / kItems - 1) & 1, deadline, abort_flag)))
+      break;
+    Item it = {};
+    it.run = -1;
+    int next = 0;
+    if (idx < n_items) {
+      next = atomicAdd(&p.t.head[1], 1);  // (used when this item's loads are issued)
+      const int4 u = *reinterpret_cast<const int4*>(&p.t.units[idx / p.n_hp]);
+      const int hp = idx % p.n_hp;
+      const int4 r = *reinterpret_cast<const int4*>(&p.t.runs[u.x]);
+      it.run = u.x;
+      it.tile = u.y;
+      it.shard = r.x;
+      it.row0 = r.y;
+      it.len = r.z;
+      it.first_run = r.w;
+      if (p.pair) {
+        it.head = 2 * hp;
+        it.n[0] = it.n[1] = u.z;
+      } else {
+        it.head = hp;
+        const bool two = (u.y + 1) * kTileRows < r.z;
+        it.n[0] = two ? u.z - 1 : u.z;
+        it.n[1] = two ? u.z : 0;
+      }
+    }
+    bars.item[slot] = it;
+    mbar_arrive(smem_u32(&bars.item_full[slot]));
+    if (it.run < 0) break;
+    const int n = max(it.n[0], it.n[1]), kv_head = it.head / p.G;
+    KeyTiles kt;
+    kt.begin(p.t, it);
+    for (int s = 0; s < n; ++s) {
+      if (!(ok = group(true, kt.shard, kt.row0, kv_head))) break;
+      if (s == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || !it.n[i]) continue;
+          if (n_q[i] && !(ok = mbar_wait(smem_u32(&bars.q_empty[i]), (n_q[i] - 1) & 1, deadline, abort_flag)))
+            continue;
+          const uint32_t bq = smem_u32(&bars.q_full[i]);
+          mbar_arrive_expect_tx(bq, C::kTileBytes);
+          tma_load_tile(sQ + i * C::kTileBytes, &p.tq[it.shard], bq, p.pair ? it.head + i : it.head,
+                        it.row0 + (p.pair ? it.tile : it.tile + i) * kTileRows);
+          ++n_q[i];
+        }
+        if (!ok) break;
+      }
+      if (s + 1 < n) kt.next();
+    }
+    idx = next;
+  }
+  if (ok && g > 0) ok = group(false, 0, 0, 0);
+  if (!ok) record_timeout(p, abort_flag);
+  if (*abort_flag) {
+    // no copy lands in shared memory after the CTA has left (a withheld one
+    // costs the bound)
+    const uint64_t dl = globaltimer_ns() + 100000000ull;
+    volatile int never = 0;
+    for (int f = g > C::kHalf ? g - C::kHalf : 0; f < g; ++f)
+      mbar_wait(smem_u32(&bars.full[f % C::kHalf]), (f / C::kHalf) & 1, dl, &never);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (n_q[i]) mbar_wait(smem_u32(&bars.q_full[i]), (n_q[i] - 1) & 1, dl, &never);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV, uint32_t tmem,
+                                       uint64_t deadline) {
+  using C = PCfg<D>;
+  volatile int* abort_flag = &bars.abort_flag;
+  // descriptors as in attn.cu: a fixed high part and the start address / 16
+  const uint64_t hi_s = sdesc_sw128(0, 16, 1024);              // Q and K: K-major
+  const uint64_t hi_v = sdesc_sw128(0, C::kPanelBytes, 1024);  // V: MN-major
+  const uint32_t q_lo = (sQ & 0x3FFFFu) >> 4, kv_lo = (sKV & 0x3FFFFu) >> 4;
+  constexpr uint32_t kTileLo = C::kTileBytes >> 4;
+  uint64_t dq[2][C::kQkSteps], dk[C::kHalf][C::kQkSteps], dv[C::kHalf][C::kPvSteps];
+#pragma unroll
+  for (int k = 0; k < C::kQkSteps; ++k) {
+    const uint32_t off = ((k >> 2) * C::kPanelBytes + (k & 3) * 32) >> 4;
+    dq[0][k] = hi_s | (q_lo + off);
+    dq[1][k] = hi_s | (q_lo + kTileLo + off);
+#pragma unroll
+    for (int u = 0; u < C::kHalf; ++u) dk[u][k] = hi_s | (kv_lo + ((2 * u + 2) % C::kSlots) * kTileLo + off);
+  }
+#pragma unroll
+  for (int u = 0; u < C::kHalf; ++u)
+#pragma unroll
+    for (int k = 0; k < C::kPvSteps; ++k) dv[u][k] = hi_v | (kv_lo + (2 * u + 1) * kTileLo + ((k * 16 * 128) >> 4));
+
+  int n_item = 0;                       // items read
+  int left[2] = {0, 0};                 // steps of this item that a tile still has, this one included
+  int n_p[2] = {0, 0}, n_q[2] = {0, 0}; // P tiles and Q tiles waited for
+  bool first = true;                    // this item's first step
+  bool ok = true;
+  auto read_item = [&](int (&n)[2]) {
+    const int slot = n_item % kItems;
+    if (!mbar_wait(smem_u32(&bars.item_full[slot]), (n_item / kItems) & 1, deadline, abort_flag)) return false;
+    const bool end = bars.item[slot].run < 0;
+    n[0] = end ? 0 : bars.item[slot].n[0];
+    n[1] = end ? 0 : bars.item[slot].n[1];
+    mbar_arrive(smem_u32(&bars.item_empty[slot]));
+    ++n_item;
+    return true;
+  };
+  // scores of tile i for the step whose K is described by dk[u]; `more`: steps
+  // that the tile has from this one on, `fresh`: it is the item's first
+  auto scores = [&](int i, const uint64_t (&kd)[C::kQkSteps], int more, bool fresh) {
+    if (fresh) {
+      if (!mbar_wait(smem_u32(&bars.q_full[i]), n_q[i] & 1, deadline, abort_flag)) return false;
+      ++n_q[i];
+      tc_fence_after();
+    }
+#pragma unroll
+    for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem + 128 * i, dq[i][k], kd[k], C::kIdescS, k > 0);
+    mma_commit(smem_u32(&bars.s_full[i]));
+    if (more == 1) mma_commit(smem_u32(&bars.q_empty[i]));
+    return true;
+  };
+  auto values = [&](int i, const uint64_t (&vd)[C::kPvSteps]) {
+    if (!mbar_wait(smem_u32(&bars.p_full[i]), n_p[i] & 1, deadline, abort_flag)) return false;
+    ++n_p[i];
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < C::kPvSteps; ++k)
+      mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, vd[k], C::kIdescO, !first || k > 0);
+    if (left[i] == 1) mma_commit(smem_u32(&bars.o_done[i]));
+    return true;
+  };
+  ok = read_item(left);
+  if (ok && (left[0] || left[1])) {
+    ok = mbar_wait(smem_u32(&bars.full[0]), 0, deadline, abort_flag);
+    tc_fence_after();
+    // K of step 0 is in slot 0, which is dk[kHalf - 1]
+    if (ok && left[0]) ok = scores(0, dk[C::kHalf - 1], left[0], true);
+    if (ok && left[1]) ok = scores(1, dk[C::kHalf - 1], left[1], true);
+    if (ok) mma_commit(smem_u32(&bars.empty[0]));
+    uint32_t turn = 0;  // parity of the ring's turn
+    bool more = true;
+    while (ok && more) {
+#pragma unroll
+      for (int u = 0; u < C::kHalf; ++u) {  // step s = turn * kHalf + u; its V and the next K are group s + 1
+        if (!ok || !more) break;
+        int next[2];
+        const bool last = max(left[0], left[1]) == 1;
+        if (last) {
+          if (!(ok = read_item(next))) break;
+          more = next[0] || next[1];
+        } else {
+          next[0] = max(left[0] - 1, 0);
+          next[1] = max(left[1] - 1, 0);
+        }
+        constexpr int kLastU = C::kHalf - 1;
+        const int bi = (u + 1) % C::kHalf;
+        if (!(ok = mbar_wait(smem_u32(&bars.full[bi]), u == kLastU ? (turn + 1) & 1 : turn & 1, deadline, abort_flag)))
+          break;
+        tc_fence_after();
+        if (left[0] && !(ok = values(0, dv[u]))) break;
+        if (next[0] && !(ok = scores(0, dk[u], next[0], last))) break;
+        if (left[1] && !(ok = values(1, dv[u]))) break;
+        if (next[1] && !(ok = scores(1, dk[u], next[1], last))) break;
+        if (more) mma_commit(smem_u32(&bars.empty[bi]));
+        left[0] = next[0];
+        left[1] = next[1];
+        first = last;
+      }
+      ++turn;
+    }
+  }
+  if (!ok) record_timeout(p, abort_flag);
+  // every MMA has completed before TMEM is released
+  mma_commit(smem_u32(&bars.drain));
+  volatile int never = 0;
+  if (!mbar_wait(smem_u32(&bars.drain), 0, globaltimer_ns() + 100000000ull, &never)) record_timeout(p, abort_flag);
+}
+
+template <int D>
+__device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint32_t sKV, uint32_t sStage,
+                                        uint32_t tmem, int warp, int lane, uint64_t deadline) {
+  using C = PCfg<D>;
+  volatile int* abort_flag = &bars.abort_flag;
+  const int wg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+  const uint32_t tS = tmem + lane_off + 128 * wg, tO = tmem + lane_off + 256 + D * wg;
+  const uint32_t stage = sStage + warp * C::kStageBytes;
+  const float sl2 = p.scale_log2;
+  int n_s = 0, n_o = 0, step0 = 0;  // S tiles and O tiles waited for; steps of the items before
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int slot = k % kItems;
+    if (!__all_sync(0xffffffffu,
+                    mbar_wait(smem_u32(&bars.item_full[slot]), (k / kItems) & 1, deadline, abort_flag))) {
+      ok = false;
+      break;
+    }
+    const Item it = bars.item[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[slot]));
+    if (it.run < 0) break;
+    const int n = wg ? it.n[1] : it.n[0];
+    if (n > 0) {
+      float m_ref = -INFINITY, l_run = 0.f;
+      KeyTiles kt;
+      kt.begin(p.t, it);
+      for (int s = 0; s < n; ++s) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[wg]), n_s & 1, deadline, abort_flag))) {
+          ok = false;
+          break;
+        }
+        ++n_s;
+        tc_fence_after();
+        uint32_t a[4][32];
+        const bool diagonal = s + 1 == n, cut = kt.left < kTileRows;
+        const int valid = kt.left;  // keys of the tile that the run has (128 or more: all)
+        float m_row;
+        if (!diagonal && !cut) {
+          float mc[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, a[c], mc[c]);
+          tmem_wait_ld();
+          m_row = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, a[c]);
+          tmem_wait_ld();
+          mask_from(a, diagonal ? min(valid, row + 1) : valid);
+          m_row = row_max(a);
+        }
+        if (s + 1 < n) kt.next();
+        const float m_new = m_row * sl2;
+        float alpha = 1.f;
+        if (m_new > m_ref + 8.f) {
+          alpha = ex2_approx(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        float sum = exp_store<0, 2>(a, sl2, neg, tS);
+        // (the product before this S, which used O, has completed with it)
+        if (s > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st16(tO + c0, o);
+          }
+        }
+        sum += exp_store<2, 4>(a, sl2, neg, tS);
+        if (cut) {
+          // V's rows behind the run's end: zero (both tiles' warps do it, each
+          // before its own product)
+          const int st = step0 + s, gr = st + 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[gr % C::kHalf]), (gr / C::kHalf) & 1, deadline,
+                                                 abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (row >= valid) {
+            const uint32_t v = sKV + (2 * st + 1) % C::kSlots * C::kTileBytes + row * 128;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) st_shared_v4(v + i * C::kPanelBytes + 16 * c, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[wg]));
+        l_run = l_run * alpha + sum;
+      }
+      if (!ok) break;
+      // ---- epilogue
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.o_done[wg]), n_o & 1, deadline, abort_flag))) {
+        ok = false;
+        break;
+      }
+      ++n_o;
+      tc_fence_after();
+      const int tile = p.pair ? it.tile : it.tile + wg, head = p.pair ? it.head + wg : it.head;
+      const int row0 = tile * kTileRows + q4 * 32;  // the warp's first row inside the run
+      const float inv = 1.f / l_run;  // (a row has itself: l_run > 0, NaN inputs aside)
+      uint8_t* const base = p.out[it.shard] + static_cast<int64_t>(head) * D * 2 + (lane & 7) * 16;
+      const int64_t row_bytes = static_cast<int64_t>(p.Hq) * D * 2;
+      const int shard_rows = p.shard_begin[it.shard + 1] - p.shard_begin[it.shard];
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        // 64 columns of the warp's rows through shared memory: 16-byte piece c
+        // of row r at piece c ^ (r mod 8); stored eight lanes a row
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[32];
+          tmem_ld32(tO + c0 + 32 * half, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+            st_shared_v4(stage + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int r = i + (lane >> 3);
+          if (row0 + r < it.len && in_bounds(&g_prompt_violations, it.row0 + row0 + r, 1, shard_rows))
+            *reinterpret_cast<uint4*>(base + (it.row0 + row0 + r) * row_bytes + c0 * 2) =
+                ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        }
+        __syncwarp();
+      }
+      if (p.lse_out && row0 + lane < it.len && in_bounds(&g_prompt_violations, it.row0 + row0 + lane, 1, shard_rows))
+        p.lse[it.shard][static_cast<int64_t>(it.row0 + row0 + lane) * p.Hq + head] =
+            (m_ref + lg2_approx(l_run)) * 0.6931471805599453f;
+    }
+    step0 += max(it.n[0], it.n[1]);
+  }
+  if (!ok) record_timeout(p, abort_flag);
+}
+
+template <int D>
+__global__ void __launch_bounds__(320, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  using C = PCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PBars bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = sbase, sKV = sbase + 2 * C::kTileBytes, sStage = sKV + C::kSlots * C::kTileBytes;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.q_full[i]), 1);
+      mbar_init(smem_u32(&bars.q_empty[i]), 1);
+      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.p_full[i]), 4);
+      mbar_init(smem_u32(&bars.o_done[i]), 1);
+    }
+    for (int i = 0; i < C::kHalf; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_u32(&bars.item_full[i]), 1);
+      mbar_init(smem_u32(&bars.item_empty[i]), 9);  // the softmax warps and the issuer
+    }
+    mbar_init(smem_u32(&bars.drain), 1);
+    bars.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&bars.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  wait_for_previous_launch();  // the tables
+  const uint32_t tmem = bars.tmem_base;
+  const int n_items = p.t.head[0] * p.n_hp;
+  const uint64_t deadline = globaltimer_ns() + p.wait_ns;
+  if (blockIdx.x < n_items) {
+    if (warp == 8) {
+      if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, deadline);
+    } else if (warp == 9) {
+      if (lane == 0) issuer<D>(p, bars, sQ, sKV, tmem, deadline);
+    } else {
+      softmax<D>(p, bars, sKV, sStage, tmem, warp, lane, deadline);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const PromptParams& p, cudaStream_t s) {
+  using C = PCfg<D>;
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  tables_kernel<<<1, 1024, 0, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the attention's CTAs come up while the tables are written
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<D>, p);
+}
+
+}  // namespace
+
 cudaError_t launch_prompt(const PromptParams& p, int D, cudaStream_t s) {
-  const dim3 grid(p.shard_begin[p.P], (p.Hq + 7) / 8);
-  if (D == 128)
-    prompt_kernel<128><<<grid, 256, 0, s>>>(p);
-  else
-    prompt_kernel<64><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return D == 128 ? launch<128>(p, s) : launch<64>(p, s);
 }
 
 }  // namespace uly

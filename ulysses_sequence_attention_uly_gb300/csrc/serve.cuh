@@ -10,17 +10,54 @@ uint64_t cache_violations(bool reset);
 
 // --------------------------------------------------------------- prompts --
 // Causal attention over packed sequences on the shards (uly_sp_prompt_attention).
+
+// Rows of one sequence in one shard, in global row order.
+struct PromptRun {
+  int32_t shard;
+  int32_t row0;       // first row inside the shard
+  int32_t len;        // at least 1
+  int32_t first_run;  // the sequence's first run
+};
+
+// Query rows that a CTA takes at a time: one 128-row tile of two q heads, or
+// (an odd number of q heads a kv head) two tiles of one head.
+struct PromptUnit {
+  int32_t run;
+  int32_t tile;       // its (first) tile inside the run
+  int32_t n_kv;       // 128-key tiles up to the diagonal of its (last) tile
+  int32_t pad;
+};
+
+// Written by tables_kernel, in the caller's workspace.
+struct PromptTables {
+  int32_t* head;      // [0] units, [1] the next item that no CTA has taken
+  PromptRun* runs;    // [n_seqs + P]
+  int32_t* run_unit;  // [n_seqs + P + 1] units before the run
+  int32_t* run_kv;    // [n_seqs + P] 128-key tiles of the sequence before the run
+  PromptUnit* units;  // [max_units] those with most tiles first
+  int32_t max_runs, max_units;
+};
+
 struct PromptParams {
-  const uint8_t* q[kMaxRanks];
-  const uint8_t* k[kMaxRanks];
-  const uint8_t* v[kMaxRanks];
+  CUtensorMap tq[kMaxRanks];
+  CUtensorMap tk[kMaxRanks];
+  CUtensorMap tv[kMaxRanks];
+  PromptTables t;
   uint8_t* out[kMaxRanks];
   float* lse[kMaxRanks];
   int32_t shard_begin[kMaxRanks + 1];  // global row of each shard's first row; [P]: all rows
-  int32_t P, Hq, Hkv, G, n_seqs, lse_out;
+  int32_t P, Hq, G, n_seqs, lse_out;
+  int32_t pair;       // two q heads of one kv head an item (else two tiles of one head)
+  int32_t n_hp;       // items of one unit: Hq / 2 or Hq
+  int32_t sort_shift; // a unit's place in the order goes by n_kv >> sort_shift
+  int32_t grid;
   const int32_t* seq_starts;
   float scale_log2;
+  int32_t* status;
+  uint64_t wait_ns;
+  int32_t withhold_fill;  // test hook, as in AttnParams
 };
+constexpr int kSortBuckets = 2048;
 
 // ----------------------------------------------------------------- cache --
 struct CacheParams {

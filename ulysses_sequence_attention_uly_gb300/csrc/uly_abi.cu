@@ -1736,7 +1736,26 @@ constexpr int64_t kMaxRows = 1LL << 27;
 
 bool misaligned(const void* p, uintptr_t to) { return !p || (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-int64_t prompt_work(const uly_plan* pl, int32_t n_seqs) { return 256; }
+// Tables of the prompt kernels (serve.cuh) in the workspace.  A sequence's rows
+// are cut where a shard ends, so there are less than n_seqs + P runs; 128-row
+// tiles of them, less than one for every 128 rows and one a run.
+int64_t prompt_tables(const uly_plan* pl, int32_t n_seqs, uint8_t* ws, PromptTables* t) {
+  const int64_t runs = static_cast<int64_t>(n_seqs) + pl->d.P, units = pl->nq / kTileRows + runs;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* const a = ws + at;
+    at = align256(at + bytes);
+    return a;
+  };
+  t->head = reinterpret_cast<int32_t*>(take(8));
+  t->runs = reinterpret_cast<PromptRun*>(take(runs * sizeof(PromptRun)));
+  t->run_unit = reinterpret_cast<int32_t*>(take((runs + 1) * 4));
+  t->run_kv = reinterpret_cast<int32_t*>(take(runs * 4));
+  t->units = reinterpret_cast<PromptUnit*>(take(units * sizeof(PromptUnit)));
+  t->max_runs = static_cast<int32_t>(runs);
+  t->max_units = static_cast<int32_t>(units);
+  return at;
+}
 
 // Rows of H heads that may be more than a row apart: bytes between rows, and of
 // all of them; 0 for a bad stride.
@@ -1794,7 +1813,8 @@ int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t 
 extern "C" {
 
 int64_t uly_sp_prompt_attention_workspace(const uly_plan* plan, int32_t n_seqs) {
-  return plan && n_seqs >= 0 ? prompt_work(plan, n_seqs) : -1;
+  PromptTables t;
+  return plan && n_seqs >= 0 ? prompt_tables(plan, n_seqs, nullptr, &t) : -1;
 }
 
 int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const void* const* k, const void* const* v,
@@ -1813,21 +1833,20 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
       if (misaligned(lse[i], 4)) return ULY_ERR_INVALID;
   if (n_seqs < 0 || misaligned(seq_starts, 4)) return ULY_ERR_INVALID;
   if (!(scale > 0.f) || !(scale < 3.0e38f)) return ULY_ERR_INVALID;
-  if (misaligned(workspace, 256) || workspace_bytes < prompt_work(plan, n_seqs)) return ULY_ERR_INVALID;
-  if ((rc = check_device(plan))) return rc;
-
-  static thread_local PromptParams p;
+  static thread_local PromptParams p;  // ~7 KB: keep it off the stack
   static thread_local Spans spans;
   memset(&p, 0, sizeof(p));
+  if (misaligned(workspace, 256) ||
+      workspace_bytes < prompt_tables(plan, n_seqs, static_cast<uint8_t*>(workspace), &p.t))
+    return ULY_ERR_INVALID;
+  if ((rc = check_device(plan))) return rc;
+
   spans.n = 0;
   spans.add(workspace, workspace_bytes, true);
   spans.add(seq_starts, (static_cast<int64_t>(n_seqs) + 1) * 4, false);
   for (int i = 0; i < P; ++i) {
     const int64_t rows = plan->lens[i], qb = rows * d.Hq * d.D * 2, kb = rows * d.Hkv * d.D * 2;
     p.shard_begin[i + 1] = p.shard_begin[i] + plan->lens[i];
-    p.q[i] = static_cast<const uint8_t*>(q[i]);
-    p.k[i] = static_cast<const uint8_t*>(k[i]);
-    p.v[i] = static_cast<const uint8_t*>(v[i]);
     p.out[i] = static_cast<uint8_t*>(o[i]);
     p.lse[i] = lse ? lse[i] : nullptr;
     spans.add(q[i], qb, false);
@@ -1838,10 +1857,27 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
   }
   if (spans.clash()) return ULY_ERR_INVALID;
   if (!n_seqs) return ULY_OK;
+  for (int i = 0; i < P; ++i) {
+    const int64_t rows = plan->lens[i];
+    if ((rc = encode_panel_map(&p.tq[i], q[i], d.D, d.Hq, rows, rows, 1)) ||
+        (rc = encode_panel_map(&p.tk[i], k[i], d.D, d.Hkv, rows, rows, 1)) ||
+        (rc = encode_panel_map(&p.tv[i], v[i], d.D, d.Hkv, rows, rows, 1)))
+      return rc;
+  }
   p.P = P;
   p.Hq = d.Hq;
-  p.Hkv = d.Hkv;
   p.G = d.Hq / d.Hkv;
+  // two heads that share k and v walk the same tiles to the end; with two tiles
+  // of one head the first idles for the last tile's time
+  p.pair = p.G % 2 == 0;
+  p.n_hp = p.pair ? d.Hq / 2 : d.Hq;
+  if (static_cast<int64_t>(p.t.max_units) * p.n_hp > 0x7FFF0000) return ULY_ERR_UNSUPPORTED;
+  for (int64_t tiles = plan->nq / kTileRows + P; (tiles >> p.sort_shift) >= kSortBuckets;) ++p.sort_shift;
+  p.grid = plan->sm_count;
+  if (static_cast<int64_t>(p.t.max_units) * p.n_hp < p.grid) p.grid = p.t.max_units * p.n_hp;
+  p.status = plan->status;
+  p.wait_ns = plan->wait_ns;
+  p.withhold_fill = plan->withhold_fill;
   p.n_seqs = n_seqs;
   p.lse_out = lse != nullptr;
   p.seq_starts = seq_starts;
