@@ -354,7 +354,6 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     it.run = -1;
     int next = 0;
     if (idx < n_items) {
-      next = atomicAdd(&p.t.head[1], 1);  // (used when this item's loads are issued)
       const int4 u = *reinterpret_cast<const int4*>(&p.t.units[idx / p.n_hp]);
       const int hp = idx % p.n_hp;
       const int4 r = *reinterpret_cast<const int4*>(&p.t.runs[u.x]);
@@ -381,6 +380,9 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     KeyTiles kt;
     kt.begin(p.t, it);
     for (int s = 0; s < n; ++s) {
+      // the next item is taken as late as it can be without a wait for it:
+      // whoever is behind takes less
+      if (s == max(n - 2, 0)) next = atomicAdd(&p.t.head[1], 1);
       if (!(ok = group(true, kt.shard, kt.row0, kv_head))) break;
       if (s == 0) {
 #pragma unroll
@@ -425,6 +427,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
   const uint64_t hi_v = sdesc_sw128(0, C::kPanelBytes, 1024);  // V: MN-major
   const uint32_t q_lo = (sQ & 0x3FFFFu) >> 4, kv_lo = (sKV & 0x3FFFFu) >> 4;
   constexpr uint32_t kTileLo = C::kTileBytes >> 4;
+  constexpr int kUnroll = 4;  // steps a turn of the loop: the jump back costs the issuer
   uint64_t dq[2][C::kQkSteps], dk[C::kHalf][C::kQkSteps], dv[C::kHalf][C::kPvSteps];
 #pragma unroll
   for (int k = 0; k < C::kQkSteps; ++k) {
@@ -439,83 +442,128 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
 #pragma unroll
     for (int k = 0; k < C::kPvSteps; ++k) dv[u][k] = hi_v | (kv_lo + (2 * u + 1) * kTileLo + ((k * 16 * 128) >> 4));
 
-  int n_item = 0;                       // items read
-  int left[2] = {0, 0};                 // steps of this item that a tile still has, this one included
-  int n_p[2] = {0, 0}, n_q[2] = {0, 0}; // P tiles and Q tiles waited for
-  bool first = true;                    // this item's first step
-  bool ok = true;
-  auto read_item = [&](int (&n)[2]) {
+  int n_item = 0;                // items read
+  int left0 = 0, left1 = 0;      // steps of this item that a tile still has, this one included
+  uint32_t par_p0 = 0, par_p1 = 0, par_q0 = 0, par_q1 = 0;
+  uint32_t acc = 0;              // the item has had a step
+  uint32_t turn = 0;             // turns of the ring: step s = turn * kHalf + u
+  int u = 0;
+  bool ok = true, more = false;
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    ok = mbar_wait(smem_u32(&bar), parity & 1, deadline, abort_flag);
+    tc_fence_after();
+    return ok;
+  };
+  auto read_item = [&](int& n0, int& n1) {
     const int slot = n_item % kItems;
-    if (!mbar_wait(smem_u32(&bars.item_full[slot]), (n_item / kItems) & 1, deadline, abort_flag)) return false;
+    if (!wait(bars.item_full[slot], n_item / kItems)) return false;
     const bool end = bars.item[slot].run < 0;
-    n[0] = end ? 0 : bars.item[slot].n[0];
-    n[1] = end ? 0 : bars.item[slot].n[1];
+    n0 = end ? 0 : bars.item[slot].n[0];
+    n1 = end ? 0 : bars.item[slot].n[1];
     mbar_arrive(smem_u32(&bars.item_empty[slot]));
     ++n_item;
     return true;
   };
-  // scores of tile i for the step whose K is described by dk[u]; `more`: steps
-  // that the tile has from this one on, `fresh`: it is the item's first
-  auto scores = [&](int i, const uint64_t (&kd)[C::kQkSteps], int more, bool fresh) {
+  // Any step: a tile may end, or begin the next item.  The descriptors are
+  // worked out here; K of the next step is in slot 2u + 2, V of this one in 2u + 1.
+  auto scores = [&](int i, int ku, int steps, bool fresh, uint32_t& par_q) {
     if (fresh) {
-      if (!mbar_wait(smem_u32(&bars.q_full[i]), n_q[i] & 1, deadline, abort_flag)) return false;
-      ++n_q[i];
-      tc_fence_after();
+      if (!wait(bars.q_full[i], par_q)) return;
+      par_q ^= 1;
     }
+    const uint32_t k_lo = kv_lo + (2 * ku + 2) % C::kSlots * kTileLo;
 #pragma unroll
-    for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem + 128 * i, dq[i][k], kd[k], C::kIdescS, k > 0);
+    for (int k = 0; k < C::kQkSteps; ++k) {
+      const uint32_t off = ((k >> 2) * C::kPanelBytes + (k & 3) * 32) >> 4;
+      mma_bf16_ss(tmem + 128 * i, hi_s | (q_lo + i * kTileLo + off), hi_s | (k_lo + off), C::kIdescS, k > 0);
+    }
     mma_commit(smem_u32(&bars.s_full[i]));
-    if (more == 1) mma_commit(smem_u32(&bars.q_empty[i]));
-    return true;
+    if (steps == 1) mma_commit(smem_u32(&bars.q_empty[i]));  // the item's last scores of this tile
   };
-  auto values = [&](int i, const uint64_t (&vd)[C::kPvSteps]) {
-    if (!mbar_wait(smem_u32(&bars.p_full[i]), n_p[i] & 1, deadline, abort_flag)) return false;
-    ++n_p[i];
-    tc_fence_after();
+  auto values = [&](int i, int steps, uint32_t& par_p) {
+    if (!wait(bars.p_full[i], par_p)) return;
+    par_p ^= 1;
+    const uint32_t v_lo = kv_lo + (2 * u + 1) * kTileLo;
 #pragma unroll
     for (int k = 0; k < C::kPvSteps; ++k)
-      mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, vd[k], C::kIdescO, !first || k > 0);
-    if (left[i] == 1) mma_commit(smem_u32(&bars.o_done[i]));
-    return true;
+      mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, hi_v | (v_lo + ((k * 16 * 128) >> 4)), C::kIdescO,
+                  acc | (k > 0));
+    if (steps == 1) mma_commit(smem_u32(&bars.o_done[i]));
   };
-  ok = read_item(left);
-  if (ok && (left[0] || left[1])) {
-    ok = mbar_wait(smem_u32(&bars.full[0]), 0, deadline, abort_flag);
-    tc_fence_after();
-    // K of step 0 is in slot 0, which is dk[kHalf - 1]
-    if (ok && left[0]) ok = scores(0, dk[C::kHalf - 1], left[0], true);
-    if (ok && left[1]) ok = scores(1, dk[C::kHalf - 1], left[1], true);
-    if (ok) mma_commit(smem_u32(&bars.empty[0]));
-    uint32_t turn = 0;  // parity of the ring's turn
-    bool more = true;
-    while (ok && more) {
+  auto any_step = [&]() {
+    int next0, next1;
+    const bool last = max(left0, left1) == 1;
+    if (last) {
+      if (!read_item(next0, next1)) return;
+      more = next0 || next1;
+    } else {
+      next0 = max(left0 - 1, 0);
+      next1 = max(left1 - 1, 0);
+    }
+    const int bi = (u + 1) % C::kHalf;
+    if (!wait(bars.full[bi], turn + (u == C::kHalf - 1 ? 1 : 0))) return;
+    if (left0) values(0, left0, par_p0);
+    if (ok && next0) scores(0, u, next0, last, par_q0);
+    if (ok && left1) values(1, left1, par_p1);
+    if (ok && next1) scores(1, u, next1, last, par_q1);
+    if (!ok) return;
+    if (more) mma_commit(smem_u32(&bars.empty[bi]));
+    left0 = next0;
+    left1 = next1;
+    acc = last ? 0 : 1;
+    u = bi;
+    if (!bi) ++turn;
+  };
+  if (read_item(left0, left1) && (left0 || left1)) {
+    more = true;
+    if (wait(bars.full[0], 0)) {
+      // (K of step 0 is in slot 0)
+      if (left0) scores(0, C::kHalf - 1, left0, true, par_q0);
+      if (ok && left1) scores(1, C::kHalf - 1, left1, true, par_q1);
+      if (ok) mma_commit(smem_u32(&bars.empty[0]));
+    }
+  }
+  while (ok && more) {
+    // Steps in the middle of an item, both tiles going on: with nothing to
+    // decide and every descriptor ready, since what the issuer spends between
+    // two instructions the tensor core waits for.
+    int plain = u ? 0 : min(left0, left1) - 1;
+    if (plain <= 0) {
+      any_step();
+      continue;
+    }
+    left0 -= plain;
+    left1 -= plain;
+    while (ok && plain > 0) {
 #pragma unroll
-      for (int u = 0; u < C::kHalf; ++u) {  // step s = turn * kHalf + u; its V and the next K are group s + 1
-        if (!ok || !more) break;
-        int next[2];
-        const bool last = max(left[0], left[1]) == 1;
-        if (last) {
-          if (!(ok = read_item(next))) break;
-          more = next[0] || next[1];
-        } else {
-          next[0] = max(left[0] - 1, 0);
-          next[1] = max(left[1] - 1, 0);
-        }
+      for (int w = 0; w < kUnroll; ++w) {
         constexpr int kLastU = C::kHalf - 1;
-        const int bi = (u + 1) % C::kHalf;
-        if (!(ok = mbar_wait(smem_u32(&bars.full[bi]), u == kLastU ? (turn + 1) & 1 : turn & 1, deadline, abort_flag)))
-          break;
-        tc_fence_after();
-        if (left[0] && !(ok = values(0, dv[u]))) break;
-        if (next[0] && !(ok = scores(0, dk[u], next[0], last))) break;
-        if (left[1] && !(ok = values(1, dv[u]))) break;
-        if (next[1] && !(ok = scores(1, dk[u], next[1], last))) break;
-        if (more) mma_commit(smem_u32(&bars.empty[bi]));
-        left[0] = next[0];
-        left[1] = next[1];
-        first = last;
+        const int uu = w % C::kHalf, bi = (uu + 1) % C::kHalf;
+        if (plain == 0) break;
+        if (!wait(bars.full[bi], uu == kLastU ? turn + 1 : turn)) break;
+        if (!wait(bars.p_full[0], par_p0)) break;
+#pragma unroll
+        for (int k = 0; k < C::kPvSteps; ++k) mma_bf16_ts(tmem + 256, tmem + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
+#pragma unroll
+        for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem, dq[0][k], dk[uu][k], C::kIdescS, k > 0);
+        mma_commit(smem_u32(&bars.s_full[0]));
+        if (plain == 1 && left0 == 1) mma_commit(smem_u32(&bars.q_empty[0]));
+        if (!wait(bars.p_full[1], par_p1)) break;
+#pragma unroll
+        for (int k = 0; k < C::kPvSteps; ++k)
+          mma_bf16_ts(tmem + 256 + D, tmem + 128 + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
+#pragma unroll
+        for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem + 128, dq[1][k], dk[uu][k], C::kIdescS, k > 0);
+        mma_commit(smem_u32(&bars.s_full[1]));
+        if (plain == 1 && left1 == 1) mma_commit(smem_u32(&bars.q_empty[1]));
+        mma_commit(smem_u32(&bars.empty[bi]));
+        par_p0 ^= 1;
+        par_p1 ^= 1;
+        acc = 1;
+        u = bi;
+        if (uu == kLastU) ++turn;
+        --plain;
       }
-      ++turn;
     }
   }
   if (!ok) record_timeout(p, abort_flag);
@@ -544,9 +592,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
       ok = false;
       break;
     }
-    const Item it = bars.item[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[slot]));
+    const Item& it = bars.item[slot];
     if (it.run < 0) break;
     const int n = wg ? it.n[1] : it.n[0];
     if (n > 0) {
@@ -670,6 +716,8 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
             (m_ref + lg2_approx(l_run)) * 0.6931471805599453f;
     }
     step0 += max(it.n[0], it.n[1]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[slot]));
   }
   if (!ok) record_timeout(p, abort_flag);
 }
