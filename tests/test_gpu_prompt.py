@@ -27,6 +27,11 @@ CASES = [
     R.Prompt("long rows", (2000, 1300), (3200,), 4, 2, 128, first=7, std=0.7),
     R.Prompt("long rows, odd group", (2000, 1300), (3200,), 6, 2, 64, first=7),
     R.Prompt("peaked", (512,), (512,), 4, 2, 128, std=4.0),
+    # (more items than SMs: the ones above mostly have fewer)
+    R.Prompt("tile ends, many heads", (1500,), (127, 128, 129, 255, 256, 257, 1), 48, 8, 128, first=100),
+    R.Prompt("tile ends, many odd groups", (1500,), (127, 128, 129, 255, 256, 257, 1), 24, 8, 64, first=100),
+    R.Prompt("long rows, many heads", (2000, 1300, 9, 700), (3200, 0, 77, 700), 32, 8, 128, first=7, std=0.7),
+    R.Prompt("long rows, many odd groups", (2000, 1300), (3200, 50), 20, 20, 128, first=7),
     R.Prompt("no rows", (64,), (0, 0), 2, 2, 64, first=9),
 ]
 

@@ -78,7 +78,8 @@ struct Item {
   int32_t head;     // first q head
   int32_t n[2];     // key tiles of the two q tiles (0: no such tile)
   int32_t shard, row0, len, first_run;
-  int32_t pad[3];
+  int32_t first_len;  // rows of the sequence's first run
+  int32_t pad[2];
 };
 
 struct PBars {
@@ -88,6 +89,8 @@ struct PBars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
   Item item[kItems];
+  PromptRun run[kMaxRanks];  // direct: the runs of the CTA's sequence
+  PromptUnit unit;           // direct: the CTA's unit, its run among them
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -98,6 +101,19 @@ __device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(0), "r"(0)
       : "memory");
+}
+
+// Has the phase completed?  (Does not wait.)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // wait for the launch before this one in the stream (a programmatic dependency)
@@ -155,7 +171,7 @@ __device__ __forceinline__ int units_of(int len, int pair) {
 // One CTA: runs and units of all sequences.  The units are put in order of
 // their key tiles (counting sort, largest first; which of two alike comes first
 // is chance and changes nothing).
-__global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(1024) tables_kernel(const __grid_constant__ PromptCut p) {
   __shared__ uint64_t sums[32];
   __shared__ int32_t run_unit_s[kSortBuckets];
   __shared__ int32_t bucket[kSortBuckets];
@@ -244,67 +260,133 @@ __device__ __forceinline__ void record_timeout(const PromptParams& p, volatile i
   atomicOr(p.status, kStatusTimeout);
 }
 
-// The scores of columns from `limit` on become -inf.
-__device__ __forceinline__ void mask_from(uint32_t (&a)[4][32], int limit) {
-  const uint32_t ninf = __float_as_uint(-INFINITY);
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (32 * c + k >= limit) a[c][k] = ninf;
-}
-
-__device__ __forceinline__ float row_max(const uint32_t (&a)[4][32]) {
-  float m[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    m[c] = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) m[c] = max3f(m[c], __uint_as_float(a[c][k]), __uint_as_float(a[c][k + 1]));
-  }
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-}
-
-// p = 2^(s * sl2 + neg) for the 32-score chunks [C0, C1) of a row, in bf16 to
-// TMEM at tP as the A operand of P V; returns the sum of the f32 values.
-template <int C0, int C1>
-__device__ __forceinline__ float exp_store(const uint32_t (&a)[4][32], float sl2, float neg, uint32_t tP) {
+// p = 2^(s * sl2 + neg) for 32 scores of a row, in bf16 to TMEM at tP as part of
+// the A operand of P V; adds the f32 values to acc.
+__device__ __forceinline__ void exp_store(const uint32_t (&a)[32], float sl2, float neg, uint32_t tP,
+                                          uint64_t (&acc)[4]) {
   const uint64_t mul = f2(sl2, sl2), add = f2(neg, neg);
-  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+  uint32_t pk[16];
 #pragma unroll
-  for (int c = C0; c < C1; ++c) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float x0, x1;
-      f2_split(f2_fma(f2(__uint_as_float(a[c][2 * q]), __uint_as_float(a[c][2 * q + 1])), mul, add), x0, x1);
-      const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-      acc[q & 3] = f2_add(acc[q & 3], f2(e0, e1));
-      pk[q] = pack_bf16x2(e0, e1);
-    }
-    tmem_st16(tP + 16 * c, pk);
+  for (int q = 0; q < 16; ++q) {
+    float x0, x1;
+    f2_split(f2_fma(f2(__uint_as_float(a[2 * q]), __uint_as_float(a[2 * q + 1])), mul, add), x0, x1);
+    const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+    acc[q & 3] = f2_add(acc[q & 3], f2(e0, e1));
+    pk[q] = pack_bf16x2(e0, e1);
   }
+  tmem_st16(tP, pk);
+}
+
+// The running output to a new reference maximum.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t tO, float alpha) {
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += 16) {
+    uint32_t o[16];
+    tmem_ld16(tO + c0, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st16(tO + c0, o);
+  }
+}
+
+// The reference maximum (log2 domain) after a tile whose largest score is m_row:
+// raised only when that grows by more than 2^8.  Returns what is then to be
+// multiplied into the running sum and output.
+__device__ __forceinline__ float raise(float m_row, float sl2, float& m_ref) {
+  const float m_new = m_row * sl2;
+  if (!(m_new > m_ref + 8.f)) return 1.f;
+  const float alpha = ex2_approx(m_ref - m_new);
+  m_ref = m_new;
+  return alpha;
+}
+
+// One row of a 128 x 128 tile of scores (TMEM at tS) to its exponentials in place,
+// with the running reference maximum, sum and output (TMEM at tO) brought along.
+// (The product before these scores, which used O, has completed with them.)
+template <int D>
+__device__ __forceinline__ void whole_row(uint32_t tS, uint32_t tO, float sl2, bool first, float& m_ref, float& l_run) {
+  uint32_t a[4][32];
+  float mc[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, a[c], mc[c]);
+  tmem_wait_ld();
+  const float alpha = raise(fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])), sl2, m_ref);
+  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+  float sum = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+    exp_store(a[2 * h], sl2, neg, tS + 32 * h, acc);
+    exp_store(a[2 * h + 1], sl2, neg, tS + 32 * h + 16, acc);
+    float s0, s1;
+    f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+    sum += s0 + s1;
+    if (h == 0 && !first && __any_sync(0xffffffffu, alpha != 1.f)) rescale<D>(tO, alpha);
+  }
+  l_run = l_run * alpha + sum;
+}
+
+// The same where the row sees the columns before `limit` only: of the warp's
+// first `chunks` chunks of 32 columns all but the last whole, and nothing of the
+// others.  A chunk at a time, twice, in little code: short prompts go through it
+// once an item and wait for instructions as much as for anything.  (P of a chunk
+// takes columns of chunks that are done.)
+template <int D>
+__device__ __forceinline__ void edge_row(uint32_t tS, uint32_t tO, float sl2, bool first, int limit, int chunks,
+                                         float& m_ref, float& l_run) {
+  uint32_t a[32];
+  float m_row = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c + 1 < chunks; ++c) {
+    float m;
+    tmem_ld32_max(tS + 32 * c, a, m);
+    tmem_wait_ld();
+    m_row = fmaxf(m_row, m);
+  }
+  tmem_ld32(tS + 32 * (chunks - 1), a);
+  tmem_wait_ld();
+  const int cut = limit - 32 * (chunks - 1);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < cut) m_row = fmaxf(m_row, __uint_as_float(a[i]));
+  const float alpha = raise(m_row, sl2, m_ref);
+  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+  uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    if (c < chunks) {
+      tmem_ld32(tS + 32 * c, a);
+      tmem_wait_ld();
+    }
+    const int n = c < chunks ? limit - 32 * c : 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= n) a[i] = __float_as_uint(-INFINITY);
+    exp_store(a, sl2, neg, tS + 16 * c, acc);
+  }
+  if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale<D>(tO, alpha);
   float s0, s1;
   f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-  return s0 + s1;
+  l_run = l_run * alpha + (s0 + s1);
 }
 
 // Key tiles of an item in order: the runs of its sequence from the first on.
 struct KeyTiles {
   const PromptRun* runs;
-  int run, tile, left;  // left: rows of the run from this tile on
+  int run, left;  // left: rows of the run from this tile on
   int shard, row0;
-  __device__ __forceinline__ void begin(const PromptTables& t, const Item& it) {
-    runs = t.runs;
-    run = it.first_run;
-    enter();
+  // `first`: the sequence's first run
+  __device__ __forceinline__ void begin(const PromptRun* r, int first_run, const int4& first) {
+    runs = r;
+    run = first_run;
+    enter(first);
   }
-  __device__ __forceinline__ void enter() {
-    const int4 v = *reinterpret_cast<const int4*>(runs + run);
+  __device__ __forceinline__ void enter(const int4& v) {
     shard = v.x;
     row0 = v.y;
     left = v.z;
-    tile = 0;
   }
   // (not after the item's last tile: there may be no run behind it)
   __device__ __forceinline__ void next() {
@@ -313,14 +395,67 @@ struct KeyTiles {
       row0 += kTileRows;
     } else {
       ++run;
-      enter();
+      enter(*reinterpret_cast<const int4*>(runs + run));
     }
   }
 };
 
+// Direct: unit `w` of the sequences in their own order, by one warp; run -1 where
+// there is none.
+__device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars, int lane) {
+  const int N = p.shard_begin[p.P];
+  int reached = 0, units_before = 0;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+    // rows [a, b) of sequence s0 + lane, as in tables_kernel
+    const int s = s0 + lane;
+    int a = s < p.n_seqs ? min(max(p.seq_starts[s], 0), N) : 0;
+    const int end = s < p.n_seqs ? min(max(p.seq_starts[s + 1], 0), N) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, a, d);
+      if (lane >= d) a = max(a, y);
+    }
+    a = max(a, reached);
+    const int b = s < p.n_seqs ? max(a, end) : a;
+    int units = 0;
+    for (int i = 0; i < p.P; ++i) {
+      const int len = min(b, p.shard_begin[i + 1]) - max(a, p.shard_begin[i]);
+      if (len > 0) units += units_of(len, p.pair);
+    }
+    int upto = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    upto += units_before;
+    const bool mine = upto - units <= w && w < upto;
+    if (mine) {  // one lane's sequence has it
+      int r = 0, kv = 0, at = upto - units;
+      for (int i = 0; i < p.P; ++i) {
+        const int lo = max(a, p.shard_begin[i]), len = min(b, p.shard_begin[i + 1]) - lo;
+        if (len <= 0) continue;
+        bars.run[r] = PromptRun{i, lo - p.shard_begin[i], len, 0};
+        const int here = units_of(len, p.pair), tiles = (len + kTileRows - 1) / kTileRows;
+        if (w >= at && w < at + here) {
+          const int tile = (w - at) * (p.pair ? 1 : 2);
+          bars.unit = PromptUnit{r, tile, kv + (p.pair ? tile : min(tile + 1, tiles - 1)) + 1, 0};
+        }
+        at += here;
+        kv += tiles;
+        ++r;
+      }
+    }
+    if (__any_sync(0xffffffffu, mine)) return;
+    reached = __shfl_sync(0xffffffffu, b, 31);
+    units_before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) bars.unit.run = -1;
+}
+
 template <int D>
-__device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV, int n_items,
-                                         uint64_t deadline) {
+__device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV,
+                                         int n_items, const PromptRun* runs, uint64_t deadline) {
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   bool ok = true;
@@ -344,7 +479,8 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     ++g;
     return true;
   };
-  int idx = blockIdx.x;
+  int idx = blockIdx.x, known = -1;
+  int4 u, r, f;  // the item's unit, its run, its sequence's first run
   for (int k = 0; ok; ++k) {
     const int slot = k % kItems;
     if (k >= kItems &&
@@ -352,18 +488,22 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
       break;
     Item it = {};
     it.run = -1;
-    int next = 0;
     if (idx < n_items) {
-      const int4 u = *reinterpret_cast<const int4*>(&p.t.units[idx / p.n_hp]);
-      const int hp = idx % p.n_hp;
-      const int4 r = *reinterpret_cast<const int4*>(&p.t.runs[u.x]);
+      const int w = idx / p.n_hp, hp = idx - w * p.n_hp;
+      if (w != known) {
+        known = w;
+        u = *reinterpret_cast<const int4*>(p.direct ? &bars.unit : &p.cut.t.units[w]);
+        f = r = *reinterpret_cast<const int4*>(runs + u.x);
+        if (r.w != u.x) f = *reinterpret_cast<const int4*>(runs + r.w);
+      }
       it.run = u.x;
       it.tile = u.y;
       it.shard = r.x;
       it.row0 = r.y;
       it.len = r.z;
       it.first_run = r.w;
-      if (p.pair) {
+      it.first_len = f.z;
+      if (p.cut.pair) {
         it.head = 2 * hp;
         it.n[0] = it.n[1] = u.z;
       } else {
@@ -378,11 +518,12 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     if (it.run < 0) break;
     const int n = max(it.n[0], it.n[1]), kv_head = it.head / p.G;
     KeyTiles kt;
-    kt.begin(p.t, it);
+    kt.begin(runs, it.first_run, f);
+    int next = n_items;
     for (int s = 0; s < n; ++s) {
-      // the next item is taken as late as it can be without a wait for it:
-      // whoever is behind takes less
-      if (s == max(n - 2, 0)) next = atomicAdd(&p.t.head[1], 1);
+      // the next item is taken late, so that whoever is behind takes less; the
+      // steps under way cover what finding out about it costs
+      if (s == max(n - 3, 0) && !p.direct) next = atomicAdd(&p.cut.t.head[1], 1);
       if (!(ok = group(true, kt.shard, kt.row0, kv_head))) break;
       if (s == 0) {
 #pragma unroll
@@ -392,8 +533,8 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
             continue;
           const uint32_t bq = smem_u32(&bars.q_full[i]);
           mbar_arrive_expect_tx(bq, C::kTileBytes);
-          tma_load_tile(sQ + i * C::kTileBytes, &p.tq[it.shard], bq, p.pair ? it.head + i : it.head,
-                        it.row0 + (p.pair ? it.tile : it.tile + i) * kTileRows);
+          tma_load_tile(sQ + i * C::kTileBytes, &p.tq[it.shard], bq, p.cut.pair ? it.head + i : it.head,
+                        it.row0 + (p.cut.pair ? it.tile : it.tile + i) * kTileRows);
           ++n_q[i];
         }
         if (!ok) break;
@@ -503,8 +644,12 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     const int bi = (u + 1) % C::kHalf;
     if (!wait(bars.full[bi], turn + (u == C::kHalf - 1 ? 1 : 0))) return;
     if (left0) values(0, left0, par_p0);
-    if (ok && next0) scores(0, u, next0, last, par_q0);
+    // where the next item's queries are not here yet, this one's second product
+    // does not wait for them
+    const bool here = next0 && !(last && !mbar_test(smem_u32(&bars.q_full[0]), par_q0 & 1));
+    if (ok && here) scores(0, u, next0, last, par_q0);
     if (ok && left1) values(1, left1, par_p1);
+    if (ok && next0 && !here) scores(0, u, next0, last, par_q0);
     if (ok && next1) scores(1, u, next1, last, par_q1);
     if (!ok) return;
     if (more) mma_commit(smem_u32(&bars.empty[bi]));
@@ -575,7 +720,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
 
 template <int D>
 __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint32_t sKV, uint32_t sStage,
-                                        uint32_t tmem, int warp, int lane, uint64_t deadline) {
+                                        uint32_t tmem, const PromptRun* runs, int warp, int lane, uint64_t deadline) {
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   const int wg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
@@ -597,55 +742,41 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
     const int n = wg ? it.n[1] : it.n[0];
     if (n > 0) {
       float m_ref = -INFINITY, l_run = 0.f;
-      KeyTiles kt;
-      kt.begin(p.t, it);
-      for (int s = 0; s < n; ++s) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[wg]), n_s & 1, deadline, abort_flag))) {
-          ok = false;
-          break;
-        }
+      int run = it.first_run, left = it.first_len;  // rows of the run from tile s on
+      auto scores_ready = [&]() {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[wg]), n_s & 1, deadline, abort_flag))) return false;
         ++n_s;
         tc_fence_after();
-        uint32_t a[4][32];
-        const bool diagonal = s + 1 == n, cut = kt.left < kTileRows;
-        const int valid = kt.left;  // keys of the tile that the run has (128 or more: all)
-        float m_row;
-        if (!diagonal && !cut) {
-          float mc[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, a[c], mc[c]);
-          tmem_wait_ld();
-          m_row = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, a[c]);
-          tmem_wait_ld();
-          mask_from(a, diagonal ? min(valid, row + 1) : valid);
-          m_row = row_max(a);
+        return true;
+      };
+      auto probabilities_ready = [&]() {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[wg]));
+      };
+      int s = 0;
+      while (ok) {
+        // tiles that every row sees whole
+        const int whole = min(left / kTileRows, n - 1 - s);
+        left -= whole * kTileRows;
+        for (const int end = s + whole; s < end; ++s) {
+          if (!(ok = scores_ready())) break;
+          whole_row<D>(tS, tO, sl2, s == 0, m_ref, l_run);
+          probabilities_ready();
         }
-        if (s + 1 < n) kt.next();
-        const float m_new = m_row * sl2;
-        float alpha = 1.f;
-        if (m_new > m_ref + 8.f) {
-          alpha = ex2_approx(m_ref - m_new);
-          m_ref = m_new;
+        if (!ok) break;
+        const bool diagonal = s + 1 == n;
+        if (left == 0) {  // (only before the diagonal: the next run)
+          left = runs[++run].len;
+          continue;
         }
-        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-        float sum = exp_store<0, 2>(a, sl2, neg, tS);
-        // (the product before this S, which used O, has completed with it)
-        if (s > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(tO + c0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st16(tO + c0, o);
-          }
-        }
-        sum += exp_store<2, 4>(a, sl2, neg, tS);
-        if (cut) {
+        // the diagonal, where a row sees the columns up to its own, or a run's
+        // short last tile, where it sees those up to the run's end (rows behind
+        // that end, which are not stored, see what they like)
+        if (!(ok = scores_ready())) break;
+        edge_row<D>(tS, tO, sl2, s == 0, diagonal ? row + 1 : left, diagonal ? q4 + 1 : (left + 31) >> 5, m_ref, l_run);
+        if (left < kTileRows) {
           // V's rows behind the run's end: zero (both tiles' warps do it, each
           // before its own product)
           const int st = step0 + s, gr = st + 1;
@@ -654,7 +785,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
             ok = false;
             break;
           }
-          if (row >= valid) {
+          if (row >= left) {
             const uint32_t v = sKV + (2 * st + 1) % C::kSlots * C::kTileBytes + row * 128;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
@@ -663,56 +794,63 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
           }
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[wg]));
-        l_run = l_run * alpha + sum;
+        probabilities_ready();
+        ++s;
+        if (diagonal) break;
+        left = runs[++run].len;
       }
       if (!ok) break;
       // ---- epilogue
+      const int shard = it.shard, first_row = it.row0;
+      const int tile = p.cut.pair ? it.tile : it.tile + wg, head = p.cut.pair ? it.head + wg : it.head;
+      const int row0 = tile * kTileRows + q4 * 32;  // the warp's first row inside the run
+      const int rows = it.len - row0;               // the warp's rows that there are (may be 32 and more, or none)
+      const int64_t row_bytes = static_cast<int64_t>(p.Hq) * D * 2;
+      uint8_t* const base = p.out[shard] + (first_row + row0 + (lane >> 3)) * row_bytes +
+                            static_cast<int64_t>(head) * D * 2 + (lane & 7) * 16;
+      const int shard_rows = p.cut.shard_begin[shard + 1] - p.cut.shard_begin[shard];
+      const float inv = 1.f / l_run;  // (a row has itself: l_run > 0, NaN inputs aside)
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.o_done[wg]), n_o & 1, deadline, abort_flag))) {
         ok = false;
         break;
       }
       ++n_o;
       tc_fence_after();
-      const int tile = p.pair ? it.tile : it.tile + wg, head = p.pair ? it.head + wg : it.head;
-      const int row0 = tile * kTileRows + q4 * 32;  // the warp's first row inside the run
-      const float inv = 1.f / l_run;  // (a row has itself: l_run > 0, NaN inputs aside)
-      uint8_t* const base = p.out[it.shard] + static_cast<int64_t>(head) * D * 2 + (lane & 7) * 16;
-      const int64_t row_bytes = static_cast<int64_t>(p.Hq) * D * 2;
-      const int shard_rows = p.shard_begin[it.shard + 1] - p.shard_begin[it.shard];
+      uint32_t o[D / 32][32];
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 64) {
+      for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, o[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
         // 64 columns of the warp's rows through shared memory: 16-byte piece c
         // of row r at piece c ^ (r mod 8); stored eight lanes a row
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[32];
-          tmem_ld32(tO + c0 + 32 * half, o);
-          tmem_wait_ld();
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t(&x)[32] = o[2 * h + c / 4];
+          const int e = 8 * (c % 4);
+          uint32_t v[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
-            st_shared_v4(stage + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            v[i] = pack_bf16x2(__uint_as_float(x[e + 2 * i]) * inv, __uint_as_float(x[e + 2 * i + 1]) * inv);
+          st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) << 4), v[0], v[1], v[2], v[3]);
         }
         __syncwarp();
+        uint4 v[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const int r = i + (lane >> 3);
-          if (row0 + r < it.len && in_bounds(&g_prompt_violations, it.row0 + row0 + r, 1, shard_rows))
-            *reinterpret_cast<uint4*>(base + (it.row0 + row0 + r) * row_bytes + c0 * 2) =
-                ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          v[i] = ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
         }
+        uint8_t* at = base + h * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, at += 4 * row_bytes)
+          if (4 * i + (lane >> 3) < rows &&
+              in_bounds(&g_prompt_violations, first_row + row0 + 4 * i + (lane >> 3), 1, shard_rows))
+            *reinterpret_cast<uint4*>(at) = v[i];
         __syncwarp();
       }
-      if (p.lse_out && row0 + lane < it.len && in_bounds(&g_prompt_violations, it.row0 + row0 + lane, 1, shard_rows))
-        p.lse[it.shard][static_cast<int64_t>(it.row0 + row0 + lane) * p.Hq + head] =
+      if (p.lse_out && lane < rows && in_bounds(&g_prompt_violations, first_row + row0 + lane, 1, shard_rows))
+        p.lse[shard][static_cast<int64_t>(first_row + row0 + lane) * p.Hq + head] =
             (m_ref + lg2_approx(l_run)) * 0.6931471805599453f;
     }
     step0 += max(it.n[0], it.n[1]);
@@ -754,20 +892,23 @@ __global__ void __launch_bounds__(320, 1) prompt_kernel(const __grid_constant__ 
     tmem_alloc(smem_u32(&bars.tmem_base), 512);
     tmem_relinquish();
   }
+  if (warp == 8 && p.direct) find_unit(p.cut, blockIdx.x / p.n_hp, bars, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  wait_for_previous_launch();  // the tables
+  if (!p.direct) wait_for_previous_launch();  // the tables
   const uint32_t tmem = bars.tmem_base;
-  const int n_items = p.t.head[0] * p.n_hp;
+  // (direct: one item, or none past the last unit)
+  const int n_items = !p.direct ? p.cut.t.head[0] * p.n_hp : bars.unit.run < 0 ? 0 : blockIdx.x + 1;
+  const PromptRun* const runs = p.direct ? bars.run : p.cut.t.runs;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
   if (blockIdx.x < n_items) {
     if (warp == 8) {
-      if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, deadline);
+      if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, runs, deadline);
     } else if (warp == 9) {
       if (lane == 0) issuer<D>(p, bars, sQ, sKV, tmem, deadline);
     } else {
-      softmax<D>(p, bars, sKV, sStage, tmem, warp, lane, deadline);
+      softmax<D>(p, bars, sKV, sStage, tmem, runs, warp, lane, deadline);
     }
   }
   tc_fence_before();
@@ -791,12 +932,16 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
-  tables_kernel<<<1, 1024, 0, s>>>(p);
+  if (p.direct) {
+    prompt_kernel<D><<<p.cut.grid, C::kThreads, C::kSmem, s>>>(p);
+    return cudaGetLastError();
+  }
+  tables_kernel<<<1, 1024, 0, s>>>(p.cut);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the attention's CTAs come up while the tables are written
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid);
+  cfg.gridDim = dim3(p.cut.grid);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;

@@ -12,7 +12,7 @@ uint64_t cache_violations(bool reset);
 // Causal attention over packed sequences on the shards (uly_sp_prompt_attention).
 
 // Rows of one sequence in one shard, in global row order.
-struct PromptRun {
+struct alignas(16) PromptRun {
   int32_t shard;
   int32_t row0;       // first row inside the shard
   int32_t len;        // at least 1
@@ -21,7 +21,7 @@ struct PromptRun {
 
 // Query rows that a CTA takes at a time: one 128-row tile of two q heads, or
 // (an odd number of q heads a kv head) two tiles of one head.
-struct PromptUnit {
+struct alignas(16) PromptUnit {
   int32_t run;
   int32_t tile;       // its (first) tile inside the run
   int32_t n_kv;       // 128-key tiles up to the diagonal of its (last) tile
@@ -38,20 +38,27 @@ struct PromptTables {
   int32_t max_runs, max_units;
 };
 
+// How the rows are cut: all that the tables are made from.
+struct PromptCut {
+  PromptTables t;
+  int32_t shard_begin[kMaxRanks + 1];  // global row of each shard's first row; [P]: all rows
+  int32_t P, n_seqs;
+  int32_t pair;       // two q heads of one kv head an item (else two tiles of one head)
+  int32_t sort_shift; // a unit's place in the order goes by n_kv >> sort_shift
+  int32_t grid;
+  const int32_t* seq_starts;
+};
+
 struct PromptParams {
   CUtensorMap tq[kMaxRanks];
   CUtensorMap tk[kMaxRanks];
   CUtensorMap tv[kMaxRanks];
-  PromptTables t;
+  PromptCut cut;
   uint8_t* out[kMaxRanks];
   float* lse[kMaxRanks];
-  int32_t shard_begin[kMaxRanks + 1];  // global row of each shard's first row; [P]: all rows
-  int32_t P, Hq, G, n_seqs, lse_out;
-  int32_t pair;       // two q heads of one kv head an item (else two tiles of one head)
+  int32_t Hq, G, lse_out;
   int32_t n_hp;       // items of one unit: Hq / 2 or Hq
-  int32_t sort_shift; // a unit's place in the order goes by n_kv >> sort_shift
-  int32_t grid;
-  const int32_t* seq_starts;
+  int32_t direct;     // no tables: CTA b works item b out by itself
   float scale_log2;
   int32_t* status;
   uint64_t wait_ns;

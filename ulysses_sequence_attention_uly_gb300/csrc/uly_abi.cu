@@ -1836,8 +1836,9 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
   static thread_local PromptParams p;  // ~7 KB: keep it off the stack
   static thread_local Spans spans;
   memset(&p, 0, sizeof(p));
+  PromptCut& c = p.cut;
   if (misaligned(workspace, 256) ||
-      workspace_bytes < prompt_tables(plan, n_seqs, static_cast<uint8_t*>(workspace), &p.t))
+      workspace_bytes < prompt_tables(plan, n_seqs, static_cast<uint8_t*>(workspace), &c.t))
     return ULY_ERR_INVALID;
   if ((rc = check_device(plan))) return rc;
 
@@ -1846,7 +1847,7 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
   spans.add(seq_starts, (static_cast<int64_t>(n_seqs) + 1) * 4, false);
   for (int i = 0; i < P; ++i) {
     const int64_t rows = plan->lens[i], qb = rows * d.Hq * d.D * 2, kb = rows * d.Hkv * d.D * 2;
-    p.shard_begin[i + 1] = p.shard_begin[i] + plan->lens[i];
+    c.shard_begin[i + 1] = c.shard_begin[i] + plan->lens[i];
     p.out[i] = static_cast<uint8_t*>(o[i]);
     p.lse[i] = lse ? lse[i] : nullptr;
     spans.add(q[i], qb, false);
@@ -1864,23 +1865,26 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
         (rc = encode_panel_map(&p.tv[i], v[i], d.D, d.Hkv, rows, rows, 1)))
       return rc;
   }
-  p.P = P;
+  c.P = P;
   p.Hq = d.Hq;
   p.G = d.Hq / d.Hkv;
   // two heads that share k and v walk the same tiles to the end; with two tiles
   // of one head the first idles for the last tile's time
-  p.pair = p.G % 2 == 0;
-  p.n_hp = p.pair ? d.Hq / 2 : d.Hq;
-  if (static_cast<int64_t>(p.t.max_units) * p.n_hp > 0x7FFF0000) return ULY_ERR_UNSUPPORTED;
-  for (int64_t tiles = plan->nq / kTileRows + P; (tiles >> p.sort_shift) >= kSortBuckets;) ++p.sort_shift;
-  p.grid = plan->sm_count;
-  if (static_cast<int64_t>(p.t.max_units) * p.n_hp < p.grid) p.grid = p.t.max_units * p.n_hp;
+  c.pair = p.G % 2 == 0;
+  p.n_hp = c.pair ? d.Hq / 2 : d.Hq;
+  if (static_cast<int64_t>(c.t.max_units) * p.n_hp > 0x7FFF0000) return ULY_ERR_UNSUPPORTED;
+  for (int64_t tiles = plan->nq / kTileRows + P; (tiles >> c.sort_shift) >= kSortBuckets;) ++c.sort_shift;
+  // with no more items than SMs each CTA finds its own, which saves the launch
+  // before it (one prompt of 17 rows: 23.5 -> 19.8 us a call)
+  c.grid = plan->sm_count;
+  p.direct = static_cast<int64_t>(c.t.max_units) * p.n_hp <= c.grid;
+  if (p.direct) c.grid = c.t.max_units * p.n_hp;
   p.status = plan->status;
   p.wait_ns = plan->wait_ns;
   p.withhold_fill = plan->withhold_fill;
-  p.n_seqs = n_seqs;
+  c.n_seqs = n_seqs;
   p.lse_out = lse != nullptr;
-  p.seq_starts = seq_starts;
+  c.seq_starts = seq_starts;
   p.scale_log2 = scale * 1.4426950408889634f;
   return launch_prompt(p, d.D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
