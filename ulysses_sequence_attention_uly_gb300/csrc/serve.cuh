@@ -87,8 +87,20 @@ struct AppendParams {
   int32_t group;             // rows that a CTA looks after
 };
 
+// A unit whose first part is a CTA's last one: how many CTAs, from that one on,
+// have a part of it (0: there is none).
+struct alignas(16) CachedPart {
+  int32_t n, seq, tile, head;
+};
+constexpr int kCachedCtas = 512;  // most CTAs of a launch
+constexpr int kCachedPerSm[2] = {3, 2};  // CTAs an SM, with one and two 8-row tiles of queries
+
 struct CachedParams {
   CacheParams c;
+  CachedPart* parts;   // [grid]
+  float* sums;         // [2 * grid][8 * row_tiles][D + 4]: O, M, m, l of a CTA's unfinished units
+  int32_t grid;
+  int32_t row_tiles;   // 8-row tiles of queries a unit: 1 or 2
   const uint8_t* q;
   int64_t q_row_bytes;
   int32_t Hq, G;

@@ -1806,7 +1806,18 @@ int setup_cache(const uly_cache* cache, int64_t n_rows, const int32_t* starts, c
   return ULY_OK;
 }
 
-int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) { return 256; }
+// 8-row tiles of queries that a unit of uly_cache_attention takes: two where a
+// sequence has more than eight rows (new tokens times heads of a group) on
+// average, so that the cache is read half as often.
+int cached_row_tiles(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
+  return n_rows * (Hq / cache->H) > 8LL * (n_seqs > 0 ? n_seqs : 1) ? 2 : 1;
+}
+
+// Workspace: a note for each CTA, and the sums of two units for each.
+int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
+  const int64_t rows = 8 * cached_row_tiles(cache, Hq, n_rows, n_seqs);
+  return align256(kCachedCtas * sizeof(CachedPart)) + align256(2 * kCachedCtas * rows * (cache->D + 4) * 4);
+}
 
 }  // namespace
 
@@ -1913,7 +1924,7 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
 }
 
 int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
-  if (!cache || Hq < 1 || cache->H < 1 || Hq % cache->H || n_rows < 0 || n_seqs < 0) return -1;
+  if (!cache || Hq < 1 || cache->H < 1 || cache->D < 1 || Hq % cache->H || n_rows < 0 || n_seqs < 0) return -1;
   return cached_work(cache, Hq, n_rows, n_seqs);
 }
 
@@ -1944,6 +1955,22 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = static_cast<uint8_t*>(o);
   p.lse = lse;
+  p.row_tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
+  // blocks of all units: a sequence's row tiles times heads times its blocks of
+  // 64 keys (times a CTA's number it has to fit 64 bits)
+  const int64_t tiles = n_rows * p.G / (8 * p.row_tiles) + n_seqs;
+  const int64_t blocks = (static_cast<int64_t>(table_width) * cache->page_rows + 63) / 64;
+  if (blocks > (1LL << 50) / cache->H / tiles) return ULY_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return ULY_ERR_CUDA;
+  p.grid = sms * kCachedPerSm[p.row_tiles - 1];
+  if (p.grid > kCachedCtas) p.grid = kCachedCtas;
+  if (blocks * cache->H * tiles < p.grid) p.grid = static_cast<int32_t>(blocks * cache->H * tiles);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.parts = reinterpret_cast<CachedPart*>(ws);
+  p.sums = reinterpret_cast<float*>(ws + align256(kCachedCtas * sizeof(CachedPart)));
   return launch_cache_attention(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
 
