@@ -9,7 +9,7 @@ import torch
 import ulysses_sequence_attention_uly_gb300 as uly
 from tests import _serve as R
 
-A = 1 << 20  # an address that is never followed: every call below returns before it would be
+A = 1 << 24  # an address that is never followed: every call below returns before it would be
 
 
 def cache(**change):
@@ -52,7 +52,7 @@ def test_sequences_that_are_refused(change, want):
 
 
 @pytest.mark.parametrize("change", [dict(k=0), dict(v=6 * A + 8), dict(ks=127), dict(vs=132), dict(ks=-8),
-                                    dict(vs=1 << 41), dict(k=A), dict(v=2 * A + 64), dict(k=3 * A), dict(k=4 * A)],
+                                    dict(vs=(1 << 41)), dict(k=A), dict(v=2 * A + 64), dict(k=3 * A), dict(k=4 * A)],
                          ids=str)
 def test_append_refuses(change):
     assert append(**change) == uly.ULY_ERR_INVALID
@@ -72,15 +72,15 @@ def test_append_refuses_pools_that_overlap_each_other_or_the_tables():
                                     dict(ws_bytes=8), dict(o=5 * A), dict(lse=10 * A), dict(o=A), dict(o=8 * A),
                                     dict(ws=10 * A), dict(ws=5 * A)], ids=str)
 def test_attention_refuses(change):
-    a = dict(ws_bytes=1 << 19)
+    a = dict(ws_bytes=1 << 23)
     need = uly.lib().uly_cache_attention_workspace(cache(), 4, 3, 2)
-    assert 0 < need <= 1 << 19
+    assert 0 < need <= 1 << 23
     assert attention(**{**a, **change}) == uly.ULY_ERR_INVALID
 
 
 def test_nothing_to_do():
     assert append(rows=0) == append(n=0) == uly.ULY_OK
-    assert attention(rows=0, ws_bytes=1 << 19) == attention(n=0, ws_bytes=1 << 19) == uly.ULY_OK
+    assert attention(rows=0, ws_bytes=1 << 23) == attention(n=0, ws_bytes=1 << 23) == uly.ULY_OK
 
 
 def test_null_arguments_and_workspaces():

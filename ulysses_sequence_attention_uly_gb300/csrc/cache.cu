@@ -1,7 +1,6 @@
 // cache.cu -- the 8-bit paged cache: k and v rows of new tokens into its pages,
 // and the attention of the newest tokens over it.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <atomic>
 
 #include "serve.cuh"
 #include "tc.cuh"
@@ -180,14 +179,14 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 // below what the tensor cores do in the time that HBM takes for it.
 //
 // A unit is (sequence, 8 NT rows of its queries, cache head); a row is (token, q
-// head of the group).  All units' blocks of 64 keys, in a row, are cut into as
-// many equal parts as there are CTAs, so that a long sequence beside short ones
-// keeps every SM busy and no SM more than the others.  A CTA's part covers some
-// units whole, whose rows it stores, and up to two in part, whose sums it leaves
-// in the workspace; combine_kernel adds those up, in order.
+// head of the group).  A unit's keys, in blocks of 64, are cut into equal parts of
+// about the same length for all units, several times as many as CTAs run at once:
+// SMs differ by a third in how fast they get data, so the GPU gives the next part
+// to whoever is done.  A part that is a whole unit stores its rows; the sums of the
+// others go through the workspace, and combine_kernel adds them up, in order.
 //
-// A warp takes 16 keys at a time (they are in one page), straight from memory
-// into the registers that the matrix instructions want, two steps ahead:
+// A warp takes 16 keys at a time (they are in one page) through a ring of its own
+// in shared memory, and from there as the matrix instructions want them:
 //   S^T = K Q^T   A = K: a lane has bytes 16 c to 16 c + 15 (and 64 on) of keys g
 //                 and g + 8 (lane = 4 g + c); which of a row's elements meet in
 //                 one instruction does not matter, as long as Q's are the same.
@@ -204,7 +203,7 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 namespace {
 
 constexpr int kBlockKeys = 64;   // keys of a block: 16 for each of a CTA's warps
-constexpr int kBuffers = 2;      // a warp's steps in registers: one worked on, the others on their way
+constexpr int kCachedStages = 3; // a warp's steps in shared memory: one worked on, the others on their way
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -219,18 +218,32 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 (4) bytes from global to shared memory, asynchronously; `there` false: zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint2 load8(const uint8_t* p) {
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// wait for the launch before this one in the stream (a programmatic dependency)
+__device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // What a sequence has to do: rows, key limit of its last row, blocks, units of
 // one head.
@@ -270,82 +283,153 @@ __device__ __forceinline__ void store_row(const CachedParams& p, const SeqWork& 
   if (d == 0 && p.lse) p.lse[at] = any ? (m + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-__device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// 16 keys of one head, as a lane holds them.
-template <int D>
-struct Step {
-  uint4 k[2][D / 64];  // keys g and g + 8
-  uint32_t v[4][D / 32];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
-  float ks, vs;
-  bool there;          // in a real page
+// A warp's ring in shared memory: a stage has 16 keys' codes of k, then of v, in
+// 16-byte pieces, and the two scales.  Piece i of row r is at piece i ^ (r mod 8)
+// (64-wide rows: i ^ (r / 2 mod 4)), so that the reads below go without bank
+// conflicts (64-wide v: two lanes a bank).
+template <int D, int NT>
+struct CachedCfg {
+  static constexpr int kStages = kCachedStages;
+  static constexpr int kHalf = 16 * D;                  // codes of k (or v)
+  static constexpr int kStageBytes = 2 * kHalf + 16;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kPart = 8 * NT * (D + 4);        // floats: a warp's sums, which take the ring's place
+  static constexpr int kSmem = 4 * (kWarpBytes > 4 * kPart ? kWarpBytes : 4 * kPart);
+  __device__ static __forceinline__ uint32_t piece(int row, int i) {
+    return D == 128 ? row * 128 + ((i ^ (row & 7)) << 4) : row * 64 + ((i ^ ((row >> 1) & 3)) << 4);
+  }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const __grid_constant__ CachedParams p) {
-  constexpr int RT = 8 * NT, KS = D / 16, MT = D / 16;
-  const CacheParams& c = p.c;
-  __shared__ int64_t sums[4];
-  __shared__ int first_seq;
-  __shared__ int64_t first_before;
-  __shared__ float part[4][RT][D + 4];  // a warp's sums: O, then M, m, l
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
+// ---- parts
+// Blocks of a part, for `total` blocks of all units.
+__device__ __forceinline__ int64_t part_blocks(const CachedParams& p, int64_t total) {
+  return max((total + p.want_parts - 1) / p.want_parts, int64_t{1});
+}
+__device__ __forceinline__ int unit_parts(const SeqWork& w, int64_t blocks) {
+  return static_cast<int>(min(max((w.blocks + blocks / 2) / blocks, int64_t{1}), int64_t{kMaxUnitParts}));
+}
 
-  // ---- this CTA's part of all blocks
-  const int per = (c.n_seqs + 127) / 128, s0 = min(tid * per, c.n_seqs), s1 = min(s0 + per, c.n_seqs);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    const SeqWork w = seq_work<RT>(p, s);
-    mine += static_cast<int64_t>(w.tiles) * w.blocks * c.H;
-  }
-  int64_t upto = mine;
+// Sums over the CTA's 128 threads, exclusive; *total receives the whole.
+__device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* shared, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t upto = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += y;
   }
-  if (lane == 31) sums[warp] = upto;
+  if (lane == 31) shared[warp] = upto;
   __syncthreads();
-  int64_t before = upto - mine, total = 0;
+  int64_t before = upto - v, all = 0;
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (i < warp) before += sums[i];
-    total += sums[i];
+    if (i < warp) before += shared[i];
+    all += shared[i];
   }
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-  CachedPart* const note = p.parts + blockIdx.x;
-  if (blockIdx.x >= ctas) {
-    if (tid == 0) note->n = 0;
-    return;
+  __syncthreads();
+  *total = all;
+  return before;
+}
+
+// More than 128 sequences: the parts before each of them, [n_seqs + 1], and the
+// blocks of a part, by one CTA.
+template <int RT>
+__global__ void __launch_bounds__(128) parts_kernel(const __grid_constant__ CachedParams p) {
+  __shared__ int64_t shared[4];
+  let_next_launch_start();
+  const CacheParams& c = p.c;
+  int64_t mine = 0, total;
+  for (int s = threadIdx.x; s < c.n_seqs; s += 128) {
+    const SeqWork w = seq_work<RT>(p, s);
+    mine += static_cast<int64_t>(w.tiles) * w.blocks * c.H;
   }
-  // (total is below 2^50, see the host; ctas below 2^10)
-  int64_t lo = total * blockIdx.x / ctas;
-  const int64_t hi = total * (blockIdx.x + 1) / ctas;
-  if (before <= lo && lo < before + mine) {
-    int64_t at = before;
-    for (int s = s0; s < s1; ++s) {
+  sum_before(mine, shared, &total);
+  const int64_t blocks = part_blocks(p, total);
+  int64_t done = 0;
+  for (int s0 = 0; s0 < c.n_seqs; s0 += 128) {
+    const int s = s0 + threadIdx.x;
+    int64_t n = 0, all;
+    if (s < c.n_seqs) {
       const SeqWork w = seq_work<RT>(p, s);
-      const int64_t n = static_cast<int64_t>(w.tiles) * w.blocks * c.H;
-      if (lo < at + n) {
-        first_seq = s;
-        first_before = at;
-        break;
+      n = static_cast<int64_t>(w.tiles) * unit_parts(w, blocks) * c.H;
+    }
+    const int64_t at = done + sum_before(n, shared, &all);
+    if (s < c.n_seqs) p.before[s] = at;
+    done += all;
+  }
+  if (threadIdx.x == 0) {
+    p.before[c.n_seqs] = done;
+    p.before[c.n_seqs + 1] = blocks;
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const __grid_constant__ CachedParams p) {
+  using C = CachedCfg<D, NT>;
+  constexpr int RT = 8 * NT, KS = D / 16, MT = D / 16;
+  const CacheParams& c = p.c;
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  __shared__ int64_t shared[4];
+  __shared__ int my_seq;
+  __shared__ int64_t my_before, my_blocks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
+  float(*const part)[RT][D + 4] = reinterpret_cast<float(*)[RT][D + 4]>(ring_raw);  // a warp's sums: O, then M, m, l
+  const uint32_t ring = smem_u32(ring_raw) + warp * C::kWarpBytes;
+  CachedPart* const note = p.parts + blockIdx.x;
+  let_next_launch_start();
+
+  // ---- which part
+  if (tid == 0) my_seq = -1;
+  if (c.n_seqs <= 128) {
+    // a sequence a thread
+    SeqWork w = {};
+    int64_t total, all;
+    if (tid < c.n_seqs) w = seq_work<RT>(p, tid);
+    sum_before(static_cast<int64_t>(w.tiles) * w.blocks * c.H, shared, &total);
+    const int64_t blocks = part_blocks(p, total);
+    const int64_t n = tid < c.n_seqs ? static_cast<int64_t>(w.tiles) * unit_parts(w, blocks) * c.H : 0;
+    const int64_t at = sum_before(n, shared, &all);
+    if (at <= blockIdx.x && blockIdx.x < at + n) {
+      my_seq = tid;
+      my_before = at;
+      my_blocks = blocks;
+    }
+  } else {
+    wait_for_previous_launch();
+    __syncthreads();
+    if (warp == 0 && blockIdx.x < p.before[c.n_seqs]) {
+      // the last sequence that begins at or before the part, 32 ways at a time
+      int lo = 0, n = c.n_seqs;
+      while (n > 1) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const uint32_t yes = __ballot_sync(0xffffffffu, i < n && p.before[lo + i] <= blockIdx.x);
+        const int k = 31 - __clz(yes);  // (lane 0 always)
+        lo += k * step;
+        n = min(step, n - k * step);
       }
-      at += n;
+      if (lane == 0) {
+        my_seq = lo;
+        my_before = p.before[lo];
+        my_blocks = p.before[c.n_seqs + 1];
+      }
     }
   }
   __syncthreads();
-  int s = first_seq;
-  int64_t off = lo - first_before;  // the part's first block among the sequence's
-  SeqWork w = seq_work<RT>(p, s);
-  int left_parts = 0;               // of a unit that others finish: how many parts it has
-  CachedPart left = {};
+  const int s = my_seq;
+  if (s < 0) {
+    if (tid == 0) note->n = 0;
+    return;
+  }
+  const SeqWork w = seq_work<RT>(p, s);
+  const int parts = unit_parts(w, my_blocks);
+  const int64_t off = blockIdx.x - my_before, unit = off / parts;
+  const int idx = static_cast<int>(off - unit * parts);
+  const int tile = static_cast<int>(unit / c.H), h = static_cast<int>(unit - static_cast<int64_t>(tile) * c.H);
+  const int b0 = static_cast<int>(static_cast<int64_t>(w.blocks) * idx / parts);
+  const int b1 = static_cast<int>(static_cast<int64_t>(w.blocks) * (idx + 1) / parts);
+  if (tid == 0) *note = CachedPart{parts, idx, s, tile, h, {}};
 
-  while (lo < hi) {
-    const int64_t unit = off / w.blocks;
-    const int b0 = static_cast<int>(off - unit * w.blocks);
-    const int b1 = static_cast<int>(min(static_cast<int64_t>(w.blocks), b0 + (hi - lo)));
-    const int tile = static_cast<int>(unit / c.H), h = static_cast<int>(unit - static_cast<int64_t>(tile) * c.H);
-
+  {
     // ---- the queries: lane 4 g + c has elements 16 c on of rows g (+ 8) for
     // the scores; of the sums it has rows 2 c and 2 c + 1
     uint32_t qf[NT][KS][2];
@@ -414,58 +498,47 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
     const int32_t* const table = c.table + static_cast<int64_t>(s) * c.table_width;
     const int end = min(b1 * kBlockKeys, most);  // keys of this piece that some row sees
     auto page_of = [&](int key) { return key < end ? __ldg(table + (key >> c.page_shift)) : -1; };
-    auto fetch = [&](Step<D>& st, int key, int page) {
-      st.there = key < end && page >= 0 && page < c.n_pages;
-      if (!st.there) return;
-      const int64_t ph = static_cast<int64_t>(page) * c.H + h;
-      const int slot = key & (c.page_rows - 1);
-      const uint8_t* const k = c.k_pages + (ph * c.page_rows + slot) * D;
-      const uint8_t* const v = c.v_pages + (ph * c.page_rows + slot) * D;
-      st.ks = __ldg(c.k_scale + ph);
-      st.vs = __ldg(c.v_scale + ph);
+    // copies of the step at `key` into a stage; is there anything in it?
+    auto fetch = [&](int stage, int key, int page) {
+      const bool there = key < end && page >= 0 && page < c.n_pages;
+      if (there) {
+        const int64_t ph = static_cast<int64_t>(page) * c.H + h;
+        const int64_t at = (ph * c.page_rows + (key & (c.page_rows - 1))) * D;
+        const uint32_t to = ring + stage * C::kStageBytes;
+        constexpr int kPieces = D / 16, kRows = 32 / kPieces;  // pieces of a row; rows that a warp copies at once
+        const int i = lane % kPieces;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) st.k[i][j] = load16(k + (g + 8 * i) * D + 64 * j + 16 * cc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // (codes behind the last key may be NaN, and 0 times that would be)
-        const int row = 2 * cc + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) st.v[i][j] = 0u;
-        if (key + row < end) {
-          if constexpr (D == 128) {
-            const uint4 x = load16(v + row * D + 16 * g);
-            st.v[i][0] = x.x;
-            st.v[i][1] = x.y;
-            st.v[i][2] = x.z;
-            st.v[i][3] = x.w;
-          } else {
-            const uint2 x = load8(v + row * D + 8 * g);
-            st.v[i][0] = x.x;
-            st.v[i][1] = x.y;
-          }
+        for (int r0 = 0; r0 < 16; r0 += kRows) {
+          const int r = r0 + lane / kPieces;
+          const uint32_t x = C::piece(r, i);
+          copy16(to + x, c.k_pages + at + r * D + 16 * i, true);
+          // (codes behind the last key may be NaN, and 0 times that would be)
+          copy16(to + C::kHalf + x, c.v_pages + at + r * D + 16 * i, key + r < end);
         }
+        if (lane < 2) copy4(to + 2 * C::kHalf + 4 * lane, (lane ? c.v_scale : c.k_scale) + ph);
       }
+      copies_commit();
+      return there;
     };
-    auto work = [&](const Step<D>& st, int key) {
-      if (!st.there) return;
+    auto work = [&](uint32_t st, int key) {
       float sc[NT][4] = {};
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        const uint4 &x = st.k[0][j / 4], &y = st.k[1][j / 4];
-        const uint32_t u = j % 4 == 0 ? x.x : j % 4 == 1 ? x.y : j % 4 == 2 ? x.z : x.w;
-        const uint32_t z = j % 4 == 0 ? y.x : j % 4 == 1 ? y.y : j % 4 == 2 ? y.z : y.w;
-        const uint32_t a0 = f16x2_of_e4m3(static_cast<uint16_t>(u)), a2 = f16x2_of_e4m3(static_cast<uint16_t>(u >> 16));
-        const uint32_t a1 = f16x2_of_e4m3(static_cast<uint16_t>(z)), a3 = f16x2_of_e4m3(static_cast<uint16_t>(z >> 16));
+      for (int j = 0; j < D / 64; ++j) {
+        const uint4 x = ld_shared_v4(st + C::piece(g, 4 * j + cc)), y = ld_shared_v4(st + C::piece(g + 8, 4 * j + cc));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(sc[t], a0, a1, a2, a3, qf[t][j][0], qf[t][j][1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = f16x2_of_e4m3(static_cast<uint16_t>(u[i])), a2 = f16x2_of_e4m3(static_cast<uint16_t>(u[i] >> 16));
+          const uint32_t a1 = f16x2_of_e4m3(static_cast<uint16_t>(z[i])), a3 = f16x2_of_e4m3(static_cast<uint16_t>(z[i] >> 16));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(sc[t], a0, a1, a2, a3, qf[t][4 * j + i][0], qf[t][4 * j + i][1]);
+        }
       }
-      const float lv = lg2_approx(st.vs);
+      const float ks = ld_shared_f32(st + 2 * C::kHalf), lv = lg2_approx(ld_shared_f32(st + 2 * C::kHalf + 4));
       uint32_t pb[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float f0 = rf[t][0] * st.ks, f1 = rf[t][1] * st.ks;
+        const float f0 = rf[t][0] * ks, f1 = rf[t][1] * ks;
         float x[4] = {sc[t][0] * f0, sc[t][1] * f1, sc[t][2] * f0, sc[t][3] * f1};  // keys g, g, g + 8, g + 8
         if (key + 16 > least) {
 #pragma unroll
@@ -506,11 +579,27 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         pb[t][0] = transpose8(pack_f16x2(e[0], e[1]));
         pb[t][1] = transpose8(pack_f16x2(e[2], e[3]));
       }
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * cc + (i & 1) + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint4 x = ld_shared_v4(st + C::kHalf + C::piece(row, g));
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+          v[i][2] = x.z;
+          v[i][3] = x.w;
+        } else {
+          const uint2 x = ld_shared_v2(st + C::kHalf + C::piece(row, g >> 1) + 8 * (g & 1));
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+        }
+      }
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         // four elements of a lane's piece: two of the products' tiles
-        const uint32_t a01 = __byte_perm(st.v[0][q], st.v[1][q], 0x5140), a23 = __byte_perm(st.v[0][q], st.v[1][q], 0x7362);
-        const uint32_t b01 = __byte_perm(st.v[2][q], st.v[3][q], 0x5140), b23 = __byte_perm(st.v[2][q], st.v[3][q], 0x7362);
+        const uint32_t a01 = __byte_perm(v[0][q], v[1][q], 0x5140), a23 = __byte_perm(v[0][q], v[1][q], 0x7362);
+        const uint32_t b01 = __byte_perm(v[2][q], v[3][q], 0x5140), b23 = __byte_perm(v[2][q], v[3][q], 0x7362);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t a = i ? a23 : a01, b = i ? b23 : b01;
@@ -522,25 +611,29 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
       }
     };
 
-    // ---- steps of this warp, two loads ahead of the arithmetic
+    // ---- steps of this warp: copies of the next stages under way
     {
-      constexpr int kStride = kBlockKeys, kAhead = kBuffers - 1;
+      constexpr int kAhead = C::kStages - 1;
       int key = b0 * kBlockKeys + 16 * warp;
-      Step<D> st[kBuffers];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(st[i], key + i * kStride, page_of(key + i * kStride));
-      int page = page_of(key + kAhead * kStride);
-      while (key < end) {
-#pragma unroll
-        for (int i = 0; i < kBuffers; ++i) {
-          const int next = page_of(key + (kAhead + 1) * kStride);
-          fetch(st[(i + kAhead) % kBuffers], key + kAhead * kStride, page);
-          page = next;
-          work(st[i], key);
-          key += kStride;
-        }
+      uint32_t there = 0;  // by stage
+      for (int i = 0; i < kAhead; ++i)
+        there |= fetch(i, key + i * kBlockKeys, page_of(key + i * kBlockKeys)) ? 1u << i : 0u;
+      int page = page_of(key + kAhead * kBlockKeys), stage = 0, to = kAhead;
+      for (; key < end; key += kBlockKeys) {
+        copies_wait<kAhead - 1>();
+        __syncwarp();
+        // (the stage that is filled now was read in the step before)
+        const int next = page_of(key + (kAhead + 1) * kBlockKeys);
+        there = (there & ~(1u << to)) | (fetch(to, key + kAhead * kBlockKeys, page) ? 1u << to : 0u);
+        page = next;
+        if ((there >> stage) & 1u) work(ring + stage * C::kStageBytes, key);
+        __syncwarp();
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        to = to + 1 == C::kStages ? 0 : to + 1;
       }
+      copies_wait<0>();
     }
+    __syncthreads();  // the sums take the ring's place
 
     // ---- the four warps' sums
 #pragma unroll
@@ -563,9 +656,9 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
               make_float4(o[t][q][i], o[t][q][2 + i], o[t][q + 1][i], o[t][q + 1][2 + i]);
       }
     __syncthreads();
-    const bool whole = b0 == 0 && b1 == w.blocks;
-    float* const slot = p.sums + (static_cast<int64_t>(2 * blockIdx.x + (b0 == 0)) * RT) * (D + 4);
-    for (int i = tid; i < RT * (D / 4); i += 128) {
+    float* const slot = p.sums + static_cast<int64_t>(blockIdx.x) * RT * (D + 4);
+    const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - static_cast<int64_t>(tile) * RT, int64_t{RT}));
+    for (int i = tid; i < live * (D / 4); i += 128) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       float Mx = -INFINITY, mx = -INFINITY;
 #pragma unroll
@@ -586,119 +679,120 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         sum.w += f * x.w;
         ls += f2 * part[k][r][D + 2];
       }
-      if (whole) {
+      if (parts == 1) {
         store_row<D>(p, w, static_cast<int64_t>(tile) * RT + r, h, d, sum, Mx, mx, ls);
       } else {
         *reinterpret_cast<float4*>(slot + r * (D + 4) + d) = sum;
         if (d == 0) *reinterpret_cast<float4*>(slot + r * (D + 4) + D) = make_float4(Mx, mx, ls, 0.f);
       }
     }
-    __syncthreads();  // `part` is free again
-    if (b0 == 0 && !whole) {
-      // the unit's last block is in the part of the CTA that has block lo + blocks - 1
-      const int64_t last = lo + w.blocks - 1;
-      int64_t cta = last * ctas / total;
-      while (cta + 1 < ctas && total * (cta + 1) / ctas <= last) ++cta;
-      while (total * cta / ctas > last) --cta;
-      left = CachedPart{static_cast<int32_t>(cta - blockIdx.x + 1), s, tile, h};
-    }
-    lo += b1 - b0;
-    off += b1 - b0;
-    while (lo < hi && off >= static_cast<int64_t>(w.tiles) * w.blocks * c.H) {
-      off -= static_cast<int64_t>(w.tiles) * w.blocks * c.H;
-      w = seq_work<RT>(p, ++s);
-    }
   }
-  if (tid == 0) *note = left;
 }
 
-// The rows of a unit that several CTAs have parts of: one CTA a row, its warps
-// taking the parts in turn.
+// The rows of units in several parts: a CTA for each part, which takes the rows
+// idx, idx + parts, ... of its unit; its warps share the parts of a row.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CachedParams p) {
-  constexpr int RT = 8 * NT;
-  __shared__ float4 sums[8][D / 4];
-  __shared__ float ref[8][4];
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CachedParams p) {
+  constexpr int RT = 8 * NT, kStep = RT * (D + 4);
+  __shared__ float4 sums[4][D / 4];
+  __shared__ float ref[4][4];
   wait_for_previous_launch();
-  const CachedPart part = p.parts[blockIdx.x];
-  if (!part.n) return;
-  const SeqWork w = seq_work<RT>(p, part.seq);
-  const int64_t r = static_cast<int64_t>(part.tile) * RT + blockIdx.y;
-  if (r >= static_cast<int64_t>(w.rows) * p.G) return;
+  const CachedPart note = p.parts[blockIdx.x];
+  if (note.n <= 1 || note.idx >= RT) return;
+  const SeqWork w = seq_work<RT>(p, note.seq);
+  const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - static_cast<int64_t>(note.tile) * RT, int64_t{RT}));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int k) {
-    return p.sums + (static_cast<int64_t>(2 * (blockIdx.x + k) + (k == 0)) * RT + blockIdx.y) * (D + 4);
-  };
-  // references first, then the sums against them
-  float Mx = -INFINITY, mx = -INFINITY;
-  for (int k = threadIdx.x; k < part.n; k += 256) {
-    const float* const x = slot(k) + D;
-    Mx = fmaxf(Mx, x[0]);
-    mx = fmaxf(mx, x[1]);
-  }
+  for (int r = note.idx; r < live; r += note.n) {
+    const float* const first = p.sums + (static_cast<int64_t>(blockIdx.x) - note.idx) * kStep + r * (D + 4);
+    // a warp's parts against the largest references of them (a lane a part)
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Mx = -INFINITY, mx = -INFINITY, ls = 0.f;
+    const int per = (note.n + 3) / 4, k0 = warp * per, k1 = min(k0 + per, note.n);  // at most 32
+    float4 h = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (k0 + lane < k1) h = *reinterpret_cast<const float4*>(first + static_cast<int64_t>(k0 + lane) * kStep + D);
+    Mx = h.x;
+    mx = h.y;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, d));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  }
-  if (lane == 0) {
-    ref[warp][0] = Mx;
-    ref[warp][1] = mx;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    Mx = fmaxf(Mx, ref[k][0]);
-    mx = fmaxf(mx, ref[k][1]);
-  }
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float ls = 0.f;
-  for (int k = warp; k < part.n; k += 8) {
-    const float* const x = slot(k);
-    const float4 h = *reinterpret_cast<const float4*>(x + D);
-    const float f = h.x == -INFINITY ? 0.f : ex2_approx(h.x - Mx), f2 = h.y == -INFINITY ? 0.f : ex2_approx(h.y - mx);
-    if (lane < D / 4) {
-      const float4 y = *reinterpret_cast<const float4*>(x + 4 * lane);
-      sum.x += f * y.x;
-      sum.y += f * y.y;
-      sum.z += f * y.z;
-      sum.w += f * y.w;
+    for (int d = 16; d; d >>= 1) {
+      Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, d));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     }
-    ls += f2 * h.z;
-  }
-  if (lane < D / 4) sums[warp][lane] = sum;
-  if (lane == 0) ref[warp][2] = ls;
-  __syncthreads();
-  if (warp == 0 && lane < D / 4) {
-    ls = 0.f;
-    sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float f = h.x == -INFINITY ? 0.f : ex2_approx(h.x - Mx);
+    ls = h.y == -INFINITY ? h.z : h.z * ex2_approx(h.y - mx);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float4 y = sums[k][lane];
-      sum.x += y.x;
-      sum.y += y.y;
-      sum.z += y.z;
-      sum.w += y.w;
-      ls += ref[k][2];
+    for (int d = 16; d; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k - k0);
+      if (lane < D / 4) {
+        const float4 y = *reinterpret_cast<const float4*>(first + static_cast<int64_t>(k) * kStep + 4 * lane);
+        sum.x += fk * y.x;
+        sum.y += fk * y.y;
+        sum.z += fk * y.z;
+        sum.w += fk * y.w;
+      }
     }
-    store_row<D>(p, w, r, part.head, 4 * lane, sum, Mx, mx, ls);
+    if (lane < D / 4) sums[warp][lane] = sum;
+    if (lane == 0) {
+      ref[warp][0] = Mx;
+      ref[warp][1] = mx;
+      ref[warp][2] = ls;
+    }
+    __syncthreads();
+    if (warp == 0 && lane < D / 4) {
+      Mx = fmaxf(fmaxf(ref[0][0], ref[1][0]), fmaxf(ref[2][0], ref[3][0]));
+      mx = fmaxf(fmaxf(ref[0][1], ref[1][1]), fmaxf(ref[2][1], ref[3][1]));
+      ls = 0.f;
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 y = sums[k][lane];
+        const float fk = ref[k][0] == -INFINITY ? 0.f : ex2_approx(ref[k][0] - Mx);
+        sum.x += fk * y.x;
+        sum.y += fk * y.y;
+        sum.z += fk * y.z;
+        sum.w += fk * y.w;
+        ls += ref[k][1] == -INFINITY ? ref[k][2] : ref[k][2] * ex2_approx(ref[k][1] - mx);
+      }
+      store_row<D>(p, w, static_cast<int64_t>(note.tile) * RT + r, note.head, 4 * lane, sum, Mx, mx, ls);
+    }
+    __syncthreads();
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_cached(const CachedParams& p, cudaStream_t s) {
-  cached_kernel<D, NT><<<p.grid, 128, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  using C = CachedCfg<D, NT>;
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(cached_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  // (each launch may come up while the one before it ends)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, 8 * NT);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
+  if (p.c.n_seqs > 128) {
+    parts_kernel<8 * NT><<<1, 128, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(p.grid);
+  cfg.dynamicSmemBytes = C::kSmem;
+  e = cudaLaunchKernelEx(&cfg, cached_kernel<D, NT>, p);
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, combine_kernel<D, NT>, p);
 }
 

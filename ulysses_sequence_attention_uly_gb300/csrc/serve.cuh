@@ -87,19 +87,23 @@ struct AppendParams {
   int32_t group;             // rows that a CTA looks after
 };
 
-// A unit whose first part is a CTA's last one: how many CTAs, from that one on,
-// have a part of it (0: there is none).
-struct alignas(16) CachedPart {
-  int32_t n, seq, tile, head;
+// What a CTA of the attention over a cache worked on: part idx of n of a unit (n
+// = 0: nothing).
+struct alignas(32) CachedPart {
+  int32_t n, idx, seq, tile, head;
+  int32_t pad[3];
 };
-constexpr int kCachedCtas = 512;  // most CTAs of a launch
-constexpr int kCachedPerSm[2] = {3, 2};  // CTAs an SM, with one and two 8-row tiles of queries
+constexpr int kMaxUnitParts = 128;         // (a warp of combine_kernel has a lane for each of a quarter of them)
+constexpr int kCachedPerSm[2] = {4, 2};    // CTAs an SM, with one and two 8-row tiles of queries
+constexpr int kCachedRounds = 3;           // parts for each CTA that runs at once
 
 struct CachedParams {
   CacheParams c;
+  int64_t* before;     // more than 128 sequences: [n_seqs + 2], see parts_kernel
   CachedPart* parts;   // [grid]
-  float* sums;         // [2 * grid][8 * row_tiles][D + 4]: O, M, m, l of a CTA's unfinished units
+  float* sums;         // [grid][8 * row_tiles][D + 4]: O, M, m, l of parts of units
   int32_t grid;
+  int32_t want_parts;  // parts that the blocks of all units are to be cut into
   int32_t row_tiles;   // 8-row tiles of queries a unit: 1 or 2
   const uint8_t* q;
   int64_t q_row_bytes;

@@ -1813,10 +1813,23 @@ int cached_row_tiles(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t
   return n_rows * (Hq / cache->H) > 8LL * (n_seqs > 0 ? n_seqs : 1) ? 2 : 1;
 }
 
-// Workspace: a note for each CTA, and the sums of two units for each.
+// uly_cache_attention: parts (CTAs) that the blocks of all units are to make; each
+// unit's rounding may add one.  The workspace counts kCachedSms SMs.
+constexpr int kCachedSms = 160;
+int64_t cached_want(int row_tiles, int sms) {
+  return static_cast<int64_t>(sms) * kCachedPerSm[row_tiles - 1] * kCachedRounds;
+}
+int64_t cached_units(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs, int row_tiles) {
+  return cache->H * (n_rows * (Hq / cache->H) / (8 * row_tiles) + n_seqs);
+}
+
+// Workspace: parts before each sequence, a note and the sums of 8 row_tiles rows
+// for each part.
 int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
-  const int64_t rows = 8 * cached_row_tiles(cache, Hq, n_rows, n_seqs);
-  return align256(kCachedCtas * sizeof(CachedPart)) + align256(2 * kCachedCtas * rows * (cache->D + 4) * 4);
+  const int tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
+  const int64_t parts = cached_want(tiles, kCachedSms) + cached_units(cache, Hq, n_rows, n_seqs, tiles);
+  return align256((static_cast<int64_t>(n_seqs) + 2) * 8) + align256(parts * sizeof(CachedPart)) +
+         align256(parts * 8 * tiles * (cache->D + 4) * 4);
 }
 
 }  // namespace
@@ -1956,21 +1969,26 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
   p.out = static_cast<uint8_t*>(o);
   p.lse = lse;
   p.row_tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
-  // blocks of all units: a sequence's row tiles times heads times its blocks of
-  // 64 keys (times a CTA's number it has to fit 64 bits)
-  const int64_t tiles = n_rows * p.G / (8 * p.row_tiles) + n_seqs;
+  // blocks of all units, and parts: both have to fit their counters
+  const int64_t units = cached_units(cache, Hq, n_rows, n_seqs, p.row_tiles);
   const int64_t blocks = (static_cast<int64_t>(table_width) * cache->page_rows + 63) / 64;
-  if (blocks > (1LL << 50) / cache->H / tiles) return ULY_ERR_UNSUPPORTED;
+  if (blocks > (1LL << 60) / units || units > (1LL << 30)) return ULY_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ULY_ERR_CUDA;
-  p.grid = sms * kCachedPerSm[p.row_tiles - 1];
-  if (p.grid > kCachedCtas) p.grid = kCachedCtas;
-  if (blocks * cache->H * tiles < p.grid) p.grid = static_cast<int32_t>(blocks * cache->H * tiles);
-  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.want_parts = static_cast<int32_t>(cached_want(p.row_tiles, sms < kCachedSms ? sms : kCachedSms));
+  // a unit has at most kMaxUnitParts and at most one a block
+  int64_t grid = p.want_parts + units;
+  const int64_t most = blocks < kMaxUnitParts ? blocks : kMaxUnitParts;
+  if (units * most < grid) grid = units * most;
+  p.grid = static_cast<int32_t>(grid);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.before = reinterpret_cast<int64_t*>(ws);
+  ws += align256((static_cast<int64_t>(n_seqs) + 2) * 8);
   p.parts = reinterpret_cast<CachedPart*>(ws);
-  p.sums = reinterpret_cast<float*>(ws + align256(kCachedCtas * sizeof(CachedPart)));
+  const int64_t all = cached_want(p.row_tiles, kCachedSms) + units;
+  p.sums = reinterpret_cast<float*>(ws + align256(all * sizeof(CachedPart)));
   return launch_cache_attention(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
 
