@@ -203,7 +203,7 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 namespace {
 
 constexpr int kBlockKeys = 64;   // keys of a block: 16 for each of a CTA's warps
-constexpr int kCachedStages = 3; // a warp's steps in shared memory: one worked on, the others on their way
+constexpr int kLongPart = 320 << 10;  // bytes of codes
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -266,14 +266,17 @@ __device__ __forceinline__ SeqWork seq_work(const CachedParams& p, int s) {
   return w;
 }
 
+// A unit's row r: its place among all rows and heads of q (first_row: the
+// sequence's first).
+__device__ __forceinline__ int64_t row_place(const CachedParams& p, int first_row, int h, int64_t r) {
+  return (first_row + r / p.G) * p.Hq + h * p.G + r % p.G;
+}
+
 // Four elements of a finished row: o = O 2^(M - m) / l, and once a row its
 // log-sum-exp; zero and -inf where no key was seen.
 template <int D>
-__device__ __forceinline__ void store_row(const CachedParams& p, const SeqWork& w, int64_t r, int h, int d,
-                                          const float4& sum, float M, float m, float l) {
-  if (r >= static_cast<int64_t>(w.rows) * p.G) return;
-  const int token = static_cast<int>(r / p.G), head = h * p.G + static_cast<int>(r % p.G);
-  const int64_t at = static_cast<int64_t>(w.a + token) * p.Hq + head;
+__device__ __forceinline__ void store_row(const CachedParams& p, int64_t at, int d, const float4& sum, float M, float m,
+                                          float l) {
   if (!in_bounds(&g_cache_violations, at, 1, static_cast<int64_t>(p.c.n_rows) * p.Hq)) return;
   const bool any = l > 0.f || l != l;
   const float f = any ? ex2_approx(M - m) / l : 0.f;
@@ -289,7 +292,10 @@ __device__ __forceinline__ void store_row(const CachedParams& p, const SeqWork& 
 // conflicts (64-wide v: two lanes a bank).
 template <int D, int NT>
 struct CachedCfg {
-  static constexpr int kStages = kCachedStages;
+  // one worked on, the others on their way: 4 KB a warp, either way (more is
+  // slower: two contexts of 120 to 131 thousand tokens with two stages 85 us, with
+  // three 92)
+  static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kHalf = 16 * D;                  // codes of k (or v)
   static constexpr int kStageBytes = 2 * kHalf + 16;
   static constexpr int kWarpBytes = kStages * kStageBytes;
@@ -301,12 +307,22 @@ struct CachedCfg {
 };
 
 // ---- parts
-// Blocks of a part, for `total` blocks of all units.
-__device__ __forceinline__ int64_t part_blocks(const CachedParams& p, int64_t total) {
-  return max((total + p.want_parts - 1) / p.want_parts, int64_t{1});
-}
-__device__ __forceinline__ int unit_parts(const SeqWork& w, int64_t blocks) {
-  return static_cast<int>(min(max((w.blocks + blocks / 2) / blocks, int64_t{1}), int64_t{kMaxUnitParts}));
+// Parts of a unit, for `total` blocks of all units.  Few units have many parts
+// each: as many in all as CTAs run at once, and none more, since one more would
+// run alone.  Of many units the parts cannot be that even, and where they are
+// long, half of that length keeps the last ones from running alone (64 sequences,
+// 8 heads: 71 -> 65 us; 64-wide, half as long: 39 -> 44).
+template <int D>
+__device__ __forceinline__ int unit_parts(const CachedParams& p, const SeqWork& w, int64_t total) {
+  int64_t n;
+  if (p.few) {
+    n = static_cast<int64_t>(w.blocks) * p.slots / total;
+  } else {
+    const int64_t slots = total > p.slots * (kLongPart / (kBlockKeys * 2 * D)) ? 2 * p.slots : p.slots;
+    const int64_t blocks = (total + slots - 1) / slots;
+    n = (w.blocks + blocks / 2) / blocks;
+  }
+  return static_cast<int>(min(max(n, int64_t{1}), static_cast<int64_t>(min(w.blocks, max_unit_parts(p.few)))));
 }
 
 // Sums over the CTA's 128 threads, exclusive; *total receives the whole.
@@ -332,8 +348,8 @@ __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* shared, int64_
 }
 
 // More than 128 sequences: the parts before each of them, [n_seqs + 1], and the
-// blocks of a part, by one CTA.
-template <int RT>
+// blocks of all units, by one CTA.
+template <int D, int RT>
 __global__ void __launch_bounds__(128) parts_kernel(const __grid_constant__ CachedParams p) {
   __shared__ int64_t shared[4];
   let_next_launch_start();
@@ -344,14 +360,13 @@ __global__ void __launch_bounds__(128) parts_kernel(const __grid_constant__ Cach
     mine += static_cast<int64_t>(w.tiles) * w.blocks * c.H;
   }
   sum_before(mine, shared, &total);
-  const int64_t blocks = part_blocks(p, total);
   int64_t done = 0;
   for (int s0 = 0; s0 < c.n_seqs; s0 += 128) {
     const int s = s0 + threadIdx.x;
     int64_t n = 0, all;
     if (s < c.n_seqs) {
       const SeqWork w = seq_work<RT>(p, s);
-      n = static_cast<int64_t>(w.tiles) * unit_parts(w, blocks) * c.H;
+      n = static_cast<int64_t>(w.tiles) * unit_parts<D>(p, w, total) * c.H;
     }
     const int64_t at = done + sum_before(n, shared, &all);
     if (s < c.n_seqs) p.before[s] = at;
@@ -359,7 +374,7 @@ __global__ void __launch_bounds__(128) parts_kernel(const __grid_constant__ Cach
   }
   if (threadIdx.x == 0) {
     p.before[c.n_seqs] = done;
-    p.before[c.n_seqs + 1] = blocks;
+    p.before[c.n_seqs + 1] = total;
   }
 }
 
@@ -371,7 +386,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   extern __shared__ __align__(16) uint8_t ring_raw[];
   __shared__ int64_t shared[4];
   __shared__ int my_seq;
-  __shared__ int64_t my_before, my_blocks;
+  __shared__ int64_t my_before, my_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
   float(*const part)[RT][D + 4] = reinterpret_cast<float(*)[RT][D + 4]>(ring_raw);  // a warp's sums: O, then M, m, l
   const uint32_t ring = smem_u32(ring_raw) + warp * C::kWarpBytes;
@@ -379,6 +394,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   let_next_launch_start();
 
   // ---- which part
+  wait_for_previous_launch();
   if (tid == 0) my_seq = -1;
   if (c.n_seqs <= 128) {
     // a sequence a thread
@@ -386,16 +402,14 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
     int64_t total, all;
     if (tid < c.n_seqs) w = seq_work<RT>(p, tid);
     sum_before(static_cast<int64_t>(w.tiles) * w.blocks * c.H, shared, &total);
-    const int64_t blocks = part_blocks(p, total);
-    const int64_t n = tid < c.n_seqs ? static_cast<int64_t>(w.tiles) * unit_parts(w, blocks) * c.H : 0;
+    const int64_t n = tid < c.n_seqs ? static_cast<int64_t>(w.tiles) * unit_parts<D>(p, w, total) * c.H : 0;
     const int64_t at = sum_before(n, shared, &all);
     if (at <= blockIdx.x && blockIdx.x < at + n) {
       my_seq = tid;
       my_before = at;
-      my_blocks = blocks;
+      my_total = total;
     }
   } else {
-    wait_for_previous_launch();
     __syncthreads();
     if (warp == 0 && blockIdx.x < p.before[c.n_seqs]) {
       // the last sequence that begins at or before the part, 32 ways at a time
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
       if (lane == 0) {
         my_seq = lo;
         my_before = p.before[lo];
-        my_blocks = p.before[c.n_seqs + 1];
+        my_total = p.before[c.n_seqs + 1];
       }
     }
   }
@@ -421,33 +435,74 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
     return;
   }
   const SeqWork w = seq_work<RT>(p, s);
-  const int parts = unit_parts(w, my_blocks);
-  const int64_t off = blockIdx.x - my_before, unit = off / parts;
-  const int idx = static_cast<int>(off - unit * parts);
+  const int parts = unit_parts<D>(p, w, my_total);
+  // (the heads of a page are next to each other in memory: neighbouring CTAs take
+  // them, at the same time)
+  const int64_t off = blockIdx.x - my_before, units = static_cast<int64_t>(w.tiles) * c.H, unit = off % units;
+  const int idx = static_cast<int>(off / units);
   const int tile = static_cast<int>(unit / c.H), h = static_cast<int>(unit - static_cast<int64_t>(tile) * c.H);
   const int b0 = static_cast<int>(static_cast<int64_t>(w.blocks) * idx / parts);
   const int b1 = static_cast<int>(static_cast<int64_t>(w.blocks) * (idx + 1) / parts);
-  if (tid == 0) *note = CachedPart{parts, idx, s, tile, h, {}};
+  const int64_t row0 = static_cast<int64_t>(tile) * RT;  // the unit's rows among the sequence's
+  const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - row0, int64_t{RT}));
+  if (tid == 0) *note = CachedPart{parts, idx, static_cast<int32_t>(units), live, row_place(p, w.a, h, row0), row0};
 
   {
+    const int32_t* const table = c.table + static_cast<int64_t>(s) * c.table_width;
+    // (its last row sees most; a position below zero sees nothing)
+    const int64_t all_see = static_cast<int64_t>(c.lens[s]) - w.rows + 1;
+    auto sees = [&](int token) { return static_cast<int>(min(max(all_see + token, int64_t{0}), static_cast<int64_t>(w.len))); };
+    const int end = min(b1 * kBlockKeys, sees(static_cast<int>((row0 + live - 1) / p.G)));  // keys that some row sees
+    auto page_of = [&](int key) { return key < end ? __ldg(table + (key >> c.page_shift)) : -1; };
+    // copies of the step at `key` into a stage; is there anything in it?
+    auto fetch = [&](int stage, int key, int page) {
+      const bool there = key < end && page >= 0 && page < c.n_pages;
+      if (there) {
+        const int64_t ph = static_cast<int64_t>(page) * c.H + h;
+        const int64_t at = (ph * c.page_rows + (key & (c.page_rows - 1))) * D;
+        const uint32_t to = ring + stage * C::kStageBytes;
+        constexpr int kPieces = D / 16, kRows = 32 / kPieces;  // pieces of a row; rows that a warp copies at once
+        const int i = lane % kPieces;
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += kRows) {
+          const int r = r0 + lane / kPieces;
+          const uint32_t x = C::piece(r, i);
+          copy16(to + x, c.k_pages + at + r * D + 16 * i, true);
+          // (codes behind the last key may be NaN, and 0 times that would be)
+          copy16(to + C::kHalf + x, c.v_pages + at + r * D + 16 * i, key + r < end);
+        }
+        if (lane < 2) copy4(to + 2 * C::kHalf + 4 * lane, (lane ? c.v_scale : c.k_scale) + ph);
+      }
+      copies_commit();
+      return there;
+    };
+    // the first steps' copies, before anything else
+    constexpr int kAhead = C::kStages - 1;
+    int key = b0 * kBlockKeys + 16 * warp;
+    uint32_t there = 0;  // by stage
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      there |= fetch(i, key + i * kBlockKeys, page_of(key + i * kBlockKeys)) ? 1u << i : 0u;
+    int page = page_of(key + kAhead * kBlockKeys);
+
     // ---- the queries: lane 4 g + c has elements 16 c on of rows g (+ 8) for
     // the scores; of the sums it has rows 2 c and 2 c + 1
     uint32_t qf[NT][KS][2];
     float rf[NT][2];   // what turns a row's product into log2 scores, without k's scale
     int lim[NT][2];    // keys that a row sees
-    int least = 0x7FFFFFFF, most = 0;
+    int least = 0x7FFFFFFF;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int64_t r = static_cast<int64_t>(tile) * RT + 8 * t + g;
-      const bool live = r < static_cast<int64_t>(w.rows) * p.G;
-      const int token = live ? static_cast<int>(r / p.G) : 0, head = h * p.G + static_cast<int>(live ? r % p.G : 0);
+      const bool mine = 8 * t + g < live;
+      const int64_t r = mine ? row0 + 8 * t + g : 0;
+      const int token = static_cast<int>(r / p.G), head = h * p.G + static_cast<int>(r % p.G);
       uint4 x[D / 64][2];
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           x[i][j] = make_uint4(0u, 0u, 0u, 0u);
-          if (live && in_bounds(&g_cache_violations, w.a + token, 1, c.n_rows))
+          if (mine && in_bounds(&g_cache_violations, w.a + token, 1, c.n_rows))
             x[i][j] = *reinterpret_cast<const uint4*>(p.q + (w.a + token) * p.q_row_bytes +
                                                       (static_cast<int64_t>(head) * D + 64 * i + 16 * cc + 8 * j) * 2);
         }
@@ -473,16 +528,14 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         qf[t][j][0] = pack_f16x2(__uint_as_float(e0 << 16) * down, __uint_as_float(e0 & 0xFFFF0000u) * down);
         qf[t][j][1] = pack_f16x2(__uint_as_float(e1 << 16) * down, __uint_as_float(e1 & 0xFFFF0000u) * down);
       }
-      // (a position below zero sees nothing; a row past the sequence's what it likes)
-      const int64_t see = static_cast<int64_t>(c.lens[s]) - w.rows + token + 1;
-      const int my_lim = live ? static_cast<int>(min(max(see, int64_t{0}), static_cast<int64_t>(w.len))) : 0x7FFFFFFF;
+      // (a row past the sequence's sees what it likes)
+      const int my_lim = mine ? sees(token) : 0x7FFFFFFF;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         rf[t][i] = __shfl_sync(0xffffffffu, up, (2 * cc + i) * 4);
         lim[t][i] = __shfl_sync(0xffffffffu, my_lim, (2 * cc + i) * 4);
       }
       least = min(least, __reduce_min_sync(0xffffffffu, my_lim));
-      most = max(most, __reduce_max_sync(0xffffffffu, live ? my_lim : 0));
     }
 
     float o[NT][MT][4] = {};
@@ -495,31 +548,6 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         l[t][i] = 0.f;
       }
 
-    const int32_t* const table = c.table + static_cast<int64_t>(s) * c.table_width;
-    const int end = min(b1 * kBlockKeys, most);  // keys of this piece that some row sees
-    auto page_of = [&](int key) { return key < end ? __ldg(table + (key >> c.page_shift)) : -1; };
-    // copies of the step at `key` into a stage; is there anything in it?
-    auto fetch = [&](int stage, int key, int page) {
-      const bool there = key < end && page >= 0 && page < c.n_pages;
-      if (there) {
-        const int64_t ph = static_cast<int64_t>(page) * c.H + h;
-        const int64_t at = (ph * c.page_rows + (key & (c.page_rows - 1))) * D;
-        const uint32_t to = ring + stage * C::kStageBytes;
-        constexpr int kPieces = D / 16, kRows = 32 / kPieces;  // pieces of a row; rows that a warp copies at once
-        const int i = lane % kPieces;
-#pragma unroll
-        for (int r0 = 0; r0 < 16; r0 += kRows) {
-          const int r = r0 + lane / kPieces;
-          const uint32_t x = C::piece(r, i);
-          copy16(to + x, c.k_pages + at + r * D + 16 * i, true);
-          // (codes behind the last key may be NaN, and 0 times that would be)
-          copy16(to + C::kHalf + x, c.v_pages + at + r * D + 16 * i, key + r < end);
-        }
-        if (lane < 2) copy4(to + 2 * C::kHalf + 4 * lane, (lane ? c.v_scale : c.k_scale) + ph);
-      }
-      copies_commit();
-      return there;
-    };
     auto work = [&](uint32_t st, int key) {
       float sc[NT][4] = {};
 #pragma unroll
@@ -613,12 +641,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
 
     // ---- steps of this warp: copies of the next stages under way
     {
-      constexpr int kAhead = C::kStages - 1;
-      int key = b0 * kBlockKeys + 16 * warp;
-      uint32_t there = 0;  // by stage
-      for (int i = 0; i < kAhead; ++i)
-        there |= fetch(i, key + i * kBlockKeys, page_of(key + i * kBlockKeys)) ? 1u << i : 0u;
-      int page = page_of(key + kAhead * kBlockKeys), stage = 0, to = kAhead;
+      int stage = 0, to = kAhead;
       for (; key < end; key += kBlockKeys) {
         copies_wait<kAhead - 1>();
         __syncwarp();
@@ -657,7 +680,6 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
       }
     __syncthreads();
     float* const slot = p.sums + static_cast<int64_t>(blockIdx.x) * RT * (D + 4);
-    const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - static_cast<int64_t>(tile) * RT, int64_t{RT}));
     for (int i = tid; i < live * (D / 4); i += 128) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       float Mx = -INFINITY, mx = -INFINITY;
@@ -680,7 +702,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         ls += f2 * part[k][r][D + 2];
       }
       if (parts == 1) {
-        store_row<D>(p, w, static_cast<int64_t>(tile) * RT + r, h, d, sum, Mx, mx, ls);
+        store_row<D>(p, row_place(p, w.a, h, static_cast<int64_t>(tile) * RT + r), d, sum, Mx, mx, ls);
       } else {
         *reinterpret_cast<float4*>(slot + r * (D + 4) + d) = sum;
         if (d == 0) *reinterpret_cast<float4*>(slot + r * (D + 4) + D) = make_float4(Mx, mx, ls, 0.f);
@@ -689,75 +711,97 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   }
 }
 
+// The sums of a row's parts [k0, k1), at most 32 of them, by a warp: O against the
+// largest M in four elements a lane (D / 4 lanes), l against the largest m in
+// every lane.  A lane looks after a part's references; the parts' sums come eight
+// at a time.
+struct RowSum {
+  float4 o;
+  float M, m, l;
+};
+template <int D>
+__device__ __forceinline__ RowSum sum_parts(const float* first, int64_t step, int k0, int k1, int lane) {
+  float4 h = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+  if (k0 + lane < k1) h = *reinterpret_cast<const float4*>(first + (k0 + lane) * step + D);
+  RowSum r = {make_float4(0.f, 0.f, 0.f, 0.f), h.x, h.y, 0.f};
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    r.M = fmaxf(r.M, __shfl_xor_sync(0xffffffffu, r.M, d));
+    r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, d));
+  }
+  // (a part without a key has references of -inf and sums of 0)
+  const float f = h.x == -INFINITY ? 0.f : ex2_approx(h.x - r.M);
+  r.l = h.y == -INFINITY ? h.z : h.z * ex2_approx(h.y - r.m);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) r.l += __shfl_xor_sync(0xffffffffu, r.l, d);
+  for (int k = k0; k < k1; k += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = *reinterpret_cast<const float4*>(first + min(k + i, k1 - 1) * step + 4 * (lane % (D / 4)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (k + i >= k1) continue;
+      const float g = __shfl_sync(0xffffffffu, f, k + i - k0);
+      r.o.x += g * x[i].x;
+      r.o.y += g * x[i].y;
+      r.o.z += g * x[i].z;
+      r.o.w += g * x[i].w;
+    }
+  }
+  return r;
+}
+
 // The rows of units in several parts: a CTA for each part, which takes the rows
-// idx, idx + parts, ... of its unit; its warps share the parts of a row.
-template <int D, int NT>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CachedParams p) {
-  constexpr int RT = 8 * NT, kStep = RT * (D + 4);
-  __shared__ float4 sums[4][D / 4];
-  __shared__ float ref[4][4];
+// idx, idx + parts, ... of the unit: a warp a row, or, of more than 16 parts (then
+// there is one row at most), all warps one row.
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W) combine_kernel(const __grid_constant__ CachedParams p) {
+  constexpr int kStep = 8 * NT * (D + 4);
+  __shared__ float4 sums[W][D / 4];
+  __shared__ float4 ref[W];
+  static_assert(8 * NT <= 16 && max_unit_parts(W > 4) <= 32 * W, "rows of a CTA, parts of a warp");
   wait_for_previous_launch();
   const CachedPart note = p.parts[blockIdx.x];
-  if (note.n <= 1 || note.idx >= RT) return;
-  const SeqWork w = seq_work<RT>(p, note.seq);
-  const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - static_cast<int64_t>(note.tile) * RT, int64_t{RT}));
+  if (note.n <= 1 || note.idx >= note.live) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = note.idx; r < live; r += note.n) {
-    const float* const first = p.sums + (static_cast<int64_t>(blockIdx.x) - note.idx) * kStep + r * (D + 4);
-    // a warp's parts against the largest references of them (a lane a part)
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Mx = -INFINITY, mx = -INFINITY, ls = 0.f;
-    const int per = (note.n + 3) / 4, k0 = warp * per, k1 = min(k0 + per, note.n);  // at most 32
-    float4 h = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-    if (k0 + lane < k1) h = *reinterpret_cast<const float4*>(first + static_cast<int64_t>(k0 + lane) * kStep + D);
-    Mx = h.x;
-    mx = h.y;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, d));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    }
-    const float f = h.x == -INFINITY ? 0.f : ex2_approx(h.x - Mx);
-    ls = h.y == -INFINITY ? h.z : h.z * ex2_approx(h.y - mx);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-#pragma unroll 4
-    for (int k = k0; k < k1; ++k) {
-      const float fk = __shfl_sync(0xffffffffu, f, k - k0);
-      if (lane < D / 4) {
-        const float4 y = *reinterpret_cast<const float4*>(first + static_cast<int64_t>(k) * kStep + 4 * lane);
-        sum.x += fk * y.x;
-        sum.y += fk * y.y;
-        sum.z += fk * y.z;
-        sum.w += fk * y.w;
-      }
-    }
-    if (lane < D / 4) sums[warp][lane] = sum;
-    if (lane == 0) {
-      ref[warp][0] = Mx;
-      ref[warp][1] = mx;
-      ref[warp][2] = ls;
-    }
-    __syncthreads();
-    if (warp == 0 && lane < D / 4) {
-      Mx = fmaxf(fmaxf(ref[0][0], ref[1][0]), fmaxf(ref[2][0], ref[3][0]));
-      mx = fmaxf(fmaxf(ref[0][1], ref[1][1]), fmaxf(ref[2][1], ref[3][1]));
-      ls = 0.f;
-      sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 y = sums[k][lane];
-        const float fk = ref[k][0] == -INFINITY ? 0.f : ex2_approx(ref[k][0] - Mx);
-        sum.x += fk * y.x;
-        sum.y += fk * y.y;
-        sum.z += fk * y.z;
-        sum.w += fk * y.w;
-        ls += ref[k][1] == -INFINITY ? ref[k][2] : ref[k][2] * ex2_approx(ref[k][1] - mx);
-      }
-      store_row<D>(p, w, static_cast<int64_t>(note.tile) * RT + r, note.head, 4 * lane, sum, Mx, mx, ls);
-    }
-    __syncthreads();
+  const int64_t step = static_cast<int64_t>(note.stride) * kStep;  // from a part to the next
+  const float* const first = p.sums + blockIdx.x * static_cast<int64_t>(kStep) - note.idx * step;
+  auto store = [&](int r, const RowSum& x) {
+    // (row r of the unit is r places on in the tokens' order of heads)
+    const int64_t u = note.row0 + r;
+    if (lane < D / 4)
+      store_row<D>(p, note.place + (u / p.G - note.row0 / p.G) * p.Hq + (u % p.G - note.row0 % p.G), 4 * lane, x.o, x.M,
+                   x.m, x.l);
+  };
+  if (note.n <= 16) {
+    for (int r = note.idx + warp * note.n; r < note.live; r += W * note.n)
+      store(r, sum_parts<D>(first + r * (D + 4), step, 0, note.n, lane));
+    return;
   }
+  const int per = (note.n + W - 1) / W, k0 = min(warp * per, note.n);
+  const RowSum mine = sum_parts<D>(first + note.idx * (D + 4), step, k0, min(k0 + per, note.n), lane);
+  if (lane < D / 4) sums[warp][lane] = mine.o;
+  if (lane == 0) ref[warp] = make_float4(mine.M, mine.m, mine.l, 0.f);
+  __syncthreads();
+  if (warp) return;
+  RowSum all = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, -INFINITY, 0.f};
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    all.M = fmaxf(all.M, ref[k].x);
+    all.m = fmaxf(all.m, ref[k].y);
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const float4 x = sums[k][lane % (D / 4)];
+    const float f = ref[k].x == -INFINITY ? 0.f : ex2_approx(ref[k].x - all.M);
+    all.o.x += f * x.x;
+    all.o.y += f * x.y;
+    all.o.z += f * x.z;
+    all.o.w += f * x.w;
+    all.l += ref[k].y == -INFINITY ? ref[k].z : ref[k].z * ex2_approx(ref[k].y - all.m);
+  }
+  store(note.idx, all);
 }
 
 template <int D, int NT>
@@ -781,19 +825,20 @@ cudaError_t launch_cached(const CachedParams& p, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (p.c.n_seqs > 128) {
-    parts_kernel<8 * NT><<<1, 128, 0, s>>>(p);
+    parts_kernel<D, 8 * NT><<<1, 128, 0, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;
   }
   cfg.gridDim = dim3(p.grid);
   cfg.dynamicSmemBytes = C::kSmem;
   e = cudaLaunchKernelEx(&cfg, cached_kernel<D, NT>, p);
   if (e != cudaSuccess) return e;
-  cfg.numAttrs = 1;
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, NT>, p);
+  cfg.blockDim = dim3(p.few ? 256 : 128);
+  return p.few ? cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 8>, p)
+               : cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 4>, p);
 }
 
 }  // namespace

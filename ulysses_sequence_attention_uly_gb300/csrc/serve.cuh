@@ -89,13 +89,17 @@ struct AppendParams {
 
 // What a CTA of the attention over a cache worked on: part idx of n of a unit (n
 // = 0: nothing).
-struct alignas(32) CachedPart {
-  int32_t n, idx, seq, tile, head;
-  int32_t pad[3];
+struct alignas(16) CachedPart {
+  int32_t n, idx;
+  int32_t stride;  // CTAs from a part of the unit to its next
+  int32_t live;    // rows of the unit that there are
+  int64_t place;   // of its first row among all rows and heads of q
+  int64_t row0;    // and among the sequence's
 };
-constexpr int kMaxUnitParts = 128;         // (a warp of combine_kernel has a lane for each of a quarter of them)
-constexpr int kCachedPerSm[2] = {4, 2};    // CTAs an SM, with one and two 8-row tiles of queries
-constexpr int kCachedRounds = 3;           // parts for each CTA that runs at once
+// Most parts of a unit: a lane of combine_kernel for each, which has eight warps
+// where there are few units, and four where its CTAs are many.
+__host__ __device__ constexpr int max_unit_parts(bool few) { return few ? 256 : 128; }
+constexpr int kCachedPerSm[2] = {4, 3};    // CTAs an SM, with one and two 8-row tiles of queries
 
 struct CachedParams {
   CacheParams c;
@@ -103,7 +107,8 @@ struct CachedParams {
   CachedPart* parts;   // [grid]
   float* sums;         // [grid][8 * row_tiles][D + 4]: O, M, m, l of parts of units
   int32_t grid;
-  int32_t want_parts;  // parts that the blocks of all units are to be cut into
+  int32_t slots;       // CTAs that run at once
+  int32_t few;         // units: at most one for eight of those
   int32_t row_tiles;   // 8-row tiles of queries a unit: 1 or 2
   const uint8_t* q;
   int64_t q_row_bytes;

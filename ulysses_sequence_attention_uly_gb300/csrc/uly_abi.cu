@@ -1813,12 +1813,8 @@ int cached_row_tiles(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t
   return n_rows * (Hq / cache->H) > 8LL * (n_seqs > 0 ? n_seqs : 1) ? 2 : 1;
 }
 
-// uly_cache_attention: parts (CTAs) that the blocks of all units are to make; each
-// unit's rounding may add one.  The workspace counts kCachedSms SMs.
+// The workspace of uly_cache_attention counts this many SMs.
 constexpr int kCachedSms = 160;
-int64_t cached_want(int row_tiles, int sms) {
-  return static_cast<int64_t>(sms) * kCachedPerSm[row_tiles - 1] * kCachedRounds;
-}
 int64_t cached_units(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs, int row_tiles) {
   return cache->H * (n_rows * (Hq / cache->H) / (8 * row_tiles) + n_seqs);
 }
@@ -1827,7 +1823,7 @@ int64_t cached_units(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t
 // for each part.
 int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
   const int tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
-  const int64_t parts = cached_want(tiles, kCachedSms) + cached_units(cache, Hq, n_rows, n_seqs, tiles);
+  const int64_t parts = 2LL * kCachedSms * kCachedPerSm[tiles - 1] + cached_units(cache, Hq, n_rows, n_seqs, tiles);
   return align256((static_cast<int64_t>(n_seqs) + 2) * 8) + align256(parts * sizeof(CachedPart)) +
          align256(parts * 8 * tiles * (cache->D + 4) * 4);
 }
@@ -1977,17 +1973,20 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ULY_ERR_CUDA;
-  p.want_parts = static_cast<int32_t>(cached_want(p.row_tiles, sms < kCachedSms ? sms : kCachedSms));
-  // a unit has at most kMaxUnitParts and at most one a block
-  int64_t grid = p.want_parts + units;
-  const int64_t most = blocks < kMaxUnitParts ? blocks : kMaxUnitParts;
+  p.slots = (sms < kCachedSms ? sms : kCachedSms) * kCachedPerSm[p.row_tiles - 1];
+  p.few = units * 8 <= p.slots;
+  // parts: the blocks make 2 slots of them (1 where there are few units), and each
+  // unit's rounding adds at most one; a unit has at most max_unit_parts and at
+  // most one a block
+  int64_t grid = (p.few ? 1LL : 2LL) * p.slots + units;
+  const int64_t most = blocks < max_unit_parts(p.few) ? blocks : max_unit_parts(p.few);
   if (units * most < grid) grid = units * most;
   p.grid = static_cast<int32_t>(grid);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.before = reinterpret_cast<int64_t*>(ws);
   ws += align256((static_cast<int64_t>(n_seqs) + 2) * 8);
   p.parts = reinterpret_cast<CachedPart*>(ws);
-  const int64_t all = cached_want(p.row_tiles, kCachedSms) + units;
+  const int64_t all = 2LL * kCachedSms * kCachedPerSm[p.row_tiles - 1] + units;
   p.sums = reinterpret_cast<float*>(ws + align256(all * sizeof(CachedPart)));
   return launch_cache_attention(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
