@@ -541,8 +541,9 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
                             const int32_t* seq_starts, int32_t n_seqs, float scale, void* const* o,
                             float* const* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace of uly_sp_prompt_attention for n_seqs sequences (36 bytes a
- * sequence and 16 for 128 rows, about), or -1 for a NULL plan or n_seqs < 0. */
+/* Bytes of workspace of uly_sp_prompt_attention for n_seqs sequences (40 bytes a
+ * sequence and 16 for 128 rows, about; 0 for a little work, then workspace may be
+ * NULL), or -1 for a NULL plan or n_seqs < 0. */
 int64_t uly_sp_prompt_attention_workspace(const uly_plan* plan, int32_t n_seqs);
 
 /* ---- 8-bit paged cache --------------------------------------------------
@@ -621,9 +622,11 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
                         int32_t table_width, float scale, void* o, float* lse, void* workspace,
                         int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace of uly_cache_attention on the current device, or -1 for a
- * bad argument. */
-int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs);
+/* Bytes of workspace of uly_cache_attention (0 where a table's width holds no more
+ * than 1024 tokens, with up to 128 sequences; then workspace may be NULL), or -1
+ * for a bad argument. */
+int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs,
+                                      int32_t table_width);
 
 /* Allocation-free fused attention.  The source pages have no counterpart:
  * this entry point exists for callers that cannot call cudaMalloc -- an

@@ -291,7 +291,7 @@ def test_the_same_bits_every_time_streams_and_graph():
     assert torch.equal(o.view(torch.int16), first.view(torch.int16))
     R.check_cached(c, e, p, None)
     # two graphs that share a workspace, replayed one after the other, with lengths that change
-    ws = torch.empty(cache.attention_workspace(8, c.rows, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(cache.attention_workspace(8, c.rows, 4, d["table"].shape[1]), dtype=torch.uint8, device="cuda")
     graphs = []
     for x, y in ((d, o), (e, p)):
         g = torch.cuda.CUDAGraph()
@@ -364,7 +364,7 @@ def test_prompt_cache_and_generation_together():
 
 def test_refusals():
     import ulysses_sequence_attention_uly_gb300 as uly
-    c = R.Cached("refused", (10, 3), (2, 1), 2, 64, 16, G=2)
+    c = R.Cached("refused", (1030, 3), (2, 1), 2, 64, 16, G=2)
     d = R.cache_inputs(c, 22)
     cache = R.cache_of(d)
     o = torch.empty_like(d["q"])
@@ -377,7 +377,8 @@ def test_refusals():
                    dict(k=torch.zeros((3 * 132,), dtype=torch.bfloat16, device="cuda").as_strided((3, 2, 64), (132, 64, 1)))):
         with pytest.raises(ValueError):
             cache.append(**{**a, **change})
-    need = cache.attention_workspace(4, 3, 2)
+    need = cache.attention_workspace(4, 3, 2, d["table"].shape[1])
+    assert need > 0
     for change in (dict(q=d["q"][:, :3]), dict(o=o[:2]), dict(o=o.float()), dict(lse=torch.zeros((3, 3), device="cuda")),
                    dict(q=d["q"][0]), dict(workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(ValueError):

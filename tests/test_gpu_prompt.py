@@ -113,13 +113,15 @@ def test_plain_attention_of_the_last_row():
     assert float(diff.max()) <= 4 * 2.0 ** -8 * float(d["v"][0].abs().max())
 
 
-def test_streams_workspaces_and_graph():
-    c = R.Prompt("graph", (500, 400), (123, 456, 200), 4, 2, 128, first=30)
+@pytest.mark.parametrize("Hq", [64, 4])  # more items than two an SM, and so few that no workspace is needed
+def test_streams_workspaces_and_graph(Hq):
+    c = R.Prompt("graph", (500, 400), (123, 456, 200), Hq, 4 if Hq > 4 else 2, 128, first=30)
     d = R.prompt_inputs(c, 7)
     plan = run(c, d)  # outside a capture
     side = torch.cuda.Stream()
     # two calls at once on two streams, their workspaces their own
     e = R.prompt_inputs(c, 8)
+    assert (plan.prompt_attention_workspace(3) > 0) == (Hq == 64)
     ws = [torch.empty(plan.prompt_attention_workspace(3), dtype=torch.uint8, device="cuda") for _ in range(2)]
     torch.cuda.synchronize()
     for _ in range(10):
@@ -189,11 +191,12 @@ def test_a_withheld_load_times_out_and_the_next_call_is_right(fill):
 
 def test_refusals():
     import ulysses_sequence_attention_uly_gb300 as uly
-    c = R.Prompt("refused", (64, 64), (100,), 4, 2, 64)
+    c = R.Prompt("refused", (64, 64), (100,), 256, 2, 64)
     d = R.prompt_inputs(c, 10)
     plan = R.plan_of(c)
     ok = dict(q=d["q"], k=d["k"], v=d["v"], o=d["o"], seq_starts=d["starts"], lse=d["lse"])
     need = plan.prompt_attention_workspace(1)
+    assert need > 0
     for change in (dict(q=d["q"][:1]), dict(k=d["q"]), dict(o=[x.float() for x in d["o"]]), dict(lse=d["lse"][:1]),
                    dict(seq_starts=d["starts"].long()), dict(seq_starts=d["starts"].cpu()), dict(seq_starts=[0, 1]),
                    dict(seq_starts=d["starts"][:0]), dict(v=[x.transpose(1, 2) for x in d["v"]]),

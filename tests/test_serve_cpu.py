@@ -25,8 +25,8 @@ def append(c=None, **change):
 
 
 def attention(c=None, **change):
-    a = dict(q=5 * A, qs=0, Hq=4, rows=3, starts=7 * A, lens=8 * A, table=9 * A, n=2, width=4, scale=0.125, o=10 * A,
-             lse=11 * A, ws=12 * A, ws_bytes=1 << 40)
+    a = dict(q=5 * A, qs=0, Hq=4, rows=3, starts=7 * A, lens=8 * A, table=9 * A, n=2, width=400, scale=0.125, o=10 * A,
+             lse=11 * A, ws=12 * A, ws_bytes=1 << 40)  # (a width of more than 1024 tokens: with a workspace)
     a.update(change)
     return uly.lib().uly_cache_attention(c or cache(), *a.values(), None)
 
@@ -73,7 +73,7 @@ def test_append_refuses_pools_that_overlap_each_other_or_the_tables():
                                     dict(ws=10 * A), dict(ws=5 * A)], ids=str)
 def test_attention_refuses(change):
     a = dict(ws_bytes=1 << 23)
-    need = uly.lib().uly_cache_attention_workspace(cache(), 4, 3, 2)
+    need = uly.lib().uly_cache_attention_workspace(cache(), 4, 3, 2, 400)
     assert 0 < need <= 1 << 23
     assert attention(**{**a, **change}) == uly.ULY_ERR_INVALID
 
@@ -90,8 +90,9 @@ def test_null_arguments_and_workspaces():
     assert L.uly_sp_prompt_attention_workspace(None, 1) == -1
     assert L.uly_cache_append(None, A, A, 0, 0, 1, A, A, A, 1, 1, None) == uly.ULY_ERR_INVALID
     assert L.uly_cache_attention(None, A, 0, 4, 1, A, A, A, 1, 1, 0.1, A, A, A, 1, None) == uly.ULY_ERR_INVALID
-    for a in ((None, 4, 3, 2), (cache(H=0), 4, 3, 2), (cache(), 3, 3, 2), (cache(), 0, 3, 2), (cache(), 4, -1, 2),
-              (cache(), 4, 3, -1)):
+    assert L.uly_cache_attention_workspace(cache(), 4, 3, 2, 64) == 0 < L.uly_cache_attention_workspace(cache(), 4, 3, 2, 65)
+    for a in ((None, 4, 3, 2, 1), (cache(H=0), 4, 3, 2, 1), (cache(), 3, 3, 2, 1), (cache(), 0, 3, 2, 1),
+              (cache(), 4, -1, 2, 1), (cache(), 4, 3, -1, 1), (cache(), 4, 3, 2, 0), (cache(page_rows=0), 4, 3, 2, 1)):
         assert L.uly_cache_attention_workspace(*a) == -1
 
 

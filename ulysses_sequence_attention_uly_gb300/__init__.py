@@ -124,7 +124,7 @@ def lib():
         L.uly_cache_append.argtypes = [cache, vp, vp, i64, i64, i64, vp, vp, vp, i32, i32, vp]
         L.uly_cache_attention.argtypes = [cache, vp, i64, i32, i64, vp, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp,
                                           i64, vp]
-        L.uly_cache_attention_workspace.argtypes = [cache, i32, i64, i32]
+        L.uly_cache_attention_workspace.argtypes = [cache, i32, i64, i32, i32]
         L.uly_cache_attention_workspace.restype = i64
         L.uly_device_sm_count.argtypes = [ctypes.c_int]
         L.uly_device_sm_count.restype = i32
@@ -763,9 +763,12 @@ class Plan:
         n_seqs = _vector_len(seq_starts, "seq_starts", dev) - 1
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
-        workspace = _workspace(workspace, self.prompt_attention_workspace(n_seqs), dev, stream)
-        st = lib().uly_sp_prompt_attention(self._h, pq, pk, pv, seq_starts.data_ptr(), n_seqs, scale, po, pl,
-                                           workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+        ws, nbytes = None, self.prompt_attention_workspace(n_seqs)
+        if nbytes or workspace is not None:
+            workspace = _workspace(workspace, nbytes, dev, stream)
+            ws, nbytes = workspace.data_ptr(), workspace.numel()
+        st = lib().uly_sp_prompt_attention(self._h, pq, pk, pv, seq_starts.data_ptr(), n_seqs, scale, po, pl, ws, nbytes,
+                                           _raw_stream(stream, dev))
         if st != ULY_OK:
             raise UlyError(st, "uly_sp_prompt_attention")
 
@@ -845,7 +848,6 @@ class Cache:
         self.tensors = (k_pages, v_pages, k_scale, v_scale)
         self._d = _CacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, rows,
                              H, D)
-        self._work = {}
 
     def _sequences(self, starts, lens, table):
         dev, i32 = self.device, _torch().int32
@@ -881,16 +883,15 @@ class Cache:
             self._call(lib().uly_cache_append, "uly_cache_append", pk, pv, sk, sv, rows, starts.data_ptr(),
                        lens.data_ptr(), table.data_ptr(), n, width, _raw_stream(stream, self.device))
 
-    def attention_workspace(self, Hq: int, n_rows: int, n_seqs: int) -> int:
-        """Bytes of workspace of attention."""
-        with _torch().cuda.device(self.device):
-            return int(lib().uly_cache_attention_workspace(self._d, Hq, n_rows, n_seqs))
+    def attention_workspace(self, Hq: int, n_rows: int, n_seqs: int, width: int) -> int:
+        """Bytes of workspace of attention with a table of that width (0: none is needed)."""
+        return int(lib().uly_cache_attention_workspace(self._d, Hq, n_rows, n_seqs, width))
 
     def attention(self, q, o, starts, lens, table, scale=None, lse=None, workspace=None, stream=None):
         """Attention of the newest tokens (q, o bf16 [rows, Hq, D]) over the cache
         (uly_cache_attention).  lse: f32 [rows, Hq] or None.  workspace: a uint8
-        tensor of attention_workspace(Hq, rows, n_seqs) bytes; by default one is
-        allocated on the call's stream."""
+        tensor of attention_workspace(Hq, rows, n_seqs, width) bytes; by default one
+        is allocated on the call's stream."""
         torch = _torch()
         n, width = self._sequences(starts, lens, table)
         _, H, _, D = self.shape
@@ -905,13 +906,9 @@ class Cache:
             return
         if scale is None:
             scale = 1.0 / math.sqrt(D)
-        key = (Hq, rows, n)
-        nbytes = self._work.get(key)
-        if nbytes is None:
-            if len(self._work) > 256:
-                self._work.clear()
-            nbytes = self._work[key] = self.attention_workspace(*key)
-        workspace = _workspace(workspace, nbytes, dev, stream)
+        ws, nbytes = None, self.attention_workspace(Hq, rows, n, width)
+        if nbytes or workspace is not None:
+            workspace = _workspace(workspace, nbytes, dev, stream)
+            ws, nbytes = workspace.data_ptr(), workspace.numel()
         self._call(lib().uly_cache_attention, "uly_cache_attention", pq, sq, Hq, rows, starts.data_ptr(),
-                   lens.data_ptr(), table.data_ptr(), n, width, scale, po, pl, workspace.data_ptr(),
-                   workspace.numel(), _raw_stream(stream, dev))
+                   lens.data_ptr(), table.data_ptr(), n, width, scale, po, pl, ws, nbytes, _raw_stream(stream, dev))

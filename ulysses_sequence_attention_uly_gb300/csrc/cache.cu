@@ -315,6 +315,7 @@ struct CachedCfg {
 template <int D>
 __device__ __forceinline__ int unit_parts(const CachedParams& p, const SeqWork& w, int64_t total) {
   int64_t n;
+  if (p.whole) return 1;
   if (p.few) {
     n = static_cast<int64_t>(w.blocks) * p.slots / total;
   } else {
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   __syncthreads();
   const int s = my_seq;
   if (s < 0) {
-    if (tid == 0) note->n = 0;
+    if (tid == 0 && !p.whole) note->n = 0;
     return;
   }
   const SeqWork w = seq_work<RT>(p, s);
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   const int b1 = static_cast<int>(static_cast<int64_t>(w.blocks) * (idx + 1) / parts);
   const int64_t row0 = static_cast<int64_t>(tile) * RT;  // the unit's rows among the sequence's
   const int live = static_cast<int>(min(static_cast<int64_t>(w.rows) * p.G - row0, int64_t{RT}));
-  if (tid == 0) *note = CachedPart{parts, idx, static_cast<int32_t>(units), live, row_place(p, w.a, h, row0), row0};
+  if (tid == 0 && !p.whole) *note = CachedPart{parts, idx, static_cast<int32_t>(units), live, row_place(p, w.a, h, row0), row0};
 
   {
     const int32_t* const table = c.table + static_cast<int64_t>(s) * c.table_width;
@@ -834,7 +835,7 @@ cudaError_t launch_cached(const CachedParams& p, cudaStream_t s) {
   cfg.gridDim = dim3(p.grid);
   cfg.dynamicSmemBytes = C::kSmem;
   e = cudaLaunchKernelEx(&cfg, cached_kernel<D, NT>, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   cfg.dynamicSmemBytes = 0;
   cfg.blockDim = dim3(p.few ? 256 : 128);
   return p.few ? cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 8>, p)

@@ -89,8 +89,8 @@ struct PBars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain;
   Item item[kItems];
-  PromptRun run[kMaxRanks];  // direct: the runs of the CTA's sequence
-  PromptUnit unit;           // direct: the CTA's unit, its run among them
+  PromptRun run[kDirectItems * kMaxRanks];  // direct: the runs of the sequences of the CTA's items
+  PromptUnit unit[kDirectItems];            // direct: the items' units, their runs among them
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -400,9 +400,9 @@ struct KeyTiles {
   }
 };
 
-// Direct: unit `w` of the sequences in their own order, by one warp; run -1 where
-// there is none.
-__device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars, int lane) {
+// Direct: unit `w` of the sequences in their own order for the CTA's item k, by one
+// warp; run -1 where there is none.
+__device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars, int k, int lane) {
   const int N = p.shard_begin[p.P];
   int reached = 0, units_before = 0;
   for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
@@ -431,15 +431,16 @@ __device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars
     upto += units_before;
     const bool mine = upto - units <= w && w < upto;
     if (mine) {  // one lane's sequence has it
-      int r = 0, kv = 0, at = upto - units;
+      const int first = k * kMaxRanks;
+      int r = first, kv = 0, at = upto - units;
       for (int i = 0; i < p.P; ++i) {
         const int lo = max(a, p.shard_begin[i]), len = min(b, p.shard_begin[i + 1]) - lo;
         if (len <= 0) continue;
-        bars.run[r] = PromptRun{i, lo - p.shard_begin[i], len, 0};
+        bars.run[r] = PromptRun{i, lo - p.shard_begin[i], len, first};
         const int here = units_of(len, p.pair), tiles = (len + kTileRows - 1) / kTileRows;
         if (w >= at && w < at + here) {
           const int tile = (w - at) * (p.pair ? 1 : 2);
-          bars.unit = PromptUnit{r, tile, kv + (p.pair ? tile : min(tile + 1, tiles - 1)) + 1, 0};
+          bars.unit[k] = PromptUnit{r, tile, kv + (p.pair ? tile : min(tile + 1, tiles - 1)) + 1, 0};
         }
         at += here;
         kv += tiles;
@@ -450,7 +451,7 @@ __device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars
     reached = __shfl_sync(0xffffffffu, b, 31);
     units_before = __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (lane == 0) bars.unit.run = -1;
+  if (lane == 0) bars.unit[k].run = -1;
 }
 
 template <int D>
@@ -490,9 +491,9 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     it.run = -1;
     if (idx < n_items) {
       const int w = idx / p.n_hp, hp = idx - w * p.n_hp;
-      if (w != known) {
+      if (w != known || p.direct) {
         known = w;
-        u = *reinterpret_cast<const int4*>(p.direct ? &bars.unit : &p.cut.t.units[w]);
+        u = *reinterpret_cast<const int4*>(p.direct ? &bars.unit[k] : &p.cut.t.units[w]);
         f = r = *reinterpret_cast<const int4*>(runs + u.x);
         if (r.w != u.x) f = *reinterpret_cast<const int4*>(runs + r.w);
       }
@@ -519,7 +520,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     const int n = max(it.n[0], it.n[1]), kv_head = it.head / p.G;
     KeyTiles kt;
     kt.begin(runs, it.first_run, f);
-    int next = n_items;
+    int next = idx + p.cut.grid;  // direct
     for (int s = 0; s < n; ++s) {
       // the next item is taken late, so that whoever is behind takes less; the
       // steps under way cover what finding out about it costs
@@ -892,14 +893,23 @@ __global__ void __launch_bounds__(320, 1) prompt_kernel(const __grid_constant__ 
     tmem_alloc(smem_u32(&bars.tmem_base), 512);
     tmem_relinquish();
   }
-  if (warp == 8 && p.direct) find_unit(p.cut, blockIdx.x / p.n_hp, bars, lane);
+  if (warp == 8 && p.direct) {
+    for (int k = 0; k < kDirectItems; ++k)
+      find_unit(p.cut, (static_cast<int>(blockIdx.x) + k * p.cut.grid) / p.n_hp, bars, k, lane);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (!p.direct) wait_for_previous_launch();  // the tables
   const uint32_t tmem = bars.tmem_base;
-  // (direct: one item, or none past the last unit)
-  const int n_items = !p.direct ? p.cut.t.head[0] * p.n_hp : bars.unit.run < 0 ? 0 : blockIdx.x + 1;
+  // (direct: up to the CTA's first item past the last unit)
+  int n_items = 0;
+  if (!p.direct) {
+    n_items = p.cut.t.head[0] * p.n_hp;
+  } else {
+    for (int k = 0; k < kDirectItems; ++k)
+      if (bars.unit[k].run >= 0) n_items = blockIdx.x + k * p.cut.grid + 1;
+  }
   const PromptRun* const runs = p.direct ? bars.run : p.cut.t.runs;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
   if (blockIdx.x < n_items) {

@@ -58,13 +58,14 @@ struct PromptParams {
   float* lse[kMaxRanks];
   int32_t Hq, G, lse_out;
   int32_t n_hp;       // items of one unit: Hq / 2 or Hq
-  int32_t direct;     // no tables: CTA b works item b out by itself
+  int32_t direct;     // no tables: CTA b works items b and b + grid out by itself
   float scale_log2;
   int32_t* status;
   uint64_t wait_ns;
   int32_t withhold_fill;  // test hook, as in AttnParams
 };
 constexpr int kSortBuckets = 2048;
+constexpr int kDirectItems = 2;  // items that a CTA works out by itself, at most
 
 // ----------------------------------------------------------------- cache --
 struct CacheParams {
@@ -109,6 +110,7 @@ struct CachedParams {
   int32_t grid;
   int32_t slots;       // CTAs that run at once
   int32_t few;         // units: at most one for eight of those
+  int32_t whole;       // units in one part each
   int32_t row_tiles;   // 8-row tiles of queries a unit: 1 or 2
   const uint8_t* q;
   int64_t q_row_bytes;

@@ -1737,10 +1737,31 @@ constexpr int64_t kMaxRows = 1LL << 27;
 bool misaligned(const void* p, uintptr_t to) { return !p || (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 // Tables of the prompt kernels (serve.cuh) in the workspace.  A sequence's rows
-// are cut where a shard ends, so there are less than n_seqs + P runs; 128-row
-// tiles of them, less than one for every 128 rows and one a run.
+// are cut where a shard ends, so there are less than n_seqs + P runs; units of 128
+// (or 256) rows of them, less than one for as many rows and one a run.  Where the
+// CTAs work their items out by themselves there are none.
+struct PromptShape {
+  int32_t pair;          // two heads that share k and v walk the same tiles to the end; with two tiles of one head
+                         // the first idles for the last tile's time
+  int64_t n_hp;          // items of a unit
+  int64_t runs, units;   // at most
+  bool direct(int sms) const { return units * n_hp <= kDirectItems * sms; }
+};
+PromptShape prompt_shape(const uly_plan* pl, int32_t n_seqs) {
+  PromptShape s;
+  s.pair = pl->d.Hq / pl->d.Hkv % 2 == 0;
+  s.n_hp = s.pair ? pl->d.Hq / 2 : pl->d.Hq;
+  s.runs = static_cast<int64_t>(n_seqs) + pl->d.P;
+  s.units = pl->nq / (s.pair ? kTileRows : kUnitRows) + s.runs;
+  return s;
+}
+
 int64_t prompt_tables(const uly_plan* pl, int32_t n_seqs, uint8_t* ws, PromptTables* t) {
-  const int64_t runs = static_cast<int64_t>(n_seqs) + pl->d.P, units = pl->nq / kTileRows + runs;
+  const PromptShape s = prompt_shape(pl, n_seqs);
+  const int64_t runs = s.runs, units = s.units;
+  t->max_runs = static_cast<int32_t>(runs);
+  t->max_units = static_cast<int32_t>(units);
+  if (s.direct(pl->sm_count)) return 0;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* const a = ws + at;
@@ -1752,8 +1773,6 @@ int64_t prompt_tables(const uly_plan* pl, int32_t n_seqs, uint8_t* ws, PromptTab
   t->run_unit = reinterpret_cast<int32_t*>(take((runs + 1) * 4));
   t->run_kv = reinterpret_cast<int32_t*>(take(runs * 4));
   t->units = reinterpret_cast<PromptUnit*>(take(units * sizeof(PromptUnit)));
-  t->max_runs = static_cast<int32_t>(runs);
-  t->max_units = static_cast<int32_t>(units);
   return at;
 }
 
@@ -1819,13 +1838,31 @@ int64_t cached_units(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t
   return cache->H * (n_rows * (Hq / cache->H) / (8 * row_tiles) + n_seqs);
 }
 
-// Workspace: parts before each sequence, a note and the sums of 8 row_tiles rows
-// for each part.
-int64_t cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
+// Keys that a sequence's pages can hold, in blocks of 64.
+int64_t cached_blocks(const uly_cache* cache, int32_t table_width) {
+  return (static_cast<int64_t>(table_width) * cache->page_rows + 63) / 64;
+}
+
+// Are units left whole?  Up to 16 blocks (1024 keys) a second launch and a
+// workspace cost more than the split gains (499 tokens, 32 heads on 8, a call:
+XX
+bool cached_whole(const uly_cache* cache, int32_t table_width) { return cached_blocks(cache, table_width) <= 16; }
+
+// Workspace: with more than 128 sequences the parts before each of them; with
+// units in parts a note and the sums of 8 row_tiles rows for each part.
+struct CachedWork {
+  int64_t before, parts, sums, total;
+};
+CachedWork cached_work(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs, int32_t table_width) {
   const int tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
+  CachedWork w = {};
+  if (n_seqs > 128) w.total = align256((static_cast<int64_t>(n_seqs) + 2) * 8);
+  w.parts = w.sums = w.total;
+  if (cached_whole(cache, table_width)) return w;
   const int64_t parts = 2LL * kCachedSms * kCachedPerSm[tiles - 1] + cached_units(cache, Hq, n_rows, n_seqs, tiles);
-  return align256((static_cast<int64_t>(n_seqs) + 2) * 8) + align256(parts * sizeof(CachedPart)) +
-         align256(parts * 8 * tiles * (cache->D + 4) * 4);
+  w.sums = w.parts + align256(parts * sizeof(CachedPart));
+  w.total = w.sums + align256(parts * 8 * tiles * (cache->D + 4) * 4);
+  return w;
 }
 
 }  // namespace
@@ -1857,13 +1894,12 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
   static thread_local Spans spans;
   memset(&p, 0, sizeof(p));
   PromptCut& c = p.cut;
-  if (misaligned(workspace, 256) ||
-      workspace_bytes < prompt_tables(plan, n_seqs, static_cast<uint8_t*>(workspace), &c.t))
-    return ULY_ERR_INVALID;
+  const int64_t need = prompt_tables(plan, n_seqs, static_cast<uint8_t*>(workspace), &c.t);
+  if (need && (misaligned(workspace, 256) || workspace_bytes < need)) return ULY_ERR_INVALID;
   if ((rc = check_device(plan))) return rc;
 
   spans.n = 0;
-  spans.add(workspace, workspace_bytes, true);
+  spans.add(workspace, need ? workspace_bytes : 0, true);
   spans.add(seq_starts, (static_cast<int64_t>(n_seqs) + 1) * 4, false);
   for (int i = 0; i < P; ++i) {
     const int64_t rows = plan->lens[i], qb = rows * d.Hq * d.D * 2, kb = rows * d.Hkv * d.D * 2;
@@ -1888,17 +1924,16 @@ int uly_sp_prompt_attention(const uly_plan* plan, const void* const* q, const vo
   c.P = P;
   p.Hq = d.Hq;
   p.G = d.Hq / d.Hkv;
-  // two heads that share k and v walk the same tiles to the end; with two tiles
-  // of one head the first idles for the last tile's time
-  c.pair = p.G % 2 == 0;
-  p.n_hp = c.pair ? d.Hq / 2 : d.Hq;
-  if (static_cast<int64_t>(c.t.max_units) * p.n_hp > 0x7FFF0000) return ULY_ERR_UNSUPPORTED;
+  const PromptShape s = prompt_shape(plan, n_seqs);
+  c.pair = s.pair;
+  p.n_hp = static_cast<int32_t>(s.n_hp);
+  if (s.units * s.n_hp > 0x7FFF0000) return ULY_ERR_UNSUPPORTED;
   for (int64_t tiles = plan->nq / kTileRows + P; (tiles >> c.sort_shift) >= kSortBuckets;) ++c.sort_shift;
-  // with no more items than SMs each CTA finds its own, which saves the launch
-  // before it (one prompt of 17 rows: 23.5 -> 19.8 us a call)
+  // with no more than two items an SM each CTA finds its own, which saves a launch
+  // and the workspace (one prompt of 17 rows: 23.5 -> 11.4 us a call)
+  p.direct = s.direct(plan->sm_count);
   c.grid = plan->sm_count;
-  p.direct = static_cast<int64_t>(c.t.max_units) * p.n_hp <= c.grid;
-  if (p.direct) c.grid = c.t.max_units * p.n_hp;
+  if (s.units * s.n_hp < c.grid) c.grid = static_cast<int32_t>(s.units * s.n_hp);
   p.status = plan->status;
   p.wait_ns = plan->wait_ns;
   p.withhold_fill = plan->withhold_fill;
@@ -1932,9 +1967,12 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
   return launch_cache_append(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
 
-int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs) {
-  if (!cache || Hq < 1 || cache->H < 1 || cache->D < 1 || Hq % cache->H || n_rows < 0 || n_seqs < 0) return -1;
-  return cached_work(cache, Hq, n_rows, n_seqs);
+int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs,
+                                      int32_t table_width) {
+  if (!cache || Hq < 1 || cache->H < 1 || cache->D < 1 || cache->page_rows < 1 || Hq % cache->H || n_rows < 0 ||
+      n_seqs < 0 || table_width < 1)
+    return -1;
+  return cached_work(cache, Hq, n_rows, n_seqs, table_width).total;
 }
 
 int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_stride, int32_t Hq, int64_t n_rows,
@@ -1951,11 +1989,12 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
   if (misaligned(q, 16) || misaligned(o, 16) || (lse && misaligned(lse, 4)) ||
       !(p.q_row_bytes = row_step(q_row_stride, dense)))
     return ULY_ERR_INVALID;
-  if (misaligned(workspace, 256) || workspace_bytes < cached_work(cache, Hq, n_rows, n_seqs)) return ULY_ERR_INVALID;
+  const CachedWork work = cached_work(cache, Hq, n_rows, n_seqs, table_width);
+  if (work.total && (misaligned(workspace, 256) || workspace_bytes < work.total)) return ULY_ERR_INVALID;
   spans.add(q, rows_bytes(n_rows, p.q_row_bytes, dense), false);
   spans.add(o, n_rows * dense * 2, true);
   spans.add(lse, n_rows * Hq * 4, true);
-  spans.add(workspace, workspace_bytes, true);
+  spans.add(workspace, work.total ? workspace_bytes : 0, true);
   if (spans.clash()) return ULY_ERR_INVALID;
   if (!n_rows || !n_seqs) return ULY_OK;
   p.q = static_cast<const uint8_t*>(q);
@@ -1967,7 +2006,7 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
   p.row_tiles = cached_row_tiles(cache, Hq, n_rows, n_seqs);
   // blocks of all units, and parts: both have to fit their counters
   const int64_t units = cached_units(cache, Hq, n_rows, n_seqs, p.row_tiles);
-  const int64_t blocks = (static_cast<int64_t>(table_width) * cache->page_rows + 63) / 64;
+  const int64_t blocks = cached_blocks(cache, table_width);
   if (blocks > (1LL << 60) / units || units > (1LL << 30)) return ULY_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1975,19 +2014,18 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
     return ULY_ERR_CUDA;
   p.slots = (sms < kCachedSms ? sms : kCachedSms) * kCachedPerSm[p.row_tiles - 1];
   p.few = units * 8 <= p.slots;
+  p.whole = cached_whole(cache, table_width);
   // parts: the blocks make 2 slots of them (1 where there are few units), and each
   // unit's rounding adds at most one; a unit has at most max_unit_parts and at
   // most one a block
   int64_t grid = (p.few ? 1LL : 2LL) * p.slots + units;
-  const int64_t most = blocks < max_unit_parts(p.few) ? blocks : max_unit_parts(p.few);
+  const int64_t most = p.whole ? 1 : blocks < max_unit_parts(p.few) ? blocks : max_unit_parts(p.few);
   if (units * most < grid) grid = units * most;
   p.grid = static_cast<int32_t>(grid);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
   p.before = reinterpret_cast<int64_t*>(ws);
-  ws += align256((static_cast<int64_t>(n_seqs) + 2) * 8);
-  p.parts = reinterpret_cast<CachedPart*>(ws);
-  const int64_t all = 2LL * kCachedSms * kCachedPerSm[p.row_tiles - 1] + units;
-  p.sums = reinterpret_cast<float*>(ws + align256(all * sizeof(CachedPart)));
+  p.parts = reinterpret_cast<CachedPart*>(ws + work.parts);
+  p.sums = reinterpret_cast<float*>(ws + work.sums);
   return launch_cache_attention(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
 
