@@ -27,7 +27,10 @@ CASES = [
     R.Prompt("long rows", (2000, 1300), (3200,), 4, 2, 128, first=7, std=0.7),
     R.Prompt("long rows, odd group", (2000, 1300), (3200,), 6, 2, 64, first=7),
     R.Prompt("peaked", (512,), (512,), 4, 2, 128, std=4.0),
-    # (more items than SMs: the ones above mostly have fewer)
+    # (more items than SMs, and more than two an SM: the ones above mostly have fewer)
+    R.Prompt("tile ends, some heads", (800, 700), (127, 128, 129, 255, 256, 257, 1), 28, 14, 128, first=100),
+    R.Prompt("tile ends, some odd groups", (800, 700), (127, 128, 129, 255, 256, 257, 1), 20, 20, 64, first=100),
+    R.Prompt("long rows, some heads", (2100,), (2100,), 16, 8, 64),
     R.Prompt("tile ends, many heads", (1500,), (127, 128, 129, 255, 256, 257, 1), 48, 8, 128, first=100),
     R.Prompt("tile ends, many odd groups", (1500,), (127, 128, 129, 255, 256, 257, 1), 24, 8, 64, first=100),
     R.Prompt("long rows, many heads", (2000, 1300, 9, 700), (3200, 0, 77, 700), 32, 8, 128, first=7, std=0.7),

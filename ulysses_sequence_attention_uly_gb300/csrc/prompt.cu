@@ -355,16 +355,19 @@ __device__ __forceinline__ void edge_row(uint32_t tS, uint32_t tO, float sl2, bo
   const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
   uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    if (c < chunks) {
-      tmem_ld32(tS + 32 * c, a);
-      tmem_wait_ld();
-    }
-    const int n = c < chunks ? limit - 32 * c : 0;
+  for (int c = 0; c < chunks; ++c) {
+    tmem_ld32(tS + 32 * c, a);
+    tmem_wait_ld();
+    const int n = limit - 32 * c;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (i >= n) a[i] = __float_as_uint(-INFINITY);
     exp_store(a, sl2, neg, tS + 16 * c, acc);
+  }
+#pragma unroll 1
+  for (int c = chunks; c < 4; ++c) {
+    const uint32_t none[16] = {};
+    tmem_st16(tS + 16 * c, none);
   }
   if (!first && __any_sync(0xffffffffu, alpha != 1.f)) rescale<D>(tO, alpha);
   float s0, s1;
@@ -400,58 +403,65 @@ struct KeyTiles {
   }
 };
 
-// Direct: unit `w` of the sequences in their own order for the CTA's item k, by one
-// warp; run -1 where there is none.
-__device__ __forceinline__ void find_unit(const PromptCut& p, int w, PBars& bars, int k, int lane) {
+// Direct, by one warp: the CTA's items among all in the order of the sequences.
+// CTA b has item b and, where there are more items than CTAs, the one as far from
+// the end: of one sequence a short one and a long one.
+__device__ __forceinline__ void find_items(const PromptCut& p, int n_hp, PBars& bars, int lane) {
   const int N = p.shard_begin[p.P];
-  int reached = 0, units_before = 0;
-  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-    // rows [a, b) of sequence s0 + lane, as in tables_kernel
-    const int s = s0 + lane;
-    int a = s < p.n_seqs ? min(max(p.seq_starts[s], 0), N) : 0;
-    const int end = s < p.n_seqs ? min(max(p.seq_starts[s + 1], 0), N) : 0;
+  int total = 0;
+  if (lane < kDirectItems) bars.unit[lane].run = -1;
+  // first how many units there are, then the items' own
+  for (int k = -1; k < kDirectItems; ++k) {
+    const int idx = k <= 0 ? static_cast<int>(blockIdx.x) : total * n_hp - 1 - static_cast<int>(blockIdx.x);
+    if (k >= 0 && (idx >= total * n_hp || (k > 0 && idx < p.grid))) break;
+    const int w = k < 0 ? -1 : idx / n_hp;
+    int reached = 0, units_before = 0;
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+      // rows [a, b) of sequence s0 + lane, as in tables_kernel
+      const int s = s0 + lane;
+      int a = s < p.n_seqs ? min(max(p.seq_starts[s], 0), N) : 0;
+      const int end = s < p.n_seqs ? min(max(p.seq_starts[s + 1], 0), N) : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, a, d);
-      if (lane >= d) a = max(a, y);
-    }
-    a = max(a, reached);
-    const int b = s < p.n_seqs ? max(a, end) : a;
-    int units = 0;
-    for (int i = 0; i < p.P; ++i) {
-      const int len = min(b, p.shard_begin[i + 1]) - max(a, p.shard_begin[i]);
-      if (len > 0) units += units_of(len, p.pair);
-    }
-    int upto = units;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    upto += units_before;
-    const bool mine = upto - units <= w && w < upto;
-    if (mine) {  // one lane's sequence has it
-      const int first = k * kMaxRanks;
-      int r = first, kv = 0, at = upto - units;
-      for (int i = 0; i < p.P; ++i) {
-        const int lo = max(a, p.shard_begin[i]), len = min(b, p.shard_begin[i + 1]) - lo;
-        if (len <= 0) continue;
-        bars.run[r] = PromptRun{i, lo - p.shard_begin[i], len, first};
-        const int here = units_of(len, p.pair), tiles = (len + kTileRows - 1) / kTileRows;
-        if (w >= at && w < at + here) {
-          const int tile = (w - at) * (p.pair ? 1 : 2);
-          bars.unit[k] = PromptUnit{r, tile, kv + (p.pair ? tile : min(tile + 1, tiles - 1)) + 1, 0};
-        }
-        at += here;
-        kv += tiles;
-        ++r;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, a, d);
+        if (lane >= d) a = max(a, y);
       }
+      a = max(a, reached);
+      const int b = s < p.n_seqs ? max(a, end) : a;
+      int units = 0;
+      for (int i = 0; i < p.P; ++i) {
+        const int len = min(b, p.shard_begin[i + 1]) - max(a, p.shard_begin[i]);
+        if (len > 0) units += units_of(len, p.pair);
+      }
+      int upto = units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      upto += units_before;
+      if (upto - units <= w && w < upto) {  // one lane's sequence has it
+        const int first = k * kMaxRanks;
+        int r = first, kv = 0, at = upto - units;
+        for (int i = 0; i < p.P; ++i) {
+          const int lo = max(a, p.shard_begin[i]), len = min(b, p.shard_begin[i + 1]) - lo;
+          if (len <= 0) continue;
+          bars.run[r] = PromptRun{i, lo - p.shard_begin[i], len, first};
+          const int here = units_of(len, p.pair), tiles = (len + kTileRows - 1) / kTileRows;
+          if (w >= at && w < at + here) {
+            const int tile = (w - at) * (p.pair ? 1 : 2);
+            bars.unit[k] = PromptUnit{r, tile, kv + (p.pair ? tile : min(tile + 1, tiles - 1)) + 1, idx - w * n_hp};
+          }
+          at += here;
+          kv += tiles;
+          ++r;
+        }
+      }
+      reached = __shfl_sync(0xffffffffu, b, 31);
+      units_before = __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (__any_sync(0xffffffffu, mine)) return;
-    reached = __shfl_sync(0xffffffffu, b, 31);
-    units_before = __shfl_sync(0xffffffffu, upto, 31);
+    if (k < 0) total = units_before;
   }
-  if (lane == 0) bars.unit[k].run = -1;
 }
 
 template <int D>
@@ -480,7 +490,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     ++g;
     return true;
   };
-  int idx = blockIdx.x, known = -1;
+  int idx = p.direct ? 0 : blockIdx.x, known = -1;
   int4 u, r, f;  // the item's unit, its run, its sequence's first run
   for (int k = 0; ok; ++k) {
     const int slot = k % kItems;
@@ -490,10 +500,12 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     Item it = {};
     it.run = -1;
     if (idx < n_items) {
-      const int w = idx / p.n_hp, hp = idx - w * p.n_hp;
+      const int w = idx / p.n_hp;
+      int hp = idx - w * p.n_hp;
       if (w != known || p.direct) {
         known = w;
         u = *reinterpret_cast<const int4*>(p.direct ? &bars.unit[k] : &p.cut.t.units[w]);
+        if (p.direct) hp = u.w;
         f = r = *reinterpret_cast<const int4*>(runs + u.x);
         if (r.w != u.x) f = *reinterpret_cast<const int4*>(runs + r.w);
       }
@@ -520,7 +532,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
     const int n = max(it.n[0], it.n[1]), kv_head = it.head / p.G;
     KeyTiles kt;
     kt.begin(runs, it.first_run, f);
-    int next = idx + p.cut.grid;  // direct
+    int next = idx + 1;  // direct
     for (int s = 0; s < n; ++s) {
       // the next item is taken late, so that whoever is behind takes less; the
       // steps under way cover what finding out about it costs
@@ -586,7 +598,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
 
   int n_item = 0;                // items read
   int left0 = 0, left1 = 0;      // steps of this item that a tile still has, this one included
-  uint32_t par_p0 = 0, par_p1 = 0, par_q0 = 0, par_q1 = 0;
+  uint32_t par_p = 0, par_q = 0;  // parities of the two tiles' barriers, a bit each
   uint32_t acc = 0;              // the item has had a step
   uint32_t turn = 0;             // turns of the ring: step s = turn * kHalf + u
   int u = 0;
@@ -606,30 +618,32 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     ++n_item;
     return true;
   };
-  // Any step: a tile may end, or begin the next item.  The descriptors are
-  // worked out here; K of the next step is in slot 2u + 2, V of this one in 2u + 1.
-  auto scores = [&](int i, int ku, int steps, bool fresh, uint32_t& par_q) {
+  // Any step: a tile may end, or begin the next item.  All of it in loops that are
+  // not unrolled: short items come here with every step, and what a CTA's roles
+  // go through once an item does not stay in the instruction cache when it is
+  // long (1024-row prompts 77.0 -> 75.4 us, 128-row ones of 64-wide heads 21.1 -> 20.1).
+  // K of the step after one in turn u is in slot 2u + 2, V of that one in 2u + 1.
+  auto scores = [&](int i, int ku, int steps, bool fresh) {
     if (fresh) {
-      if (!wait(bars.q_full[i], par_q)) return;
-      par_q ^= 1;
+      if (!wait(bars.q_full[i], par_q >> i)) return;
+      par_q ^= 1u << i;
     }
-    const uint32_t k_lo = kv_lo + (2 * ku + 2) % C::kSlots * kTileLo;
-#pragma unroll
+    const uint32_t a_lo = q_lo + i * kTileLo, b_lo = kv_lo + (2 * ku + 2) % C::kSlots * kTileLo, d = tmem + 128 * i;
+#pragma unroll 1
     for (int k = 0; k < C::kQkSteps; ++k) {
       const uint32_t off = ((k >> 2) * C::kPanelBytes + (k & 3) * 32) >> 4;
-      mma_bf16_ss(tmem + 128 * i, hi_s | (q_lo + i * kTileLo + off), hi_s | (k_lo + off), C::kIdescS, k > 0);
+      mma_bf16_ss(d, hi_s | (a_lo + off), hi_s | (b_lo + off), C::kIdescS, k > 0);
     }
     mma_commit(smem_u32(&bars.s_full[i]));
     if (steps == 1) mma_commit(smem_u32(&bars.q_empty[i]));  // the item's last scores of this tile
   };
-  auto values = [&](int i, int steps, uint32_t& par_p) {
-    if (!wait(bars.p_full[i], par_p)) return;
-    par_p ^= 1;
-    const uint32_t v_lo = kv_lo + (2 * u + 1) * kTileLo;
-#pragma unroll
+  auto values = [&](int i, int steps) {
+    if (!wait(bars.p_full[i], par_p >> i)) return;
+    par_p ^= 1u << i;
+    const uint32_t v_lo = kv_lo + (2 * u + 1) * kTileLo, d = tmem + 256 + D * i, pa = tmem + 128 * i;
+#pragma unroll 1
     for (int k = 0; k < C::kPvSteps; ++k)
-      mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, hi_v | (v_lo + ((k * 16 * 128) >> 4)), C::kIdescO,
-                  acc | (k > 0));
+      mma_bf16_ts(d, pa + 8 * k, hi_v | (v_lo + ((k * 16 * 128) >> 4)), C::kIdescO, acc | (k > 0));
     if (steps == 1) mma_commit(smem_u32(&bars.o_done[i]));
   };
   auto any_step = [&]() {
@@ -644,14 +658,20 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     }
     const int bi = (u + 1) % C::kHalf;
     if (!wait(bars.full[bi], turn + (u == C::kHalf - 1 ? 1 : 0))) return;
-    if (left0) values(0, left0, par_p0);
-    // where the next item's queries are not here yet, this one's second product
-    // does not wait for them
-    const bool here = next0 && !(last && !mbar_test(smem_u32(&bars.q_full[0]), par_q0 & 1));
-    if (ok && here) scores(0, u, next0, last, par_q0);
-    if (ok && left1) values(1, left1, par_p1);
-    if (ok && next0 && !here) scores(0, u, next0, last, par_q0);
-    if (ok && next1) scores(1, u, next1, last, par_q1);
+    bool late = false;  // the next item's queries are not here yet: this one's second product does not wait for them
+#pragma unroll 1
+    for (int a = 0; ok && a < 4; ++a) {
+      const int i = late ? a & 1 : a >> 1;
+      const bool pv = late ? a < 2 : (a & 1) == 0;
+      const int steps = pv ? (i ? left1 : left0) : (i ? next1 : next0);
+      if (!steps) continue;
+      if (pv) {
+        values(i, steps);
+        if (a == 0) late = ok && last && next0 && left1 && !mbar_test(smem_u32(&bars.q_full[0]), par_q & 1);
+      } else {
+        scores(i, u, steps, last);
+      }
+    }
     if (!ok) return;
     if (more) mma_commit(smem_u32(&bars.empty[bi]));
     left0 = next0;
@@ -664,8 +684,9 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     more = true;
     if (wait(bars.full[0], 0)) {
       // (K of step 0 is in slot 0)
-      if (left0) scores(0, C::kHalf - 1, left0, true, par_q0);
-      if (ok && left1) scores(1, C::kHalf - 1, left1, true, par_q1);
+#pragma unroll 1
+      for (int i = 0; ok && i < 2; ++i)
+        if (i ? left1 : left0) scores(i, C::kHalf - 1, i ? left1 : left0, true);
       if (ok) mma_commit(smem_u32(&bars.empty[0]));
     }
   }
@@ -687,14 +708,14 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
         const int uu = w % C::kHalf, bi = (uu + 1) % C::kHalf;
         if (plain == 0) break;
         if (!wait(bars.full[bi], uu == kLastU ? turn + 1 : turn)) break;
-        if (!wait(bars.p_full[0], par_p0)) break;
+        if (!wait(bars.p_full[0], par_p)) break;
 #pragma unroll
         for (int k = 0; k < C::kPvSteps; ++k) mma_bf16_ts(tmem + 256, tmem + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
 #pragma unroll
         for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem, dq[0][k], dk[uu][k], C::kIdescS, k > 0);
         mma_commit(smem_u32(&bars.s_full[0]));
         if (plain == 1 && left0 == 1) mma_commit(smem_u32(&bars.q_empty[0]));
-        if (!wait(bars.p_full[1], par_p1)) break;
+        if (!wait(bars.p_full[1], par_p >> 1)) break;
 #pragma unroll
         for (int k = 0; k < C::kPvSteps; ++k)
           mma_bf16_ts(tmem + 256 + D, tmem + 128 + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
@@ -703,8 +724,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
         mma_commit(smem_u32(&bars.s_full[1]));
         if (plain == 1 && left1 == 1) mma_commit(smem_u32(&bars.q_empty[1]));
         mma_commit(smem_u32(&bars.empty[bi]));
-        par_p0 ^= 1;
-        par_p1 ^= 1;
+        par_p ^= 3;
         acc = 1;
         u = bi;
         if (uu == kLastU) ++turn;
@@ -893,26 +913,17 @@ __global__ void __launch_bounds__(320, 1) prompt_kernel(const __grid_constant__ 
     tmem_alloc(smem_u32(&bars.tmem_base), 512);
     tmem_relinquish();
   }
-  if (warp == 8 && p.direct) {
-    for (int k = 0; k < kDirectItems; ++k)
-      find_unit(p.cut, (static_cast<int>(blockIdx.x) + k * p.cut.grid) / p.n_hp, bars, k, lane);
-  }
+  if (warp == 8 && p.direct) find_items(p.cut, p.n_hp, bars, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (!p.direct) wait_for_previous_launch();  // the tables
   const uint32_t tmem = bars.tmem_base;
-  // (direct: up to the CTA's first item past the last unit)
-  int n_items = 0;
-  if (!p.direct) {
-    n_items = p.cut.t.head[0] * p.n_hp;
-  } else {
-    for (int k = 0; k < kDirectItems; ++k)
-      if (bars.unit[k].run >= 0) n_items = blockIdx.x + k * p.cut.grid + 1;
-  }
+  const int n_items = p.direct ? (bars.unit[0].run >= 0) + (bars.unit[1].run >= 0) : p.cut.t.head[0] * p.n_hp;
+  static_assert(kDirectItems == 2, "items are counted above");
   const PromptRun* const runs = p.direct ? bars.run : p.cut.t.runs;
   const uint64_t deadline = globaltimer_ns() + p.wait_ns;
-  if (blockIdx.x < n_items) {
+  if ((p.direct ? 0 : static_cast<int>(blockIdx.x)) < n_items) {
     if (warp == 8) {
       if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, runs, deadline);
     } else if (warp == 9) {

@@ -25,7 +25,7 @@ struct alignas(16) PromptUnit {
   int32_t run;
   int32_t tile;       // its (first) tile inside the run
   int32_t n_kv;       // 128-key tiles up to the diagonal of its (last) tile
-  int32_t pad;
+  int32_t hp;         // direct: the item's place among the unit's
 };
 
 // Written by tables_kernel, in the caller's workspace.
@@ -58,7 +58,7 @@ struct PromptParams {
   float* lse[kMaxRanks];
   int32_t Hq, G, lse_out;
   int32_t n_hp;       // items of one unit: Hq / 2 or Hq
-  int32_t direct;     // no tables: CTA b works items b and b + grid out by itself
+  int32_t direct;     // no tables: a CTA works its items, up to kDirectItems, out by itself
   float scale_log2;
   int32_t* status;
   uint64_t wait_ns;
