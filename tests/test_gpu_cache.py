@@ -19,6 +19,9 @@ APPENDS = [
     R.Cached("many rows", (0, 100, 7), (1500, 900, 31), 2, 64, 32),
     R.Cached("wide page", (100, 0), (200, 129), 2, 64, 128),
     R.Cached("small page", (3, 0), (50, 17), 2, 128, 16),
+    # (few rows a sequence on average)
+    R.Cached("a long one among tokens", (5,) * 12 + (3,), (1,) * 12 + (75,), 5, 128, 64),
+    R.Cached("long ones among tokens", (0, 100) + (126, 127, 0) * 10, (90, 30) + (1, 2, 3) * 10, 3, 64, 128),
 ]
 
 

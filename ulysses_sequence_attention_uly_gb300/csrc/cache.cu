@@ -52,14 +52,73 @@ __device__ __forceinline__ void seq_rows(const CacheParams& c, int s, int& a, in
   b = min(max(c.starts[s + 1], a), c.n_rows);
 }
 
+// Does `row` lead, that is, is it the first new row of its page?  Then its page,
+// slot and the number of the page's new rows.
+__device__ __forceinline__ bool leads(const CacheParams& c, int row, int& page, int& slot, int& rows) {
+  int lo = 0, hi = c.n_seqs;  // the first sequence that ends behind the row
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c.starts[mid + 1] > row)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  if (lo >= c.n_seqs) return false;
+  int a, b;
+  seq_rows(c, lo, a, b);
+  const int64_t pos = static_cast<int64_t>(c.lens[lo]) - (b - a) + (row - a);
+  slot = static_cast<int>(pos & (c.page_rows - 1));
+  if (row < a || pos < 0 || (pos >> c.page_shift) >= c.table_width || (row != a && slot != 0)) return false;
+  page = c.table[static_cast<int64_t>(lo) * c.table_width + (pos >> c.page_shift)];
+  rows = min(b - row, c.page_rows - slot);
+  return page >= 0 && page < c.n_pages;
+}
+
+// Largest magnitude of eight bf16 values (fmaxf leaves a NaN out).
+__device__ __forceinline__ float largest(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+  return m;
+}
+
+// Eight bf16 values times f, as codes.
+__device__ __forceinline__ uint2 codes_of(const uint4& v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint16_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    o[k] = e4m3x2_of_f32(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+  return make_uint2(pack_b16x2(o[0], o[1]), pack_b16x2(o[2], o[3]));
+}
+
+// Eight codes brought from one scale to another, f their ratio.
+__device__ __forceinline__ void bring(uint2* at, float f) {
+  uint2 b = *at;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float f0, f1, f2, f3;
+    f16x2_to_f32(f16x2_of_e4m3(static_cast<uint16_t>(w[k])), f0, f1);
+    f16x2_to_f32(f16x2_of_e4m3(static_cast<uint16_t>(w[k] >> 16)), f2, f3);
+    w[k] = pack_b16x2(e4m3x2_of_f32(f0 * f, f1 * f), e4m3x2_of_f32(f2 * f, f3 * f));
+  }
+  *at = b;
+}
+
 // One CTA looks after `group` new rows of one head of k (blockIdx.z 0) or v (1).
 // A page's first new row leads: whoever has it quantises all new rows of that
 // page, so that the page's scale is one CTA's business.  The rows stay in
 // registers between the maximum and the codes: one read, one write.
 //   PASSES rows of 16 bytes a thread: page_rows * D * 2 / (16 * 128).
-// Bound by HBM for prompts, by latency for single tokens.
+// Bound by HBM; what a row's place hangs on is three accesses in a row, so that
+// many CTAs an SM count (16384 rows, 8 heads of 128, pages of 64: with five 22.0
+// us, with seven 20.6, 4900 GB/s).
 template <int D, int PASSES>
-__global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(128, PASSES <= 4 ? 12 : PASSES == 8 ? 7 : 4)
+    append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;             // threads a row
   constexpr int kRows = 128 / kLanes;       // rows a pass
   const CacheParams& c = p.c;
@@ -69,35 +128,16 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
   __shared__ float top[4];
   if (tid == 0) n_task = 0;
   __syncthreads();
-  const int64_t row64 = static_cast<int64_t>(blockIdx.x) * p.group + tid;
-  if (tid < p.group && row64 < c.n_rows) {
-    const int row = static_cast<int>(row64);
-    int lo = 0, hi = c.n_seqs;  // the first sequence that ends behind the row
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (c.starts[mid + 1] > row)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    if (lo < c.n_seqs) {
-      int a, b;
-      seq_rows(c, lo, a, b);
-      const int64_t pos = static_cast<int64_t>(c.lens[lo]) - (b - a) + (row - a);
-      const int slot = static_cast<int>(pos & (c.page_rows - 1));
-      if (row >= a && pos >= 0 && (pos >> c.page_shift) < c.table_width && (row == a || slot == 0)) {
-        const int page = c.table[static_cast<int64_t>(lo) * c.table_width + (pos >> c.page_shift)];
-        if (page >= 0 && page < c.n_pages)
-          task[atomicAdd(&n_task, 1)] = make_int4(page, slot, min(b - row, c.page_rows - slot), row);
-      }
-    }
-  }
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * p.group + tid;
+  int page, slot, rows;
+  if (tid < p.group && row < c.n_rows && leads(c, static_cast<int>(row), page, slot, rows))
+    task[atomicAdd(&n_task, 1)] = make_int4(page, slot, rows, static_cast<int>(row));
   __syncthreads();
   const int n = n_task;  // (the tasks do not depend on one another: any order)
   const int sub = tid / kLanes, piece = tid % kLanes;
   for (int i = 0; i < n; ++i) {
     const int page = task[i].x, slot0 = task[i].y, rows = task[i].z, row0 = task[i].w;
-    const uint8_t* x = p.x[t] + static_cast<int64_t>(h) * D * 2 + piece * 16;
+    const uint8_t* const x = p.x[t] + static_cast<int64_t>(h) * D * 2 + piece * 16;
     uint4 v[PASSES];
     float m = 0.f;
 #pragma unroll
@@ -106,57 +146,88 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
       v[q] = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows && in_bounds(&g_cache_violations, row0 + r, 1, c.n_rows))
         v[q] = *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row0 + r) * p.row_bytes[t]);
-      const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)  // (fmaxf leaves a NaN out)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
     }
+#pragma unroll
+    for (int q = 0; q < PASSES; ++q) m = fmaxf(m, largest(v[q]));
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if ((tid & 31) == 0) top[tid >> 5] = m;
-    float* const scale = (t ? c.v_scale : c.k_scale) + static_cast<int64_t>(page) * c.H + h;
+    const int64_t ph = static_cast<int64_t>(page) * c.H + h;
+    float* const scale = (t ? c.v_scale : c.k_scale) + ph;
     const float have = slot0 ? *scale : 0.f;
     __syncthreads();
-    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const float now = fmaxf(scale_of(m), have);
-    uint8_t* const codes = (t ? c.v_pages : c.k_pages) + (static_cast<int64_t>(page) * c.H + h) * c.page_rows * D;
-    if (slot0 && now != have) {
-      // the page's older codes to the larger scale
-      const float f = have / now;
-      for (int e = tid; e < slot0 * (D / 8); e += 128) {
-        uint2* const at = reinterpret_cast<uint2*>(codes) + e;
-        uint2 b = *at;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&b);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float f0, f1, f2, f3;
-          f16x2_to_f32(f16x2_of_e4m3(static_cast<uint16_t>(w[k])), f0, f1);
-          f16x2_to_f32(f16x2_of_e4m3(static_cast<uint16_t>(w[k] >> 16)), f2, f3);
-          w[k] = pack_b16x2(e4m3x2_of_f32(f0 * f, f1 * f), e4m3x2_of_f32(f2 * f, f3 * f));
-        }
-        *at = b;
-      }
-    }
+    const float now = fmaxf(scale_of(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))), have);
+    uint8_t* const codes = (t ? c.v_pages : c.k_pages) + ph * c.page_rows * D;
+    if (slot0 && now != have)  // the page's older codes to the larger scale
+      for (int e = tid; e < slot0 * (D / 8); e += 128) bring(reinterpret_cast<uint2*>(codes) + e, have / now);
     const float inv = 1.f / now;  // (exact: a power of two, unless the page came with another scale)
 #pragma unroll
     for (int q = 0; q < PASSES; ++q) {
       const int r = q * kRows + sub;
-      if (r >= rows || !in_bounds(&g_cache_violations, slot0 + r, 1, c.page_rows)) continue;
-      const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-      uint16_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = e4m3x2_of_f32(__uint_as_float(w[k] << 16) * inv, __uint_as_float(w[k] & 0xFFFF0000u) * inv);
-      *reinterpret_cast<uint2*>(codes + (slot0 + r) * D + piece * 8) =
-          make_uint2(pack_b16x2(o[0], o[1]), pack_b16x2(o[2], o[3]));
+      if (r < rows && in_bounds(&g_cache_violations, slot0 + r, 1, c.page_rows))
+        *reinterpret_cast<uint2*>(codes + (slot0 + r) * D + piece * 8) = codes_of(v[q], inv);
     }
     if (tid == 0) *scale = now;
     __syncthreads();  // `top` is free again
   }
 }
 
+// The same for a few tokens a sequence: a warp for each row and head, half of it
+// for k and half for v, where the row leads.  Up to kHeld rows a lane stay in
+// registers; of more, all are read again for their codes.
+template <int D>
+__global__ void __launch_bounds__(128) append_few_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 8;        // lanes a row
+  constexpr int kRows = 16 / kLanes;   // rows that half a warp takes at once
+  constexpr int kHeld = 4;
+  const CacheParams& c = p.c;
+  const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), t = lane >> 4;
+  const int sub = (lane & 15) / kLanes, piece = lane % kLanes;
+  int page, slot0, rows;
+  if (h >= c.H || !leads(c, blockIdx.x, page, slot0, rows)) return;
+  const int row0 = blockIdx.x;
+  const uint8_t* const x = (t ? p.x[1] : p.x[0]) + static_cast<int64_t>(h) * D * 2 + piece * 16;
+  const int64_t row_bytes = t ? p.row_bytes[1] : p.row_bytes[0];
+  const int64_t ph = static_cast<int64_t>(page) * c.H + h;
+  float* const scale = (t ? c.v_scale : c.k_scale) + ph;
+  const float have = slot0 ? *scale : 0.f;
+  auto load = [&](int r) {
+    return r < rows && in_bounds(&g_cache_violations, row0 + r, 1, c.n_rows)
+               ? *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row0 + r) * row_bytes)
+               : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 v[kHeld];
+  float m = 0.f;
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) v[q] = load(q * kRows + sub);
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) m = fmaxf(m, largest(v[q]));
+#pragma unroll 4
+  for (int r = kHeld * kRows; r < rows; r += kRows) m = fmaxf(m, largest(load(r + sub)));
+#pragma unroll
+  for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float now = fmaxf(scale_of(m), have);
+  uint8_t* const codes = (t ? c.v_pages : c.k_pages) + ph * c.page_rows * D;
+  if (slot0 && now != have)
+    for (int e = lane & 15; e < slot0 * (D / 8); e += 16) bring(reinterpret_cast<uint2*>(codes) + e, have / now);
+  const float inv = 1.f / now;
+  auto store = [&](int r, const uint4& y) {
+    if (r < rows && in_bounds(&g_cache_violations, slot0 + r, 1, c.page_rows))
+      *reinterpret_cast<uint2*>(codes + (slot0 + r) * D + piece * 8) = codes_of(y, inv);
+  };
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) store(q * kRows + sub, v[q]);
+#pragma unroll 4
+  for (int r = kHeld * kRows; r < rows; r += kRows) store(r + sub, load(r + sub));
+  if ((lane & 15) == 0) *scale = now;
+}
+
 template <int D>
 static cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+  if (!p.group) {
+    append_few_kernel<D><<<dim3(p.c.n_rows, (p.c.H + 3) / 4), 128, 0, s>>>(p);
+    return cudaGetLastError();
+  }
   const dim3 grid((p.c.n_rows + p.group - 1) / p.group, p.c.H, 2);
   switch (p.c.page_rows * D / 1024) {
     case 1: append_kernel<D, 1><<<grid, 128, 0, s>>>(p); break;

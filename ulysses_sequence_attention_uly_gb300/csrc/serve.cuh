@@ -85,7 +85,7 @@ struct AppendParams {
   CacheParams c;
   const uint8_t* x[2];       // k, v rows
   int64_t row_bytes[2];
-  int32_t group;             // rows that a CTA looks after
+  int32_t group;             // rows that a CTA looks after; 0: a warp a row (append_few_kernel)
 };
 
 // What a CTA of the attention over a cache worked on: part idx of n of a unit (n

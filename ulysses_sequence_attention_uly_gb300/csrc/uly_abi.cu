@@ -1961,9 +1961,10 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
   }
   if (spans.clash()) return ULY_ERR_INVALID;
   if (!n_rows || !n_seqs) return ULY_OK;
-  // a CTA for every row where that is few CTAs or where most rows lead a page
-  // (a few tokens a sequence); else one for every page_rows rows
-  p.group = n_rows * cache->H * 2 <= 4096 || n_rows < 8LL * n_seqs ? 1 : cache->page_rows;
+  // a warp for every row and head where most rows lead a page (a few tokens a
+  // sequence; 512 single tokens, 8 heads: 28.4 -> 4.1 us); a CTA for every row where that is few CTAs; else one for
+  // every page_rows rows
+  p.group = n_rows < 8LL * n_seqs ? 0 : n_rows * cache->H * 2 <= 4096 ? 1 : cache->page_rows;
   return launch_cache_append(p, cache->D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ULY_OK : ULY_ERR_CUDA;
 }
 
