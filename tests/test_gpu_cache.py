@@ -140,6 +140,10 @@ ATTENTION = [
     R.Cached("long", (20000,), (1,), 2, 128, 64, G=4, std=0.7),
     R.Cached("long and short", (9000, 3, 70, 2500), (1, 2, 1, 1), 2, 64, 128, G=2),
     R.Cached("many", tuple((i * 37) % 150 for i in range(300)), tuple(i % 3 for i in range(300)), 1, 64, 16, G=2),
+    R.Cached("many, some long", tuple(2500 if i % 70 == 3 else (i * 37) % 150 for i in range(200)),
+             tuple(i % 3 for i in range(200)), 2, 64, 32, G=2),
+    R.Cached("one long among many", (12, 9, 130) * 16 + (20000, 3), (1,) * 50, 2, 64, 64, G=2),
+    R.Cached("two long among many, wide", (12, 9, 130) * 16 + (5000, 7000), (1,) * 48 + (3, 5), 2, 128, 128, G=4),
     R.Cached("peaked", (700,), (2,), 2, 128, 64, G=4, std=6.0),
 ]
 

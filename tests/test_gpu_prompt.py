@@ -223,3 +223,23 @@ def test_refusals():
     plan.prompt_attention(**{**ok, "seq_starts": d["starts"][:1]})  # no sequence: nothing happens
     torch.cuda.synchronize()
     assert all((x == 7.0).all() for x in d["o"])
+
+
+def test_the_wait_limit_is_a_waits_and_not_the_calls():
+    """A call that takes longer than the limit in all (about 1.3 ms), no wait of it
+    does (a CTA's item: at most 128 steps of 2 us)."""
+    from ulysses_sequence_attention_uly_gb300 import Plan
+    plan = Plan(1, 1, 16384, 0, "none", 32, 8, 128)
+    q, k, v = (torch.randn((1, 16384, h, 128), device="cuda").to(torch.bfloat16) for h in (32, 8, 8))
+    o, again = torch.empty_like(q), torch.empty_like(q)
+    starts = torch.tensor([0, 16384], dtype=torch.int32, device="cuda")
+    plan.prompt_attention([q], [k], [v], [o], starts)
+    torch.cuda.synchronize()
+    plan.set_wait_limit(700_000)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    plan.prompt_attention([q], [k], [v], [again], starts)
+    b.record()
+    assert plan.sync_status() == 0
+    assert a.elapsed_time(b) > 0.7
+    assert torch.equal(o.view(torch.int16), again.view(torch.int16))

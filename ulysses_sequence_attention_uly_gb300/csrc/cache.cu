@@ -1,7 +1,5 @@
 // cache.cu -- the 8-bit paged cache: k and v rows of new tokens into its pages,
 // and the attention of the newest tokens over it.
-#include <atomic>
-
 #include "serve.cuh"
 #include "tc.cuh"
 
@@ -372,6 +370,7 @@ struct CachedCfg {
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kPart = 8 * NT * (D + 4);        // floats: a warp's sums, which take the ring's place
   static constexpr int kSmem = 4 * (kWarpBytes > 4 * kPart ? kWarpBytes : 4 * kPart);
+  static_assert(kSmem <= 48 * 1024, "no attribute is set for more");
   __device__ static __forceinline__ uint32_t piece(int row, int i) {
     return D == 128 ? row * 128 + ((i ^ (row & 7)) << 4) : row * 64 + ((i ^ ((row >> 1) & 3)) << 4);
   }
@@ -388,10 +387,10 @@ __device__ __forceinline__ int unit_parts(const CachedParams& p, const SeqWork& 
   int64_t n;
   if (p.whole) return 1;
   if (p.few) {
-    n = static_cast<int64_t>(w.blocks) * p.slots / total;
+    n = static_cast<int64_t>(w.blocks) * p.slots / max(total, int64_t{1});
   } else {
     const int64_t slots = total > p.slots * (kLongPart / (kBlockKeys * 2 * D)) ? 2 * p.slots : p.slots;
-    const int64_t blocks = (total + slots - 1) / slots;
+    const int64_t blocks = max((total + slots - 1) / slots, int64_t{1});
     n = (w.blocks + blocks / 2) / blocks;
   }
   return static_cast<int>(min(max(n, int64_t{1}), static_cast<int64_t>(min(w.blocks, max_unit_parts(p.few)))));
@@ -879,16 +878,7 @@ __global__ void __launch_bounds__(32 * W) combine_kernel(const __grid_constant__
 template <int D, int NT>
 cudaError_t launch_cached(const CachedParams& p, cudaStream_t s) {
   using C = CachedCfg<D, NT>;
-  static std::atomic<uint64_t> configured{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(cached_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_relaxed);
-  }
+  cudaError_t e = cudaSuccess;
   // (each launch may come up while the one before it ends)
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(128);

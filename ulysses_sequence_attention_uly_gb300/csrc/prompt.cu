@@ -31,7 +31,9 @@
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D).
 //
 // The arithmetic of an item does not depend on which CTA takes it: the same
-// bits on every call.  Every wait is bounded, as in attn.cu.
+// bits on every call.  Every wait is bounded, as in attn.cu, by a deadline that a
+// role puts off with every item (a CTA may be at work for seconds; a reading of
+// the clock before every wait cost up to a tenth).
 #include <atomic>
 
 #include "serve.cuh"
@@ -466,7 +468,8 @@ __device__ __forceinline__ void find_items(const PromptCut& p, int n_hp, PBars& 
 
 template <int D>
 __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV,
-                                         int n_items, const PromptRun* runs, uint64_t deadline) {
+                                         int n_items, const PromptRun* runs, uint64_t wait_ns) {
+  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   bool ok = true;
@@ -526,6 +529,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
         it.n[1] = two ? u.z : 0;
       }
     }
+    deadline = globaltimer_ns() + wait_ns;
     bars.item[slot] = it;
     mbar_arrive(smem_u32(&bars.item_full[slot]));
     if (it.run < 0) break;
@@ -573,7 +577,8 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
 
 template <int D>
 __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV, uint32_t tmem,
-                                       uint64_t deadline) {
+                                       uint64_t wait_ns) {
+  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   // descriptors as in attn.cu: a fixed high part and the start address / 16
@@ -616,6 +621,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     n1 = end ? 0 : bars.item[slot].n[1];
     mbar_arrive(smem_u32(&bars.item_empty[slot]));
     ++n_item;
+    deadline = globaltimer_ns() + wait_ns;
     return true;
   };
   // Any step: a tile may end, or begin the next item.  All of it in loops that are
@@ -741,7 +747,8 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
 
 template <int D>
 __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint32_t sKV, uint32_t sStage,
-                                        uint32_t tmem, const PromptRun* runs, int warp, int lane, uint64_t deadline) {
+                                        uint32_t tmem, const PromptRun* runs, int warp, int lane, uint64_t wait_ns) {
+  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   const int wg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
@@ -760,6 +767,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
     }
     const Item& it = bars.item[slot];
     if (it.run < 0) break;
+    deadline = globaltimer_ns() + wait_ns;
     const int n = wg ? it.n[1] : it.n[0];
     if (n > 0) {
       float m_ref = -INFINITY, l_run = 0.f;
@@ -922,14 +930,13 @@ __global__ void __launch_bounds__(320, 1) prompt_kernel(const __grid_constant__ 
   const int n_items = p.direct ? (bars.unit[0].run >= 0) + (bars.unit[1].run >= 0) : p.cut.t.head[0] * p.n_hp;
   static_assert(kDirectItems == 2, "items are counted above");
   const PromptRun* const runs = p.direct ? bars.run : p.cut.t.runs;
-  const uint64_t deadline = globaltimer_ns() + p.wait_ns;
   if ((p.direct ? 0 : static_cast<int>(blockIdx.x)) < n_items) {
     if (warp == 8) {
-      if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, runs, deadline);
+      if (lane == 0) producer<D>(p, bars, sQ, sKV, n_items, runs, p.wait_ns);
     } else if (warp == 9) {
-      if (lane == 0) issuer<D>(p, bars, sQ, sKV, tmem, deadline);
+      if (lane == 0) issuer<D>(p, bars, sQ, sKV, tmem, p.wait_ns);
     } else {
-      softmax<D>(p, bars, sKV, sStage, tmem, runs, warp, lane, deadline);
+      softmax<D>(p, bars, sKV, sStage, tmem, runs, warp, lane, p.wait_ns);
     }
   }
   tc_fence_before();
