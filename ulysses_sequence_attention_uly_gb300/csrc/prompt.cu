@@ -105,19 +105,6 @@ __device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// Has the phase completed?  (Does not wait.)
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // wait for the launch before this one in the stream (a programmatic dependency)
 __device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -586,7 +573,6 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
   const uint64_t hi_v = sdesc_sw128(0, C::kPanelBytes, 1024);  // V: MN-major
   const uint32_t q_lo = (sQ & 0x3FFFFu) >> 4, kv_lo = (sKV & 0x3FFFFu) >> 4;
   constexpr uint32_t kTileLo = C::kTileBytes >> 4;
-  constexpr int kUnroll = 4;  // steps a turn of the loop: the jump back costs the issuer
   uint64_t dq[2][C::kQkSteps], dk[C::kHalf][C::kQkSteps], dv[C::kHalf][C::kPvSteps];
 #pragma unroll
   for (int k = 0; k < C::kQkSteps; ++k) {
@@ -605,8 +591,10 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
   int left0 = 0, left1 = 0;      // steps of this item that a tile still has, this one included
   uint32_t par_p = 0, par_q = 0;  // parities of the two tiles' barriers, a bit each
   uint32_t acc = 0;              // the item has had a step
-  uint32_t turn = 0;             // turns of the ring: step s = turn * kHalf + u
-  int u = 0;
+  uint32_t turn = 0;             // turns of the ring
+  constexpr int kUnroll = 4;     // steps a turn of the plain loop: the jump back costs the issuer
+  constexpr int kPlain = 8;
+  static_assert(kUnroll % C::kHalf == 0, "whole turns of the ring");
   bool ok = true, more = false;
   auto wait = [&](uint64_t& bar, uint32_t parity) {
     ok = mbar_wait(smem_u32(&bar), parity & 1, deadline, abort_flag);
@@ -624,120 +612,101 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     deadline = globaltimer_ns() + wait_ns;
     return true;
   };
-  // Any step: a tile may end, or begin the next item.  All of it in loops that are
-  // not unrolled: short items come here with every step, and what a CTA's roles
-  // go through once an item does not stay in the instruction cache when it is
-  // long (1024-row prompts 77.0 -> 75.4 us, 128-row ones of 64-wide heads 21.1 -> 20.1).
-  // K of the step after one in turn u is in slot 2u + 2, V of that one in 2u + 1.
-  auto scores = [&](int i, int ku, int steps, bool fresh) {
-    if (fresh) {
-      if (!wait(bars.q_full[i], par_q >> i)) return;
-      par_q ^= 1u << i;
-    }
-    const uint32_t a_lo = q_lo + i * kTileLo, b_lo = kv_lo + (2 * ku + 2) % C::kSlots * kTileLo, d = tmem + 128 * i;
-#pragma unroll 1
-    for (int k = 0; k < C::kQkSteps; ++k) {
-      const uint32_t off = ((k >> 2) * C::kPanelBytes + (k & 3) * 32) >> 4;
-      mma_bf16_ss(d, hi_s | (a_lo + off), hi_s | (b_lo + off), C::kIdescS, k > 0);
-    }
-    mma_commit(smem_u32(&bars.s_full[i]));
-    if (steps == 1) mma_commit(smem_u32(&bars.q_empty[i]));  // the item's last scores of this tile
-  };
-  auto values = [&](int i, int steps) {
-    if (!wait(bars.p_full[i], par_p >> i)) return;
-    par_p ^= 1u << i;
-    const uint32_t v_lo = kv_lo + (2 * u + 1) * kTileLo, d = tmem + 256 + D * i, pa = tmem + 128 * i;
-#pragma unroll 1
-    for (int k = 0; k < C::kPvSteps; ++k)
-      mma_bf16_ts(d, pa + 8 * k, hi_v | (v_lo + ((k * 16 * 128) >> 4)), C::kIdescO, acc | (k > 0));
-    if (steps == 1) mma_commit(smem_u32(&bars.o_done[i]));
-  };
-  auto any_step = [&]() {
-    int next0, next1;
-    const bool last = max(left0, left1) == 1;
-    if (last) {
-      if (!read_item(next0, next1)) return;
-      more = next0 || next1;
-    } else {
-      next0 = max(left0 - 1, 0);
-      next1 = max(left1 - 1, 0);
-    }
-    const int bi = (u + 1) % C::kHalf;
-    if (!wait(bars.full[bi], turn + (u == C::kHalf - 1 ? 1 : 0))) return;
-    bool late = false;  // the next item's queries are not here yet: this one's second product does not wait for them
-#pragma unroll 1
-    for (int a = 0; ok && a < 4; ++a) {
-      const int i = late ? a & 1 : a >> 1;
-      const bool pv = late ? a < 2 : (a & 1) == 0;
-      const int steps = pv ? (i ? left1 : left0) : (i ? next1 : next0);
-      if (!steps) continue;
-      if (pv) {
-        values(i, steps);
-        if (a == 0) late = ok && last && next0 && left1 && !mbar_test(smem_u32(&bars.q_full[0]), par_q & 1);
-      } else {
-        scores(i, u, steps, last);
-      }
-    }
-    if (!ok) return;
-    if (more) mma_commit(smem_u32(&bars.empty[bi]));
-    left0 = next0;
-    left1 = next1;
-    acc = last ? 0 : 1;
-    u = bi;
-    if (!bi) ++turn;
-  };
+  // Scores of a tile (constants: every descriptor is ready, since what the issuer
+  // spends between two instructions the tensor core waits for), and its product
+  // with V.  `steps`: that the tile has from these scores (this product) on, 0: more
+  // than one.
+#define ULY_SCORES(i, kd, steps, fresh)                                                                       \
+  do {                                                                                                       \
+    if (fresh) {                                                                                             \
+      if (!wait(bars.q_full[i], par_q >> i)) break;                                                          \
+      par_q ^= 1u << i;                                                                                      \
+    }                                                                                                        \
+    _Pragma("unroll") for (int k = 0; k < C::kQkSteps; ++k)                                                  \
+        mma_bf16_ss(tmem + 128 * i, dq[i][k], kd[k], C::kIdescS, k > 0);                                     \
+    mma_commit(smem_u32(&bars.s_full[i]));                                                                   \
+    if ((steps) == 1) mma_commit(smem_u32(&bars.q_empty[i]));                                                \
+  } while (0)
+#define ULY_VALUES(i, vd, steps)                                                                              \
+  do {                                                                                                       \
+    if (!wait(bars.p_full[i], par_p >> i)) break;                                                            \
+    par_p ^= 1u << i;                                                                                        \
+    _Pragma("unroll") for (int k = 0; k < C::kPvSteps; ++k)                                                  \
+        mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, vd[k], C::kIdescO, acc | (k > 0));           \
+    if ((steps) == 1) mma_commit(smem_u32(&bars.o_done[i]));                                                 \
+  } while (0)
   if (read_item(left0, left1) && (left0 || left1)) {
     more = true;
     if (wait(bars.full[0], 0)) {
-      // (K of step 0 is in slot 0)
-#pragma unroll 1
-      for (int i = 0; ok && i < 2; ++i)
-        if (i ? left1 : left0) scores(i, C::kHalf - 1, i ? left1 : left0, true);
+      // (K of step 0 is in slot 0, which is dk[kHalf - 1])
+      if (left0) ULY_SCORES(0, dk[C::kHalf - 1], left0, true);
+      if (ok && left1) ULY_SCORES(1, dk[C::kHalf - 1], left1, true);
       if (ok) mma_commit(smem_u32(&bars.empty[0]));
     }
   }
   while (ok && more) {
-    // Steps in the middle of an item, both tiles going on: with nothing to
-    // decide and every descriptor ready, since what the issuer spends between
-    // two instructions the tensor core waits for.
-    int plain = u ? 0 : min(left0, left1) - 1;
-    if (plain <= 0) {
-      any_step();
-      continue;
-    }
+    // Steps in the middle of an item, both tiles going on: nothing to decide (a
+    // 16384-row sequence: 1.49 ms without this loop, 1.29 with it).  Whole turns of
+    // the ring, and kPlain steps at least: items of few stay in one piece of code,
+    // since what a CTA's roles go through does not stay in the instruction cache
+    // when it is long (512-row prompts 59.0 -> 54.5 us; from four steps on, 1024-row
+    // ones take 83 us, from eight 76).
+    int plain = min(left0, left1) - 2;  // (the last scores of a tile free its queries' slot)
+    plain = plain < kPlain ? 0 : plain - plain % C::kHalf;
     left0 -= plain;
     left1 -= plain;
     while (ok && plain > 0) {
 #pragma unroll
       for (int w = 0; w < kUnroll; ++w) {
-        constexpr int kLastU = C::kHalf - 1;
-        const int uu = w % C::kHalf, bi = (uu + 1) % C::kHalf;
+        const int u = w % C::kHalf, bi = (u + 1) % C::kHalf;
         if (plain == 0) break;
-        if (!wait(bars.full[bi], uu == kLastU ? turn + 1 : turn)) break;
-        if (!wait(bars.p_full[0], par_p)) break;
-#pragma unroll
-        for (int k = 0; k < C::kPvSteps; ++k) mma_bf16_ts(tmem + 256, tmem + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
-#pragma unroll
-        for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem, dq[0][k], dk[uu][k], C::kIdescS, k > 0);
-        mma_commit(smem_u32(&bars.s_full[0]));
-        if (plain == 1 && left0 == 1) mma_commit(smem_u32(&bars.q_empty[0]));
-        if (!wait(bars.p_full[1], par_p >> 1)) break;
-#pragma unroll
-        for (int k = 0; k < C::kPvSteps; ++k)
-          mma_bf16_ts(tmem + 256 + D, tmem + 128 + 8 * k, dv[uu][k], C::kIdescO, acc | (k > 0));
-#pragma unroll
-        for (int k = 0; k < C::kQkSteps; ++k) mma_bf16_ss(tmem + 128, dq[1][k], dk[uu][k], C::kIdescS, k > 0);
-        mma_commit(smem_u32(&bars.s_full[1]));
-        if (plain == 1 && left1 == 1) mma_commit(smem_u32(&bars.q_empty[1]));
+        if (!wait(bars.full[bi], u == C::kHalf - 1 ? turn + 1 : turn)) break;
+        ULY_VALUES(0, dv[u], 0);
+        ULY_SCORES(0, dk[u], 0, false);
+        if (!ok) break;
+        ULY_VALUES(1, dv[u], 0);
+        ULY_SCORES(1, dk[u], 0, false);
+        if (!ok) break;
         mma_commit(smem_u32(&bars.empty[bi]));
-        par_p ^= 3;
         acc = 1;
-        u = bi;
-        if (uu == kLastU) ++turn;
+        if (u == C::kHalf - 1) ++turn;
         --plain;
       }
     }
+    // Any step s = turn * kHalf + u: a tile may end, or begin the next item.
+#pragma unroll
+    for (int u = 0; u < C::kHalf; ++u) {
+      if (!ok || !more) break;
+      const int bi = (u + 1) % C::kHalf;
+      int next0 = left0 - 1, next1 = left1 - 1;
+      bool last = false;
+      if (min(next0, next1) <= 0) {  // a tile ends
+        last = max(next0, next1) <= 0;
+        if (last) {
+          if (!read_item(next0, next1)) break;
+          more = next0 || next1;
+        } else {
+          next0 = max(next0, 0);
+          next1 = max(next1, 0);
+        }
+      }
+      if (!wait(bars.full[bi], u == C::kHalf - 1 ? turn + 1 : turn)) break;
+      if (left0) ULY_VALUES(0, dv[u], left0);
+      // (an item's last product does not wait for the next one's queries)
+      if (last && ok && left1) ULY_VALUES(1, dv[u], left1);
+      if (ok && next0) ULY_SCORES(0, dk[u], next0, last);
+      if (!last && ok && left1) ULY_VALUES(1, dv[u], left1);
+      if (ok && next1) ULY_SCORES(1, dk[u], next1, last);
+      if (!ok) break;
+      if (more) mma_commit(smem_u32(&bars.empty[bi]));
+      left0 = next0;
+      left1 = next1;
+      acc = last ? 0 : 1;
+    }
+    ++turn;
   }
+#undef ULY_SCORES
+#undef ULY_VALUES
   if (!ok) record_timeout(p, abort_flag);
   // every MMA has completed before TMEM is released
   mma_commit(smem_u32(&bars.drain));
