@@ -584,8 +584,9 @@ typedef struct uly_cache {
  *     rows of no sequence are not read.  lens: device int32 [n_seqs].
  *     A row whose position is negative or past the table's width, or whose page
  *     is outside [0, n_pages), is dropped.
- *   A page may take new rows of one sequence only.  Values have to be finite (a
- *   NaN stays a NaN; an infinity takes the precision of its page and head).
+ *   A page may take new rows at one place of the table only: not of two
+ *     sequences, and not twice of one.  Values have to be finite (a NaN stays a
+ *   NaN; an infinity takes the precision of its page and head).
  * Works on the current device; no workspace; may be captured into a CUDA graph.
  * ULY_ERR_INVALID for NULL, misaligned or overlapping pointers, bad strides or
  * sizes; ULY_ERR_UNSUPPORTED for other page sizes or D, more than 65535 heads,
