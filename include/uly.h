@@ -580,7 +580,7 @@ typedef struct uly_cache {
  *     8 and at least H * D (k and v parts of a packed projection are read in
  *     place); 0 = dense.
  *   starts: device int32 [n_seqs + 1], non-decreasing, within [0, n_rows]
- *     (clamped; what becomes of rows that two sequences claim is not defined);
+ *     (clamped; where they fall, what becomes of the call's rows is not defined);
  *     rows of no sequence are not read.  lens: device int32 [n_seqs].
  *     A row whose position is negative or past the table's width, or whose page
  *     is outside [0, n_pages), is dropped.

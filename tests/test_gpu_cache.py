@@ -243,6 +243,26 @@ def test_rows_of_no_sequence_stay_and_starts_are_clamped():
         R.check_cached(c, d, o, lse)
 
 
+@pytest.mark.parametrize("seqs", [100, 150])
+def test_starts_that_fall(seqs):
+    """Rows that two sequences claim may get anything, but the call ends, writes to
+    no other row and leaves the next one right."""
+    c = R.Cached("falling", (3000,) * seqs, (1,) * seqs, 2, 64, 64, G=4)
+    d = R.cache_inputs(c, 18)
+    cache = R.cache_of(d)
+    cache.append(d["k"], d["v"], d["starts"], d["lens"], d["table"])
+    right = d["starts"]
+    d["starts"] = R.ints([2, c.rows - 2] * (seqs // 2) + [2])
+    o, lse = R.attend(cache, c, d)
+    torch.cuda.synchronize()
+    for got in (o, lse):
+        assert (got[:2] == 7.0).all() and (got[-2:] == 7.0).all()
+    d["starts"] = right
+    o, lse = R.attend(cache, c, d)
+    torch.cuda.synchronize()
+    R.check_cached(c, d, o, lse)
+
+
 def test_strided_queries_and_no_lse():
     c = R.Cached("strided", (60, 300), (3, 2), 2, 128, 32, G=3)
     d = R.cache_inputs(c, 17)

@@ -92,7 +92,8 @@ def test_null_arguments_and_workspaces():
     assert L.uly_cache_attention(None, A, 0, 4, 1, A, A, A, 1, 1, 0.1, A, A, A, 1, None) == uly.ULY_ERR_INVALID
     assert L.uly_cache_attention_workspace(cache(), 4, 3, 2, 64) == 0 < L.uly_cache_attention_workspace(cache(), 4, 3, 2, 65)
     for a in ((None, 4, 3, 2, 1), (cache(H=0), 4, 3, 2, 1), (cache(), 3, 3, 2, 1), (cache(), 0, 3, 2, 1),
-              (cache(), 4, -1, 2, 1), (cache(), 4, 3, -1, 1), (cache(), 4, 3, 2, 0), (cache(page_rows=0), 4, 3, 2, 1)):
+              (cache(), 4, -1, 2, 1), (cache(), 4, 3, -1, 1), (cache(), 4, 3, 2, 0), (cache(page_rows=0), 4, 3, 2, 1),
+              (cache(), 4, 1 << 62, 2, 100)):
         assert L.uly_cache_attention_workspace(*a) == -1
 
 

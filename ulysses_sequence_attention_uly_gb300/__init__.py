@@ -907,7 +907,7 @@ class Cache:
         if scale is None:
             scale = 1.0 / math.sqrt(D)
         ws, nbytes = None, self.attention_workspace(Hq, rows, n, width)
-        if nbytes or workspace is not None:
+        if nbytes > 0 or workspace is not None:  # (-1: the call refuses)
             workspace = _workspace(workspace, nbytes, dev, stream)
             ws, nbytes = workspace.data_ptr(), workspace.numel()
         self._call(lib().uly_cache_attention, "uly_cache_attention", pq, sq, Hq, rows, starts.data_ptr(),

@@ -248,11 +248,11 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 // below what even mma.sync does in the time that HBM takes for it (tensor pipe 16%
 // of cycles).  32 heads on 8 of 128: two sequences of 120 and 131 thousand tokens
 // 84 us, 6.1 TB/s (the loads alone, without arithmetic: 82); 64 sequences of 200 to
-// 8000 tokens 66 us, 5.1 TB/s; one of 499 tokens 7 us.
+// 8000 tokens 66 us, 5.1 TB/s; one of 499 tokens 8 us.
 //
 // A unit is (sequence, 8 NT rows of its queries, cache head); a row is (token, q
 // head of the group).  A unit's keys, in blocks of 64, are cut into equal parts of
-// about the same length for all units, several times as many as CTAs run at once:
+// about the same length for all units, up to twice as many as CTAs run at once:
 // SMs differ by a third in how fast they get data, so the GPU gives the next part
 // to whoever is done.  A part that is a whole unit stores its rows; the sums of the
 // others go through the workspace, and combine_kernel adds them up, in order.
@@ -513,6 +513,13 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
   // (the heads of a page are next to each other in memory: neighbouring CTAs take
   // them, at the same time)
   const int64_t off = blockIdx.x - my_before, units = static_cast<int64_t>(w.tiles) * c.H, unit = off % units;
+  // starts that fall give rows to several sequences, and more parts than the grid
+  // has been made for: units that are not all there are left out, so that
+  // combine_kernel finds every part it looks for
+  if (my_before + units * parts > gridDim.x) {
+    if (tid == 0 && !p.whole) note->n = 0;
+    return;
+  }
   const int idx = static_cast<int>(off / units);
   const int tile = static_cast<int>(unit / c.H), h = static_cast<int>(unit - static_cast<int64_t>(tile) * c.H);
   const int b0 = static_cast<int>(static_cast<int64_t>(w.blocks) * idx / parts);
@@ -838,6 +845,8 @@ __global__ void __launch_bounds__(32 * W) combine_kernel(const __grid_constant__
   wait_for_previous_launch();
   const CachedPart note = p.parts[blockIdx.x];
   if (note.n <= 1 || note.idx >= note.live) return;
+  const int64_t left = static_cast<int64_t>(note.n - 1 - note.idx) * note.stride;  // parts behind this one's
+  if (!in_bounds(&g_cache_violations, blockIdx.x, left + 1, gridDim.x)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(note.stride) * kStep;  // from a part to the next
   const float* const first = p.sums + blockIdx.x * static_cast<int64_t>(kStep) - note.idx * step;

@@ -1971,7 +1971,7 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
 int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs,
                                       int32_t table_width) {
   if (!cache || Hq < 1 || cache->H < 1 || cache->D < 1 || cache->page_rows < 1 || Hq % cache->H || n_rows < 0 ||
-      n_seqs < 0 || table_width < 1)
+      n_rows > kMaxRows || n_seqs < 0 || table_width < 1)
     return -1;
   return cached_work(cache, Hq, n_rows, n_seqs, table_width).total;
 }
