@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(32 * W) combine_kernel(const __grid_constant__
   constexpr int kStep = 8 * NT * (D + 4);
   __shared__ float4 sums[W][D / 4];
   __shared__ float4 ref[W];
-  static_assert(8 * NT <= 16 && max_unit_parts(W > 4) <= 32 * W, "rows of a CTA, parts of a warp");
+  static_assert(8 * NT <= 16 && max_unit_parts(W / 8) == 32 * W, "rows of a CTA, parts of a warp");
   wait_for_previous_launch();
   const CachedPart note = p.parts[blockIdx.x];
   if (note.n <= 1 || note.idx >= note.live) return;
@@ -910,9 +910,10 @@ cudaError_t launch_cached(const CachedParams& p, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, cached_kernel<D, NT>, p);
   if (e != cudaSuccess || p.whole) return e;
   cfg.dynamicSmemBytes = 0;
-  cfg.blockDim = dim3(p.few ? 256 : 128);
-  return p.few ? cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 8>, p)
-               : cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 4>, p);
+  cfg.blockDim = dim3(max_unit_parts(p.few));
+  return p.few == 2   ? cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 16>, p)
+         : p.few == 1 ? cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 8>, p)
+                      : cudaLaunchKernelEx(&cfg, combine_kernel<D, NT, 4>, p);
 }
 
 }  // namespace

@@ -97,9 +97,10 @@ struct alignas(16) CachedPart {
   int64_t place;   // of its first row among all rows and heads of q
   int64_t row0;    // and among the sequence's
 };
-// Most parts of a unit: a lane of combine_kernel for each, which has eight warps
-// where there are few units, and four where its CTAs are many.
-__host__ __device__ constexpr int max_unit_parts(bool few) { return few ? 256 : 128; }
+// Most parts of a unit: a lane of combine_kernel for each, which has sixteen warps
+// where a unit or two are all (200 thousand tokens of one cache head: 22.0 -> 20.8
+// us), eight where units are few, and four where its CTAs are many.
+__host__ __device__ constexpr int max_unit_parts(int few) { return 128 << few; }
 constexpr int kCachedPerSm[2] = {4, 3};    // CTAs an SM, with one and two 8-row tiles of queries
 
 struct CachedParams {
@@ -109,7 +110,7 @@ struct CachedParams {
   float* sums;         // [grid][8 * row_tiles][D + 4]: O, M, m, l of parts of units
   int32_t grid;
   int32_t slots;       // CTAs that run at once
-  int32_t few;         // units: at most one for eight of those
+  int32_t few;         // 1: one unit at most for eight of those, 2: one for 256, 0: more
   int32_t whole;       // units in one part each
   int32_t row_tiles;   // 8-row tiles of queries a unit: 1 or 2
   const uint8_t* q;

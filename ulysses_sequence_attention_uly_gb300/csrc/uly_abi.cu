@@ -2014,7 +2014,7 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ULY_ERR_CUDA;
   p.slots = (sms < kCachedSms ? sms : kCachedSms) * kCachedPerSm[p.row_tiles - 1];
-  p.few = units * 8 <= p.slots;
+  p.few = units * 256 <= p.slots ? 2 : units * 8 <= p.slots;
   p.whole = cached_whole(cache, table_width);
   // parts: the blocks make 2 slots of them (1 where there are few units), and each
   // unit's rounding adds at most one; a unit has at most max_unit_parts and at
