@@ -243,3 +243,24 @@ def test_the_wait_limit_is_a_waits_and_not_the_calls():
     assert plan.sync_status() == 0
     assert a.elapsed_time(b) > 0.7
     assert torch.equal(o.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("heads", [2, 400])  # items that CTAs find by themselves, and from the tables
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_withheld_v_of_a_short_tile(heads, D):
+    """V of a sequence's only tile, which is short, does not come: the warps that
+    would zero its rows behind the end give up with their P just stored.  The call
+    ends with a timeout, TMEM is free again, and the next calls are right."""
+    from ulysses_sequence_attention_uly_gb300 import ULY_ERR_TIMEOUT
+    c = R.Prompt("short v", (100,), (100,), heads, heads // 2, D)
+    d = R.prompt_inputs(c, 14)
+    plan = R.plan_of(c)
+    for _ in range(3):
+        plan.set_wait_limit(5_000_000)
+        plan.test_withhold_fill(1)  # K of step 0 is copy 0, its V copy 1
+        plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"])
+        assert plan.sync_status() == ULY_ERR_TIMEOUT
+        plan.test_withhold_fill(-1)
+        plan.set_wait_limit(4_000_000_000)
+        run(c, d, plan)
+        R.check_prompt(c, d, d["o"], d["lse"])

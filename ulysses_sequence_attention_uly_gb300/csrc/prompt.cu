@@ -790,6 +790,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
           const int st = step0 + s, gr = st + 1;
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[gr % C::kHalf]), (gr / C::kHalf) & 1, deadline,
                                                  abort_flag))) {
+            tmem_wait_st();  // (P is on its way: TMEM is not freed before it is there)
             ok = false;
             break;
           }
