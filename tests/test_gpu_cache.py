@@ -52,6 +52,26 @@ def test_append(c, big):
     check_append(c, d)
 
 
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 128), (128, 64)])
+def test_append_a_token_that_raises_every_scale(D, page):
+    """A token to every sequence, larger than all before it, again and again: the
+    page's scale is read by all lanes of a warp and written by one, and the older
+    codes are brought along each time."""
+    n, old = 60, page // 2
+    c = R.Cached("raised", (old,) * n, (1,) * n, 7, D, page)
+    d = R.cache_inputs(c, 9)
+    lens = list(c.lens)
+    for step in range(8):
+        before = {t: d[t + "_scale"].clone() for t in "kv"}
+        for t in "kv":
+            d[t] = (torch.randn((n, 7, D), device="cuda").clamp(-4, 4) + 20).to(torch.bfloat16) * 4.0 ** step
+        d["lens"] = R.ints([x + step for x in lens])
+        check_append(c, d)
+        pages = d["table"][:, 0].long()
+        for t in "kv":
+            assert (d[t + "_scale"][pages] > before[t][pages]).all() or step == 0
+
+
 def test_append_from_a_packed_projection():
     c = R.Cached("packed", (17, 0, 250, 16), (3, 40, 1, 16), 3, 64, 16)
     d = R.cache_inputs(c, 2)

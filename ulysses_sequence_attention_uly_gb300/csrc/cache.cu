@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(128) append_few_kernel(const __grid_constant__
 #pragma unroll
   for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float now = fmaxf(scale_of(m), have);
+  __syncwarp();  // every lane has read the scale before one writes it (shuffles order no memory)
   uint8_t* const codes = (t ? c.v_pages : c.k_pages) + ph * c.page_rows * D;
   if (slot0 && now != have)
     for (int e = lane & 15; e < slot0 * (D / 8); e += 16) bring(reinterpret_cast<uint2*>(codes) + e, have / now);
