@@ -63,6 +63,46 @@ def test_scale_and_no_lse(c):
     R.check_prompt(c, d, d["o"], None, scale=0.031)
 
 
+def _mixed(n, most, empty=()):
+    return tuple(0 if i in empty else 1 + (i * 29) % most for i in range(n))
+
+
+# more sequences than a warp has lanes, and yet so little work that the CTAs find their items by themselves
+FOUND = [
+    R.Prompt("33", (700,), _mixed(33, 40), 2, 1, 128),
+    R.Prompt("64, empty ones at a turn's end", (950,), _mixed(64, 30, (30, 31, 32, 33, 63)), 2, 1, 64, first=3),
+    R.Prompt("65, the last alone", (300,), (0,) * 64 + (300,), 2, 1, 128),
+    R.Prompt("33, the first 32 empty", (270, 20), (0,) * 32 + (290,), 4, 2, 64),
+    R.Prompt("a long one over a turn's end", (500, 600), _mixed(31, 9) + (700,) + _mixed(12, 9), 4, 2, 128, first=5),
+    R.Prompt("100 over shards", (400, 350), _mixed(100, 13, (31, 32)), 4, 2, 128, first=7),
+    R.Prompt("40 over shards, odd groups", (333, 400), _mixed(32, 9) + (300, 0, 5, 4, 3, 2, 1, 1), 6, 2, 64, first=2),
+    R.Prompt("90, odd group", (2000,), _mixed(90, 20, (32, 64)), 3, 1, 128, first=1),
+    R.Prompt("220, two items a CTA", (700,), _mixed(220, 4, (31, 95, 96)), 2, 1, 64),
+]
+
+
+@pytest.mark.parametrize("c", FOUND, ids=lambda c: c.name)
+def test_more_sequences_than_lanes(c):
+    d = R.prompt_inputs(c, 15)
+    plan = R.plan_of(c)
+    assert plan.prompt_attention_workspace(len(c.seqs)) == 0
+    run(c, d, plan)
+    R.check_prompt(c, d, d["o"], d["lse"])
+
+
+def test_starts_that_fall_at_a_turn_of_lanes():
+    c = R.Prompt("falling", (500, 300), (800,), 4, 2, 64)
+    starts = [8 * i for i in range(31)] + [400, 30, 20, 10] + [250 + 5 * i for i in range(29)] + [0, 0, 640, 90] + [700]
+    d = R.prompt_inputs(c, 16)
+    d["starts"] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    plan = R.plan_of(c)
+    assert plan.prompt_attention_workspace(len(starts) - 1) == 0
+    run(c, d, plan)
+    top = torch.tensor(starts).cummax(0).values.tolist()
+    as_is = R.Prompt("falling", c.shards, tuple(b - a for a, b in zip(top, top[1:])), 4, 2, 64, first=top[0])
+    R.check_prompt(as_is, d, d["o"], d["lse"])
+
+
 def test_more_sequences_than_threads():
     lens = tuple((i * 7) % 4 for i in range(2500))
     c = R.Prompt("many", (2200, 2000), lens, 2, 2, 64, first=11)

@@ -409,6 +409,7 @@ __device__ __forceinline__ void find_items(const PromptCut& p, int n_hp, PBars& 
   const int N = p.shard_begin[p.P];
   int total = 0;
   if (lane < kDirectItems) bars.unit[lane].run = -1;
+  __syncwarp();  // before another lane puts an item there (shuffles order no memory)
   // first how many units there are, then the items' own
   for (int k = -1; k < kDirectItems; ++k) {
     const int idx = k <= 0 ? static_cast<int>(blockIdx.x) : total * n_hp - 1 - static_cast<int>(blockIdx.x);
