@@ -150,7 +150,11 @@ void uly_plan_destroy(uly_plan* plan);
 /* Limit, in nanoseconds, of every device-side wait (default 4e9).  A wait
  * that expires makes the kernel record ULY_ERR_TIMEOUT and return.  (The
  * hardware waits a while by itself before the clock is read, so that limits of
- * microseconds do not expire in a call that makes progress.) */
+ * microseconds do not expire in a call that makes progress.)  The kernels of
+ * uly_sp_attention and its relatives, and the gradients', count it from the start
+ * of a CTA, whose work is one unit of query rows (or tile of keys);
+ * uly_sp_prompt_attention's, whose CTAs take one piece of work after another,
+ * from the start of each wait. */
 int uly_plan_set_wait_limit(uly_plan* plan, uint64_t ns);
 
 /* Failure-detection test hook: when fill >= 0, the attention kernels' TMA

@@ -304,3 +304,21 @@ def test_a_withheld_v_of_a_short_tile(heads, D):
         plan.set_wait_limit(4_000_000_000)
         run(c, d, plan)
         R.check_prompt(c, d, d["o"], d["lse"])
+
+
+def test_a_wait_for_a_tile_of_the_other_warps_is_no_timeout():
+    """One head of its own k and v and an odd number of tiles: a unit has a single
+    tile, through which (2049 steps, 1.4 ms and more) the other four warps have
+    nothing to do.  No wait of the roles at work comes near the limit."""
+    from ulysses_sequence_attention_uly_gb300 import Plan
+    n = 2049 * 128
+    plan = Plan(1, 1, n, 0, "none", 1, 1, 64)
+    q, k, v = (torch.randn((1, n, 1, 64), device="cuda").to(torch.bfloat16) for _ in range(3))
+    o, again = torch.empty_like(q), torch.empty_like(q)
+    starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    plan.prompt_attention([q], [k], [v], [o], starts)
+    assert plan.sync_status() == 0
+    plan.set_wait_limit(400_000)
+    plan.prompt_attention([q], [k], [v], [again], starts)
+    assert plan.sync_status() == 0
+    assert torch.equal(o.view(torch.int16), again.view(torch.int16))

@@ -31,9 +31,9 @@
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D,256+2D).
 //
 // The arithmetic of an item does not depend on which CTA takes it: the same
-// bits on every call.  Every wait is bounded, as in attn.cu, by a deadline that a
-// role puts off with every item (a CTA may be at work for seconds; a reading of
-// the clock before every wait cost up to a tenth).
+// bits on every call.  Every wait is bounded, each for itself (a CTA may be at
+// work for seconds): its clock is first read when it has been waited for a while,
+// since a reading before every wait cost up to a tenth.
 //
 // What bounds it (ncu, 8192 rows of 32 heads on 8): long items run at 2500 to 2600
 // cycles a step, of which the four products take 2048 and the operands' way through
@@ -112,6 +112,28 @@ __device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(0), "r"(0)
       : "memory");
+}
+
+// A wait on a barrier that gives up after limit_ns, or when another role has.  The
+// limit counts from the 64th try on (each is waited for by the hardware a while).
+// Out of line: the roles wait in many places of unrolled code, which has to stay
+// small (24 prompts of 30 to 900 rows: inline 62.5 us, out of line 59.4).
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                           volatile int* abort_flag) {
+  uint32_t spins = 0;
+  uint64_t since = 0;
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((++spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (!since) since = now;
+      if (now - since > limit_ns) return false;
+    }
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || bar_wait_long(bar, parity, limit_ns, abort_flag);
 }
 
 // wait for the launch before this one in the stream (a programmatic dependency)
@@ -467,7 +489,6 @@ __device__ __forceinline__ void find_items(const PromptCut& p, int n_hp, PBars& 
 template <int D>
 __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV,
                                          int n_items, const PromptRun* runs, uint64_t wait_ns) {
-  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   bool ok = true;
@@ -477,7 +498,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
   // group g: V of step g - 1 and K of step g
   auto group = [&](bool has_k, int shard, int row, int head) {
     const int bi = g % C::kHalf;
-    if (g >= C::kHalf && !mbar_wait(smem_u32(&bars.empty[bi]), (g / C::kHalf - 1) & 1, deadline, abort_flag))
+    if (g >= C::kHalf && !bar_wait(smem_u32(&bars.empty[bi]), (g / C::kHalf - 1) & 1, wait_ns, abort_flag))
       return false;
     const uint32_t bf = smem_u32(&bars.full[bi]);
     mbar_arrive_expect_tx(bf, (g > 0 && has_k ? 2 : 1) * C::kTileBytes);
@@ -496,7 +517,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
   for (int k = 0; ok; ++k) {
     const int slot = k % kItems;
     if (k >= kItems &&
-        !(ok = mbar_wait(smem_u32(&bars.item_empty[slot]), (k / kItems - 1) & 1, deadline, abort_flag)))
+        !(ok = bar_wait(smem_u32(&bars.item_empty[slot]), (k / kItems - 1) & 1, wait_ns, abort_flag)))
       break;
     Item it = {};
     it.run = -1;
@@ -527,7 +548,6 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
         it.n[1] = two ? u.z : 0;
       }
     }
-    deadline = globaltimer_ns() + wait_ns;
     bars.item[slot] = it;
     mbar_arrive(smem_u32(&bars.item_full[slot]));
     if (it.run < 0) break;
@@ -544,7 +564,7 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!ok || !it.n[i]) continue;
-          if (n_q[i] && !(ok = mbar_wait(smem_u32(&bars.q_empty[i]), (n_q[i] - 1) & 1, deadline, abort_flag)))
+          if (n_q[i] && !(ok = bar_wait(smem_u32(&bars.q_empty[i]), (n_q[i] - 1) & 1, wait_ns, abort_flag)))
             continue;
           const uint32_t bq = smem_u32(&bars.q_full[i]);
           mbar_arrive_expect_tx(bq, C::kTileBytes);
@@ -576,7 +596,6 @@ __device__ __forceinline__ void producer(const PromptParams& p, PBars& bars, uin
 template <int D>
 __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint32_t sQ, uint32_t sKV, uint32_t tmem,
                                        uint64_t wait_ns) {
-  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   // descriptors as in attn.cu: a fixed high part and the start address / 16
@@ -608,7 +627,7 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
   static_assert(kUnroll % C::kHalf == 0, "whole turns of the ring");
   bool ok = true, more = false;
   auto wait = [&](uint64_t& bar, uint32_t parity) {
-    ok = mbar_wait(smem_u32(&bar), parity & 1, deadline, abort_flag);
+    ok = bar_wait(smem_u32(&bar), parity & 1, wait_ns, abort_flag);
     tc_fence_after();
     return ok;
   };
@@ -620,7 +639,6 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
     n1 = end ? 0 : bars.item[slot].n[1];
     mbar_arrive(smem_u32(&bars.item_empty[slot]));
     ++n_item;
-    deadline = globaltimer_ns() + wait_ns;
     return true;
   };
   // Scores of a tile (constants: every descriptor is ready, since what the issuer
@@ -728,7 +746,6 @@ __device__ __forceinline__ void issuer(const PromptParams& p, PBars& bars, uint3
 template <int D>
 __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint32_t sKV, uint32_t sStage,
                                         uint32_t tmem, const PromptRun* runs, int warp, int lane, uint64_t wait_ns) {
-  uint64_t deadline = globaltimer_ns() + wait_ns;  // of an item: put off with every new one
   using C = PCfg<D>;
   volatile int* abort_flag = &bars.abort_flag;
   const int wg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
@@ -737,23 +754,29 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
   const uint32_t stage = sStage + warp * C::kStageBytes;
   const float sl2 = p.scale_log2;
   int n_s = 0, n_o = 0, step0 = 0;  // S tiles and O tiles waited for; steps of the items before
+  int idle = 0;  // steps of the item before in which these warps had no tile
   bool ok = true;
   for (int k = 0; ok; ++k) {
     const int slot = k % kItems;
-    if (!__all_sync(0xffffffffu,
-                    mbar_wait(smem_u32(&bars.item_full[slot]), (k / kItems) & 1, deadline, abort_flag))) {
+    // The next item comes near the end of this one.  Warps without a tile in this one
+    // wait as long as the other roles may in its steps, where up to four waits (for
+    // K and V, scores, P, a free slot) follow upon each other; when one of those gives
+    // up, so do they.
+    bool there = false;
+    for (int i = 0; i <= 4 * idle && !there && !*abort_flag; ++i)
+      there = bar_wait(smem_u32(&bars.item_full[slot]), (k / kItems) & 1, wait_ns, abort_flag);
+    if (!__all_sync(0xffffffffu, there)) {
       ok = false;
       break;
     }
     const Item& it = bars.item[slot];
     if (it.run < 0) break;
-    deadline = globaltimer_ns() + wait_ns;
     const int n = wg ? it.n[1] : it.n[0];
     if (n > 0) {
       float m_ref = -INFINITY, l_run = 0.f;
       int run = it.first_run, left = it.first_len;  // rows of the run from tile s on
       auto scores_ready = [&]() {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[wg]), n_s & 1, deadline, abort_flag))) return false;
+        if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&bars.s_full[wg]), n_s & 1, wait_ns, abort_flag))) return false;
         ++n_s;
         tc_fence_after();
         return true;
@@ -789,7 +812,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
           // V's rows behind the run's end: zero (both tiles' warps do it, each
           // before its own product)
           const int st = step0 + s, gr = st + 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[gr % C::kHalf]), (gr / C::kHalf) & 1, deadline,
+          if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&bars.full[gr % C::kHalf]), (gr / C::kHalf) & 1, wait_ns,
                                                  abort_flag))) {
             tmem_wait_st();  // (P is on its way: TMEM is not freed before it is there)
             ok = false;
@@ -820,7 +843,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
                             static_cast<int64_t>(head) * D * 2 + (lane & 7) * 16;
       const int shard_rows = p.cut.shard_begin[shard + 1] - p.cut.shard_begin[shard];
       const float inv = 1.f / l_run;  // (a row has itself: l_run > 0, NaN inputs aside)
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.o_done[wg]), n_o & 1, deadline, abort_flag))) {
+      if (!__all_sync(0xffffffffu, bar_wait(smem_u32(&bars.o_done[wg]), n_o & 1, wait_ns, abort_flag))) {
         ok = false;
         break;
       }
@@ -863,6 +886,7 @@ __device__ __forceinline__ void softmax(const PromptParams& p, PBars& bars, uint
         p.lse[shard][static_cast<int64_t>(first_row + row0 + lane) * p.Hq + head] =
             (m_ref + lg2_approx(l_run)) * 0.6931471805599453f;
     }
+    idle = n > 0 ? 0 : max(it.n[0], it.n[1]);
     step0 += max(it.n[0], it.n[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[slot]));
