@@ -617,7 +617,8 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
  *   workspace: device memory of at least uly_cache_attention_workspace(...)
  *     bytes, 256-byte aligned, owned by the caller; its contents mean nothing
  *     before and after the call.
- * P (after the exponential) is rounded to f16 and q to f16 with a power of two
+ * A key's weight (the exponential times its page's v_scale) is rounded to f16, or by
+ * 2^-32 of the row's largest where that is more, and q to f16 with a power of two
  * taken out of each row; everything else is f32.  The same bits on every call
  * on a device.  Works on the current device; may be captured into a CUDA graph;
  * a replay reads starts, lens and the table anew.

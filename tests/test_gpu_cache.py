@@ -190,6 +190,28 @@ def test_attention_other_scales(c):
     R.check_cached(c, d, o, lse, scale=0.05)
 
 
+@pytest.mark.parametrize("D,T", [(64, 1), (128, 1), (128, 5)])  # (five tokens of two heads: two tiles of queries)
+def test_attention_a_page_of_a_far_larger_scale(D, T):
+    """The first page's v scale 2^20 times the others', its codes zero in every second
+    element (a warp has 16 of every 64 keys, so that all of them see it first):
+    there the output is made of weights 2^-20 of the largest, which f16 has to hold
+    to 2^-11.  The reference exponent leaves seven binary orders above the largest
+    weight, so that half a step of the smallest is 2^-32 of it."""
+    c = R.Cached("far", (100,), (T,), 2, D, 64, G=2, std=0.3)
+    d = R.cache_inputs(c, 23)
+    cache = R.cache_of(d)
+    cache.append(d["k"], d["v"], d["starts"], d["lens"], d["table"])
+    page = int(d["table"][0, 0])
+    d["v_scale"].fill_(1.0)
+    d["v_scale"][page] = 2.0 ** 20
+    d["v_pages"].view(torch.uint8)[page, :, :, ::2] = 0
+    o, lse = R.attend(cache, c, d)
+    torch.cuda.synchronize()
+    want, wl, err, _ = R.cached_reference(c, d, small=2.0 ** -32)
+    R.check_rows(o, want, err, "o")
+    R.check_rows(lse, wl, 2.0 ** -13 + 2.0 ** -22 * wl.abs(), "lse")
+
+
 @pytest.mark.parametrize("e", [-60, -20, 60, 100])
 def test_attention_scales_at_their_ends(e):
     """All of v's scales at an end of their range, and one page at the least one."""

@@ -270,12 +270,16 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 // each row (so that no element overflows, and none matters that underflows), and
 // P is rounded to f16, whose 11 bits are finer than what k and v have left.
 // The scales of k multiply the scores.  Those of v go into P: its weight is
-// 2^(s - M + log2 v_scale) with a reference maximum M of s + log2 v_scale, beside
-// the sum of 2^(s - m), whose reference is m; so f16 holds the weights whatever
-// the scales are.
+// 2^(s - M + log2 v_scale) with a reference M that follows the maximum of s + log2
+// v_scale, beside the sum of 2^(s - m), whose reference is m.  M is kRoom below that
+// maximum when it is raised, and is raised when a weight would pass 2^(8 + kRoom):
+// f16's upper orders are used, and weights down to 2^-21 of the largest keep its 11
+// bits (with a page's scale 2^20 above the others', the others' weights do); one
+// that is smaller is off by 2^-32 of the largest at most.
 namespace {
 
 constexpr int kBlockKeys = 64;   // keys of a block: 16 for each of a CTA's warps
+constexpr float kRoom = 7.f;     // 2^(8 + kRoom), with the exponential's error, is in f16's range
 constexpr int kLongPart = 320 << 10;  // bytes of codes
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -645,6 +649,7 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         }
       }
       const float ks = ld_shared_f32(st + 2 * C::kHalf), lv = lg2_approx(ld_shared_f32(st + 2 * C::kHalf + 4));
+      const float lr = lv - kRoom;  // from a score to the reference that it asks for
       uint32_t pb[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -656,8 +661,8 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
             if (key + g + 8 * (i >> 1) >= lim[t][i & 1]) x[i] = -INFINITY;
         }
         const float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
-        if (__any_sync(0xffffffffu, t0 > m[t][0] + 8.f || t1 > m[t][1] + 8.f || t0 + lv > M[t][0] + 8.f ||
-                                        t1 + lv > M[t][1] + 8.f)) {
+        if (__any_sync(0xffffffffu, t0 > m[t][0] + 8.f || t1 > m[t][1] + 8.f || t0 + lr > M[t][0] + 8.f ||
+                                        t1 + lr > M[t][1] + 8.f)) {
           float r[2] = {t0, t1};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -667,9 +672,9 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
               l[t][i] *= ex2_approx(m[t][i] - r[i]);
               m[t][i] = r[i];
             }
-            if (r[i] + lv > M[t][i]) {
-              const float f = ex2_approx(M[t][i] - (r[i] + lv));
-              M[t][i] = r[i] + lv;
+            if (r[i] + lr > M[t][i]) {
+              const float f = ex2_approx(M[t][i] - (r[i] + lr));
+              M[t][i] = r[i] + lr;
 #pragma unroll
               for (int q = 0; q < MT; ++q) {
                 o[t][q][i] *= f;
