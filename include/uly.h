@@ -619,7 +619,8 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
  *     before and after the call.
  * A key's weight (the exponential times its page's v_scale) is rounded to f16, or by
  * 2^-32 of the row's largest where that is more, and q to f16 with a power of two
- * taken out of each row; everything else is f32.  The same bits on every call
+ * taken out of each row (exact but for elements below 2^-31 of the row's largest);
+ * everything else is f32.  The same bits on every call
  * on a device.  Works on the current device; may be captured into a CUDA graph;
  * a replay reads starts, lens and the table anew.
  * Errors as uly_cache_append, and ULY_ERR_INVALID for Hq % H, a bad scale or a

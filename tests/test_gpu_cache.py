@@ -247,6 +247,40 @@ def test_large_and_small_queries():
         R.check_rows(lse[rows], wl[rows], 2.0 ** -13 + 2.0 ** -22 * wl[rows].abs(), "lse")
 
 
+@pytest.mark.parametrize("D,T", [(64, 1), (128, 5)])
+def test_one_large_element_of_q(D, T):
+    """An element of q 2^20 times the others meets codes of zero: the scores are made
+    of the small ones, which f16 holds exactly down to 2^-31 of the largest.  (The
+    bound: q, 8 bits wide, is exact, so that the reference's stands as it is.)"""
+    c = R.Cached("outlier", (200,), (T,), 2, D, 32, G=2)
+    d = R.cache_inputs(c, 24)
+    cache = R.cache_of(d)
+    cache.append(d["k"], d["v"], d["starts"], d["lens"], d["table"])
+    d["k_pages"].view(torch.uint8)[..., 5] = 0
+    d["q"][..., 5] = 2.0 ** 20
+    o, lse = R.attend(cache, c, d, scale=0.125)
+    torch.cuda.synchronize()
+    R.check_cached(c, d, o, lse, scale=0.125)
+
+
+@pytest.mark.parametrize("e", [127, 126, -112, -120, -126])
+def test_queries_at_the_ends_of_bf16(e):
+    """Largest elements of q at both ends of bf16's exponents."""
+    c = R.Cached("ends of q", (60,), (2,), 1, 64, 32, G=2)
+    d = R.cache_inputs(c, 25)
+    cache = R.cache_of(d)
+    cache.append(d["k"], d["v"], d["starts"], d["lens"], d["table"])
+    d["k_scale"].fill_(2.0 ** -20 if e > 0 else 2.0 ** 30)
+    d["q"].clamp_(-1.99, 1.99)
+    d["q"][..., 0] = 1.9921875
+    d["q"] = (d["q"].float() * 2.0 ** e).to(torch.bfloat16)
+    assert torch.isfinite(d["q"]).all()
+    scale = 2.0 ** (20 - e - 9) if e > 0 else 2.0 ** (-e - 30 - 9)  # scores of about one
+    o, lse = R.attend(cache, c, d, scale=scale)
+    torch.cuda.synchronize()
+    R.check_cached(c, d, o, lse, scale=scale)
+
+
 def test_bad_pages_and_lengths():
     """Tokens in bad pages take no part; a length past the table ends with it; a
     row before the first position has no key."""

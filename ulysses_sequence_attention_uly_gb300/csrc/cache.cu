@@ -267,8 +267,8 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 //                 codes it pairs up by byte permutation before the conversion;
 //                 P^T is S^T transposed in registers (movmatrix).
 // e4m3 codes are exact in f16.  q goes to f16 with a power of two taken out of
-// each row (so that no element overflows, and none matters that underflows), and
-// P is rounded to f16, whose 11 bits are finer than what k and v have left.
+// each row, so that no element overflows and those down to 2^-31 of the largest are
+// exact, and P is rounded to f16, whose 11 bits are finer than what k and v have left.
 // The scales of k multiply the scores.  Those of v go into P: its weight is
 // 2^(s - M + log2 v_scale) with a reference M that follows the maximum of s + log2
 // v_scale, beside the sum of 2^(s - m), whose reference is m.  M is kRoom below that
@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(128, kCachedPerSm[NT - 1]) cached_kernel(const
         }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e2 = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126), 126);
+      // the largest element to between 2^14 and 2^15, near f16's end: elements down to
+      // 2^-31 of it are exact
+      const int e2 = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 127) - 14;
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) * p.scale_log2;
 #pragma unroll
