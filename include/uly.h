@@ -632,7 +632,7 @@ int uly_cache_attention(const uly_cache* cache, const void* q, int64_t q_row_str
 
 /* Bytes of workspace of uly_cache_attention (0 where a table's width holds no more
  * than 1024 tokens, with up to 128 sequences; then workspace may be NULL), or -1
- * for a bad argument. */
+ * for an argument that the call refuses. */
 int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs,
                                       int32_t table_width);
 

@@ -97,6 +97,19 @@ def test_null_arguments_and_workspaces():
         assert L.uly_cache_attention_workspace(*a) == -1
 
 
+def test_workspace_of_what_the_call_refuses():
+    """-1 where uly_cache_attention refuses the sizes, and no wrapped product of them."""
+    L = uly.lib()
+    for a in ((cache(H=1), (1 << 31) - 1, 1 << 27, 2, 400), (cache(), 65536, 1 << 27, 2, 400),
+              (cache(D=(1 << 31) - 4), 4, 1 << 27, 2, 400), (cache(D=96), 4, 3, 2, 400),
+              (cache(page_rows=24), 4, 3, 2, 400), (cache(H=65536), 65536, 3, 2, 400), (cache(), 4, 3, 65537, 400)):
+        assert L.uly_cache_attention_workspace(*a) == -1, a[1:]
+    # the largest that is taken: units of 16 rows, their notes and sums
+    most = L.uly_cache_attention_workspace(cache(H=65535, D=128, page_rows=128), 65535, 1 << 27, 65536, (1 << 31) - 1)
+    parts = 2 * 160 * 3 + 65535 * ((1 << 27) // 16 + 65536)
+    assert abs(most - (65538 * 8 + parts * (32 + 16 * 132 * 4))) < 1024
+
+
 class _Shape(uly.Plan):
     """A plan's shape without the library's plan: the binding's own checks."""
 

@@ -1785,6 +1785,13 @@ int64_t row_step(int64_t stride, int64_t dense) {
 
 int64_t rows_bytes(int64_t rows, int64_t step, int64_t dense) { return rows > 0 ? (rows - 1) * step + dense * 2 : 0; }
 
+// Sizes that the cache calls take, and that no product of theirs passes 64 bits with.
+bool cache_supported(const uly_cache& a, int64_t n_rows, int32_t n_seqs) {
+  return (a.D == 64 || a.D == 128) &&
+         (a.page_rows == 16 || a.page_rows == 32 || a.page_rows == 64 || a.page_rows == 128) && a.H <= 65535 &&
+         n_seqs <= kMaxSeqs && n_rows <= kMaxRows;
+}
+
 // What the two cache calls check and fill in alike.
 int setup_cache(const uly_cache* cache, int64_t n_rows, const int32_t* starts, const int32_t* lens,
                 const int32_t* table, int32_t n_seqs, int32_t table_width, CacheParams& c, Spans& spans, bool write) {
@@ -1792,10 +1799,7 @@ int setup_cache(const uly_cache* cache, int64_t n_rows, const int32_t* starts, c
   const uly_cache& a = *cache;
   if (a.n_pages < 1 || a.page_rows < 1 || a.H < 1 || a.D < 1 || n_rows < 0 || n_seqs < 0 || table_width < 1)
     return ULY_ERR_INVALID;
-  if ((a.D != 64 && a.D != 128) ||
-      (a.page_rows != 16 && a.page_rows != 32 && a.page_rows != 64 && a.page_rows != 128) || a.H > 65535 ||
-      n_seqs > kMaxSeqs || n_rows > kMaxRows)
-    return ULY_ERR_UNSUPPORTED;
+  if (!cache_supported(a, n_rows, n_seqs)) return ULY_ERR_UNSUPPORTED;
   if (misaligned(a.k_pages, 16) || misaligned(a.v_pages, 16) || misaligned(a.k_scale, 4) ||
       misaligned(a.v_scale, 4) || misaligned(starts, 4) || misaligned(lens, 4) || misaligned(table, 4))
     return ULY_ERR_INVALID;
@@ -1970,8 +1974,8 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
 
 int64_t uly_cache_attention_workspace(const uly_cache* cache, int32_t Hq, int64_t n_rows, int32_t n_seqs,
                                       int32_t table_width) {
-  if (!cache || Hq < 1 || cache->H < 1 || cache->D < 1 || cache->page_rows < 1 || Hq % cache->H || n_rows < 0 ||
-      n_rows > kMaxRows || n_seqs < 0 || table_width < 1)
+  if (!cache || Hq < 1 || Hq > 65535 || cache->H < 1 || Hq % cache->H || n_rows < 0 || n_seqs < 0 ||
+      table_width < 1 || !cache_supported(*cache, n_rows, n_seqs))
     return -1;
   return cached_work(cache, Hq, n_rows, n_seqs, table_width).total;
 }
