@@ -178,6 +178,38 @@ def test_attention_against_64_bits(c):
     R.check_cached(c, d, o, lse)
 
 
+def _ragged(n, lo, hi):
+    """n lengths between lo and hi, even over the logarithm, in no order."""
+    return tuple(int(lo * (hi / lo) ** ((i * 37 % n) / (n - 1))) for i in range(n))
+
+
+# so many long units that their parts are half as long as what a CTA's share would be
+FULL = [
+    R.Cached("batch", _ragged(64, 400, 12000), (1,) * 64, 8, 128, 64, G=4),
+    R.Cached("batch, 64 wide", _ragged(64, 1000, 16000), (1,) * 64, 8, 64, 32, G=4),
+    R.Cached("more sequences than a CTA has threads", _ragged(200, 100, 6000), (1,) * 200, 8, 128, 128, G=2),
+    R.Cached("two tiles of queries", _ragged(64, 400, 9000), (3,) * 64, 8, 128, 64, G=4, std=0.7),
+    R.Cached("three tiles, 64 wide", _ragged(64, 400, 9000), (9,) * 40 + (0, 11) * 12, 8, 64, 16, G=4),
+    R.Cached("more sequences, two tiles, 64 wide", _ragged(150, 300, 6000), (4, 2, 5) * 50, 8, 64, 64, G=3),
+]
+
+
+@pytest.mark.parametrize("c", FULL, ids=lambda c: c.name)
+def test_attention_full_batches(c):
+    # the case does reach that way: blocks of 64 keys, and what a CTA slot has of them (320 KB of codes and more)
+    tiles = 2 if c.rows * c.G > 8 * len(c.new) else 1
+    slots = min(torch.cuda.get_device_properties(0).multi_processor_count, 160) * (4, 3)[tiles - 1]
+    blocks = sum(-(-t * c.G // (8 * tiles)) * -(-n // 64) for n, t in zip(c.lens, c.new)) * c.H
+    assert blocks > slots * ((320 << 10) // (64 * 2 * c.D))
+    assert max(c.lens) > 1024 and len(c.lens) * c.H * 8 > slots  # neither whole units nor few of them
+    d = R.cache_inputs(c, 26)
+    cache = R.cache_of(d)
+    cache.append(d["k"], d["v"], d["starts"], d["lens"], d["table"])
+    o, lse = R.attend(cache, c, d)
+    torch.cuda.synchronize()
+    R.check_cached(c, d, o, lse)
+
+
 @pytest.mark.parametrize("c", ATTENTION[2:9:3], ids=lambda c: c.name)
 def test_attention_other_scales(c):
     """Scales of any value, far apart between pages, and another softmax scale."""
