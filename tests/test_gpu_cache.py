@@ -447,6 +447,46 @@ def test_the_same_bits_every_time_streams_and_graph():
             R.check_cached(c, x, y, None)
 
 
+@pytest.mark.parametrize("old", [(3000, 20, 700, 0), (300, 20, 70, 0)])  # in parts, and whole without a workspace
+def test_two_threads(old):
+    """Appends and attention from two threads at once, each with a stream and a cache
+    of its own: the bits of calls alone."""
+    import threading
+    c = R.Cached("threads", old, (1, 3, 1, 2), 2, 128, 64, G=4)
+    jobs, wrong = [], []
+
+    def step(x):
+        o, lse = torch.full_like(x["q"], 7.0), torch.full(x["q"].shape[:2], 7.0, device="cuda")
+        cache = R.cache_of(x)
+        cache.append(x["k"], x["v"], x["starts"], x["lens"], x["table"])
+        cache.attention(x["q"], o, x["starts"], x["lens"], x["table"], lse=lse)
+        return [o, lse] + [x[n].view(torch.uint8) for n in ("k_pages", "v_pages")]
+
+    for seed in (60, 61):
+        x = R.cache_inputs(c, seed)
+        jobs.append((x, [t.clone() for t in step(x)]))
+    torch.cuda.synchronize()
+
+    def work(x, want):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    got = step(x)  # (the same rows again: the same codes)
+                    s.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        wrong.append("other bits")
+        except Exception as e:  # noqa: BLE001 - reported below
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+
+
 def test_prompt_cache_and_generation_together():
     """Prompts through the causal attention and into the cache, then tokens one by
     one (and three at once): each step's output against attention over all keys

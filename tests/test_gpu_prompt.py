@@ -111,6 +111,82 @@ def test_more_sequences_than_threads():
     R.check_prompt(c, d, d["o"], d["lse"])
 
 
+MANY = [
+    # more runs than shared memory holds the first units of (2048), with longer ones at both ends and in the middle
+    R.Prompt("runs", (3500, 3000, 2500), (700,) + tuple(1 + i % 3 for i in range(1500)) + (900, 0, 257) +
+             tuple(1 + i % 2 for i in range(1700)) + (600,), 6, 3, 64, first=13),
+    R.Prompt("runs, odd groups", (6000, 2500), (700,) + tuple(1 + i % 3 for i in range(1500)) + (900, 0, 257) +
+             tuple(1 + i % 2 for i in range(1000)) + (600,), 2, 2, 128, first=13),
+    # so many rows that units of like length share a place in the order
+    R.Prompt("rows", (140000, 130000), (9000,) + tuple(300 + (i * 797) % 2400 for i in range(150)) + (5000, 1, 128),
+             4, 2, 64, first=129),
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=lambda c: c.name)
+def test_tables_of_many_runs_and_many_rows(c):
+    runs = sum(1 for a, b in zip(c.bounds, c.bounds[1:]) if b > a)
+    assert c.bounds[-1] <= c.n and (runs > 2048 or c.n // 128 + len(c.shards) >= 2048)
+    d = R.prompt_inputs(c, 17)
+    plan = R.plan_of(c)
+    assert plan.prompt_attention_workspace(len(c.seqs)) > 0
+    run(c, d, plan)
+    R.check_prompt(c, d, d["o"], d["lse"])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 4, 128), (4, 4, 64)])
+def test_the_same_rows_in_one_two_and_four_shards(Hq, Hkv, D):
+    """Key tiles begin anew where a shard does, so that bits differ between the
+    numbers of shards; each is within the bound of the same 64-bit result."""
+    seqs = (300, 256, 1, 467)
+    whole = R.prompt_inputs(R.Prompt("whole", (1024,), seqs, Hq, Hkv, D), 18)
+    for shards in ((1024,), (512, 512), (700, 324), (256,) * 4, (130, 500, 1, 393)):
+        c = R.Prompt("split", shards, seqs, Hq, Hkv, D)
+        d = {n: [y.contiguous() for y in whole[n][0].split(list(shards), 1)] for n in ("q", "k", "v")}
+        d["o"] = [torch.full_like(x, 7.0) for x in d["q"]]
+        d["lse"] = [torch.full(x.shape[:3], 7.0, device="cuda") for x in d["q"]]
+        d["starts"] = whole["starts"]
+        run(c, d)
+        R.check_prompt(c, d, d["o"], d["lse"])
+
+
+@pytest.mark.parametrize("Hq", [96, 4])  # with tables, and without
+def test_two_threads_one_plan(Hq):
+    """Calls of one plan from two threads at once, each on a stream and with tensors
+    of its own: the bits of calls alone."""
+    import threading
+    c = R.Prompt("threads", (500, 400), (123, 456, 200), Hq, Hq // 2, 128, first=30)
+    plan = R.plan_of(c)
+    assert (plan.prompt_attention_workspace(3) > 0) == (Hq == 96)
+    jobs, wrong = [], []
+    for seed in (50, 51):
+        d = R.prompt_inputs(c, seed)
+        run(c, d, plan)
+        jobs.append((d, [x.clone() for x in d["o"] + d["lse"]]))
+
+    def work(d, want):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    for x in d["o"] + d["lse"]:
+                        x.fill_(7.0)
+                    plan.prompt_attention(d["q"], d["k"], d["v"], d["o"], d["starts"], lse=d["lse"])
+                    s.synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(d["o"] + d["lse"], want)):
+                        wrong.append("other bits")
+        except Exception as e:  # noqa: BLE001 - reported below
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+    assert plan.sync_status() == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 3)])
 def test_what_other_rows_hold_does_not_matter(Hq, Hkv):
     """Rows of no sequence, and of a neighbour, may hold NaN and infinities."""
