@@ -112,6 +112,39 @@ def test_append_an_infinity_takes_its_page_and_head_alone():
         assert torch.equal(a, b)
 
 
+def test_append_shard_by_shard():
+    """The rows of sequences that lie across shards, a call for each shard in order:
+    its starts clamped to its rows, the lengths those up to its end.  Pages that a
+    shard's end cuts are taken up again, also where the later rows raise their scale."""
+    shards, first, old, new = (70, 1, 129, 100), 9, (20, 0, 5, 33), (40, 130, 0, 111)
+    c = R.Cached("shards", old, new, 2, 64, 32)
+    d = R.cache_inputs(c, 28)
+    rows = sum(shards)
+    assert first + c.rows <= rows
+    at = [first]
+    for n in new:
+        at.append(at[-1] + n)
+    whole = {t: (torch.randn((rows, 2, 64), device="cuda") * torch.arange(1, rows + 1, device="cuda")[:, None, None])
+             .to(torch.bfloat16) for t in "kv"}  # (larger and larger: every cut page's scale is raised)
+    lo, cache = 0, R.cache_of(d)
+    for n in shards:
+        part = R.Cached("shard", old, new, 2, 64, 32)
+        x = {**d, "k": whole["k"][lo:lo + n], "v": whole["v"][lo:lo + n],
+             "starts": R.ints([min(max(a - lo, 0), n) for a in at]),
+             "lens": R.ints([o + min(max(lo + n - a, 0), m) for o, a, m in zip(old, at, new)])}
+        check_append(part, x, lambda: cache.append(x["k"], x["v"], x["starts"], x["lens"], x["table"]))
+        lo += n
+    for s, (a, m) in enumerate(zip(at, new)):  # every row is there
+        for i in range(m):
+            pos = old[s] + i
+            page, slot = int(d["table"][s, pos // 32]), pos % 32
+            for t in "kv":
+                scale = d[t + "_scale"][page].double()[:, None]
+                was, got = whole[t][a + i].double(), d[t + "_pages"][page, :, slot].double() * scale
+                # rounded once for its call's scale and, where that is subnormal in a later one, once more
+                assert ((got - was).abs() <= 2.0 ** -4 * was.abs() + 2.0 ** -9 * scale).all()
+
+
 def test_append_drops_rows_without_a_place():
     """Positions below zero or past the table, bad pages: nothing else is written."""
     c = R.Cached("dropped", (10, 0, 40), (20, 5, 30), 2, 64, 16)
@@ -349,6 +382,51 @@ def test_rows_of_no_sequence_stay_and_starts_are_clamped():
         torch.cuda.synchronize()
         d["starts"] = d["starts"].clamp(0, 5)
         R.check_cached(c, d, o, lse)
+
+
+@pytest.mark.parametrize("width", [2, 70])  # units whole, and in parts that the table's width asks for
+def test_the_most_sequences(width):
+    """65536 sequences of 20 tokens, one of them new, against 64 bits in one piece."""
+    import ulysses_sequence_attention_uly_gb300 as uly
+    n, D, page, L = 65536, 64, 16, 20
+    g = torch.Generator(device="cuda").manual_seed(27)
+    x = {t: torch.zeros((2 * n, 1, page, D), dtype=torch.float8_e4m3fn, device="cuda") for t in ("k_pages", "v_pages")}
+    x |= {t: torch.zeros((2 * n, 1), device="cuda") for t in ("k_scale", "v_scale")}
+    cache = R.cache_of(x)
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = torch.randperm(2 * n, generator=g, device="cuda").int().view(n, 2)
+    k, v = (torch.randn((n, L, 1, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    for a, b in ((0, L - 1), (L - 1, L)):  # the first tokens, then the newest one
+        cache.append(k[:, a:b].reshape(-1, 1, D), v[:, a:b].reshape(-1, 1, D),
+                     torch.arange(0, n * (b - a) + 1, b - a, dtype=torch.int32, device="cuda"),
+                     torch.full((n,), b, dtype=torch.int32, device="cuda"), table)
+    kk, vv = ((x[t + "_pages"].double() * x[t + "_scale"].double()[..., None, None])[table[:, :2].long()]
+              .reshape(n, 2 * page, D)[:, :L] for t in "kv")
+    for got, was in ((kk, k), (vv, v)):  # what the cache holds: within an e4m3 rounding of what came
+        was = was[:, :, 0].double()
+        # a scale s is at most twice top / 448, half a step of the smallest codes 2^-10 s: 2^-9 top / 448 for a
+        # page that was written once.  The second page's first tokens were rounded for a scale s' <= s / 2 before
+        # they came to s: small ones by 2^-10 s' + 2^-10 s at most, which is 1.5 times that
+        top = was.abs().amax((1, 2))[:, None, None] / 448
+        off = (got - was).abs() - 2.0 ** -4 * was.abs()
+        assert (off[:, :page] <= 2.0 ** -9 * top).all() and (off[:, page:] <= 1.5 * 2.0 ** -9 * top).all()
+    q = torch.randn((n, 2, D), generator=g, device="cuda").to(torch.bfloat16)
+    o, lse = torch.full_like(q, 7.0), torch.full((n, 2), 7.0, device="cuda")
+    starts, lens = torch.arange(n + 1, dtype=torch.int32, device="cuda"), torch.full((n,), L, dtype=torch.int32, device="cuda")
+    cache.attention(q, o, starts, lens, table, scale=0.125, lse=lse)
+    torch.cuda.synchronize()
+    s = torch.einsum("nhd,njd->nhj", q.double(), kk) * 0.125
+    p = s.softmax(-1)
+    want = torch.einsum("nhj,njd->nhd", p, vv)
+    err = torch.einsum("nhj,njd->nhd", p, vv.abs()) * (2.0 ** -11 + 2.0 ** -13) + 2.0 ** -8 * want.abs()
+    # (weights below f16's normal range: 2^-32 of the largest, for values of 448 scales at most)
+    err = err * (1 + 2.0 ** -8) + L * 2.0 ** -32 * 448 * x["v_scale"].amax().double() + 1e-30
+    R.check_rows(o, want, err, "o")
+    R.check_rows(lse, s.logsumexp(-1), 2.0 ** -13 + 2.0 ** -22 * s.logsumexp(-1).abs(), "lse")
+    with pytest.raises(uly.UlyError) as e:
+        cache.attention(q, o, R.ints([0] * (n + 2)), R.ints([0] * (n + 1)), torch.zeros((n + 1, 1), dtype=torch.int32,
+                                                                                      device="cuda"))
+    assert e.value.status == uly.ULY_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("seqs", [100, 150])

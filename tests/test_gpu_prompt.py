@@ -103,6 +103,55 @@ def test_starts_that_fall_at_a_turn_of_lanes():
     R.check_prompt(as_is, d, d["o"], d["lse"])
 
 
+def test_the_most_sequences():
+    """65536 sequences of two rows: the second row's weights in closed form."""
+    import ulysses_sequence_attention_uly_gb300 as uly
+    n, D = 65536, 64
+    plan = uly.Plan(1, 2, n, 0, "none", 4, 2, D)
+    g = torch.Generator(device="cuda").manual_seed(19)
+    q, k, v = ([torch.randn((1, n, h, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+               for h in (4, 2, 2))
+    o, lse = [torch.full_like(x, 7.0) for x in q], [torch.full((1, n, 4), 7.0, device="cuda") for _ in range(2)]
+    starts = torch.arange(0, 2 * n + 1, 2, dtype=torch.int32, device="cuda")
+    plan.prompt_attention(q, k, v, o, starts, scale=0.125, lse=lse)
+    assert plan.sync_status() == 0
+    qq, kk, vv = (torch.cat(x, 1)[0].double().view(n, 2, -1, D) for x in (q, k, v))
+    kk, vv = (x.repeat_interleave(2, 2) for x in (kk, vv))
+    s = (qq[:, 1, None] * kk).sum(-1) * 0.125  # [n, 2 keys, heads]
+    p = s.softmax(1)[..., None]
+    want = torch.stack((vv[:, 0], (p * vv).sum(1)), 1)
+    u, r = 2.0 ** -8, 2.0 ** -13  # as in the reference of the other cases
+    err = torch.stack((vv[:, 0].abs(), (p * vv.abs()).sum(1)), 1) * (u + r) * (1 + u) + u * want.abs() + 1e-30
+    R.check_rows(torch.cat(o, 1)[0].view(n, 2, 4, D), want, err, "o")
+    wl = torch.stack(((qq[:, 0] * kk[:, 0]).sum(-1) * 0.125, s.logsumexp(1)), 1)
+    R.check_rows(torch.cat(lse, 1)[0].view(n, 2, 4), wl, 2.0 ** -13 + 2.0 ** -22 * wl.abs(), "lse")
+    too_many = torch.zeros(n + 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(uly.UlyError) as e:
+        plan.prompt_attention(q, k, v, o, too_many)
+    assert e.value.status == uly.ULY_ERR_UNSUPPORTED
+
+
+def test_offsets_past_32_bits():
+    """A sequence at the end of tensors of more than 2^32 bytes."""
+    from ulysses_sequence_attention_uly_gb300 import Plan
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    n, H, D, tail = 450000, 40, 128, 1000
+    plan = Plan(1, 1, n, 0, "none", H, H, D)
+    c = R.Prompt("tail", (tail,), (300, 77), H, H, D, first=500)
+    small = R.prompt_inputs(c, 20)
+    big = {}
+    for t in ("q", "k", "v", "o", "lse"):
+        x = small[t][0]
+        big[t] = torch.zeros((1, n) + x.shape[2:], dtype=x.dtype, device="cuda")
+        big[t][:, n - tail:] = x
+    starts = (small["starts"] + (n - tail)).int()
+    plan.prompt_attention([big["q"]], [big["k"]], [big["v"]], [big["o"]], starts, lse=[big["lse"]])
+    assert plan.sync_status() == 0
+    R.check_prompt(c, small, [big["o"][:, n - tail:]], [big["lse"][:, n - tail:]])
+    assert not big["o"][:, :n - tail].any() and not big["lse"][:, :n - tail].any()
+
+
 def test_more_sequences_than_threads():
     lens = tuple((i * 7) % 4 for i in range(2500))
     c = R.Prompt("many", (2200, 2000), lens, 2, 2, 64, first=11)
