@@ -522,7 +522,9 @@ int64_t uly_norm_rope_backward_workspace(const uly_plan* plan);
  * sequence s holds the rows [seq_starts[s], seq_starts[s + 1]) of the global row
  * order, wherever the shards' ends lie, and its row i attends to its rows j <= i:
  *     o_i = sum_j softmax_j(scale <q_i, k_j>) v_j        (bf16, rounded once)
- * q head h uses kv head h / (Hq/Hkv); q, k, v, o are shards as in
+ * P (after the exponential) is rounded to bf16 as an operand of the product with
+ * V, as in uly_sp_attention; scores, the sum of the exponentials and of the product
+ * are f32.  q head h uses kv head h / (Hq/Hkv); q, k, v, o are shards as in
  * uly_sp_attention, lse (may be NULL) f32 [1, rows, Hq] per shard: the natural
  * logarithm of the sum of the row's exponentials.
  *   seq_starts: device int32 [n_seqs + 1], non-decreasing, within [0, rows]
@@ -588,6 +590,10 @@ typedef struct uly_cache {
  *     rows of no sequence are not read.  lens: device int32 [n_seqs].
  *     A row whose position is negative or past the table's width, or whose page
  *     is outside [0, n_pages), is dropped.
+ *   Rows that lie in several tensors (the shards of uly_sp_prompt_attention) go in
+ *     with a call for each, in the rows' order on one stream: starts less the
+ *     tensor's first row and clamped to its rows, lens the tokens up to its end.  A
+ *     page that a tensor's end cuts is taken up again, as any page that holds tokens.
  *   A page may take new rows at one place of the table only: not of two
  *     sequences, and not twice of one.  Values have to be finite (a NaN stays a
  *   NaN; an infinity takes the precision of its page and head).
@@ -606,7 +612,10 @@ int uly_cache_append(const uly_cache* cache, const void* k, const void* v, int64
  * k and v as the cache holds them:
  *     o = sum_j softmax_j(scale <q, k_j>) v_j            (bf16, rounded once)
  * q head h uses cache head h / (Hq / H).  One row a sequence is plain
- * generation; a few are a guess that is checked, or the end of a prompt.
+ * generation; a few are a guess that is checked, or the end of a prompt.  What it
+ * costs follows the cache's bytes for up to 16 rows of q a cache head (new tokens
+ * times Hq / H); every 16 more go through the codes again, so that a chunk of
+ * hundreds of tokens costs as many times that.
  *   o: bf16 [n_rows, Hq, D]; lse: NULL or f32 [n_rows, Hq] (natural log-sum-exp).
  *     A row that has no key (lens[s] = 0, a position below zero) gets 0 and
  *     -inf; rows of no sequence are left as they were.

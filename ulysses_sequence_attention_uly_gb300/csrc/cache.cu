@@ -248,8 +248,8 @@ cudaError_t launch_cache_append(const AppendParams& p, int D, cudaStream_t s) {
 // multiplications (G q heads a cache head, T new rows a sequence), which is far
 // below what even mma.sync does in the time that HBM takes for it (tensor pipe 16%
 // of cycles).  32 heads on 8 of 128: two sequences of 120 and 131 thousand tokens
-// 84 us, 6.1 TB/s (the loads alone, without arithmetic: 82); 64 sequences of 200 to
-// 8000 tokens 66 us, 5.1 TB/s; one of 499 tokens 8 us.
+// 86 us, 6.0 TB/s (the loads alone, without arithmetic: 82); 64 sequences of 200 to
+// 8000 tokens 67 us, 5.0 TB/s; one of 499 tokens 8 us.
 //
 // A unit is (sequence, 8 NT rows of its queries, cache head); a row is (token, q
 // head of the group).  A unit's keys, in blocks of 64, are cut into equal parts of
@@ -388,8 +388,14 @@ struct CachedCfg {
 // Parts of a unit, for `total` blocks of all units.  Few units have many parts
 // each: as many in all as CTAs run at once, and none more, since one more would
 // run alone.  Of many units the parts cannot be that even, and where they are
-// long, half of that length keeps the last ones from running alone (64 sequences,
-// 8 heads: 71 -> 65 us; 64-wide, half as long: 39 -> 44).
+// long (kLongPart and more of codes), half of that length keeps the last ones from
+// running alone.  64 ragged sequences, 8 heads, us with parts of a slot's share and
+// of half of it, by the share:
+//   128-wide   53 KB 23.1, 23.9   95 KB 28.3, 27.7   185 KB 37.7, 34.9   363 KB 58.6, 51.6   719 KB 101, 84
+//    64-wide   48 KB 18.8, 23.3   93 KB 25.3, 27.7   181 KB 35.7, 36.8   359 KB 58.4, 55.8   715 KB 104, 93
+// So 64-wide heads cross between 180 and 360 KB, 128-wide ones near 90 already; one
+// constant for both gives the latter up to 8% away in between.  200 sequences are
+// within 2% either way.
 template <int D>
 __device__ __forceinline__ int unit_parts(const CachedParams& p, const SeqWork& w, int64_t total) {
   int64_t n;

@@ -37,12 +37,11 @@
 //
 // What bounds it (ncu, 8192 rows of 32 heads on 8): long items run at 2500 to 2600
 // cycles a step, of which the four products take 2048 and the operands' way through
-// shared memory 2000 (S reads both operands from there); tensor pipe active 73% of
-// cycles, DRAM 5%.  16384 rows of 32 heads on 8: 1.29 ms, 1704 TFLOP/s of admitted
-// pairs; 27280 rows of 40 heads 4.40 ms, 1734 (for seconds on end 5.1 ms, at the
-// power limit).  Short items: what is around the steps, about 3 us an item, that
+// shared memory 2000 (S reads both operands from there); tensor pipe active 74% of
+// cycles, DRAM 5%.  27280 rows of 40 heads 4.39 ms after a pause, 1737 TFLOP/s of
+// admitted pairs (for seconds on end 5.1 ms, 1500, at the power limit).  Short items: what is around the steps, about 3 us an item, that
 // follows one upon the other (the last product, the store, the next softmax): 24
-// prompts of 30 to 900 rows 58 us, tensor pipe 32%, DRAM 20%.
+// prompts of 30 to 900 rows 58 to 59 us, tensor pipe 32%, DRAM 20%.
 #include <atomic>
 
 #include "serve.cuh"
