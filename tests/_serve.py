@@ -219,13 +219,13 @@ def to_e4m3(x):
     return ((x / step).round() * step).clamp(-448, 448)
 
 
-def cached_reference(c, d, scale=None, small=2.0 ** -25):
+def cached_reference(c, d, scale=None):
     """o [rows, Hq, D], lse and the bound of o's error.
 
     The bound: the weights (the exponentials times their pages' scales) are
     operands of an f16 product, 2^-11 of each, or half an f16 step of 2^-24 of the
-    largest weight where they are small against it (`small`: of the largest); the
-    output is rounded to bf16 once (2^-8); r = 2^-13 as for prompts."""
+    largest weight where they are small against it; the output is rounded to bf16
+    once (2^-8); r = 2^-13 as for prompts."""
     scale = 1.0 / math.sqrt(c.D) if scale is None else scale
     n_pages = d["k_pages"].shape[0]
     table, starts, lens = (d[n].tolist() for n in ("table", "starts", "lens"))
@@ -258,7 +258,7 @@ def cached_reference(c, d, scale=None, small=2.0 ** -25):
         p = p / p.sum(-1, keepdim=True).clamp(min=1e-300)
         o[a:b] = torch.einsum("hij,jhd->ihd", p, vv)
         err[a:b] = torch.einsum("hij,jhd->ihd", p, vv.abs()) * (2.0 ** -11 + 2.0 ** -13) + \
-            small * (p * vs.T[:, None]).amax(-1).T[..., None] * \
+            2.0 ** -25 * (p * vs.T[:, None]).amax(-1).T[..., None] * \
             torch.einsum("ij,jhd->ihd", ok.double(), vv.abs() / vs[..., None])
     return o, lse, err * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs() + 1e-30, inside
 

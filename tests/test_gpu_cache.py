@@ -272,8 +272,18 @@ def test_attention_a_page_of_a_far_larger_scale(D, T):
     d["v_pages"].view(torch.uint8)[page, :, :, ::2] = 0
     o, lse = R.attend(cache, c, d)
     torch.cuda.synchronize()
-    want, wl, err, _ = R.cached_reference(c, d, small=2.0 ** -32)
-    R.check_rows(o, want, err, "o")
+    want, wl, _, _ = R.cached_reference(c, d)
+    n, page = c.lens[0], c.page
+    at = d["table"][0, torch.arange(n, device="cuda") // page].long()
+    k, v = (d[t + "_pages"].double()[at, :, torch.arange(n, device="cuda") % page].repeat_interleave(2, 1) for t in "kv")
+    ks, vs = (d[t + "_scale"].double()[at].repeat_interleave(2, 1) for t in "kv")  # [keys, heads]
+    z = torch.einsum("ihd,jhd->ihj", d["q"].double(), k * ks[..., None]) / math.sqrt(D)
+    ok = torch.arange(n, device="cuda") <= n - T + torch.arange(T, device="cuda")[:, None]
+    w = z.masked_fill(~ok[:, None], -math.inf).softmax(-1) * vs.T  # weights of the codes
+    # an f16 rounding of each weight (2^-11, or 2^-32 of the largest), 32-bit sums, and bf16 once
+    err = torch.einsum("ihj,jhd->ihd", w * (2.0 ** -11 + 2.0 ** -13) + 2.0 ** -32 * w.amax(-1, keepdim=True) * ok[:, None],
+                       v.abs())
+    R.check_rows(o, want, err * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs() + 1e-30, "o")
     R.check_rows(lse, wl, 2.0 ** -13 + 2.0 ** -22 * wl.abs(), "lse")
 
 
